@@ -193,6 +193,101 @@ svpa_status svpa_paged_verify_attn(const svpa_attn_params *p, const void *q,
                                    size_t workspace_bytes, int32_t *error_flag,
                                    void *stream);
 
+/*
+ * Geometry of one prompt-attention call (svpa_paged_prompt_attn).
+ */
+typedef struct svpa_prompt_params {
+    int32_t batch;              /* B >= 0 sequences (up to 2^20)              */
+    int32_t total_q;            /* T: rows of q and out (up to 2^28)          */
+    int32_t num_q_heads;        /* Hq                                         */
+    int32_t num_kv_heads;       /* Hkv, Hq % Hkv == 0, Hq / Hkv <= 128        */
+    int32_t head_dim;           /* D: 64 or 128                               */
+    int32_t block_size;         /* tokens per page: 16                        */
+    int32_t max_blocks_per_seq; /* row stride of block_table                  */
+    int32_t num_blocks;         /* physical pages in the pool                 */
+    int32_t kv_dtype;           /* SVPA_KV_BF16 (FP8: SVPA_ERR_UNSUPPORTED)   */
+    float sm_scale;             /* softmax scale, normally 1/sqrt(D)          */
+    int32_t q_stride;           /* elements from one token of q to the next, a
+                                   multiple of 8 (a slice of a fused
+                                   projection); 0 = contiguous                */
+} svpa_prompt_params;
+
+/* Bytes of workspace svpa_paged_prompt_attn needs for `p`; to be zero-filled
+ * once before its first use (every completed call leaves its counters zero). */
+svpa_status svpa_paged_prompt_attn_workspace_size(const svpa_prompt_params *p, size_t *bytes);
+
+/*
+ * Prompt attention over pages: causal attention of packed query tokens.
+ *
+ * Sequence b has the query tokens cu_seqlens[b] .. cu_seqlens[b+1] - 1, the
+ * last of its kv_lens[b] positions (all of them for a whole prompt; fewer for
+ * a chunk behind cached or shared pages, down to a single token), whose K/V
+ * are already in its pages.  Query token i of n sees every position p <=
+ * kv_lens[b] - n + i:
+ *   out[t][h] = softmax_p( q[t][h] . K[p] * sm_scale ) . V[p]
+ * with position p in page block_table[b][p / 16] at slot p % 16 and query
+ * head h reading kv head h / (Hq / Hkv).
+ *
+ *  q            bf16 [T, Hq, D], tokens q_stride elements apart; 16-byte aligned
+ *  k_pool, v_pool  bf16 [num_blocks, Hkv, 16, D], 16-byte aligned
+ *  block_table  int32 [B, max_blocks_per_seq]; entries past a sequence's last
+ *               page are ignored
+ *  cu_seqlens   int32 [B + 1], cu_seqlens[0] = 0, non-decreasing, at most T
+ *  kv_lens      int32 [B], at least the sequence's query tokens, at most
+ *               16 * max_blocks_per_seq; not read for a sequence without any
+ *  out          bf16 [T, Hq, D] (written); rows from cu_seqlens[B] on are left
+ *               as they were
+ *  lse          fp32 [T, Hq] natural-log sum of exp(scores), or NULL
+ * A sequence with bad offsets or a bad length raises SVPA_DEVERR_BAD_VALUE, a
+ * block id outside the pool SVPA_DEVERR_BAD_BLOCK.  Scores and sums are fp32;
+ * the weights of a row are rounded to bf16 for their product with V.  K/V
+ * values of every position below kv_lens[b] must be finite (the weight of a
+ * position that a token does not see is an exact zero).
+ */
+svpa_status svpa_paged_prompt_attn(const svpa_prompt_params *p, const void *q,
+                                   const void *k_pool, const void *v_pool,
+                                   const int32_t *block_table,
+                                   const int32_t *cu_seqlens,
+                                   const int32_t *kv_lens, void *out, float *lse,
+                                   void *workspace, size_t workspace_bytes,
+                                   int32_t *error_flag, void *stream);
+
+/* Bytes of workspace svpa_prefix_verify_attn needs; zero-filled once before
+ * its first use (every completed call leaves its counters zero). */
+svpa_status svpa_prefix_verify_attn_workspace_size(const svpa_attn_params *p,
+                                                   int32_t prefix_len, size_t *bytes);
+
+/*
+ * Paged verification attention of a batch that shares a long prefix: the
+ * result of svpa_paged_verify_attn, with the attention over the shared prefix
+ * formed once for all sequences instead of once per sequence.
+ *
+ * Sources: "Speculative Decoding & KV-Cache PagedAttention in Enterprise LLM
+ * Serving", shared-prefix section (one physical copy of a system prompt's
+ * blocks, held by every request's table).
+ *
+ *  prefix_blocks int32 [prefix_len / 16]: the blocks of the prefix
+ *  prefix_len    HOST: tokens of the prefix, a multiple of 16; 0 = none
+ *                (prefix_blocks may then be NULL)
+ * The other arguments are those of svpa_paged_verify_attn, with whole block
+ * tables: a sequence joins the shared prefix when context_lens[b] >=
+ * prefix_len and its table begins with prefix_blocks, and attends its whole
+ * history by itself otherwise, so the result never depends on the prefix
+ * given.  bf16 pages; FP8 pages and variant 1 are refused
+ * (SVPA_ERR_UNSUPPORTED); split_pages is not used.  One kernel on `stream`,
+ * two when the own parts are split over idle SMs (small batches).  K/V values
+ * of every position below context_lens[b] + n_q must be finite.
+ */
+svpa_status svpa_prefix_verify_attn(const svpa_attn_params *p, const void *q,
+                                    const void *k_pool, const void *v_pool,
+                                    const int32_t *prefix_blocks, int32_t prefix_len,
+                                    const int32_t *block_table,
+                                    const int32_t *context_lens,
+                                    const uint64_t *ancestor_mask, void *out,
+                                    float *lse, void *workspace,
+                                    size_t workspace_bytes, int32_t *error_flag,
+                                    void *stream);
+
 /* Bytes of workspace the samplers take for `batch` rows of `vocab` tokens.
  * Reserved: the samplers keep no state in it (the size is 256 bytes); pass a
  * 16-byte aligned device buffer of at least that size. */

@@ -32,6 +32,8 @@ SOURCES = {
     "svpa_logits_api.cu": [],
     "svpa_step_api.cu": [],
     "wait_selftest.cu": [],
+    "packed_attn_tc.cu": [],
+    "svpa_prompt_api.cu": [],
 }
 
 

@@ -1,0 +1,43 @@
+// packed_attn.h -- arguments and launches of the packed-query attention
+// kernel (packed_attn_tc.cu): prompt attention over pages and verification
+// attention behind a shared prefix.
+#pragma once
+
+#include "svpa_internal.h"
+
+namespace svpa {
+
+// Query rows of one 128-row MMA tile: tpt tokens x G heads of one kv head.
+struct PackedArgs {
+    const int32_t *block_table;    // [B, max_blocks]
+    const int32_t *cu;             // [B + 1] packed query offsets (prompt)
+    const int32_t *lens;           // [B] kv lengths (prompt) or committed histories (verify)
+    const int32_t *prefix_blocks;  // [prefix_pages] (verify)
+    __nv_bfloat16 *out;            // [T, Hq, D]
+    float *lse;                    // [T, Hq] or null
+    float *part_o;                 // [slots, T, Hq, D] unnormalised partial outputs
+    float2 *part_ml;               // [slots, T, Hq] (reference maximum in log2 units, sum)
+    int32_t *member;               // [B] the sequence's table begins with the prefix (split verify only)
+    int32_t *sched;                // [3]: next unit, CTAs finished, warps that wrote a prefix unit; zero between calls
+    int32_t *err;
+    int32_t verify;                // 0 = prompt, 1 = verification behind a shared prefix
+    int32_t B, T, Hq, Hkv, G, n_q, tpt;
+    int32_t max_blocks, num_blocks, prefix_pages;
+    int32_t pairs;                 // prompt: unit slots per kv head; verify: tile pairs of the prefix units
+    int32_t p_units, total_units;  // prefix units come first
+    int32_t p_splits, s_splits;    // KV splits of the prefix units and of the others
+    float scale_log2;
+    unsigned long long anc[kMaxNq];
+};
+
+struct PackedMaps {
+    CUtensorMap k, v;       // one (page, kv head) tile per copy
+    CUtensorMap qt[2];      // 64-column slabs of tpt tokens x G heads
+    CUtensorMap qs[2];      // the same of n_q tokens (verify: one sequence)
+};
+
+cudaError_t launch_packed_attn(const PackedMaps &m, const PackedArgs &a, int head_dim, int grid, cudaStream_t stream);
+// Merges the partial rows when units were split (s_splits > 1).
+cudaError_t launch_packed_combine(const PackedArgs &a, int head_dim, cudaStream_t stream);
+
+}  // namespace svpa

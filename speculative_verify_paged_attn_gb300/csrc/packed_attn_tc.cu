@@ -1,0 +1,830 @@
+// packed_attn_tc.cu -- attention of many query tokens over paged K/V on the
+// 5th-generation tensor cores (tcgen05 + TMEM), sm_103a.
+//
+//   out[t][h] = sum_p softmax_p( q[t][h] . K[p] * scale ) V[p],  p visible to t
+//
+// Two entry points share it.  Prompt attention: token t of a sequence sees
+// the positions up to its own.  Verification behind a shared prefix: with the
+// visible set split as prefix + own part,
+//   m = max(m_p, m_o),  l = l_p 2^(m_p - m) + l_o 2^(m_o - m),
+//   out = (O_p 2^(m_p - m) + O_o 2^(m_o - m)) / l
+// so the prefix part (O_p, m_p, l_p) of ALL sequences' queries is formed by
+// units that read the prefix pages once per 256 query rows instead of once
+// per sequence, and joined with each sequence's own part.
+//
+// A query tile is 128 rows: 128 / G tokens x the G query heads of one kv head
+// (all heads of a group share the K/V tile).  A unit of work is
+//   pair: two query tiles A, B over the same K/V blocks (128 tokens each), or
+//   alt:  one query tile whose even blocks go to A and odd blocks to B
+//         (tiles too small to pair: one sequence's drafts, short prompts);
+// either way two softmax groups work on two score tiles in turn, so that the
+// tensor cores compute one while the exponentials of the other are taken.
+// Persistent CTAs, one per SM (TMEM 512 columns, 224 KB of shared memory),
+// take units from an atomic counter.  Warps:
+//   0      producer: decodes units, streams K and V blocks (8 pages per
+//          block, one TMA copy per page and kv head) through one ring, and
+//          the query tiles;
+//   1      MMA issuer (one thread) and TMEM owner:  S_t = Q_t K^T  and
+//          O_t += P_t V, P_t read from TMEM over S_t's own columns.  Per
+//          block: PV_A, S_A, PV_B, S_B;
+//   2-5    softmax of tile A, one thread per query row: mask, lazy running
+//   6-9    maximum (O_t rescaled only when it grows by more than 2^8), fp32
+//          row sum, P as bf16 (the MMA's input type; the sum is taken before
+//          that rounding); then the unit's epilogue.
+// A commit on S_t's barrier covers the PV_t issued before it, so a softmax
+// warp that sees S_t may rescale O_t at once.  All waits are bounded.
+#include <cuda_bf16.h>
+#include <math_constants.h>
+
+#include <algorithm>
+
+#include "packed_attn.h"
+#include "svpa_device.cuh"
+
+namespace svpa {
+
+namespace {
+
+constexpr int kThreads = 320;
+constexpr int kPagesPerBlock = 8;
+constexpr int kNB = kPagesPerBlock * kBlockSize;  // kv tokens per block
+constexpr int kRing = 5;                          // K and V tiles in flight
+constexpr float kRescaleLog2 = 8.f;
+constexpr uint32_t kTmemCols = 512, kTmemO = 0, kTmemS = 256;
+constexpr int kDonePerUnit = 8;  // softmax warps that report a prefix unit written
+constexpr float kLn2 = 0.69314718055994530942f;
+
+enum { kEnd = 0, kPair = 1, kAlt = 2 };
+
+struct Unit {
+    int32_t kind;        // kEnd, kPair, kAlt
+    int32_t h;           // kv head
+    int32_t tok0, tok1;  // query tokens [tok0, tok1) of the unit
+    int32_t nA, nB;      // blocks of tile A and tile B
+    int32_t base;        // ring index of the unit's first K tile
+    int32_t pos0;        // kv position of its first block
+    int32_t kv_end;      // positions from here on hold no token
+    int32_t lim0;        // token tok0 sees positions below lim0 ...
+    int32_t causal;      // ... and each later token one more, or
+    int32_t use_anc;     // the draft slots of its ancestors
+    int32_t slot;        // partial slot, or -1: final
+    int32_t merge;       // join the prefix partials
+    int32_t prefix;      // a prefix unit: count it when written
+};
+
+template <int D>
+struct Smem {
+    static constexpr int kTile = kNB * D * 2;
+    static constexpr int kQTile = 128 * D * 2;
+    uint8_t q[2][kQTile];  // 1024-aligned: [64-column slab][128 rows][128 B]
+    uint8_t kv[kRing][kTile];
+    uint64_t full[kRing], empty[kRing];
+    uint64_t q_full, q_empty;
+    uint64_t s_full[2], p_full[2], o_full[2];
+    uint64_t both;  // the two softmax groups meet
+    Unit unit;
+    float2 stat[2][128];
+    uint32_t tmem_base;
+};
+static_assert(sizeof(Smem<128>) <= 232448, "packed attention shared memory");
+
+__device__ __forceinline__ uint64_t policy_evict_normal() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+
+__device__ __forceinline__ int ld_acquire(const int32_t *p) {
+    int v;
+    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int c0, int c1, int c2, uint64_t *bar,
+                                            uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_"
+        "hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
+}
+
+// Largest b with cu[b] / step + b <= slot (cu[0] = 0), by the whole warp:
+// 32 candidates a round.
+__device__ __forceinline__ int find_sequence(const int32_t *cu, int B, int step, int slot, int lane) {
+    int lo = 0, n = B;  // the answer is in [lo, lo + n)
+    while (n > 1) {
+        const int stride = (n + 31) / 32;
+        const int b = lo + lane * stride;
+        const bool le = lane * stride < n && __ldg(cu + b) / step + b <= slot;
+        const unsigned m = __ballot_sync(0xffffffffu, le);
+        const int k = m ? 31 - __clz((int)m) : 0;
+        lo += k * stride;
+        n = min(stride, n - k * stride);
+    }
+    return lo;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    packed_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                       const __grid_constant__ CUtensorMap mqt0, const __grid_constant__ CUtensorMap mqt1,
+                       const __grid_constant__ CUtensorMap mqs0, const __grid_constant__ CUtensorMap mqs1,
+                       const __grid_constant__ PackedArgs a) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    using SM = Smem<D>;
+    // all of the opt-in shared memory is used, with no room to move the base:
+    // the only shared memory of this kernel, it starts on its 1 KB alignment
+    SM &sm = *reinterpret_cast<SM *>(smem_raw);
+    if (smem_u32(smem_raw) & 1023u) {
+        if (threadIdx.x == 0) raise_error(a.err, SVPA_DEVERR_BAD_VALUE);
+        return;
+    }
+    constexpr int kSlabs = D / 64;
+    constexpr int kQSlab = 128 * 128;
+    constexpr int kPageBytes = kBlockSize * D * 2;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(&sm.full[i], 1);
+            mbar_init(&sm.empty[i], 1);
+        }
+        mbar_init(&sm.both, 8);
+        mbar_init(&sm.q_full, 1);
+        mbar_init(&sm.q_empty, 9);  // the MMA issuer and the eight softmax warps
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&sm.s_full[t], 1);
+            mbar_init(&sm.p_full[t], 4);
+            mbar_init(&sm.o_full[t], 1);
+        }
+        fence_mbar_init();
+    }
+    // rows of a query tile past tpt * G are never written by the copies
+    for (int x = threadIdx.x; x < 2 * SM::kQTile / 16; x += kThreads)
+        reinterpret_cast<uint4 *>(&sm.q[0][0])[x] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+    if (warp == 1) {
+        tmem_alloc(&sm.tmem_base, kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem_base;
+
+    if (warp == 0) {
+        // ================================================= producer
+        const uint64_t keep = policy_evict_normal(), stream_once = policy_evict_first();
+        if (lane == 0) {
+            prefetch_tensormap(&mk);
+            prefetch_tensormap(&mv);
+            prefetch_tensormap(&mqt0);
+            prefetch_tensormap(&mqt1);
+        }
+        int tile = 0, units = 0;  // ring tiles issued, units started
+        bool ok = true;
+        const int tpt2 = 2 * a.tpt;
+        while (ok) {
+            int u = 0;
+            if (lane == 0) u = atomicAdd(&a.sched[0], 1);
+            u = __shfl_sync(0xffffffffu, u, 0);
+            if (u >= a.total_units) break;
+            // ---- decode
+            Unit w;
+            const int32_t *bt;
+            int n_tok_load, nblk;     // tokens of one query tile's copy, blocks
+            uint64_t pol = keep;
+            w.use_anc = w.merge = w.prefix = 0;
+            w.causal = 0;
+            w.slot = -1;
+            int page0, npages;        // of the unit's kv range
+            if (u < a.p_units) {
+                const int h = u % a.Hkv, x = u / a.Hkv;
+                const int split = x % a.p_splits, pair = x / a.p_splits;
+                w.h = h;
+                w.tok0 = pair * tpt2;
+                w.tok1 = min(w.tok0 + tpt2, a.T);
+                bt = a.prefix_blocks;
+                const int nb = (a.prefix_pages + kPagesPerBlock - 1) / kPagesPerBlock;
+                const int b0 = (int)((long long)nb * split / a.p_splits);
+                const int b1 = (int)((long long)nb * (split + 1) / a.p_splits);
+                page0 = b0 * kPagesPerBlock;
+                npages = min(a.prefix_pages, b1 * kPagesPerBlock) - page0;
+                nblk = b1 - b0;
+                w.kv_end = w.lim0 = a.prefix_pages * kBlockSize;
+                w.kind = w.tok1 - w.tok0 > a.tpt ? kPair : kAlt;
+                w.slot = split;
+                w.prefix = 1;
+                n_tok_load = a.tpt;
+            } else if (a.verify) {
+                const int x = u - a.p_units;
+                const int h = x % a.Hkv, y = x / a.Hkv;
+                const int split = y % a.s_splits, b = y / a.s_splits;
+                const int L = __ldg(a.lens + b);
+                bt = a.block_table + (size_t)b * a.max_blocks;
+                const long long total = (long long)L + a.n_q;
+                if (L < 0 || total > (long long)a.max_blocks * kBlockSize) {
+                    if (lane == 0 && split == 0 && h == 0) raise_error(a.err, SVPA_DEVERR_BAD_VALUE);
+                    continue;
+                }
+                // a sequence whose table begins with the prefix joins it; any
+                // other attends its whole history itself
+                bool mine = L >= a.prefix_pages * kBlockSize;
+                if (mine) {
+                    for (int i0 = 0; i0 < a.prefix_pages && mine; i0 += 256) {
+                        int p[8], q[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const int i = i0 + 32 * k + lane;
+                            const bool in = i < a.prefix_pages;
+                            p[k] = in ? __ldg(bt + i) : 0;
+                            q[k] = in ? __ldg(a.prefix_blocks + i) : 0;
+                        }
+                        bool same = true;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) same = same && p[k] == q[k];
+                        mine = __all_sync(0xffffffffu, same);
+                    }
+                }
+                if (a.member && lane == 0 && split == 0 && h == 0) a.member[b] = mine ? 1 : 0;
+                const int first = mine ? a.prefix_pages : 0;
+                const int pages = (int)((total + kBlockSize - 1) / kBlockSize) - first;
+                const int nb = (pages + kPagesPerBlock - 1) / kPagesPerBlock;
+                const int b0 = (int)((long long)nb * split / a.s_splits);
+                const int b1 = (int)((long long)nb * (split + 1) / a.s_splits);
+                page0 = first + b0 * kPagesPerBlock;
+                npages = min(pages, b1 * kPagesPerBlock) - b0 * kPagesPerBlock;
+                nblk = b1 - b0;
+                w.h = h;
+                w.tok0 = b * a.n_q;
+                w.tok1 = w.tok0 + a.n_q;
+                w.kv_end = (int)total;
+                w.lim0 = L;
+                w.use_anc = 1;
+                w.kind = kAlt;
+                w.merge = mine && a.s_splits == 1;
+                w.slot = a.s_splits == 1 ? -1 : a.p_splits + split;
+                n_tok_load = a.n_q;
+                pol = stream_once;
+            } else {
+                // long tiles first: the last tiles of a sequence see the most
+                const int h = u % a.Hkv, y = u / a.Hkv;
+                const int split = y % a.s_splits, slot = a.pairs - 1 - y / a.s_splits;
+                const int b = find_sequence(a.cu, a.B, tpt2, slot, lane);
+                const int c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1);
+                const int kv = __ldg(a.lens + b);
+                const int t0 = c0 + (slot - (c0 / tpt2 + b)) * tpt2;
+                if (t0 >= c1) {
+                    // no tile here; a bad row of offsets is reported with its first slot
+                    if (lane == 0 && (c0 < 0 || c1 < c0 || c1 > a.T)) raise_error(a.err, SVPA_DEVERR_BAD_VALUE);
+                    continue;
+                }
+                if (c0 < 0 || c1 > a.T || t0 < c0 || kv < c1 - c0 || kv > (long long)a.max_blocks * kBlockSize) {
+                    if (lane == 0) raise_error(a.err, SVPA_DEVERR_BAD_VALUE);
+                    continue;
+                }
+                w.h = h;
+                w.tok0 = t0;
+                w.tok1 = min(t0 + tpt2, c1);
+                w.lim0 = kv - (c1 - t0) + 1;
+                w.causal = 1;
+                w.kv_end = kv;
+                bt = a.block_table + (size_t)b * a.max_blocks;
+                const int seen = w.lim0 + (w.tok1 - 1 - t0);  // positions the unit's last token sees
+                const int pages = (seen + kBlockSize - 1) / kBlockSize;
+                const int nb = (seen + kNB - 1) / kNB;
+                const int b0 = (int)((long long)nb * split / a.s_splits);
+                const int b1 = (int)((long long)nb * (split + 1) / a.s_splits);
+                page0 = b0 * kPagesPerBlock;
+                npages = min(pages, b1 * kPagesPerBlock) - page0;
+                nblk = b1 - b0;
+                w.kind = w.tok1 - w.tok0 > a.tpt ? kPair : kAlt;
+                w.slot = a.s_splits == 1 ? -1 : split;
+                n_tok_load = a.tpt;
+            }
+            w.pos0 = page0 * kBlockSize;
+            if (w.kind == kPair) {
+                w.nB = nblk;
+                w.nA = nblk;
+                if (w.causal) {
+                    // tile A's last token may end one block or more earlier
+                    const int seenA = w.lim0 + a.tpt - 1;
+                    w.nA = min(nblk, max(0, (seenA - w.pos0 + kNB - 1) / kNB));
+                }
+            } else {
+                w.nA = (nblk + 1) / 2;
+                w.nB = nblk / 2;
+            }
+            w.base = tile;
+
+            auto issue_q = [&]() -> bool {
+                if (units >= 1) {
+                    int good = 1;
+                    if (lane == 0) good = mbar_wait(&sm.q_empty, (uint32_t)((units - 1) & 1), a.err);
+                    if (!__shfl_sync(0xffffffffu, good, 0)) return false;
+                }
+                if (lane == 0) {
+                    sm.unit = w;
+                    const bool two = w.kind == kPair;
+                    const uint32_t bytes = nblk == 0 ? 0u : (uint32_t)(n_tok_load * a.G * D * 2) * (two ? 2u : 1u);
+                    mbar_arrive_expect_tx(&sm.q_full, bytes);
+                    if (bytes) {
+                        const bool seq = w.use_anc;
+#pragma unroll
+                        for (int s = 0; s < kSlabs; ++s) {
+                            const CUtensorMap *m = seq ? (s ? &mqs1 : &mqs0) : (s ? &mqt1 : &mqt0);
+                            tma_load_3d(&sm.q[0][s * kQSlab], m, 0, w.h * a.G, w.tok0, &sm.q_full, pol);
+                            if (two)
+                                tma_load_3d(&sm.q[1][s * kQSlab], m, 0, w.h * a.G, w.tok0 + a.tpt, &sm.q_full, pol);
+                        }
+                    }
+                }
+                __syncwarp();
+                return true;
+            };
+            // K and V tiles in the order the MMA issuer takes them
+            auto issue_tile = [&](const CUtensorMap *map, int id) -> bool {
+                const int s = tile % kRing;
+                if (tile >= kRing) {
+                    int good = 1;
+                    if (lane == 0) good = mbar_wait(&sm.empty[s], (uint32_t)(((tile / kRing) & 1) ^ 1), a.err);
+                    if (!__shfl_sync(0xffffffffu, good, 0)) return false;
+                }
+                if (lane == 0) mbar_arrive_expect_tx(&sm.full[s], (uint32_t)SM::kTile);
+                __syncwarp();
+                if (lane < kPagesPerBlock)
+                    tma_load_5d(&sm.kv[s][lane * kPageBytes], map, 0, 0, 0, 0, id, &sm.full[s], pol);
+                ++tile;
+                return true;
+            };
+            const int oob = a.num_blocks * a.Hkv;  // a page that does not exist: zeros
+            int ids = 0;
+            bool q_out = false;
+            for (int j = 0; j < nblk && ok; ++j) {
+                if ((j & 3) == 0) {
+                    const int i = j * kPagesPerBlock + lane;
+                    ids = oob;
+                    if (i < npages) {
+                        int blk = __ldg(bt + page0 + i);
+                        if (blk < 0 || blk >= a.num_blocks) {
+                            raise_error(a.err, SVPA_DEVERR_BAD_BLOCK);
+                            blk = 0;
+                        }
+                        ids = blk * a.Hkv + w.h;
+                    }
+                }
+                const int id = __shfl_sync(0xffffffffu, ids, ((j & 3) * kPagesPerBlock + (lane & 7)) & 31);
+                ok = issue_tile(&mk, id);
+                if (ok) ok = issue_tile(&mv, id);
+                // the first block of the next unit is on its way before the
+                // query buffers are free
+                if (ok && !q_out) {
+                    ok = issue_q();
+                    q_out = true;
+                }
+            }
+            if (ok && !q_out) ok = issue_q();
+            ++units;
+        }
+        if (lane == 0) {
+            if (ok && units >= 1) ok = mbar_wait(&sm.q_empty, (uint32_t)((units - 1) & 1), a.err);
+            if (ok) {
+                sm.unit.kind = kEnd;
+                mbar_arrive(&sm.q_full);
+            }
+            // copies still in flight land before the CTA ends
+            for (int i = tile >= kRing ? tile - kRing : 0; i < tile; ++i)
+                if (!mbar_wait(&sm.full[i % kRing], (uint32_t)((i / kRing) & 1), a.err)) break;
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ================================================= MMA issuer
+        if (lane == 0) {
+            constexpr uint32_t idS = umma_idesc_bf16(128, kNB, false);
+            constexpr uint32_t idPV = umma_idesc_bf16(128, D, true);
+            const uint32_t qaddr = smem_u32(&sm.q[0][0]);
+            uint32_t np[2] = {0, 0};  // P tiles taken
+            bool ok = true;
+            for (int unit = 0; ok; ++unit) {
+                if (!mbar_wait(&sm.q_full, (uint32_t)(unit & 1), a.err)) break;
+                const Unit w = sm.unit;
+                if (w.kind == kEnd) break;
+                const bool pair = w.kind == kPair;
+                const int last = max(w.nA, w.nB);
+                if (last == 0) mbar_arrive(&sm.q_empty);
+                for (int j = 0; j <= last && ok && last > 0; ++j) {
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const int n = t ? w.nB : w.nA;
+                        const uint32_t dS = tmem + kTmemS + (uint32_t)t * kNB;
+                        if (ok && j >= 1 && j - 1 < n) {
+                            // O_t += P_t V
+                            const int i = w.base + 2 * (pair ? j - 1 : 2 * (j - 1) + t) + 1;
+                            ok = mbar_wait(&sm.p_full[t], np[t] & 1u, a.err) &&
+                                 mbar_wait(&sm.full[i % kRing], (uint32_t)((i / kRing) & 1), a.err);
+                            if (!ok) break;
+                            ++np[t];
+                            tc_fence_after();
+                            const uint32_t va = smem_u32(sm.kv[i % kRing]);
+                            const uint32_t dO = tmem + kTmemO + (uint32_t)t * 128;
+#pragma unroll
+                            for (int kt = 0; kt < kNB / 16; ++kt)
+                                umma_bf16_tmem_a(dO, dS + kt * 8,
+                                                 umma_desc_sw128(va + kt * kPageBytes, 1024, kSlabs * 1024), idPV,
+                                                 (j == 1 && kt == 0) ? 0u : 1u);
+                            if (!pair || t == 1) umma_commit(&sm.empty[i % kRing]);
+                            if (j == n) umma_commit(&sm.o_full[t]);
+                        }
+                        if (ok && j < n) {
+                            // S_t = Q_t K^T, over the P_t that the MMA above has read
+                            const int i = w.base + 2 * (pair ? j : 2 * j + t);
+                            ok = mbar_wait(&sm.full[i % kRing], (uint32_t)((i / kRing) & 1), a.err);
+                            if (!ok) break;
+                            tc_fence_after();
+                            const uint32_t ka = smem_u32(sm.kv[i % kRing]);
+                            const uint32_t qa = qaddr + (pair && t ? SM::kQTile : 0);
+#pragma unroll
+                            for (int kk = 0; kk < D / 16; ++kk)
+                                umma_bf16(dS, umma_desc_sw128(qa + (kk >> 2) * kQSlab + (kk & 3) * 32, 16, 1024),
+                                          umma_desc_sw128(ka + (kk >> 2) * 1024 + (kk & 3) * 32, 16, kSlabs * 1024),
+                                          idS, kk > 0 ? 1u : 0u);
+                            umma_commit(&sm.s_full[t]);
+                            if (!pair || t == 1) umma_commit(&sm.empty[i % kRing]);
+                        }
+                    }
+                    if (ok && j == last - 1) umma_commit(&sm.q_empty);
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        // ================================================= softmax and epilogue
+        const int t = warp >= 6;
+        const int quarter = warp & 3;
+        const int r = quarter * 32 + lane;  // query row of the tile == TMEM lane
+        const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+        const uint32_t tS = tmem + kTmemS + (uint32_t)t * kNB + lane_off;
+        const uint32_t tO = tmem + kTmemO + lane_off;
+        const int gtid = (warp - 2 - 4 * t) * 32 + lane;  // thread of the group
+        const int G = a.G, jq = r / G, gi = r - jq * G;
+        const float sc = a.scale_log2;
+        uint32_t ns = 0, no[2] = {0, 0};  // phases of s_full[t], o_full[0], o_full[1]
+        bool ready = false;               // every prefix partial is written
+        uint32_t nb2 = 0;                 // phases of both
+        bool ok = true;
+        // bounded waits of the whole warp: one outcome for all lanes
+        auto wait = [&](uint64_t *bar, uint32_t phase) -> bool {
+            return __all_sync(0xffffffffu, mbar_wait(bar, phase & 1u, a.err));
+        };
+        auto meet = [&]() -> bool {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.both);
+            const bool good = wait(&sm.both, nb2++);
+            tc_fence_after();
+            return good;
+        };
+        for (int unit = 0; ok; ++unit) {
+            if (!wait(&sm.q_full, (uint32_t)unit)) break;
+            const Unit w = sm.unit;
+            __syncwarp();
+            if (w.kind == kEnd) break;
+            if (lane == 0) mbar_arrive(&sm.q_empty);
+            const bool pair = w.kind == kPair;
+            const int n = t ? w.nB : w.nA;
+            const int tok = w.tok0 + (pair && t ? a.tpt : 0) + jq;
+            const int lim = w.lim0 + (w.causal ? tok - w.tok0 : 0);
+            const unsigned long long anc = w.use_anc && jq < a.n_q ? a.anc[jq] : 0ull;
+            float m_ref = -CUDART_INF_F, l_run = 0.f;
+            for (int i = 0; i < n; ++i) {
+                ok = wait(&sm.s_full[t], ns);
+                if (!ok) break;
+                ++ns;
+                tc_fence_after();
+                const int blk = pair ? i : 2 * i + t;
+                const int pos0 = w.pos0 + blk * kNB;
+                float s[kNB];
+#pragma unroll
+                for (int c = 0; c < kNB / 32; ++c) {
+                    uint32_t raw[32];
+                    tmem_ld32(tS + c * 32, raw);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) s[c * 32 + x] = __uint_as_float(raw[x]);
+                }
+                const int h0 = lim - pos0;  // tokens of the block below the limit
+                if (h0 < kNB) {
+#pragma unroll
+                    for (int x = 0; x < kNB / 64; ++x) {
+                        const int sh = h0 - 64 * x;
+                        const int hw = min(max(sh, 0), 64);
+                        unsigned long long vis = hw == 64 ? ~0ull : ((1ull << hw) - 1ull);
+                        if (sh >= 0) {
+                            if (sh < 64) vis |= anc << sh;
+                        } else if (sh > -64) {
+                            vis |= anc >> (-sh);
+                        }
+#pragma unroll
+                        for (int y = 0; y < 64; ++y)
+                            if (!((vis >> y) & 1ull)) s[64 * x + y] = -CUDART_INF_F;
+                    }
+                }
+                float pm[8];
+#pragma unroll
+                for (int x = 0; x < 8; ++x) pm[x] = s[16 * x];
+#pragma unroll
+                for (int x = 0; x < kNB; ++x)
+                    if (x & 15) pm[x >> 4] = fmaxf(pm[x >> 4], s[x]);
+                const float mraw = fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])),
+                                         fmaxf(fmaxf(pm[4], pm[5]), fmaxf(pm[6], pm[7])));
+                const float mx = mraw == -CUDART_INF_F ? -CUDART_INF_F : mraw * sc;
+                float alpha = 1.f;
+                bool rescale = false;
+                if (mx > m_ref + kRescaleLog2 || (m_ref == -CUDART_INF_F && mx != -CUDART_INF_F)) {
+                    alpha = ex2_approx(m_ref - mx);  // 0 when m_ref is -inf
+                    m_ref = mx;
+                    rescale = i > 0;
+                    l_run *= alpha;
+                }
+                const float neg_m = m_ref == -CUDART_INF_F ? 0.f : -m_ref;
+                float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < kNB / 64; ++c) {
+                    uint32_t p[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const float p0 = ex2_approx(fmaf(s[c * 64 + 2 * e], sc, neg_m));
+                        const float p1 = ex2_approx(fmaf(s[c * 64 + 2 * e + 1], sc, neg_m));
+                        ls[e & 3] += p0 + p1;
+                        p[e] = pack_bf16x2(p0, p1);
+                    }
+                    tmem_st32(tS + c * 32, p);
+                }
+                l_run += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+                // V rows behind the last token may hold anything; both groups
+                // clear them before they give out P
+                if (pos0 + kNB > w.kv_end) {
+                    const int vi = w.base + 2 * blk + 1;
+                    ok = wait(&sm.full[vi % kRing], (uint32_t)(vi / kRing));
+                    if (!ok) break;
+                    const int t0 = w.kv_end - pos0;
+                    constexpr int kVecs = kSlabs * 8;  // 16-byte words of a row
+                    uint8_t *sv = sm.kv[vi % kRing];
+                    for (int z = gtid; z < (kNB - t0) * kVecs; z += 128) {
+                        const int row = t0 + z / kVecs, c = z % kVecs;
+                        *reinterpret_cast<uint4 *>(sv + (row >> 3) * (kSlabs * 1024) + (c >> 3) * 1024 +
+                                                   (row & 7) * 128 + ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
+                    }
+                }
+                if (__any_sync(0xffffffffu, rescale)) {
+                    const float f = rescale ? alpha : 1.f;
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t raw[32];
+                        tmem_ld32(tO + t * 128 + c * 32, raw);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) raw[x] = __float_as_uint(__uint_as_float(raw[x]) * f);
+                        tmem_st32(tO + t * 128 + c * 32, raw);
+                    }
+                }
+                tmem_st_wait();
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.p_full[t]);
+            }
+            if (!ok) break;
+
+            // ---- epilogue
+            const bool live = r < a.tpt * G && tok < w.tok1;
+            const size_t row = (size_t)tok * a.Hq + (size_t)w.h * G + gi;
+            float m = m_ref, l = l_run;
+            if (pair) {
+                if (n > 0) {
+                    ok = wait(&sm.o_full[t], no[t]);
+                    if (!ok) break;
+                    tc_fence_after();
+                }
+                const float inv = l > 0.f ? 1.f / l : 0.f;
+                if (n > 0) {
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t raw[32];
+                        tmem_ld32(tO + t * 128 + c * 32, raw);
+                        tmem_ld_wait();
+                        if (!live) continue;
+                        if (w.slot < 0) {
+                            uint4 *o = reinterpret_cast<uint4 *>(a.out + row * D + c * 32);
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                const float *f = reinterpret_cast<const float *>(&raw[8 * x]);
+                                o[x] = make_uint4(pack_bf16x2(f[0] * inv, f[1] * inv), pack_bf16x2(f[2] * inv, f[3] * inv),
+                                                  pack_bf16x2(f[4] * inv, f[5] * inv), pack_bf16x2(f[6] * inv, f[7] * inv));
+                            }
+                        } else {
+                            uint4 *o = reinterpret_cast<uint4 *>(
+                                a.part_o + ((size_t)w.slot * a.T * a.Hq + row) * D + c * 32);
+#pragma unroll
+                            for (int x = 0; x < 8; ++x)
+                                o[x] = make_uint4(raw[4 * x], raw[4 * x + 1], raw[4 * x + 2], raw[4 * x + 3]);
+                        }
+                    }
+                    tc_fence_before();
+                }
+                if (live) {
+                    if (w.slot >= 0) a.part_ml[(size_t)w.slot * a.T * a.Hq + row] = make_float2(m, l);
+                    else if (a.lse) a.lse[row] = (m + __log2f(l)) * kLn2;
+                }
+            } else {
+                sm.stat[t][r] = make_float2(m_ref, l_run);
+                if (w.merge && !ready && threadIdx.x == 64) {
+                    // every prefix unit was taken by a running CTA before this
+                    // unit was: they end without waiting for anything of this one
+                    const unsigned long long start = global_ns();
+                    while (ld_acquire(a.sched + 2) < kDonePerUnit * a.p_units) {
+                        __nanosleep(200);
+                        if (global_ns() - start > kWaitLimitNs) {
+                            raise_error(a.err, SVPA_DEVERR_TIMEOUT);
+                            break;
+                        }
+                    }
+                    __threadfence();
+                }
+                ready = ready || w.merge;
+                ok = meet();
+                if (!ok) break;
+                const float2 sA = sm.stat[0][r], sB = sm.stat[1][r];
+                if (w.nA > 0) ok = wait(&sm.o_full[0], no[0]);
+                if (ok && w.nB > 0) ok = wait(&sm.o_full[1], no[1]);
+                if (!ok) break;
+                tc_fence_after();
+                m = fmaxf(sA.x, sB.x);
+                const int np = w.merge ? a.p_splits : 0;
+                const size_t rows = (size_t)a.T * a.Hq;
+                if (live)
+                    for (int p = 0; p < np; ++p) m = fmaxf(m, __ldcg(&a.part_ml[p * rows + row]).x);
+                float fA = sA.x == -CUDART_INF_F ? 0.f : ex2_approx(sA.x - m);
+                float fB = sB.x == -CUDART_INF_F ? 0.f : ex2_approx(sB.x - m);
+                l = sA.y * fA + sB.y * fB;
+                if (live)
+                    for (int p = 0; p < np; ++p) {
+                        const float2 ml = __ldcg(&a.part_ml[p * rows + row]);
+                        if (ml.y > 0.f) l += ml.y * ex2_approx(ml.x - m);
+                    }
+                const float inv = w.slot >= 0 ? 1.f : l > 0.f ? 1.f / l : 0.f;
+                fA *= inv;
+                fB *= inv;
+                // group t takes half of the columns of both accumulators
+                const int nb = w.nA + w.nB;
+                {
+#pragma unroll 1
+                    for (int c = t * (D / 64); c < (t + 1) * (D / 64); ++c) {
+                        float o[32];
+                        uint32_t raw[32];
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) o[x] = 0.f;
+                        if (w.nA > 0) {
+                            tmem_ld32(tO + c * 32, raw);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int x = 0; x < 32; ++x) o[x] = __uint_as_float(raw[x]) * fA;
+                        }
+                        if (w.nB > 0) {
+                            tmem_ld32(tO + 128 + c * 32, raw);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int x = 0; x < 32; ++x) o[x] = fmaf(__uint_as_float(raw[x]), fB, o[x]);
+                        }
+                        if (!live) continue;
+                        for (int p = 0; p < np; ++p) {
+                            const float2 ml = __ldcg(&a.part_ml[p * rows + row]);
+                            if (!(ml.y > 0.f)) continue;
+                            const float f = ex2_approx(ml.x - m) * inv;
+                            const float4 *src = reinterpret_cast<const float4 *>(a.part_o + (p * rows + row) * D + c * 32);
+#pragma unroll
+                            for (int x = 0; x < 8; ++x) {
+                                const float4 v = __ldcg(src + x);
+                                o[4 * x] = fmaf(v.x, f, o[4 * x]);
+                                o[4 * x + 1] = fmaf(v.y, f, o[4 * x + 1]);
+                                o[4 * x + 2] = fmaf(v.z, f, o[4 * x + 2]);
+                                o[4 * x + 3] = fmaf(v.w, f, o[4 * x + 3]);
+                            }
+                        }
+                        if (w.slot < 0) {
+                            uint4 *d = reinterpret_cast<uint4 *>(a.out + row * D + c * 32);
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                d[x] = make_uint4(pack_bf16x2(o[8 * x], o[8 * x + 1]), pack_bf16x2(o[8 * x + 2], o[8 * x + 3]),
+                                                  pack_bf16x2(o[8 * x + 4], o[8 * x + 5]),
+                                                  pack_bf16x2(o[8 * x + 6], o[8 * x + 7]));
+                        } else if (nb > 0) {
+                            float4 *d = reinterpret_cast<float4 *>(
+                                a.part_o + ((size_t)w.slot * rows + row) * D + c * 32);
+#pragma unroll
+                            for (int x = 0; x < 8; ++x)
+                                d[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+                        }
+                    }
+                    tc_fence_before();
+                    if (live && t == 0) {
+                        if (w.slot >= 0) a.part_ml[(size_t)w.slot * rows + row] = make_float2(m, l);
+                        else if (a.lse) a.lse[row] = (m + __log2f(l)) * kLn2;
+                    }
+                }
+                // neither group goes on to a new unit's P while the other reads O and the statistics
+                ok = meet();
+            }
+            no[0] += w.nA > 0;
+            no[1] += w.nB > 0;
+            if (w.prefix) {
+                __threadfence();
+                __syncwarp();
+                if (lane == 0) atomicAdd(a.sched + 2, 1);
+            }
+        }
+    }
+    // the softmax warps have waited for the issuer's last operations
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+    if (threadIdx.x == 0) {
+        __threadfence();
+        if (atomicAdd(&a.sched[1], 1) == (int)gridDim.x - 1) {
+            a.sched[0] = 0;
+            a.sched[1] = 0;
+            a.sched[2] = 0;
+        }
+    }
+}
+
+// One warp per (token, head) row: joins its partials with log-sum-exp weights.
+template <int D>
+__global__ void __launch_bounds__(256) packed_combine_kernel(const __grid_constant__ PackedArgs a) {
+    const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    const long long rows = (long long)a.T * a.Hq;
+    if (row >= rows) return;
+    const int tok = (int)(row / a.Hq);
+    int first = 0, slots = a.p_splits + a.s_splits;
+    if (a.verify) {
+        const int b = tok / a.n_q;
+        const int L = a.lens[b];
+        if (L < 0 || (long long)L + a.n_q > (long long)a.max_blocks * kBlockSize) return;  // reported, not computed
+        if (!a.member[b]) first = a.p_splits;
+    } else if (tok >= a.cu[a.B]) {
+        return;  // rows behind the last sequence stay as they are
+    }
+    constexpr int kPer = D / 32;
+    float m = -CUDART_INF_F, l = 0.f, o[kPer];
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) o[x] = 0.f;
+    for (int s = first; s < slots; ++s) {
+        const float2 ml = a.part_ml[s * rows + row];
+        if (!(ml.y > 0.f)) continue;
+        const float mn = fmaxf(m, ml.x);
+        const float fo = ex2_approx(m - mn), fn = ex2_approx(ml.x - mn);
+        const float *src = a.part_o + (s * rows + row) * D + lane * kPer;
+        l = l * fo + ml.y * fn;
+        m = mn;
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) o[x] = o[x] * fo + src[x] * fn;
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    __nv_bfloat162 *dst = reinterpret_cast<__nv_bfloat162 *>(a.out + row * D + lane * kPer);
+#pragma unroll
+    for (int x = 0; x < kPer / 2; ++x) dst[x] = __floats2bfloat162_rn(o[2 * x] * inv, o[2 * x + 1] * inv);
+    if (lane == 0 && a.lse) a.lse[row] = (m + __log2f(l)) * kLn2;
+}
+
+template <int D>
+cudaError_t launch_t(const PackedMaps &m, const PackedArgs &a, int grid, cudaStream_t st) {
+    const size_t smem = sizeof(Smem<D>);
+    static DeviceMemo<int> attr_set;  // the shared-memory opt-in, once per device
+    int done = 0;
+    cudaError_t e = attr_set.get(&done, [&](int *v) {
+        *v = 1;
+        return cudaFuncSetAttribute(packed_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    });
+    if (e != cudaSuccess) return e;
+    packed_attn_kernel<D><<<grid, kThreads, smem, st>>>(m.k, m.v, m.qt[0], m.qt[1], m.qs[0], m.qs[1], a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_packed_attn(const PackedMaps &m, const PackedArgs &a, int head_dim, int grid, cudaStream_t st) {
+    return head_dim == 128 ? launch_t<128>(m, a, grid, st) : launch_t<64>(m, a, grid, st);
+}
+
+cudaError_t launch_packed_combine(const PackedArgs &a, int head_dim, cudaStream_t st) {
+    const long long rows = (long long)a.T * a.Hq;
+    const int grid = (int)((rows + 7) / 8);
+    if (head_dim == 128) packed_combine_kernel<128><<<grid, 256, 0, st>>>(a);
+    else packed_combine_kernel<64><<<grid, 256, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace svpa

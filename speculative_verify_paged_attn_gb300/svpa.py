@@ -29,7 +29,9 @@ EXPORTS = ("svpa_attn_workspace_size", "svpa_attn_kernel", "svpa_paged_verify_at
            "svpa_spec_accept", "svpa_spec_accept_tree", "svpa_block_table_commit", "svpa_check_error",
            "svpa_status_string", "svpa_version", "svpa_paged_verify_attn_noalloc", "svpa_kv_append",
            "svpa_gamma_update", "svpa_attn_launches", "svpa_spec_accept_logits",
-           "svpa_spec_accept_logits_workspace_size", "svpa_wait_selftest", "svpa_spec_accept_tree_logits")
+           "svpa_spec_accept_logits_workspace_size", "svpa_wait_selftest", "svpa_spec_accept_tree_logits",
+           "svpa_paged_prompt_attn_workspace_size", "svpa_paged_prompt_attn",
+           "svpa_prefix_verify_attn_workspace_size", "svpa_prefix_verify_attn")
 
 
 class SvpaError(RuntimeError):
@@ -45,6 +47,14 @@ class AttnParams(ctypes.Structure):
                 ("num_blocks", ctypes.c_int32), ("kv_dtype", ctypes.c_int32),
                 ("sm_scale", ctypes.c_float), ("split_pages", ctypes.c_int32),
                 ("variant", ctypes.c_int32), ("scale_tile", ctypes.c_int32)]
+
+
+class PromptParams(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("total_q", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("block_size", ctypes.c_int32), ("max_blocks_per_seq", ctypes.c_int32),
+                ("num_blocks", ctypes.c_int32), ("kv_dtype", ctypes.c_int32),
+                ("sm_scale", ctypes.c_float), ("q_stride", ctypes.c_int32)]
 
 
 _lib = None
@@ -74,6 +84,10 @@ def load(path: str = LIB_PATH):
     L.svpa_paged_verify_attn_noalloc.argtypes = [ctypes.POINTER(AttnParams)] + [P] * 12
     L.svpa_kv_append.argtypes = [I] * 9 + [P] * 13
     L.svpa_gamma_update.argtypes = [I, I] + [P] * 6 + [ctypes.c_float, ctypes.c_float, P, P]
+    L.svpa_paged_prompt_attn_workspace_size.argtypes = [ctypes.POINTER(PromptParams), ctypes.POINTER(U)]
+    L.svpa_paged_prompt_attn.argtypes = [ctypes.POINTER(PromptParams)] + [P] * 9 + [U, P, P]
+    L.svpa_prefix_verify_attn_workspace_size.argtypes = [ctypes.POINTER(AttnParams), I, ctypes.POINTER(U)]
+    L.svpa_prefix_verify_attn.argtypes = [ctypes.POINTER(AttnParams)] + [P] * 4 + [I] + [P] * 6 + [U, P, P]
     L.svpa_check_error.argtypes = [P, P]
     L.svpa_wait_selftest.argtypes = [ctypes.c_uint64, P, P, P]
     L.svpa_status_string.argtypes = [I]
@@ -175,6 +189,55 @@ def paged_verify_attn_noalloc(params: AttnParams, q, k_pool, v_pool, block_table
         _p(out), _p(lse), _p(error_flag), _stream(stream))
     if check:
         _check(st, "svpa_paged_verify_attn_noalloc")
+    return st
+
+
+def prompt_params(batch, total_q, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, num_blocks, *,
+                  sm_scale=None, q_stride=0, block_size=16, kv_fp8=False) -> PromptParams:
+    """q_stride: elements from one token of q to the next (q.stride(0)); 0 = contiguous."""
+    return PromptParams(batch, total_q, num_q_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq,
+                        num_blocks, SVPA_KV_FP8_E4M3 if kv_fp8 else SVPA_KV_BF16,
+                        1.0 / math.sqrt(head_dim) if sm_scale is None else sm_scale, q_stride)
+
+
+def paged_prompt_attn_workspace_size(params: PromptParams) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().svpa_paged_prompt_attn_workspace_size(ctypes.byref(params), ctypes.byref(n)),
+           "svpa_paged_prompt_attn_workspace_size")
+    return n.value
+
+
+def paged_prompt_attn(params: PromptParams, q, k_pool, v_pool, block_table, cu_seqlens, kv_lens, out, *,
+                      workspace, error_flag, lse=None, stream=None, check=True) -> int:
+    """svpa_paged_prompt_attn: causal attention of packed prompts (or chunks) over their pages."""
+    st = load().svpa_paged_prompt_attn(
+        ctypes.byref(params), _p(q), _p(k_pool), _p(v_pool), _p(block_table), _p(cu_seqlens), _p(kv_lens),
+        _p(out), _p(lse), _p(workspace), workspace.numel() * workspace.element_size(), _p(error_flag),
+        _stream(stream))
+    if check:
+        _check(st, "svpa_paged_prompt_attn")
+    return st
+
+
+def prefix_verify_attn_workspace_size(params: AttnParams, prefix_len: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().svpa_prefix_verify_attn_workspace_size(ctypes.byref(params), prefix_len, ctypes.byref(n)),
+           "svpa_prefix_verify_attn_workspace_size")
+    return n.value
+
+
+def prefix_verify_attn(params: AttnParams, q, k_pool, v_pool, prefix_blocks, block_table, context_lens, out, *,
+                       workspace, error_flag, ancestor_mask=None, lse=None, stream=None, check=True) -> int:
+    """svpa_prefix_verify_attn: paged_verify_attn with the attention over the
+    blocks of prefix_blocks (int32, or None) formed once for all sequences."""
+    m = _mask_array(ancestor_mask)
+    st = load().svpa_prefix_verify_attn(
+        ctypes.byref(params), _p(q), _p(k_pool), _p(v_pool), _p(prefix_blocks),
+        0 if prefix_blocks is None else prefix_blocks.shape[0] * params.block_size, _p(block_table),
+        _p(context_lens), None if m is None else ctypes.cast(m, ctypes.c_void_p), _p(out), _p(lse), _p(workspace),
+        workspace.numel() * workspace.element_size(), _p(error_flag), _stream(stream))
+    if check:
+        _check(st, "svpa_prefix_verify_attn")
     return st
 
 
