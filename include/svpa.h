@@ -193,6 +193,92 @@ svpa_status svpa_paged_verify_attn(const svpa_attn_params *p, const void *q,
                                    size_t workspace_bytes, int32_t *error_flag,
                                    void *stream);
 
+/* Bytes of workspace svpa_block_table_build needs for `batch` requests (256);
+ * zero-filled once before its first use, left at zero by every completed call. */
+svpa_status svpa_block_table_build_workspace_size(int32_t batch, size_t *bytes);
+
+/*
+ * Block tables and slot maps of admitted requests, from their lengths.
+ *
+ * Sources: "Speculative Decoding & KV-Cache PagedAttention in Enterprise LLM
+ * Serving", PagedKVCacheManager.AllocateSessionBlocks (ceil(n / 16) blocks a
+ * request) and its shared-prefix section (shared blocks are referenced, one
+ * count per holder).
+ *
+ * Request b is to hold n_b = seq_lens[b] tokens, the first prefix_len of them
+ * in the shared blocks prefix_blocks; n_b = 0 is a batch slot without a
+ * request, otherwise n_b >= prefix_len.  Writes
+ *  - block_table[b]: the prefix blocks (each count raised by the number of live
+ *    requests), then the request's own pages, popped in request order (the
+ *    i-th page popped by the call is free_stack[*free_top - 1 - i], its count
+ *    set to 1), then -1;
+ *  - cu_seqlens[b] = sum of n_a - prefix_len over the live requests a < b: the
+ *    packed rows of the new tokens;
+ *  - slot_map[t]: for packed row t = cu_seqlens[b] + i the slot 16 * block + row
+ *    of position prefix_len + i, -1 for rows from cu_seqlens[B] on;
+ *  - *free_top, lowered by the pages popped (the stack's entries stay).
+ * The result does not depend on how the kernel is scheduled.
+ *
+ *  seq_lens      int32 [B]
+ *  prefix_blocks int32 [prefix_len / 16], or NULL when prefix_len is 0
+ *  prefix_len    HOST, a multiple of 16
+ *  block_table   int32 [B, max_blocks_per_seq] (written, every entry)
+ *  cu_seqlens    int32 [B + 1] (written)
+ *  slot_map      int32 [num_slots] (written, every entry)
+ *  refcount      int32 [num_blocks] (in/out); free_stack int32 [num_blocks];
+ *                free_top int32 [1] (in/out)
+ * Checked on the device before anything is written: a length that is negative,
+ * below the prefix or past the table, more new tokens than num_slots, a
+ * free_top outside [0, num_blocks] or a prefix block with count 0 raises
+ * SVPA_DEVERR_BAD_VALUE, too few free blocks SVPA_DEVERR_FREE_OVERFLOW
+ * (SVPA_ERR_OUT_OF_BLOCKS), a prefix block outside the pool
+ * SVPA_DEVERR_BAD_BLOCK; tables, counts and the stack are then unchanged.  A
+ * free-stack entry outside the pool raises SVPA_DEVERR_BAD_BLOCK; its page is
+ * -1.  Limits: batch <= 8192, num_blocks < 2^27, num_slots <= 2^30, else
+ * SVPA_ERR_UNSUPPORTED.
+ * One kernel on `stream`.
+ */
+svpa_status svpa_block_table_build(int32_t batch, int32_t block_size,
+                                   int32_t max_blocks_per_seq, int32_t num_blocks,
+                                   int32_t num_slots, const int32_t *seq_lens,
+                                   const int32_t *prefix_blocks, int32_t prefix_len,
+                                   int32_t *block_table, int32_t *cu_seqlens,
+                                   int32_t *slot_map, int32_t *refcount,
+                                   const int32_t *free_stack, int32_t *free_top,
+                                   void *workspace, size_t workspace_bytes,
+                                   int32_t *error_flag, void *stream);
+
+/*
+ * Packed K/V rows scattered into their pages through a slot map (the write of
+ * a prompt's keys and values; svpa_kv_append writes the drafts' of a step).
+ *
+ * Sources: "The Sub-Millisecond Speculative Decoding Meltdown", "Custom FP8
+ * Quantized Memory Block Layout" and implementation checklist.
+ *
+ * Row t goes to page slot_map[t] / 16, row slot_map[t] % 16 of every kv head's
+ * tile; a negative slot is a padding row and is skipped, one past the pool
+ * raises SVPA_DEVERR_BAD_BLOCK.  Two rows with the same slot: one of them is
+ * stored in each 16-byte word, which one is unspecified.  Other slots are left
+ * as they were.  FP8 pages take one scale per 64 consecutive elements
+ * (scale_tile 64): scale = amax / 448 of the tile (1 when amax is 0), codes
+ * e4m3(value / scale), as svpa_kv_append.
+ *
+ *  new_k, new_v  bf16 [T, Hkv, D], tokens k_stride / v_stride elements apart
+ *                (at least Hkv * D, multiples of 8), 16-byte aligned
+ *  slot_map      int32 [T]
+ *  k_pool, v_pool [num_blocks, Hkv, 16, D] bf16 or E4M3 bytes, 16-byte aligned
+ *  k_scale, v_scale fp32 [num_blocks, Hkv, 16, D / 64] (FP8 only, else NULL)
+ * Limits: 1 <= num_kv_heads <= 4096; head_dim a multiple of 8 up to 1024, else
+ * SVPA_ERR_INVALID_ARG; FP8 with head_dim % 64 != 0 or one scale per page
+ * (scale_tile 0) SVPA_ERR_UNSUPPORTED; num_tokens <= 2^28.  One kernel.
+ */
+svpa_status svpa_kv_write(int32_t num_tokens, int32_t num_kv_heads, int32_t head_dim,
+                          int32_t block_size, int32_t num_blocks, int32_t kv_dtype,
+                          int32_t scale_tile, const void *new_k, const void *new_v,
+                          int64_t k_stride, int64_t v_stride, const int32_t *slot_map,
+                          void *k_pool, void *v_pool, float *k_scale, float *v_scale,
+                          int32_t *error_flag, void *stream);
+
 /*
  * Geometry of one prompt-attention call (svpa_paged_prompt_attn).
  */
@@ -287,6 +373,65 @@ svpa_status svpa_prefix_verify_attn(const svpa_attn_params *p, const void *q,
                                     float *lse, void *workspace,
                                     size_t workspace_bytes, int32_t *error_flag,
                                     void *stream);
+
+/* logits element types */
+#define SVPA_LOGITS_FP32 0
+#define SVPA_LOGITS_BF16 1
+
+typedef struct svpa_logits_params {
+    int32_t batch;        /* B, 0..65535                                      */
+    int32_t rows;         /* logit rows per sequence, 1..64 (gamma + 1, or the
+                             nodes of a draft tree)                           */
+    int32_t vocab;        /* V, up to 2^24                                    */
+    int32_t max_history;  /* row stride of history                            */
+    int32_t logits_dtype; /* SVPA_LOGITS_FP32 or SVPA_LOGITS_BF16             */
+} svpa_logits_params;
+
+/*
+ * Penalties for repeated tokens, biases and grammar masks on the target's
+ * logits, before a sampler fed by logits.  The pages this library follows have
+ * no counterpart of this entry point; the samplers' target distribution is
+ * formed from its result.
+ *
+ * For row i of sequence b and token v, n(v) is the number of times v was
+ * generated before row i: in the history behind the prompt, and among the
+ * drafts on row i's path.  In this order, each operation rounded to fp32:
+ *   x = logit
+ *   x = x > 0 ? x / repetition[b] : x * repetition[b]   v in the prompt or n(v) > 0
+ *   x = x - frequency[b] * n(v)
+ *   x = x - presence[b]                                 n(v) > 0
+ *   x = x + bias(v)
+ *   x = -inf                                            v not allowed by the mask
+ * Unmarked tokens keep their value (bf16 to fp32 exactly); a row whose mask
+ * allows nothing is all -inf (which the samplers refuse).
+ *
+ *  logits       fp32 or bf16 [B, rows, V]
+ *  history      int32 [B, max_history] or NULL: prompt then generated tokens
+ *  hist_lens    int32 [B] tokens in history; prompt_lens int32 [B] of them in
+ *               the prompt, or NULL (none)
+ *  draft_tokens int32 [B, rows - 1] when parent is NULL: row i follows the
+ *               drafts 0 .. i - 1; int32 [B, rows] with parent, HOST int32
+ *               [rows] (parent[0] = -1, 0 <= parent[i] < i): row i follows
+ *               its node and the node's ancestors but the root, which is in
+ *               the history (entry 0 unused).  NULL: no drafts.
+ *  repetition, presence, frequency  fp32 [B] (repetition > 0) or NULL (1, 0, 0)
+ *  bias_offsets int32 [B + 1]; bias_tokens int32, bias_values fp32
+ *               [bias_offsets[B]]: sequence b's entries from bias_offsets[b]
+ *               on (the last entry for a token holds); bias_tokens NULL: none
+ *  mask         uint32 [B, rows, ceil(V / 32)] or NULL: bit v % 32 of word
+ *               v / 32 set = allowed
+ *  out          fp32 [B, rows, V] (written); may be `logits` when that is fp32
+ * A token id outside [0, V), a length outside [0, max_history] or falling
+ * offsets raise SVPA_DEVERR_BAD_VALUE.  One kernel on `stream`.
+ */
+svpa_status svpa_logits_process(const svpa_logits_params *p, const void *logits,
+                                const int32_t *history, const int32_t *prompt_lens,
+                                const int32_t *hist_lens, const int32_t *draft_tokens,
+                                const int32_t *parent, const float *repetition,
+                                const float *presence, const float *frequency,
+                                const int32_t *bias_offsets, const int32_t *bias_tokens,
+                                const float *bias_values, const uint32_t *mask,
+                                float *out, int32_t *error_flag, void *stream);
 
 /* Bytes of workspace the samplers take for `batch` rows of `vocab` tokens.
  * Reserved: the samplers keep no state in it (the size is 256 bytes); pass a

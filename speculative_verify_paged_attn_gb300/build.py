@@ -34,6 +34,10 @@ SOURCES = {
     "wait_selftest.cu": [],
     "packed_attn_tc.cu": [],
     "svpa_prompt_api.cu": [],
+    "block_table_build.cu": [],
+    "kv_write.cu": ["-fmad=false"],
+    "logits_process.cu": ["-fmad=false"],
+    "svpa_admit_api.cu": [],
 }
 
 

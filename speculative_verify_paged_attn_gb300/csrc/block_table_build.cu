@@ -1,0 +1,230 @@
+// block_table_build.cu -- block tables and slot maps of admitted requests,
+// from their lengths, in one launch.
+//
+// "Speculative Decoding & KV-Cache PagedAttention in Enterprise LLM Serving",
+// PagedKVCacheManager.AllocateSessionBlocks (a request takes ceil(n / 16)
+// blocks; the blocks of a shared prefix are referenced, not copied).
+//
+// With pages_b = ceil(n_b / 16), P prefix pages and own_b = pages_b - P for a
+// live request (n_b > 0), request b's i-th own page is the free stack's entry
+//   free_stack[free_top - 1 - (own_0 + .. + own_{b-1} + i)]
+// and its new tokens take the packed rows from sum of the earlier requests'
+// new tokens on.  Both are prefix sums over the batch: every CTA forms them
+// for itself in shared memory (a few kilobytes read from L2; no CTA waits for
+// another), checks the whole call the same way, then writes its share of the
+// table and the slot map.  The last CTA to finish lowers *free_top.
+#include "admit.h"
+#include "svpa_device.cuh"
+
+namespace svpa {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kChunk = 512;  // entries a warp writes at a time
+
+// Exclusive sums of two values per thread over the CTA; totals returned too.
+__device__ __forceinline__ void scan2(int &x, int &y, int &tx, int &ty, int2 *warp_sums) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int ix = x, iy = y;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int px = __shfl_up_sync(0xffffffffu, ix, o), py = __shfl_up_sync(0xffffffffu, iy, o);
+        if (lane >= o) {
+            ix += px;
+            iy += py;
+        }
+    }
+    if (lane == 31) warp_sums[warp] = make_int2(ix, iy);
+    __syncthreads();
+    int bx = 0, by = 0;
+    tx = ty = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        const int2 s = warp_sums[w];
+        if (w < warp) {
+            bx += s.x;
+            by += s.y;
+        }
+        tx += s.x;
+        ty += s.y;
+    }
+    x = bx + ix - x;
+    y = by + iy - y;
+}
+
+__global__ void __launch_bounds__(kThreads) build_kernel(const __grid_constant__ BuildArgs a) {
+    extern __shared__ int32_t sh[];
+    int32_t *first = sh;               // [B + 1] own pages of the requests before
+    int32_t *cu = sh + a.B + 1;        // [B + 1] new tokens of the requests before
+    __shared__ int2 warp_sums[kThreads / 32];
+    __shared__ int s_bad, s_live;
+    __shared__ long long s_pages, s_tokens;
+    const int P = a.prefix_pages, prefix_len = P * kBlockSize;
+    if (threadIdx.x == 0) {
+        s_bad = 0;
+        s_live = 0;
+        s_pages = s_tokens = 0;
+    }
+    __syncthreads();
+    const int top = *a.free_top;
+    // lengths: each thread takes a run of requests
+    const int per = (a.B + kThreads - 1) / kThreads;
+    const int b0 = min((int)threadIdx.x * per, a.B), b1 = min(b0 + per, a.B);
+    int bad = 0, live = 0;
+    long long lp = 0, lt = 0;
+    for (int b = b0; b < b1; ++b) {
+        const int n = a.seq_lens[b];
+        if (n < 0 || n > (long long)a.max_blocks * kBlockSize || (n > 0 && n < prefix_len)) bad |= SVPA_DEVERR_BAD_VALUE;
+        else if (n > 0) {
+            ++live;
+            lp += (n + kBlockSize - 1) / kBlockSize - P;
+            lt += n - prefix_len;
+        }
+    }
+    for (int i = threadIdx.x; i < P; i += kThreads) {
+        const int id = a.prefix_blocks[i];
+        if (id < 0 || id >= a.num_blocks) bad |= SVPA_DEVERR_BAD_BLOCK;
+        else if (*(volatile int32_t *)(a.refcount + id) < 1) bad |= SVPA_DEVERR_BAD_VALUE;
+    }
+    if (bad) atomicOr(&s_bad, bad);
+    if (live) atomicAdd(&s_live, live);
+    if (lp) atomicAdd((unsigned long long *)&s_pages, (unsigned long long)lp);
+    if (lt) atomicAdd((unsigned long long *)&s_tokens, (unsigned long long)lt);
+    __syncthreads();
+    bad = s_bad;
+    if (top < 0 || top > a.num_blocks || s_tokens > a.slots) bad |= SVPA_DEVERR_BAD_VALUE;
+    else if (s_pages > top) bad |= SVPA_DEVERR_FREE_OVERFLOW;
+    if (bad) {
+        // every CTA sees the same and leaves everything as it was
+        if (blockIdx.x == 0 && threadIdx.x == 0) raise_error(a.err, bad);
+        return;
+    }
+    // the sums fit: at most num_blocks pages and `slots` tokens
+    int x = (int)lp, y = (int)lt, tp, tt;
+    scan2(x, y, tp, tt, warp_sums);
+    for (int b = b0; b < b1; ++b) {
+        first[b] = x;
+        cu[b] = y;
+        const int n = a.seq_lens[b];
+        if (n > 0) {
+            x += (n + kBlockSize - 1) / kBlockSize - P;
+            y += n - prefix_len;
+        }
+    }
+    if (threadIdx.x == 0) {
+        first[a.B] = tp;
+        cu[a.B] = tt;
+    }
+    __syncthreads();
+
+    if (blockIdx.x == 0) {
+        for (int b = threadIdx.x; b <= a.B; b += kThreads) a.cu_seqlens[b] = cu[b];
+        if (s_live)
+            for (int i = threadIdx.x; i < P; i += kThreads) atomicAdd(&a.refcount[a.prefix_blocks[i]], s_live);
+    }
+    // the block of request b's page i, with its own pages popped in order
+    auto block_of = [&](int b, int i) -> int {
+        return i < P ? a.prefix_blocks[i] : a.free_stack[top - 1 - (first[b] + i - P)];
+    };
+    const int lane = threadIdx.x & 31;
+    const long long warps = (long long)gridDim.x * (kThreads / 32);
+    const long long w0 = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    const long long entries = (long long)a.B * a.max_blocks;
+    for (long long c = w0; c * kChunk < entries; c += warps) {
+        const long long e0 = c * kChunk;
+        const int row0 = (int)(e0 / a.max_blocks);
+        const unsigned col0 = (unsigned)(e0 - (long long)row0 * a.max_blocks);
+#pragma unroll 4
+        for (int k = lane; k < kChunk; k += 32) {
+            if (e0 + k >= entries) break;
+            const unsigned q = (col0 + k) / (unsigned)a.max_blocks;
+            const int b = row0 + (int)q, i = (int)(col0 + k - q * a.max_blocks);
+            const int own = first[b + 1] - first[b];
+            const int n = a.seq_lens[b];
+            int id = -1;
+            if (n > 0 && i < P + own) {
+                id = block_of(b, i);
+                if (i >= P) {
+                    if (id < 0 || id >= a.num_blocks) {
+                        raise_error(a.err, SVPA_DEVERR_BAD_BLOCK);
+                        id = -1;
+                    } else {
+                        a.refcount[id] = 1;
+                    }
+                }
+            }
+            a.block_table[e0 + k] = id;
+        }
+    }
+    const int total = cu[a.B];
+    for (long long c = w0; c * kChunk < a.slots; c += warps) {
+        const int s0 = (int)(c * kChunk);
+#pragma unroll 1
+        for (int k = lane * 4; k < kChunk; k += 128) {
+            const int t0 = s0 + k;
+            if (t0 >= a.slots) break;
+            int b = 0;
+            if (t0 < total) {  // the request of the first of four rows
+                int lo = 0, hi = a.B;
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (cu[mid] <= t0) lo = mid;
+                    else hi = mid;
+                }
+                b = lo;
+            }
+            int page = -1, row = -1, id = -1;
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+                const int t = t0 + z;
+                if (t >= a.slots) break;
+                int slot = -1;
+                if (t < total) {
+                    while (cu[b + 1] <= t) ++b;
+                    const int pos = prefix_len + t - cu[b];
+                    if (b != row || pos / kBlockSize != page) {
+                        row = b;
+                        page = pos / kBlockSize;
+                        id = block_of(b, page);
+                        if (id < 0 || id >= a.num_blocks) id = -1;  // raised with the table
+                    }
+                    if (id >= 0) slot = id * kBlockSize + pos % kBlockSize;
+                }
+                a.slot_map[t] = slot;
+            }
+        }
+    }
+    // *free_top is lowered once every CTA has read it
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        __threadfence();
+        if (atomicAdd(a.ticket, 1) == (int)gridDim.x - 1) {
+            *a.ticket = 0;
+            *a.free_top = top - tp;
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_block_table_build(const BuildArgs &a, cudaStream_t stream) {
+    const long long entries = (long long)a.B * a.max_blocks + a.slots;
+    const long long ctas = (entries + kChunk * (kThreads / 32) - 1) / (kChunk * (kThreads / 32));
+    const int grid = (int)(ctas < 1 ? 1 : ctas > 304 ? 304 : ctas);
+    const size_t smem = (size_t)2 * (a.B + 1) * sizeof(int32_t);
+    if (smem > 48 * 1024) {
+        static DeviceMemo<int> attr_set;
+        int done = 0;
+        const cudaError_t e = attr_set.get(&done, [](int *v) {
+            *v = 1;
+            return cudaFuncSetAttribute(build_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        (int)(2 * (kMaxBuildBatch + 1) * sizeof(int32_t)));
+        });
+        if (e != cudaSuccess) return e;
+    }
+    build_kernel<<<grid, kThreads, smem, stream>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace svpa

@@ -22,6 +22,8 @@ LIB_PATH = os.path.join(_HERE, "libsvpa.so")
 
 SVPA_KV_BF16 = 0
 SVPA_KV_FP8_E4M3 = 1
+SVPA_LOGITS_FP32 = 0
+SVPA_LOGITS_BF16 = 1
 STATUS = {0: "SVPA_OK", 1: "SVPA_ERR_INVALID_ARG", 2: "SVPA_ERR_UNSUPPORTED", 3: "SVPA_ERR_CUDA",
           4: "SVPA_ERR_OUT_OF_BLOCKS", 5: "SVPA_ERR_BAD_BLOCK", 6: "SVPA_ERR_WORKSPACE",
           7: "SVPA_ERR_TIMEOUT"}
@@ -31,7 +33,8 @@ EXPORTS = ("svpa_attn_workspace_size", "svpa_attn_kernel", "svpa_paged_verify_at
            "svpa_gamma_update", "svpa_attn_launches", "svpa_spec_accept_logits",
            "svpa_spec_accept_logits_workspace_size", "svpa_wait_selftest", "svpa_spec_accept_tree_logits",
            "svpa_paged_prompt_attn_workspace_size", "svpa_paged_prompt_attn",
-           "svpa_prefix_verify_attn_workspace_size", "svpa_prefix_verify_attn")
+           "svpa_prefix_verify_attn_workspace_size", "svpa_prefix_verify_attn",
+           "svpa_block_table_build_workspace_size", "svpa_block_table_build", "svpa_kv_write", "svpa_logits_process")
 
 
 class SvpaError(RuntimeError):
@@ -55,6 +58,11 @@ class PromptParams(ctypes.Structure):
                 ("block_size", ctypes.c_int32), ("max_blocks_per_seq", ctypes.c_int32),
                 ("num_blocks", ctypes.c_int32), ("kv_dtype", ctypes.c_int32),
                 ("sm_scale", ctypes.c_float), ("q_stride", ctypes.c_int32)]
+
+
+class LogitsParams(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("rows", ctypes.c_int32), ("vocab", ctypes.c_int32),
+                ("max_history", ctypes.c_int32), ("logits_dtype", ctypes.c_int32)]
 
 
 _lib = None
@@ -88,6 +96,10 @@ def load(path: str = LIB_PATH):
     L.svpa_paged_prompt_attn.argtypes = [ctypes.POINTER(PromptParams)] + [P] * 9 + [U, P, P]
     L.svpa_prefix_verify_attn_workspace_size.argtypes = [ctypes.POINTER(AttnParams), I, ctypes.POINTER(U)]
     L.svpa_prefix_verify_attn.argtypes = [ctypes.POINTER(AttnParams)] + [P] * 4 + [I] + [P] * 6 + [U, P, P]
+    L.svpa_block_table_build_workspace_size.argtypes = [I, ctypes.POINTER(U)]
+    L.svpa_block_table_build.argtypes = [I] * 5 + [P, P, I] + [P] * 7 + [U, P, P]
+    L.svpa_kv_write.argtypes = [I] * 7 + [P, P, ctypes.c_int64, ctypes.c_int64] + [P] * 7
+    L.svpa_logits_process.argtypes = [ctypes.POINTER(LogitsParams)] + [P] * 16
     L.svpa_check_error.argtypes = [P, P]
     L.svpa_wait_selftest.argtypes = [ctypes.c_uint64, P, P, P]
     L.svpa_status_string.argtypes = [I]
@@ -342,6 +354,75 @@ def kv_append(new_k, new_v, block_table, context_lens, refcount, free_stack, fre
         _p(k_scale), _p(v_scale), _p(error_flag), _stream(stream))
     if check:
         _check(st, "svpa_kv_append")
+    return st
+
+
+def block_table_build_workspace_size(batch: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().svpa_block_table_build_workspace_size(batch, ctypes.byref(n)),
+           "svpa_block_table_build_workspace_size")
+    return n.value
+
+
+def block_table_build(seq_lens, block_table, cu_seqlens, slot_map, refcount, free_stack, free_top, *, workspace,
+                      error_flag, prefix_blocks=None, stream=None, check=True) -> int:
+    """svpa_block_table_build: tables [B, max_blocks], packed offsets [B + 1] and
+    slots of the new tokens of requests with seq_lens [B] tokens, the first of
+    them in the shared blocks of prefix_blocks (int32, or None)."""
+    B, max_blocks = block_table.shape
+    st = load().svpa_block_table_build(
+        B, 16, max_blocks, refcount.shape[0], slot_map.shape[0], _p(seq_lens), _p(prefix_blocks),
+        0 if prefix_blocks is None else prefix_blocks.shape[0] * 16, _p(block_table), _p(cu_seqlens), _p(slot_map),
+        _p(refcount), _p(free_stack), _p(free_top), _p(workspace), workspace.numel() * workspace.element_size(),
+        _p(error_flag), _stream(stream))
+    if check:
+        _check(st, "svpa_block_table_build")
+    return st
+
+
+def _row_stride(t, what: str) -> int:
+    """Elements from one token of t [T, H, D] to the next; the tokens' own values must be contiguous."""
+    if t.shape[0] > 0 and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2])):
+        raise SvpaError(1, f"{what}: the values of a token are not contiguous")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def kv_write(new_k, new_v, slot_map, k_pool, v_pool, *, error_flag, k_scale=None, v_scale=None, scale_tile=0,
+             stream=None, check=True) -> int:
+    """svpa_kv_write: new_k/new_v [T, Hkv, D] (bf16; slices of a fused projection
+    along the heads are taken as they are) to the slots of slot_map [T]; the
+    pools are bf16 or float8_e4m3fn/uint8 [num_blocks, Hkv, 16, D]."""
+    T, Hkv, D = new_k.shape
+    st = load().svpa_kv_write(
+        T, Hkv, D, 16, k_pool.shape[0], SVPA_KV_FP8_E4M3 if k_pool.element_size() == 1 else SVPA_KV_BF16, scale_tile,
+        _p(new_k), _p(new_v), _row_stride(new_k, "new_k"), _row_stride(new_v, "new_v"), _p(slot_map), _p(k_pool),
+        _p(v_pool), _p(k_scale), _p(v_scale), _p(error_flag), _stream(stream))
+    if check:
+        _check(st, "svpa_kv_write")
+    return st
+
+
+def logits_process(logits, out, *, error_flag, history=None, prompt_lens=None, hist_lens=None, draft_tokens=None,
+                   parent: Optional[Sequence[int]] = None, repetition=None, presence=None, frequency=None,
+                   bias_offsets=None, bias_tokens=None, bias_values=None, mask=None, stream=None, check=True) -> int:
+    """svpa_logits_process: penalties, biases and grammar masks on logits [B,
+    rows, V] (fp32 or bf16) into out (fp32, may be logits); parent: host
+    sequence of the draft tree (parent[0] = -1) or None for a chain."""
+    B, rows, V = logits.shape
+    p = LogitsParams(B, rows, V, 0 if history is None else history.shape[1],
+                     SVPA_LOGITS_BF16 if logits.element_size() == 2 else SVPA_LOGITS_FP32)
+    arr = None
+    if parent is not None:
+        par = [int(x) for x in (parent.tolist() if hasattr(parent, "tolist") else parent)]
+        if len(par) != rows:
+            raise SvpaError(1, "svpa_logits_process: one parent per row")
+        arr = (ctypes.c_int32 * rows)(*par)
+    st = load().svpa_logits_process(
+        ctypes.byref(p), _p(logits), _p(history), _p(prompt_lens), _p(hist_lens), _p(draft_tokens),
+        None if arr is None else ctypes.cast(arr, ctypes.c_void_p), _p(repetition), _p(presence), _p(frequency),
+        _p(bias_offsets), _p(bias_tokens), _p(bias_values), _p(mask), _p(out), _p(error_flag), _stream(stream))
+    if check:
+        _check(st, "svpa_logits_process")
     return st
 
 
