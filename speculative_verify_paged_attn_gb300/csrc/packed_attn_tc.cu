@@ -24,11 +24,12 @@
 //   0      producer: decodes units, streams K and V blocks (8 pages per
 //          block, one TMA copy per page and kv head) through one ring, and
 //          the query tiles;
-//   1      MMA issuer (one thread) and TMEM owner:  S_t = Q_t K^T  and
-//          O_t += P_t V, P_t read from TMEM over S_t's own columns.  Per
-//          block: PV_A, S_A, PV_B, S_B;
-//   2-5    softmax of tile A, one thread per query row: mask, lazy running
-//   6-9    maximum (O_t rescaled only when it grows by more than 2^8), fp32
+//   1, 2   MMA issuers of tile A and tile B (warp 1 owns the TMEM):
+//          O_t += P_t V with P_t read from TMEM over S_t's own columns, then
+//          S_t = Q_t K^T of the next block;
+//   3      idle (it completes the warpgroup that gives up registers);
+//   4-7    softmax of tile A, one thread per query row: mask, lazy running
+//   8-11   maximum (O_t rescaled only when it grows by more than 2^8), fp32
 //          row sum, P as bf16 (the MMA's input type; the sum is taken before
 //          that rounding); then the unit's epilogue.
 // A commit on S_t's barrier covers the PV_t issued before it, so a softmax
@@ -45,7 +46,10 @@ namespace svpa {
 
 namespace {
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
+// registers are launched evenly (168 a thread, 64512 in all) and moved to the
+// softmax warps: 128 * 80 + 256 * 208 = 63488
+constexpr int kRegsFew = 80, kRegsMany = 208;
 constexpr int kPagesPerBlock = 8;
 constexpr int kNB = kPagesPerBlock * kBlockSize;  // kv tokens per block
 constexpr int kRing = 5;                          // K and V tiles in flight
@@ -82,6 +86,7 @@ struct Smem {
     uint64_t q_full, q_empty;
     uint64_t s_full[2], p_full[2], o_full[2];
     uint64_t both;  // the two softmax groups meet
+    uint64_t drain[2];
     Unit unit;
     float2 stat[2][128];
     uint32_t tmem_base;
@@ -92,6 +97,52 @@ __device__ __forceinline__ uint64_t policy_evict_normal() {
     uint64_t p;
     asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
     return p;
+}
+
+// Packed fp32 pairs: each half rounded as the scalar operation.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
+
+// Bounded wait on a barrier that is usually about to complete: the clock is
+// read only after a while (a read costs more than many probes).
+__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, int32_t *err) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    return mbar_wait(bar, parity, err);
+}
+
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 __device__ __forceinline__ int ld_acquire(const int32_t *p) {
@@ -148,15 +199,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < kRing; ++i) {
             mbar_init(&sm.full[i], 1);
-            mbar_init(&sm.empty[i], 1);
+            mbar_init(&sm.empty[i], 2);  // the two MMA issuers
         }
         mbar_init(&sm.both, 8);
         mbar_init(&sm.q_full, 1);
-        mbar_init(&sm.q_empty, 9);  // the MMA issuer and the eight softmax warps
+        mbar_init(&sm.q_empty, 10);  // the MMA issuers and the eight softmax warps
         for (int t = 0; t < 2; ++t) {
             mbar_init(&sm.s_full[t], 1);
             mbar_init(&sm.p_full[t], 4);
             mbar_init(&sm.o_full[t], 1);
+            mbar_init(&sm.drain[t], 1);
         }
         fence_mbar_init();
     }
@@ -173,7 +225,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
 
-    if (warp == 0) {
+    if (warp < 4) {
+        regs_dec<kRegsFew>();
+        if (warp == 0) {
         // ================================================= producer
         const uint64_t keep = policy_evict_normal(), stream_once = policy_evict_first();
         if (lane == 0) {
@@ -398,75 +452,132 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!mbar_wait(&sm.full[i % kRing], (uint32_t)((i / kRing) & 1), a.err)) break;
         }
         __syncwarp();
-    } else if (warp == 1) {
-        // ================================================= MMA issuer
-        if (lane == 0) {
+        } else if (warp < 3) {
+            // ================================================= MMA issuers
+            // The whole warp runs the loop with warp-uniform values and one
+            // elected lane issues: an MMA's operands then go straight through
+            // uniform registers (issued from a branch that one lane takes, an
+            // MMA cost 80 to 145 cycles of issue; it runs 64).  Each wait costs
+            // about 100 cycles even when the barrier is complete, more than the
+            // MMAs queued behind the one running can cover: hence one issuer
+            // per tile, V waited for before P, and K behind P V's issue.
+            const int t = __shfl_sync(0xffffffffu, warp - 1, 0);
             constexpr uint32_t idS = umma_idesc_bf16(128, kNB, false);
             constexpr uint32_t idPV = umma_idesc_bf16(128, D, true);
-            const uint32_t qaddr = smem_u32(&sm.q[0][0]);
-            uint32_t np[2] = {0, 0};  // P tiles taken
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const uint32_t dS = tm + kTmemS + (uint32_t)t * kNB, dO = tm + kTmemO + (uint32_t)t * 128;
+            // descriptors count 16-byte units; an address field never carries (below 2^14)
+            const uint64_t q0 = umma_desc_sw128(smem_u32(&sm.q[0][0]), 16, 1024);
+            const uint64_t k0 = umma_desc_sw128(smem_u32(&sm.kv[0][0]), 16, kSlabs * 1024);
+            const uint64_t v0 = umma_desc_sw128(smem_u32(&sm.kv[0][0]), 1024, kSlabs * 1024);
+            auto wait = [&](uint64_t *bar, uint32_t phase) -> bool {
+                return __all_sync(0xffffffffu, bar_wait(bar, phase & 1u, a.err));
+            };
+            // A barrier tells two phases apart only, so each issuer waits for
+            // every tile that lands, its own and those only the other reads
+            // (alt units, the last blocks of a pair's tile B): a slot is filled
+            // anew after one arrival of each, a commit or, for the latter, this.
+            auto tile_wait = [&](int i) -> bool { return wait(&sm.full[i % kRing], (uint32_t)(i / kRing)); };
+            auto pass_over = [&](int i) -> bool {
+                if (!tile_wait(i)) return false;
+                if (lane == 0) mbar_arrive(&sm.empty[i % kRing]);
+                __syncwarp();
+                return true;
+            };
+            uint32_t np = 0;  // phase of p_full
             bool ok = true;
             for (int unit = 0; ok; ++unit) {
-                if (!mbar_wait(&sm.q_full, (uint32_t)(unit & 1), a.err)) break;
-                const Unit w = sm.unit;
-                if (w.kind == kEnd) break;
-                const bool pair = w.kind == kPair;
-                const int last = max(w.nA, w.nB);
-                if (last == 0) mbar_arrive(&sm.q_empty);
-                for (int j = 0; j <= last && ok && last > 0; ++j) {
+                if (!wait(&sm.q_full, (uint32_t)unit)) break;
+                const int kind = __shfl_sync(0xffffffffu, sm.unit.kind, 0);
+                const int n = __shfl_sync(0xffffffffu, t ? sm.unit.nB : sm.unit.nA, 0);
+                const int other = __shfl_sync(0xffffffffu, t ? sm.unit.nA : sm.unit.nB, 0);
+                const int base = __shfl_sync(0xffffffffu, sm.unit.base, 0);
+                if (kind == kEnd) break;
+                const bool pair = kind == kPair;
+                const uint64_t qd = q0 + (pair && t ? SM::kQTile / 16 : 0);
+                if (n == 0 && lane == 0) mbar_arrive(&sm.q_empty);
+                // O_t += P_t V of block j - 1
+                auto issue_pv = [&](int j, int sv) {
+                    const uint64_t vd = v0 + (uint32_t)sv * (SM::kTile / 16);
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        const int n = t ? w.nB : w.nA;
-                        const uint32_t dS = tmem + kTmemS + (uint32_t)t * kNB;
-                        if (ok && j >= 1 && j - 1 < n) {
-                            // O_t += P_t V
-                            const int i = w.base + 2 * (pair ? j - 1 : 2 * (j - 1) + t) + 1;
-                            ok = mbar_wait(&sm.p_full[t], np[t] & 1u, a.err) &&
-                                 mbar_wait(&sm.full[i % kRing], (uint32_t)((i / kRing) & 1), a.err);
-                            if (!ok) break;
-                            ++np[t];
-                            tc_fence_after();
-                            const uint32_t va = smem_u32(sm.kv[i % kRing]);
-                            const uint32_t dO = tmem + kTmemO + (uint32_t)t * 128;
+                    for (int kt = 0; kt < kNB / 16; ++kt)
+                        umma_bf16_tmem_a(dO, dS + kt * 8, vd + kt * (kPageBytes / 16), idPV,
+                                         kt > 0 ? 1u : (uint32_t)(j - 1));
+                    if (j == n) umma_commit(&sm.o_full[t]);
+                };
+                // S_t = Q_t K^T of block j, over the P_t that the MMA before has read
+                auto issue_s = [&](int j, int sk) {
+                    const uint64_t kd = k0 + (uint32_t)sk * (SM::kTile / 16);
 #pragma unroll
-                            for (int kt = 0; kt < kNB / 16; ++kt)
-                                umma_bf16_tmem_a(dO, dS + kt * 8,
-                                                 umma_desc_sw128(va + kt * kPageBytes, 1024, kSlabs * 1024), idPV,
-                                                 (j == 1 && kt == 0) ? 0u : 1u);
-                            if (!pair || t == 1) umma_commit(&sm.empty[i % kRing]);
-                            if (j == n) umma_commit(&sm.o_full[t]);
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        umma_bf16(dS, qd + ((kk >> 2) * kQSlab + (kk & 3) * 32) / 16,
+                                  kd + ((kk >> 2) * 1024 + (kk & 3) * 32) / 16, idS, kk > 0 ? 1u : 0u);
+                    umma_commit(&sm.s_full[t]);
+                    umma_commit(&sm.empty[sk]);
+                    if (j == n - 1) umma_commit(&sm.q_empty);
+                };
+#pragma unroll 1
+                for (int j = 0; j <= n && n > 0; ++j) {
+                    const int ik = base + 2 * (pair ? j : 2 * j + t), sk = ik % kRing;
+                    const int iv = ik + 1 - (pair ? 2 : 4), sv = iv % kRing;
+                    if (pair) {
+                        // K (from L2) has landed long before P is ready: wait
+                        // for it first, and both MMAs go out together
+                        ok = (j == n || tile_wait(ik)) && (j == 0 || (tile_wait(iv) && wait(&sm.p_full[t], np++)));
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+                            if (j > 0) issue_pv(j, sv);
+                            if (j < n) issue_s(j, sk);
+                            if (j > 0) umma_commit(&sm.empty[sv]);
                         }
-                        if (ok && j < n) {
-                            // S_t = Q_t K^T, over the P_t that the MMA above has read
-                            const int i = w.base + 2 * (pair ? j : 2 * j + t);
-                            ok = mbar_wait(&sm.full[i % kRing], (uint32_t)((i / kRing) & 1), a.err);
-                            if (!ok) break;
-                            tc_fence_after();
-                            const uint32_t ka = smem_u32(sm.kv[i % kRing]);
-                            const uint32_t qa = qaddr + (pair && t ? SM::kQTile : 0);
-#pragma unroll
-                            for (int kk = 0; kk < D / 16; ++kk)
-                                umma_bf16(dS, umma_desc_sw128(qa + (kk >> 2) * kQSlab + (kk & 3) * 32, 16, 1024),
-                                          umma_desc_sw128(ka + (kk >> 2) * 1024 + (kk & 3) * 32, 16, kSlabs * 1024),
-                                          idS, kk > 0 ? 1u : 0u);
-                            umma_commit(&sm.s_full[t]);
-                            if (!pair || t == 1) umma_commit(&sm.empty[i % kRing]);
-                        }
+                        __syncwarp();
+                        continue;
                     }
-                    if (ok && j == last - 1) umma_commit(&sm.q_empty);
+                    if (j > 0) {
+                        ok = tile_wait(iv) && wait(&sm.p_full[t], np++);
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+                            issue_pv(j, sv);
+                            umma_commit(&sm.empty[sv]);
+                        }
+                        __syncwarp();
+                        if (j - 1 < other) ok = pass_over(base + 2 * (2 * (j - 1) + 1 - t) + 1);
+                        if (!ok) break;
+                    }
+                    if (j < n) {
+                        ok = tile_wait(ik);
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (elect_one()) issue_s(j, sk);
+                        __syncwarp();
+                        if (j < other) ok = pass_over(base + 2 * (2 * j + 1 - t));
+                        if (!ok) break;
+                    }
+                }
+                // blocks that only the other tile has
+                for (int j = n; j < other && ok; ++j) {
+                    const int i = base + 2 * (pair ? j : 2 * j + 1 - t);
+                    ok = pass_over(i) && pass_over(i + 1);
                 }
             }
+            if (!ok) {  // a wait ran out: the MMAs issued so far end before the CTA does
+                if (elect_one()) umma_commit(&sm.drain[t]);
+                __syncwarp();
+                wait(&sm.drain[t], 0);
+            }
         }
-        __syncwarp();
     } else {
         // ================================================= softmax and epilogue
-        const int t = warp >= 6;
+        regs_inc<kRegsMany>();
+        const int t = warp >= 8;
         const int quarter = warp & 3;
         const int r = quarter * 32 + lane;  // query row of the tile == TMEM lane
         const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
         const uint32_t tS = tmem + kTmemS + (uint32_t)t * kNB + lane_off;
         const uint32_t tO = tmem + kTmemO + lane_off;
-        const int gtid = (warp - 2 - 4 * t) * 32 + lane;  // thread of the group
+        const int gtid = (warp & 3) * 32 + lane;  // thread of the group
         const int G = a.G, jq = r / G, gi = r - jq * G;
         const float sc = a.scale_log2;
         uint32_t ns = 0, no[2] = {0, 0};  // phases of s_full[t], o_full[0], o_full[1]
@@ -475,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         // bounded waits of the whole warp: one outcome for all lanes
         auto wait = [&](uint64_t *bar, uint32_t phase) -> bool {
-            return __all_sync(0xffffffffu, mbar_wait(bar, phase & 1u, a.err));
+            return __all_sync(0xffffffffu, bar_wait(bar, phase & 1u, a.err));
         };
         auto meet = [&]() -> bool {
             tc_fence_before();
@@ -504,15 +615,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 const int blk = pair ? i : 2 * i + t;
                 const int pos0 = w.pos0 + blk * kNB;
+                // all four loads in flight, one wait
+                uint32_t raw[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, raw[c]);
+                tmem_ld_wait();
                 float s[kNB];
 #pragma unroll
-                for (int c = 0; c < kNB / 32; ++c) {
-                    uint32_t raw[32];
-                    tmem_ld32(tS + c * 32, raw);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int x = 0; x < 32; ++x) s[c * 32 + x] = __uint_as_float(raw[x]);
-                }
+                for (int x = 0; x < kNB; ++x) s[x] = __uint_as_float(raw[x >> 5][x & 31]);
                 const int h0 = lim - pos0;  // tokens of the block below the limit
                 if (h0 < kNB) {
 #pragma unroll
@@ -530,14 +640,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (!((vis >> y) & 1ull)) s[64 * x + y] = -CUDART_INF_F;
                     }
                 }
-                float pm[8];
+                float pm[4];
 #pragma unroll
-                for (int x = 0; x < 8; ++x) pm[x] = s[16 * x];
+                for (int x = 0; x < 4; ++x) pm[x] = fmaxf(s[x], s[x + 4]);
 #pragma unroll
-                for (int x = 0; x < kNB; ++x)
-                    if (x & 15) pm[x >> 4] = fmaxf(pm[x >> 4], s[x]);
-                const float mraw = fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])),
-                                         fmaxf(fmaxf(pm[4], pm[5]), fmaxf(pm[6], pm[7])));
+                for (int x = 8; x < kNB; x += 8)
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) pm[y] = fmaxf(fmaxf(pm[y], s[x + y]), s[x + y + 4]);
+                const float mraw = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]));
                 const float mx = mraw == -CUDART_INF_F ? -CUDART_INF_F : mraw * sc;
                 float alpha = 1.f;
                 bool rescale = false;
@@ -548,20 +658,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                     l_run *= alpha;
                 }
                 const float neg_m = m_ref == -CUDART_INF_F ? 0.f : -m_ref;
-                float ls[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint64_t sc2 = pack2(sc, sc), neg2 = pack2(neg_m, neg_m);
+                uint64_t ls[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
                 for (int c = 0; c < kNB / 64; ++c) {
                     uint32_t p[32];
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
-                        const float p0 = ex2_approx(fmaf(s[c * 64 + 2 * e], sc, neg_m));
-                        const float p1 = ex2_approx(fmaf(s[c * 64 + 2 * e + 1], sc, neg_m));
-                        ls[e & 3] += p0 + p1;
+                        const float2 x = unpack2(fma2(pack2(s[c * 64 + 2 * e], s[c * 64 + 2 * e + 1]), sc2, neg2));
+                        const float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
+                        ls[e & 3] = add2(ls[e & 3], pack2(p0, p1));
                         p[e] = pack_bf16x2(p0, p1);
                     }
                     tmem_st32(tS + c * 32, p);
                 }
-                l_run += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+                const float2 lsum = unpack2(add2(add2(ls[0], ls[1]), add2(ls[2], ls[3])));
+                l_run += lsum.x + lsum.y;
                 // V rows behind the last token may hold anything; both groups
                 // clear them before they give out P
                 if (pos0 + kNB > w.kv_end) {
@@ -639,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             } else {
                 sm.stat[t][r] = make_float2(m_ref, l_run);
-                if (w.merge && !ready && threadIdx.x == 64) {
+                if (w.merge && !ready && threadIdx.x == 128) {
                     // every prefix unit was taken by a running CTA before this
                     // unit was: they end without waiting for anything of this one
                     const unsigned long long start = global_ns();

@@ -139,6 +139,24 @@ def test_many_sequences_and_repeated_calls():
     assert torch.equal(c.out, first)
 
 
+def test_streams_of_own_blocks_behind_a_tree():
+    """More units than SMs, streamed from memory, odd numbers of blocks: the
+    ring's slots pass between the two tiles in every order."""
+    c = Case([200 + (997 * i) % 2500 for i in range(64)], 800, len(TREE), 32, 8, 128, masks=TREE)
+    c.call()
+    c.check()
+    first, lse = c.out.clone(), c.lse.clone()
+    flush = torch.empty(64 << 20, device=DEV)
+    for i in range(12):
+        c.out.zero_()
+        c.lse.zero_()
+        if i % 2:
+            flush.fill_(float(i))
+        c.call()
+        assert torch.equal(c.out, first) and torch.equal(c.lse, lse), i
+    c.check()
+
+
 def test_captured_replay_with_new_lengths():
     c = Case([90, 26, 140, 3], 256, 4, 8, 2, 128)
     c.call()

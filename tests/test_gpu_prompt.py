@@ -119,6 +119,22 @@ def test_random_ragged_batches():
         c.check(f"{new} {cached} {hkv} {g}")
 
 
+def test_mixed_units_repeated():
+    """Pairs and single tiles in turn on every SM, the same bits every time."""
+    new = [(131 * i) % 700 + 1 for i in range(60)]
+    c = Case(new, [(577 * i) % 900 for i in range(60)], 16, 8, 128)
+    c.call()
+    c.check()
+    first = c.out.clone()
+    flush = torch.empty(64 << 20, device=DEV)
+    for i in range(10):
+        c.out.zero_()
+        flush.fill_(float(i))
+        c.call()
+        assert torch.equal(c.out, first), i
+    c.check()
+
+
 def test_large_scores_and_growing_maxima():
     """Scores that grow along the sequence (the running maximum is replaced
     many times) and a sharp softmax."""
