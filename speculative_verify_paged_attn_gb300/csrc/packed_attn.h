@@ -15,13 +15,17 @@ struct PackedArgs {
     const int32_t *prefix_blocks;  // [prefix_pages] (verify)
     __nv_bfloat16 *out;            // [T, Hq, D]
     float *lse;                    // [T, Hq] or null
-    float *part_o;                 // [slots, T, Hq, D] unnormalised partial outputs
-    float2 *part_ml;               // [slots, T, Hq] (reference maximum in log2 units, sum)
+    // partials, one row for each (slot, kv head, 128-row query tile, row of the
+    // tile): unnormalised outputs, 32 rows at a time as [D / 4][32 rows][4]
+    // (a warp that holds one row a lane then reads and writes 512 bytes in one
+    // piece), and (reference maximum in log2 units, sum)
+    float *part_o;
+    float2 *part_ml;
     int32_t *member;               // [B] the sequence's table begins with the prefix (split verify only)
     int32_t *sched;                // [3]: next unit, CTAs finished, warps that wrote a prefix unit; zero between calls
     int32_t *err;
     int32_t verify;                // 0 = prompt, 1 = verification behind a shared prefix
-    int32_t B, T, Hq, Hkv, G, n_q, tpt;
+    int32_t B, T, Hq, Hkv, G, n_q, tpt, tiles;  // tiles: ceil(T / tpt)
     int32_t max_blocks, num_blocks, prefix_pages;
     int32_t pairs;                 // prompt: unit slots per kv head; verify: tile pairs of the prefix units
     int32_t p_units, total_units;  // prefix units come first

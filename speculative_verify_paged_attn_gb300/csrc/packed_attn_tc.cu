@@ -27,7 +27,7 @@
 //   1, 2   MMA issuers of tile A and tile B (warp 1 owns the TMEM):
 //          O_t += P_t V with P_t read from TMEM over S_t's own columns, then
 //          S_t = Q_t K^T of the next block;
-//   3      idle (it completes the warpgroup that gives up registers);
+//   3      reports prefix units whose partials are written;
 //   4-7    softmax of tile A, one thread per query row: mask, lazy running
 //   8-11   maximum (O_t rescaled only when it grows by more than 2^8), fp32
 //          row sum, P as bf16 (the MMA's input type; the sum is taken before
@@ -55,7 +55,6 @@ constexpr int kNB = kPagesPerBlock * kBlockSize;  // kv tokens per block
 constexpr int kRing = 5;                          // K and V tiles in flight
 constexpr float kRescaleLog2 = 8.f;
 constexpr uint32_t kTmemCols = 512, kTmemO = 0, kTmemS = 256;
-constexpr int kDonePerUnit = 8;  // softmax warps that report a prefix unit written
 constexpr float kLn2 = 0.69314718055994530942f;
 
 enum { kEnd = 0, kPair = 1, kAlt = 2 };
@@ -87,6 +86,7 @@ struct Smem {
     uint64_t s_full[2], p_full[2], o_full[2];
     uint64_t both;  // the two softmax groups meet
     uint64_t drain[2];
+    uint64_t written;  // a prefix unit's partials
     Unit unit;
     float2 stat[2][128];
     uint32_t tmem_base;
@@ -176,6 +176,17 @@ __device__ __forceinline__ int find_sequence(const int32_t *cu, int B, int step,
     return lo;
 }
 
+// The partial row of (slot, kv head h, token, head gi of the group).
+__device__ __forceinline__ size_t part_row(const PackedArgs &a, int slot, int h, int tok, int gi) {
+    const int tile = tok / a.tpt;
+    return (((size_t)slot * a.Hkv + h) * a.tiles + tile) * 128 + (size_t)((tok - tile * a.tpt) * a.G + gi);
+}
+// Its four columns 4 g .. 4 g + 3 are at g * 32 of this.
+template <int D>
+__device__ __forceinline__ float4 *part_cols(const PackedArgs &a, size_t row) {
+    return reinterpret_cast<float4 *>(a.part_o) + (row & ~(size_t)31) * (D / 4) + (row & 31);
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     packed_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
@@ -202,8 +213,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sm.empty[i], 2);  // the two MMA issuers
         }
         mbar_init(&sm.both, 8);
+        mbar_init(&sm.written, 8);
         mbar_init(&sm.q_full, 1);
-        mbar_init(&sm.q_empty, 10);  // the MMA issuers and the eight softmax warps
+        // the MMA issuers, the eight softmax warps and the reporter
+        mbar_init(&sm.q_empty, a.p_units > 0 ? 11 : 10);
         for (int t = 0; t < 2; ++t) {
             mbar_init(&sm.s_full[t], 1);
             mbar_init(&sm.p_full[t], 4);
@@ -567,6 +580,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 wait(&sm.drain[t], 0);
             }
+        } else {
+            // ================================================= reporter
+            // A prefix unit's partials are made visible to the other CTAs and
+            // counted here, where the fence holds up no softmax warp.
+            uint32_t done = 0;
+            for (int unit = 0; a.p_units > 0; ++unit) {
+                if (!__all_sync(0xffffffffu, bar_wait(&sm.q_full, (uint32_t)(unit & 1), a.err))) break;
+                const int kind = sm.unit.kind, prefix = sm.unit.prefix;
+                __syncwarp();
+                if (kind == kEnd) break;
+                if (lane == 0) mbar_arrive(&sm.q_empty);
+                if (!prefix) continue;
+                if (!__all_sync(0xffffffffu, bar_wait(&sm.written, done++ & 1u, a.err))) break;
+                if (lane == 0) {
+                    __threadfence();
+                    atomicAdd(a.sched + 2, 1);
+                }
+                __syncwarp();
+            }
         }
     } else {
         // ================================================= softmax and epilogue
@@ -712,6 +744,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ---- epilogue
             const bool live = r < a.tpt * G && tok < w.tok1;
             const size_t row = (size_t)tok * a.Hq + (size_t)w.h * G + gi;
+            const size_t prow = live ? part_row(a, max(w.slot, 0), w.h, tok, gi) : 0;
+            const size_t pslot = (size_t)a.Hkv * a.tiles * 128;  // partial rows of a slot
             float m = m_ref, l = l_run;
             if (pair) {
                 if (n > 0) {
@@ -736,17 +770,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                   pack_bf16x2(f[4] * inv, f[5] * inv), pack_bf16x2(f[6] * inv, f[7] * inv));
                             }
                         } else {
-                            uint4 *o = reinterpret_cast<uint4 *>(
-                                a.part_o + ((size_t)w.slot * a.T * a.Hq + row) * D + c * 32);
+                            float4 *o = part_cols<D>(a, prow) + c * 8 * 32;
 #pragma unroll
                             for (int x = 0; x < 8; ++x)
-                                o[x] = make_uint4(raw[4 * x], raw[4 * x + 1], raw[4 * x + 2], raw[4 * x + 3]);
+                                o[x * 32] = make_float4(__uint_as_float(raw[4 * x]), __uint_as_float(raw[4 * x + 1]),
+                                                        __uint_as_float(raw[4 * x + 2]), __uint_as_float(raw[4 * x + 3]));
                         }
                     }
                     tc_fence_before();
                 }
                 if (live) {
-                    if (w.slot >= 0) a.part_ml[(size_t)w.slot * a.T * a.Hq + row] = make_float2(m, l);
+                    if (w.slot >= 0) a.part_ml[prow] = make_float2(m, l);
                     else if (a.lse) a.lse[row] = (m + __log2f(l)) * kLn2;
                 }
             } else {
@@ -755,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // every prefix unit was taken by a running CTA before this
                     // unit was: they end without waiting for anything of this one
                     const unsigned long long start = global_ns();
-                    while (ld_acquire(a.sched + 2) < kDonePerUnit * a.p_units) {
+                    while (ld_acquire(a.sched + 2) < a.p_units) {
                         __nanosleep(200);
                         if (global_ns() - start > kWaitLimitNs) {
                             raise_error(a.err, SVPA_DEVERR_TIMEOUT);
@@ -774,15 +808,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 m = fmaxf(sA.x, sB.x);
                 const int np = w.merge ? a.p_splits : 0;
-                const size_t rows = (size_t)a.T * a.Hq;
                 if (live)
-                    for (int p = 0; p < np; ++p) m = fmaxf(m, __ldcg(&a.part_ml[p * rows + row]).x);
+                    for (int p = 0; p < np; ++p) m = fmaxf(m, __ldcg(&a.part_ml[p * pslot + prow]).x);
                 float fA = sA.x == -CUDART_INF_F ? 0.f : ex2_approx(sA.x - m);
                 float fB = sB.x == -CUDART_INF_F ? 0.f : ex2_approx(sB.x - m);
                 l = sA.y * fA + sB.y * fB;
                 if (live)
                     for (int p = 0; p < np; ++p) {
-                        const float2 ml = __ldcg(&a.part_ml[p * rows + row]);
+                        const float2 ml = __ldcg(&a.part_ml[p * pslot + prow]);
                         if (ml.y > 0.f) l += ml.y * ex2_approx(ml.x - m);
                     }
                 const float inv = w.slot >= 0 ? 1.f : l > 0.f ? 1.f / l : 0.f;
@@ -811,13 +844,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         if (!live) continue;
                         for (int p = 0; p < np; ++p) {
-                            const float2 ml = __ldcg(&a.part_ml[p * rows + row]);
+                            const float2 ml = __ldcg(&a.part_ml[p * pslot + prow]);
                             if (!(ml.y > 0.f)) continue;
                             const float f = ex2_approx(ml.x - m) * inv;
-                            const float4 *src = reinterpret_cast<const float4 *>(a.part_o + (p * rows + row) * D + c * 32);
+                            const float4 *src = part_cols<D>(a, p * pslot + prow) + c * 8 * 32;
 #pragma unroll
                             for (int x = 0; x < 8; ++x) {
-                                const float4 v = __ldcg(src + x);
+                                const float4 v = __ldcg(src + x * 32);
                                 o[4 * x] = fmaf(v.x, f, o[4 * x]);
                                 o[4 * x + 1] = fmaf(v.y, f, o[4 * x + 1]);
                                 o[4 * x + 2] = fmaf(v.z, f, o[4 * x + 2]);
@@ -832,16 +865,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                   pack_bf16x2(o[8 * x + 4], o[8 * x + 5]),
                                                   pack_bf16x2(o[8 * x + 6], o[8 * x + 7]));
                         } else if (nb > 0) {
-                            float4 *d = reinterpret_cast<float4 *>(
-                                a.part_o + ((size_t)w.slot * rows + row) * D + c * 32);
+                            float4 *d = part_cols<D>(a, prow) + c * 8 * 32;
 #pragma unroll
                             for (int x = 0; x < 8; ++x)
-                                d[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+                                d[x * 32] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
                         }
                     }
                     tc_fence_before();
                     if (live && t == 0) {
-                        if (w.slot >= 0) a.part_ml[(size_t)w.slot * rows + row] = make_float2(m, l);
+                        if (w.slot >= 0) a.part_ml[prow] = make_float2(m, l);
                         else if (a.lse) a.lse[row] = (m + __log2f(l)) * kLn2;
                     }
                 }
@@ -851,9 +883,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             no[0] += w.nA > 0;
             no[1] += w.nB > 0;
             if (w.prefix) {
-                __threadfence();
                 __syncwarp();
-                if (lane == 0) atomicAdd(a.sched + 2, 1);
+                if (lane == 0) mbar_arrive(&sm.written);
             }
         }
     }
@@ -872,43 +903,59 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// One warp per (token, head) row: joins its partials with log-sum-exp weights.
+// Joins the partials of 32 rows of a query tile with log-sum-exp weights: one
+// row a lane, the columns over the CTA's warps.
 template <int D>
 __global__ void __launch_bounds__(256) packed_combine_kernel(const __grid_constant__ PackedArgs a) {
-    const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    const long long rows = (long long)a.T * a.Hq;
-    if (row >= rows) return;
-    const int tok = (int)(row / a.Hq);
-    int first = 0, slots = a.p_splits + a.s_splits;
-    if (a.verify) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int kPer = D / 32;  // groups of four columns a warp takes
+    const int quarter = blockIdx.x & 3, tile = blockIdx.x >> 2, h = blockIdx.y;
+    const int r = quarter * 32 + lane, jq = r / a.G, gi = r - jq * a.G;
+    const int tok = tile * a.tpt + jq;
+    bool live = jq < a.tpt && tok < a.T;
+    int first = 0;
+    const int slots = a.p_splits + a.s_splits;
+    if (live && a.verify) {
         const int b = tok / a.n_q;
         const int L = a.lens[b];
-        if (L < 0 || (long long)L + a.n_q > (long long)a.max_blocks * kBlockSize) return;  // reported, not computed
-        if (!a.member[b]) first = a.p_splits;
-    } else if (tok >= a.cu[a.B]) {
-        return;  // rows behind the last sequence stay as they are
+        // a bad length was reported, not computed
+        live = L >= 0 && (long long)L + a.n_q <= (long long)a.max_blocks * kBlockSize;
+        if (live && !a.member[b]) first = a.p_splits;
+    } else if (live) {
+        live = tok < a.cu[a.B];  // rows behind the last sequence stay as they are
     }
-    constexpr int kPer = D / 32;
-    float m = -CUDART_INF_F, l = 0.f, o[kPer];
+    if (!live) return;
+    const size_t pslot = (size_t)a.Hkv * a.tiles * 128;
+    const size_t prow = ((size_t)h * a.tiles + tile) * 128 + r;
+    float m = -CUDART_INF_F, l = 0.f;
+    float4 o[kPer];
 #pragma unroll
-    for (int x = 0; x < kPer; ++x) o[x] = 0.f;
+    for (int x = 0; x < kPer; ++x) o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
     for (int s = first; s < slots; ++s) {
-        const float2 ml = a.part_ml[s * rows + row];
+        const float2 ml = a.part_ml[s * pslot + prow];
         if (!(ml.y > 0.f)) continue;
         const float mn = fmaxf(m, ml.x);
         const float fo = ex2_approx(m - mn), fn = ex2_approx(ml.x - mn);
-        const float *src = a.part_o + (s * rows + row) * D + lane * kPer;
+        const float4 *src = part_cols<D>(a, s * pslot + prow) + warp * kPer * 32;
         l = l * fo + ml.y * fn;
         m = mn;
 #pragma unroll
-        for (int x = 0; x < kPer; ++x) o[x] = o[x] * fo + src[x] * fn;
+        for (int x = 0; x < kPer; ++x) {
+            const float4 v = src[x * 32];
+            o[x].x = o[x].x * fo + v.x * fn;
+            o[x].y = o[x].y * fo + v.y * fn;
+            o[x].z = o[x].z * fo + v.z * fn;
+            o[x].w = o[x].w * fo + v.w * fn;
+        }
     }
     const float inv = l > 0.f ? 1.f / l : 0.f;
-    __nv_bfloat162 *dst = reinterpret_cast<__nv_bfloat162 *>(a.out + row * D + lane * kPer);
+    const size_t row = (size_t)tok * a.Hq + (size_t)h * a.G + gi;
+    uint2 *dst = reinterpret_cast<uint2 *>(a.out + row * D + warp * kPer * 4);
 #pragma unroll
-    for (int x = 0; x < kPer / 2; ++x) dst[x] = __floats2bfloat162_rn(o[2 * x] * inv, o[2 * x + 1] * inv);
-    if (lane == 0 && a.lse) a.lse[row] = (m + __log2f(l)) * kLn2;
+    for (int x = 0; x < kPer; ++x)
+        dst[x] = make_uint2(pack_bf16x2(o[x].x * inv, o[x].y * inv), pack_bf16x2(o[x].z * inv, o[x].w * inv));
+    if (warp == 0 && a.lse) a.lse[row] = (m + __log2f(l)) * kLn2;
 }
 
 template <int D>
@@ -932,8 +979,7 @@ cudaError_t launch_packed_attn(const PackedMaps &m, const PackedArgs &a, int hea
 }
 
 cudaError_t launch_packed_combine(const PackedArgs &a, int head_dim, cudaStream_t st) {
-    const long long rows = (long long)a.T * a.Hq;
-    const int grid = (int)((rows + 7) / 8);
+    const dim3 grid(4 * a.tiles, a.Hkv);
     if (head_dim == 128) packed_combine_kernel<128><<<grid, 256, 0, st>>>(a);
     else packed_combine_kernel<64><<<grid, 256, 0, st>>>(a);
     return cudaGetLastError();

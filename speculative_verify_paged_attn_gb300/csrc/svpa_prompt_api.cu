@@ -86,17 +86,18 @@ bool encode_queries(EncodeTiledFn enc, CUtensorMap m[2], const void *q, int D, i
 }
 
 struct Plan {
-    int tpt, pairs, p_units, p_splits, s_splits, total_units;
+    int tpt, tiles, pairs, p_units, p_splits, s_splits, total_units;
     size_t off_member, off_ml, off_o, bytes;
 };
 
 // Workspace: [counters][member][partial (max, sum)][partial outputs], one
 // partial slot for each KV split of the prefix units and, when split, of the others.
-svpa_status layout(Plan *pl, long long units, long long T, int Hq, int D, int members) {
+svpa_status layout(Plan *pl, long long units, long long T, int Hkv, int D, int members) {
     if (units > 0x7fffffff) return SVPA_ERR_UNSUPPORTED;
     pl->total_units = (int)units;
     const size_t slots = (size_t)pl->p_splits + (pl->s_splits > 1 ? pl->s_splits : 0);
-    const size_t rows = (size_t)T * Hq;
+    pl->tiles = ceil_div(T, pl->tpt);
+    const size_t rows = (size_t)Hkv * pl->tiles * kMaxRows;
     pl->off_member = kAlign;
     pl->off_ml = pl->off_member + align_up((size_t)members * sizeof(int32_t));
     pl->off_o = pl->off_ml + align_up(slots * rows * sizeof(float2));
@@ -116,7 +117,7 @@ svpa_status plan_prompt(const svpa_prompt_params *p, Plan *pl) {
     const int G = p->num_q_heads / p->num_kv_heads;
     if ((p->head_dim != 64 && p->head_dim != 128) || p->kv_dtype != SVPA_KV_BF16 || G > kMaxRows ||
         p->max_blocks_per_seq > (0x7fffffff - 4096) / kBlockSize ||
-        (long long)p->num_blocks * p->num_kv_heads > 0x7fffffff || p->batch > (1 << 20) || p->total_q > (1 << 28))
+        (long long)p->num_blocks * p->num_kv_heads > 0x7fffffff || p->num_kv_heads > 65535 || p->batch > (1 << 20) || p->total_q > (1 << 28))
         return SVPA_ERR_UNSUPPORTED;
     pl->tpt = kMaxRows / G;
     pl->pairs = p->total_q / (2 * pl->tpt) + p->batch;
@@ -129,7 +130,7 @@ svpa_status plan_prompt(const svpa_prompt_params *p, Plan *pl) {
     pl->s_splits = 1;
     if (units > 0 && units < sm_count())
         pl->s_splits = std::max(1, std::min({(int)(sm_count() / units), blocks / 8, kMaxSplits}));
-    return layout(pl, units * pl->s_splits, p->total_q, p->num_q_heads, p->head_dim, 0);
+    return layout(pl, units * pl->s_splits, p->total_q, p->num_kv_heads, p->head_dim, 0);
 }
 
 svpa_status plan_prefix(const svpa_attn_params *p, int32_t prefix_len, Plan *pl) {
@@ -138,7 +139,7 @@ svpa_status plan_prefix(const svpa_attn_params *p, int32_t prefix_len, Plan *pl)
     if (s != SVPA_OK) return s;
     if (prefix_len < 0 || prefix_len % kBlockSize != 0 || prefix_len / kBlockSize > p->num_blocks)
         return SVPA_ERR_INVALID_ARG;
-    if (p->kv_dtype != SVPA_KV_BF16 || p->variant == 1 || p->batch > 65535 ||
+    if (p->kv_dtype != SVPA_KV_BF16 || p->variant == 1 || p->batch > 65535 || p->num_kv_heads > 65535 ||
         (long long)p->num_blocks * p->num_kv_heads > 0x7fffffff ||
         p->max_blocks_per_seq > (0x7fffffff - 4096) / kBlockSize)
         return SVPA_ERR_UNSUPPORTED;
@@ -160,7 +161,7 @@ svpa_status plan_prefix(const svpa_attn_params *p, int32_t prefix_len, Plan *pl)
     pl->s_splits = 1;
     if (own > 0 && own < slots)
         pl->s_splits = (int)std::max<long long>(1, std::min<long long>({slots / own, sb / 8, (long long)kMaxSplits}));
-    return layout(pl, pl->p_units + own * pl->s_splits, T, p->num_q_heads, p->head_dim, p->batch);
+    return layout(pl, pl->p_units + own * pl->s_splits, T, p->num_kv_heads, p->head_dim, p->batch);
 }
 
 void fill(PackedArgs &a, const Plan &pl, void *workspace) {
@@ -170,6 +171,7 @@ void fill(PackedArgs &a, const Plan &pl, void *workspace) {
     a.part_ml = reinterpret_cast<float2 *>(ws + pl.off_ml);
     a.part_o = reinterpret_cast<float *>(ws + pl.off_o);
     a.tpt = pl.tpt;
+    a.tiles = pl.tiles;
     a.pairs = pl.pairs;
     a.p_units = pl.p_units;
     a.p_splits = pl.p_splits;
