@@ -207,7 +207,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kPageBytes = kBlockSize * D * 2;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+    // the first unit is on its way while the CTA sets itself up
+    int next = 0;
     if (threadIdx.x == 0) {
+        next = atomicAdd(&a.sched[0], 1);
         for (int i = 0; i < kRing; ++i) {
             mbar_init(&sm.full[i], 1);
             mbar_init(&sm.empty[i], 2);  // the two MMA issuers
@@ -225,10 +228,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_mbar_init();
     }
-    // rows of a query tile past tpt * G are never written by the copies
-    for (int x = threadIdx.x; x < 2 * SM::kQTile / 16; x += kThreads)
-        reinterpret_cast<uint4 *>(&sm.q[0][0])[x] = make_uint4(0, 0, 0, 0);
-    fence_proxy_async_smem();
+    // (rows of a query tile past its tokens are never written by the copies and
+    // hold anything: a row of S, P and O comes from its own row of Q alone, and
+    // theirs are not stored)
     if (warp == 1) {
         tmem_alloc(&sm.tmem_base, kTmemCols);
         tmem_relinquish();
@@ -253,10 +255,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         const int tpt2 = 2 * a.tpt;
         while (ok) {
-            int u = 0;
-            if (lane == 0) u = atomicAdd(&a.sched[0], 1);
-            u = __shfl_sync(0xffffffffu, u, 0);
+            const int u = __shfl_sync(0xffffffffu, next, 0);
             if (u >= a.total_units) break;
+            if (lane == 0) next = atomicAdd(&a.sched[0], 1);  // used after this unit
             // ---- decode
             Unit w;
             const int32_t *bt;
@@ -806,79 +807,78 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (ok && w.nB > 0) ok = wait(&sm.o_full[1], no[1]);
                 if (!ok) break;
                 tc_fence_after();
+                const int np = live && w.merge ? a.p_splits : 0;
                 m = fmaxf(sA.x, sB.x);
-                const int np = w.merge ? a.p_splits : 0;
-                if (live)
-                    for (int p = 0; p < np; ++p) m = fmaxf(m, __ldcg(&a.part_ml[p * pslot + prow]).x);
+                l = 0.f;
+                for (int p = 0; p < np; ++p) {
+                    const float2 ml = __ldcg(&a.part_ml[p * pslot + prow]);
+                    const float mn = fmaxf(m, ml.x);
+                    l = (l > 0.f ? l * ex2_approx(m - mn) : 0.f) + (ml.y > 0.f ? ml.y * ex2_approx(ml.x - mn) : 0.f);
+                    m = mn;
+                }
                 float fA = sA.x == -CUDART_INF_F ? 0.f : ex2_approx(sA.x - m);
                 float fB = sB.x == -CUDART_INF_F ? 0.f : ex2_approx(sB.x - m);
-                l = sA.y * fA + sB.y * fB;
-                if (live)
-                    for (int p = 0; p < np; ++p) {
-                        const float2 ml = __ldcg(&a.part_ml[p * pslot + prow]);
-                        if (ml.y > 0.f) l += ml.y * ex2_approx(ml.x - m);
-                    }
+                l += sA.y * fA + sB.y * fB;
                 const float inv = w.slot >= 0 ? 1.f : l > 0.f ? 1.f / l : 0.f;
                 fA *= inv;
                 fB *= inv;
                 // group t takes half of the columns of both accumulators
-                const int nb = w.nA + w.nB;
+                constexpr int kHalf = D / 2, kC = D / 64;  // columns, pieces of 32
+                float o[kHalf];
                 {
-#pragma unroll 1
-                    for (int c = t * (D / 64); c < (t + 1) * (D / 64); ++c) {
-                        float o[32];
-                        uint32_t raw[32];
+                    uint32_t ra[kC][32];
+                    if (w.nA > 0) {
 #pragma unroll
-                        for (int x = 0; x < 32; ++x) o[x] = 0.f;
-                        if (w.nA > 0) {
-                            tmem_ld32(tO + c * 32, raw);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int x = 0; x < 32; ++x) o[x] = __uint_as_float(raw[x]) * fA;
-                        }
-                        if (w.nB > 0) {
-                            tmem_ld32(tO + 128 + c * 32, raw);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int x = 0; x < 32; ++x) o[x] = fmaf(__uint_as_float(raw[x]), fB, o[x]);
-                        }
-                        if (!live) continue;
-                        for (int p = 0; p < np; ++p) {
-                            const float2 ml = __ldcg(&a.part_ml[p * pslot + prow]);
-                            if (!(ml.y > 0.f)) continue;
-                            const float f = ex2_approx(ml.x - m) * inv;
-                            const float4 *src = part_cols<D>(a, p * pslot + prow) + c * 8 * 32;
-#pragma unroll
-                            for (int x = 0; x < 8; ++x) {
-                                const float4 v = __ldcg(src + x * 32);
-                                o[4 * x] = fmaf(v.x, f, o[4 * x]);
-                                o[4 * x + 1] = fmaf(v.y, f, o[4 * x + 1]);
-                                o[4 * x + 2] = fmaf(v.z, f, o[4 * x + 2]);
-                                o[4 * x + 3] = fmaf(v.w, f, o[4 * x + 3]);
-                            }
-                        }
-                        if (w.slot < 0) {
-                            uint4 *d = reinterpret_cast<uint4 *>(a.out + row * D + c * 32);
-#pragma unroll
-                            for (int x = 0; x < 4; ++x)
-                                d[x] = make_uint4(pack_bf16x2(o[8 * x], o[8 * x + 1]), pack_bf16x2(o[8 * x + 2], o[8 * x + 3]),
-                                                  pack_bf16x2(o[8 * x + 4], o[8 * x + 5]),
-                                                  pack_bf16x2(o[8 * x + 6], o[8 * x + 7]));
-                        } else if (nb > 0) {
-                            float4 *d = part_cols<D>(a, prow) + c * 8 * 32;
-#pragma unroll
-                            for (int x = 0; x < 8; ++x)
-                                d[x * 32] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
-                        }
+                        for (int c = 0; c < kC; ++c) tmem_ld32(tO + (t * kC + c) * 32, ra[c]);
+                        tmem_ld_wait();
                     }
-                    tc_fence_before();
-                    if (live && t == 0) {
-                        if (w.slot >= 0) a.part_ml[prow] = make_float2(m, l);
-                        else if (a.lse) a.lse[row] = (m + __log2f(l)) * kLn2;
+#pragma unroll
+                    for (int x = 0; x < kHalf; ++x) o[x] = w.nA > 0 ? __uint_as_float(ra[x >> 5][x & 31]) * fA : 0.f;
+                    if (w.nB > 0) {
+#pragma unroll
+                        for (int c = 0; c < kC; ++c) tmem_ld32(tO + 128 + (t * kC + c) * 32, ra[c]);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int x = 0; x < kHalf; ++x) o[x] = fmaf(__uint_as_float(ra[x >> 5][x & 31]), fB, o[x]);
                     }
                 }
-                // neither group goes on to a new unit's P while the other reads O and the statistics
+                // O is read: the next unit's first P V may start while this one is joined and stored
                 ok = meet();
+                if (!ok) break;
+                for (int p = 0; p < np; ++p) {
+                    const float2 ml = __ldcg(&a.part_ml[p * pslot + prow]);
+                    const float4 *src = part_cols<D>(a, p * pslot + prow) + t * (kHalf / 4) * 32;
+                    float4 v[kHalf / 4];
+#pragma unroll
+                    for (int x = 0; x < kHalf / 4; ++x) v[x] = __ldcg(src + x * 32);
+                    const float f = ml.y > 0.f ? ex2_approx(ml.x - m) * inv : 0.f;
+                    if (f == 0.f) continue;  // nothing there: not even zeros
+#pragma unroll
+                    for (int x = 0; x < kHalf / 4; ++x) {
+                        o[4 * x] = fmaf(v[x].x, f, o[4 * x]);
+                        o[4 * x + 1] = fmaf(v[x].y, f, o[4 * x + 1]);
+                        o[4 * x + 2] = fmaf(v[x].z, f, o[4 * x + 2]);
+                        o[4 * x + 3] = fmaf(v[x].w, f, o[4 * x + 3]);
+                    }
+                }
+                if (live) {
+                    if (w.slot < 0) {
+                        uint4 *d = reinterpret_cast<uint4 *>(a.out + row * D + t * kHalf);
+#pragma unroll
+                        for (int x = 0; x < kHalf / 8; ++x)
+                            d[x] = make_uint4(pack_bf16x2(o[8 * x], o[8 * x + 1]), pack_bf16x2(o[8 * x + 2], o[8 * x + 3]),
+                                              pack_bf16x2(o[8 * x + 4], o[8 * x + 5]),
+                                              pack_bf16x2(o[8 * x + 6], o[8 * x + 7]));
+                        if (t == 0 && a.lse) a.lse[row] = (m + __log2f(l)) * kLn2;
+                    } else {
+                        float4 *d = part_cols<D>(a, prow) + t * (kHalf / 4) * 32;
+                        if (w.nA + w.nB > 0)
+#pragma unroll
+                            for (int x = 0; x < kHalf / 4; ++x)
+                                d[x * 32] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+                        if (t == 0) a.part_ml[prow] = make_float2(m, l);
+                    }
+                }
             }
             no[0] += w.nA > 0;
             no[1] += w.nB > 0;

@@ -150,10 +150,22 @@ svpa_status plan_prefix(const svpa_attn_params *p, int32_t prefix_len, Plan *pl)
     const int slots = sm_count();
     const int pb = ceil_div(prefix_len, 8 * kBlockSize);
     const long long tiles = (long long)pl->pairs * p->num_kv_heads;
+    // Splits of the prefix: rounds of units over the SMs times a unit's length,
+    // in blocks; a unit costs about three blocks beside its own (filling the
+    // pipeline and storing its partials), a split one block of every own part
+    // (joining them).
     pl->p_splits = 0;
-    if (pb > 0 && tiles > 0)
-        pl->p_splits = (int)std::max<long long>(
-            1, std::min<long long>({ceil_div(2 * slots, tiles), pb / 4, (long long)kMaxSplits}));
+    if (pb > 0 && tiles > 0) {
+        long long best = 0;
+        for (int sp = 1; sp <= std::min(kMaxSplits, std::max(1, pb / 2)); ++sp) {
+            const long long cost = ceil_div(tiles * sp, slots) * (long long)(ceil_div(pb, sp) + 3) +
+                                   ceil_div((long long)p->batch * p->num_kv_heads, slots) * (long long)sp;
+            if (pl->p_splits == 0 || cost < best) {
+                best = cost;
+                pl->p_splits = sp;
+            }
+        }
+    }
     pl->p_units = (int)(tiles * pl->p_splits);
     // the sequences' own parts: split when they alone leave SMs idle
     const long long own = (long long)p->batch * p->num_kv_heads;
