@@ -402,7 +402,7 @@ typedef struct svpa_logits_params {
  *   x = x - presence[b]                                 n(v) > 0
  *   x = x + bias(v)
  *   x = -inf                                            v not allowed by the mask
- * Unmarked tokens keep their value (bf16 to fp32 exactly); a row whose mask
+ * Other tokens keep their value (bf16 to fp32 exactly) and -inf stays -inf; a row whose mask
  * allows nothing is all -inf (which the samplers refuse).
  *
  *  logits       fp32 or bf16 [B, rows, V]

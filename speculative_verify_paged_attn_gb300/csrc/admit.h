@@ -54,7 +54,9 @@ struct ProcessArgs {
     const uint32_t *mask;
     int32_t *err;
     int32_t B, rows, V, max_hist, draft_stride, bf16;
+    int32_t split_rows;  // one row a CTA (set by the launch)
     unsigned long long path[kMaxNq];  // bit i of row j: draft entry i counts for row j
+    unsigned long long used;          // the entries that count for any row
 };
 cudaError_t launch_logits_process(const ProcessArgs &a, cudaStream_t stream);
 

@@ -22,6 +22,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kChunk = 512;  // entries a warp writes at a time
+constexpr int kMaxCtas = 152 * 8;  // resident at once for batches of up to about 3500
 
 // Exclusive sums of two values per thread over the CTA; totals returned too.
 __device__ __forceinline__ void scan2(int &x, int &y, int &tx, int &ty, int2 *warp_sums) {
@@ -125,7 +126,7 @@ __global__ void __launch_bounds__(kThreads) build_kernel(const __grid_constant__
     }
     // the block of request b's page i, with its own pages popped in order
     auto block_of = [&](int b, int i) -> int {
-        return i < P ? a.prefix_blocks[i] : a.free_stack[top - 1 - (first[b] + i - P)];
+        return __ldg(i < P ? a.prefix_blocks + i : a.free_stack + (top - 1 - (first[b] + i - P)));
     };
     const int lane = threadIdx.x & 31;
     const long long warps = (long long)gridDim.x * (kThreads / 32);
@@ -141,9 +142,10 @@ __global__ void __launch_bounds__(kThreads) build_kernel(const __grid_constant__
             const unsigned q = (col0 + k) / (unsigned)a.max_blocks;
             const int b = row0 + (int)q, i = (int)(col0 + k - q * a.max_blocks);
             const int own = first[b + 1] - first[b];
-            const int n = a.seq_lens[b];
             int id = -1;
-            if (n > 0 && i < P + own) {
+            // (a request without pages of its own has new tokens in none, and
+            // holds the prefix only if its length says so)
+            if (i < P + own && (own > 0 || __ldg(a.seq_lens + b) > 0)) {
                 id = block_of(b, i);
                 if (i >= P) {
                     if (id < 0 || id >= a.num_blocks) {
@@ -158,28 +160,30 @@ __global__ void __launch_bounds__(kThreads) build_kernel(const __grid_constant__
         }
     }
     const int total = cu[a.B];
+    const bool vec = (reinterpret_cast<uintptr_t>(a.slot_map) & 15) == 0;
     for (long long c = w0; c * kChunk < a.slots; c += warps) {
-        const int s0 = (int)(c * kChunk);
-#pragma unroll 1
-        for (int k = lane * 4; k < kChunk; k += 128) {
-            const int t0 = s0 + k;
-            if (t0 >= a.slots) break;
-            int b = 0;
-            if (t0 < total) {  // the request of the first of four rows
-                int lo = 0, hi = a.B;
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) >> 1;
-                    if (cu[mid] <= t0) lo = mid;
-                    else hi = mid;
-                }
-                b = lo;
+        const int s0 = (int)(c * kChunk), s1 = min(s0 + kChunk, a.slots);
+        // the requests of the chunk's first and last rows
+        auto request_of = [&](int t, int lo, int hi) -> int {  // in [lo, hi)
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (cu[mid] <= t) lo = mid;
+                else hi = mid;
             }
-            int page = -1, row = -1, id = -1;
+            return lo;
+        };
+        const int lo = s0 < total ? request_of(s0, 0, a.B) : 0;
+        const int hi = s0 < total ? request_of(min(s1, total) - 1, lo, a.B) + 1 : 1;
+#pragma unroll
+        for (int k = 0; k < kChunk / 128; ++k) {
+            const int t0 = s0 + k * 128 + lane * 4;
+            if (t0 >= s1) break;
+            int b = t0 < total ? request_of(t0, lo, hi) : 0;
+            int page = -1, row = -1, id = -1, slot[4];
 #pragma unroll
             for (int z = 0; z < 4; ++z) {
                 const int t = t0 + z;
-                if (t >= a.slots) break;
-                int slot = -1;
+                slot[z] = -1;
                 if (t < total) {
                     while (cu[b + 1] <= t) ++b;
                     const int pos = prefix_len + t - cu[b];
@@ -189,9 +193,15 @@ __global__ void __launch_bounds__(kThreads) build_kernel(const __grid_constant__
                         id = block_of(b, page);
                         if (id < 0 || id >= a.num_blocks) id = -1;  // raised with the table
                     }
-                    if (id >= 0) slot = id * kBlockSize + pos % kBlockSize;
+                    if (id >= 0) slot[z] = id * kBlockSize + pos % kBlockSize;
                 }
-                a.slot_map[t] = slot;
+            }
+            if (vec && t0 + 4 <= a.slots) {
+                *reinterpret_cast<int4 *>(a.slot_map + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+            } else {
+#pragma unroll
+                for (int z = 0; z < 4; ++z)
+                    if (t0 + z < a.slots) a.slot_map[t0 + z] = slot[z];
             }
         }
     }
@@ -211,7 +221,7 @@ __global__ void __launch_bounds__(kThreads) build_kernel(const __grid_constant__
 cudaError_t launch_block_table_build(const BuildArgs &a, cudaStream_t stream) {
     const long long entries = (long long)a.B * a.max_blocks + a.slots;
     const long long ctas = (entries + kChunk * (kThreads / 32) - 1) / (kChunk * (kThreads / 32));
-    const int grid = (int)(ctas < 1 ? 1 : ctas > 304 ? 304 : ctas);
+    const int grid = (int)(ctas < 1 ? 1 : ctas > kMaxCtas ? kMaxCtas : ctas);
     const size_t smem = (size_t)2 * (a.B + 1) * sizeof(int32_t);
     if (smem > 48 * 1024) {
         static DeviceMemo<int> attr_set;

@@ -8,12 +8,15 @@
 // in this order, each step rounded to fp32.
 //
 // Bytes only: the logits read once, the results written once.  A CTA takes a
-// slab of 4096 tokens of one sequence and all its rows.  It forms n(v) of the
-// slab in shared memory from the sequence's history (read by every slab of the
-// sequence, from L2) and marks biased tokens and drafts there, so the pass over
-// the rows needs one word of shared memory per token, kept in registers for
-// all rows; drafts, whose count differs from row to row, and biases take a slow
-// path for the few tokens that are marked.
+// slab of tokens of one sequence and its rows (or one of them, where there are
+// few CTAs).  It forms n(v) of the slab in shared memory, one word a token,
+// from the sequence's history (read by every slab of the sequence, from L2),
+// marks drafts and biased tokens there and lists the tokens that are marked at
+// all.  The rows are then streamed through with the mask alone, and the listed
+// tokens put right in the output, one a lane, while their lines are in L2: with
+// the rules applied on the way, a warp took the long path for the one token in
+// fifty that needs it (119 to 189 us on 64 x 6 rows of 128256 bf16 logits with
+// histories of 8192).
 #include "admit.h"
 #include "svpa_device.cuh"
 
@@ -21,163 +24,234 @@ namespace svpa {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kSlab = 4096;
 constexpr int kMaxDrafts = kMaxNq;
+constexpr int kBiasList = 256;  // biased tokens of a slab kept in shared memory
 
 // a token's word: times generated << 3 | biased << 2 | drafted << 1 | in the prompt
 constexpr unsigned kInPrompt = 1, kDrafted = 2, kBiased = 4, kOnce = 8;
 
+template <int SLAB>
 struct Shared {
-    unsigned word[kSlab];
-    int bias[kSlab];  // last entry of the bias list for the token
+    unsigned word[SLAB];
+    uint16_t marked[SLAB];      // tokens with a word, in no order
+    int bias_at[kBiasList];     // token of the slab
+    int bias_entry[kBiasList];  // its place in the list
+    int bias_n, marked_n;
     int drafts[kMaxDrafts];
 };
+static_assert(sizeof(Shared<8192>) <= 54 * 1024, "four CTAs per SM");
 
-__device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
-    const uint2 u = *reinterpret_cast<const uint2 *>(p);
-    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
-                       __uint_as_float(u.y & 0xffff0000u));
+__device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
+    const float4 u = __ldcs(reinterpret_cast<const float4 *>(p)), v = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
+    x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
 }
-__device__ __forceinline__ float load1(const float *p) { return *p; }
-__device__ __forceinline__ float load1(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&x)[8]) {
+    const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p));
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(u[i] << 16);
+        x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ float load1(const float *p) { return __ldcs(p); }
+__device__ __forceinline__ float load1(const __nv_bfloat16 *p) {
+    return __uint_as_float((unsigned)__ldcs(reinterpret_cast<const unsigned short *>(p)) << 16);
+}
 
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads) process_kernel(const __grid_constant__ ProcessArgs a) {
+// VEC: eight consecutive tokens a thread (V a multiple of 8, rows 16-byte
+// aligned); else four that lie 32 apart.
+template <typename T, bool VEC, int SLAB, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1536 / THREADS) process_kernel(const __grid_constant__ ProcessArgs a) {
     extern __shared__ __align__(16) uint8_t raw[];
-    Shared &sm = *reinterpret_cast<Shared *>(raw);
-    const int b = blockIdx.y, v0 = blockIdx.x * kSlab, n = min(kSlab, a.V - v0);
+    Shared<SLAB> &sm = *reinterpret_cast<Shared<SLAB> *>(raw);
+    const int b = blockIdx.y, v0 = blockIdx.x * SLAB, n = min(SLAB, a.V - v0);
+    const int r0 = a.split_rows ? blockIdx.z : 0, r1 = a.split_rows ? r0 + 1 : a.rows;
     const bool marks = a.history || a.drafts || a.bias_tokens;
+    const bool report = blockIdx.x == 0 && blockIdx.z == 0;
     if (marks) {
-        for (int i = threadIdx.x; i < kSlab; i += kThreads) sm.word[i] = 0u;
-        if (a.bias_tokens)
-            for (int i = threadIdx.x; i < kSlab; i += kThreads) sm.bias[i] = -1;
-        __syncthreads();
+        int hn = 0, pn = 0, lo = 0, hi = 0;
         if (a.history) {
-            int hn = a.hist_lens[b], pn = a.prompt_lens ? a.prompt_lens[b] : 0;
-            if (hn < 0 || hn > a.max_hist || pn < 0 || pn > hn) {
-                if (blockIdx.x == 0 && threadIdx.x == 0) raise_error(a.err, SVPA_DEVERR_BAD_VALUE);
-                hn = min(max(hn, 0), a.max_hist);
-                pn = min(max(pn, 0), hn);
-            }
-            const int32_t *h = a.history + (size_t)b * a.max_hist;
-            for (int i = threadIdx.x; i < hn; i += kThreads) {
-                const int v = h[i];
-                const unsigned x = (unsigned)(v - v0);
+            hn = a.hist_lens[b];
+            pn = a.prompt_lens ? a.prompt_lens[b] : 0;
+        }
+        if (a.bias_tokens) {
+            lo = a.bias_offsets[b];
+            hi = a.bias_offsets[b + 1];
+        }
+        if (hn < 0 || hn > a.max_hist || pn < 0 || pn > hn || lo < 0 || hi < lo) {
+            if (report && threadIdx.x == 0) raise_error(a.err, SVPA_DEVERR_BAD_VALUE);
+            hn = min(max(hn, 0), a.max_hist);
+            pn = min(max(pn, 0), hn);
+            if (lo < 0 || hi < lo) lo = hi = 0;
+        }
+        for (int i = threadIdx.x; i < SLAB / 4; i += THREADS)
+            reinterpret_cast<uint4 *>(sm.word)[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (threadIdx.x == 0) sm.bias_n = sm.marked_n = 0;
+        __syncthreads();
+        // the first mark of a token lists it
+        auto listed = [&](unsigned before, unsigned x) {
+            if (before == 0u) sm.marked[atomicAdd(&sm.marked_n, 1)] = (uint16_t)x;
+        };
+        const int32_t *h = a.history + (size_t)b * a.max_hist;
+        constexpr int kAhead = 8;  // history loads in flight per thread
+        for (int i0 = threadIdx.x; i0 < hn; i0 += kAhead * THREADS) {
+            int v[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) v[k] = i0 + k * THREADS < hn ? __ldg(h + i0 + k * THREADS) : v0;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int i = i0 + k * THREADS;
+                if (i >= hn) break;
+                const unsigned x = (unsigned)(v[k] - v0);
                 if (x < (unsigned)n) {
-                    if (i < pn) atomicOr(&sm.word[x], kInPrompt);
-                    else atomicAdd(&sm.word[x], kOnce);
-                } else if (blockIdx.x == 0 && (v < 0 || v >= a.V)) {
+                    listed(i < pn ? atomicOr(&sm.word[x], kInPrompt) : atomicAdd(&sm.word[x], kOnce), x);
+                } else if (report && (v[k] < 0 || v[k] >= a.V)) {
                     raise_error(a.err, SVPA_DEVERR_BAD_VALUE);
                 }
             }
         }
         if (a.drafts)
-            for (int i = threadIdx.x; i < a.draft_stride; i += kThreads) {
+            for (int i = threadIdx.x; i < a.draft_stride; i += THREADS) {
                 const int v = a.drafts[(size_t)b * a.draft_stride + i];
-                bool used = false;  // an entry no row counts (a tree's root) may hold anything
-                for (int j = 0; j < a.rows; ++j) used = used || ((a.path[j] >> i) & 1ull);
                 sm.drafts[i] = v;
+                if (!((a.used >> i) & 1ull)) continue;  // an entry no row counts (a tree's root) may hold anything
                 const unsigned x = (unsigned)(v - v0);
-                if (used && x < (unsigned)n) atomicOr(&sm.word[x], kDrafted);
-                else if (used && blockIdx.x == 0 && (v < 0 || v >= a.V)) raise_error(a.err, SVPA_DEVERR_BAD_VALUE);
+                if (x < (unsigned)n) listed(atomicOr(&sm.word[x], kDrafted), x);
+                else if (report && (v < 0 || v >= a.V)) raise_error(a.err, SVPA_DEVERR_BAD_VALUE);
             }
-        if (a.bias_tokens) {
-            const int lo = a.bias_offsets[b], hi = a.bias_offsets[b + 1];
-            if (lo < 0 || hi < lo) {
-                if (blockIdx.x == 0 && threadIdx.x == 0) raise_error(a.err, SVPA_DEVERR_BAD_VALUE);
-            } else {
-                for (int i = lo + threadIdx.x; i < hi; i += kThreads) {
-                    const int v = a.bias_tokens[i];
-                    const unsigned x = (unsigned)(v - v0);
-                    if (x < (unsigned)n) {
-                        atomicOr(&sm.word[x], kBiased);
-                        atomicMax(&sm.bias[x], i);
-                    } else if (blockIdx.x == 0 && (v < 0 || v >= a.V)) {
-                        raise_error(a.err, SVPA_DEVERR_BAD_VALUE);
-                    }
+        for (int i = lo + threadIdx.x; i < hi; i += THREADS) {
+            const int v = a.bias_tokens[i];
+            const unsigned x = (unsigned)(v - v0);
+            if (x < (unsigned)n) {
+                listed(atomicOr(&sm.word[x], kBiased), x);
+                const int at = atomicAdd(&sm.bias_n, 1);
+                if (at < kBiasList) {
+                    sm.bias_at[at] = (int)x;
+                    sm.bias_entry[at] = i;
                 }
+            } else if (report && (v < 0 || v >= a.V)) {
+                raise_error(a.err, SVPA_DEVERR_BAD_VALUE);
             }
         }
-        __syncthreads();
     }
+
+    // ---- every token: the mask
+    const int words = (a.V + 31) / 32;
+    const float ninf = __int_as_float(0xff800000);
+    const T *in = static_cast<const T *>(a.in) + ((size_t)b * a.rows + r0) * a.V + v0;
+    float *const out = a.out + ((size_t)b * a.rows + r0) * a.V + v0;
+    const uint32_t *mask = a.mask ? a.mask + ((size_t)b * a.rows + r0) * words + v0 / 32 : nullptr;
+    constexpr int N = VEC ? 8 : 4;
+    const int at0 = VEC ? threadIdx.x * 8 : (threadIdx.x >> 5) * 128 + (threadIdx.x & 31);
+    for (int i = at0; i < n; i += THREADS * N) {
+        const T *src = in + i;
+        float *dst = out + i;
+        const uint32_t *bits = mask ? mask + i / 32 : nullptr;
+#pragma unroll 2
+        for (int j = r0; j < r1; ++j) {
+            float x[N];
+            uint32_t ok = 0xffffffffu;
+            if constexpr (VEC) {
+                load8(src, x);
+                if (mask) ok = __ldg(bits) >> (i & 31);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (i + e * 32 >= n) continue;
+                    x[e] = load1(src + e * 32);
+                    if (mask && !((__ldg(bits + e) >> (i & 31)) & 1u)) ok &= ~(1u << e);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                if (!((ok >> e) & 1u)) x[e] = ninf;
+            if constexpr (VEC) {
+                *reinterpret_cast<float4 *>(dst) = make_float4(x[0], x[1], x[2], x[3]);
+                *(reinterpret_cast<float4 *>(dst) + 1) = make_float4(x[4], x[5], x[6], x[7]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (i + e * 32 < n) dst[e * 32] = x[e];
+            }
+            src += a.V;
+            dst += a.V;
+            bits += words;
+        }
+    }
+    if (!marks) return;
+    __syncthreads();
+
+    // ---- the marked tokens: their logits are in the output, -inf where masked
+    // (or given so: it stays)
     const float rep = a.repetition ? a.repetition[b] : 1.f;
     const float pres = a.presence ? a.presence[b] : 0.f;
     const float freq = a.frequency ? a.frequency[b] : 0.f;
-    const bool penal = a.repetition || a.presence || a.frequency;
-    const int words = (a.V + 31) / 32;
-
-    auto process = [&](float x, unsigned w, int i, int j) -> float {
-        if (w == 0u) return x;
-        unsigned count = w / kOnce;
-        if (w & kDrafted) {
-            for (unsigned long long m = a.path[j]; m; m &= m - 1)
-                count += sm.drafts[__ffsll((long long)m) - 1] == v0 + i;
+    const int m = sm.marked_n, c = sm.bias_n;
+    for (int z = threadIdx.x; z < m; z += THREADS) {
+        const int i = sm.marked[z];
+        const unsigned w = sm.word[i];
+        float bias = 0.f;
+        if (w & kBiased) {  // the last entry of the list that names the token
+            int entry = -1;
+            if (c <= kBiasList) {
+                for (int k = 0; k < c; ++k)
+                    if (sm.bias_at[k] == i) entry = max(entry, sm.bias_entry[k]);
+            } else {
+                const int lo = a.bias_offsets[b];
+                for (entry = a.bias_offsets[b + 1] - 1; entry > lo && a.bias_tokens[entry] != v0 + i; --entry) {
+                }
+            }
+            bias = a.bias_values[entry];
         }
-        if (penal) {
+        float *dst = out + i;
+#pragma unroll 4
+        for (int j = r0; j < r1; ++j, dst += a.V) {
+            float x = *dst;
+            unsigned count = w / kOnce;
+            if (w & kDrafted)
+                for (unsigned long long path = a.path[j]; path; path &= path - 1)
+                    count += sm.drafts[__ffsll((long long)path) - 1] == v0 + i;
             if ((w & kInPrompt) || count) x = x > 0.f ? __fdiv_rn(x, rep) : __fmul_rn(x, rep);
             if (count) x = __fadd_rn(__fadd_rn(x, -__fmul_rn(freq, (float)count)), -pres);
-        }
-        if (w & kBiased) x = __fadd_rn(x, a.bias_values[sm.bias[i]]);
-        return x;
-    };
-
-    const T *in = static_cast<const T *>(a.in) + ((size_t)b * a.rows) * a.V + v0;
-    float *out = a.out + ((size_t)b * a.rows) * a.V + v0;
-    const uint32_t *mask = a.mask ? a.mask + (size_t)b * a.rows * words + v0 / 32 : nullptr;
-    if (VEC) {
-        for (int i = threadIdx.x * 4; i < n; i += kThreads * 4) {
-            uint4 w = make_uint4(0u, 0u, 0u, 0u);
-            if (marks) w = *reinterpret_cast<const uint4 *>(&sm.word[i]);
-            const bool any = (w.x | w.y | w.z | w.w) != 0u;
-            for (int j0 = 0; j0 < a.rows; j0 += 4) {
-                float4 x[4];
-                uint32_t ok[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (j0 + k >= a.rows) break;
-                    x[k] = load4(in + (size_t)(j0 + k) * a.V + i);
-                    ok[k] = mask ? mask[(size_t)(j0 + k) * words + i / 32] >> (i & 31) : 15u;
-                }
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (j0 + k >= a.rows) break;
-                    if (any) {
-                        x[k].x = process(x[k].x, w.x, i, j0 + k);
-                        x[k].y = process(x[k].y, w.y, i + 1, j0 + k);
-                        x[k].z = process(x[k].z, w.z, i + 2, j0 + k);
-                        x[k].w = process(x[k].w, w.w, i + 3, j0 + k);
-                    }
-                    const float ninf = __int_as_float(0xff800000);
-                    if (!(ok[k] & 1u)) x[k].x = ninf;
-                    if (!(ok[k] & 2u)) x[k].y = ninf;
-                    if (!(ok[k] & 4u)) x[k].z = ninf;
-                    if (!(ok[k] & 8u)) x[k].w = ninf;
-                    *reinterpret_cast<float4 *>(out + (size_t)(j0 + k) * a.V + i) = x[k];
-                }
-            }
-        }
-    } else {
-        for (int i = threadIdx.x; i < n; i += kThreads) {
-            const unsigned w = marks ? sm.word[i] : 0u;
-            for (int j = 0; j < a.rows; ++j) {
-                float x = process(load1(in + (size_t)j * a.V + i), w, i, j);
-                if (mask && !((mask[(size_t)j * words + i / 32] >> (i & 31)) & 1u)) x = __int_as_float(0xff800000);
-                out[(size_t)j * a.V + i] = x;
-            }
+            if (w & kBiased) x = __fadd_rn(x, bias);
+            if (*dst != ninf) *dst = x;
         }
     }
 }
 
-template <typename T>
-cudaError_t launch_t(const ProcessArgs &a, cudaStream_t st) {
-    const bool vec = a.V % 4 == 0 && (reinterpret_cast<uintptr_t>(a.in) & (4 * sizeof(T) - 1)) == 0 &&
+template <typename T, int SLAB, int THREADS>
+cudaError_t launch_s(const ProcessArgs &a, cudaStream_t st) {
+    const bool vec = a.V % 8 == 0 && (reinterpret_cast<uintptr_t>(a.in) & 15) == 0 &&
                      (reinterpret_cast<uintptr_t>(a.out) & 15) == 0;
-    const dim3 grid((a.V + kSlab - 1) / kSlab, a.B);
-    if (vec) process_kernel<T, true><<<grid, kThreads, sizeof(Shared), st>>>(a);
-    else process_kernel<T, false><<<grid, kThreads, sizeof(Shared), st>>>(a);
+    const dim3 grid((a.V + SLAB - 1) / SLAB, a.B, a.split_rows ? a.rows : 1);
+    static DeviceMemo<int> attr_set;  // the shared-memory opt-in, once per device
+    int done = 0;
+    const cudaError_t e = attr_set.get(&done, [](int *v) {
+        *v = 1;
+        const int bytes = (int)sizeof(Shared<SLAB>);
+        cudaError_t r = cudaFuncSetAttribute(process_kernel<T, true, SLAB, THREADS>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (r == cudaSuccess)
+            r = cudaFuncSetAttribute(process_kernel<T, false, SLAB, THREADS>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        return r;
+    });
+    if (e != cudaSuccess) return e;
+    if (vec) process_kernel<T, true, SLAB, THREADS><<<grid, THREADS, sizeof(Shared<SLAB>), st>>>(a);
+    else process_kernel<T, false, SLAB, THREADS><<<grid, THREADS, sizeof(Shared<SLAB>), st>>>(a);
     return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_t(ProcessArgs a, cudaStream_t st) {
+    // the largest slab that still leaves every SM a few CTAs; below that, a
+    // row a CTA
+    const long long tokens = (long long)a.V * a.B;
+    if (tokens >= 8192LL * 152 * 6) return launch_s<T, 8192, 512>(a, st);
+    if (tokens >= 2048LL * 152 * 4) return launch_s<T, 2048, 256>(a, st);
+    a.split_rows = 1;
+    return launch_s<T, 1024, 128>(a, st);
 }
 
 }  // namespace

@@ -127,6 +127,7 @@ svpa_status svpa_logits_process(const svpa_logits_params *p, const void *logits,
         if (j == 0 ? parent[0] != -1 : (parent[j] < 0 || parent[j] >= j)) return SVPA_ERR_INVALID_ARG;
         a.path[j] = j == 0 ? 0ull : (a.path[parent[j]] | 1ull << j);
     }
+    for (int j = 0; j < p->rows; ++j) a.used |= a.path[j];
     if (p->batch == 0) return SVPA_OK;
     if (!logits || !out || !error_flag) return SVPA_ERR_INVALID_ARG;
     const bool bf16 = p->logits_dtype == SVPA_LOGITS_BF16;
