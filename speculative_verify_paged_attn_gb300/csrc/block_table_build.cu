@@ -59,15 +59,9 @@ __global__ void __launch_bounds__(kThreads) build_kernel(const __grid_constant__
     int32_t *first = sh;               // [B + 1] own pages of the requests before
     int32_t *cu = sh + a.B + 1;        // [B + 1] new tokens of the requests before
     __shared__ int2 warp_sums[kThreads / 32];
-    __shared__ int s_bad, s_live;
-    __shared__ long long s_pages, s_tokens;
+    __shared__ long long warp_pages[kThreads / 32], warp_tokens[kThreads / 32];
+    __shared__ int warp_live[kThreads / 32], warp_bad[kThreads / 32];
     const int P = a.prefix_pages, prefix_len = P * kBlockSize;
-    if (threadIdx.x == 0) {
-        s_bad = 0;
-        s_live = 0;
-        s_pages = s_tokens = 0;
-    }
-    __syncthreads();
     const int top = *a.free_top;
     // lengths: each thread takes a run of requests
     const int per = (a.B + kThreads - 1) / kThreads;
@@ -88,12 +82,35 @@ __global__ void __launch_bounds__(kThreads) build_kernel(const __grid_constant__
         if (id < 0 || id >= a.num_blocks) bad |= SVPA_DEVERR_BAD_BLOCK;
         else if (*(volatile int32_t *)(a.refcount + id) < 1) bad |= SVPA_DEVERR_BAD_VALUE;
     }
-    if (bad) atomicOr(&s_bad, bad);
-    if (live) atomicAdd(&s_live, live);
-    if (lp) atomicAdd((unsigned long long *)&s_pages, (unsigned long long)lp);
-    if (lt) atomicAdd((unsigned long long *)&s_tokens, (unsigned long long)lt);
+    {
+        // totals over the CTA, in 64 bits (a batch of bad lengths may exceed 32)
+        long long sp = lp, st = lt;
+        int sl = live, sb = bad;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            sp += __shfl_xor_sync(0xffffffffu, sp, o);
+            st += __shfl_xor_sync(0xffffffffu, st, o);
+            sl += __shfl_xor_sync(0xffffffffu, sl, o);
+            sb |= __shfl_xor_sync(0xffffffffu, sb, o);
+        }
+        if ((threadIdx.x & 31) == 0) {
+            warp_pages[threadIdx.x >> 5] = sp;
+            warp_tokens[threadIdx.x >> 5] = st;
+            warp_live[threadIdx.x >> 5] = sl;
+            warp_bad[threadIdx.x >> 5] = sb;
+        }
+    }
     __syncthreads();
-    bad = s_bad;
+    long long s_pages = 0, s_tokens = 0;
+    int s_live = 0;
+    bad = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        s_pages += warp_pages[w];
+        s_tokens += warp_tokens[w];
+        s_live += warp_live[w];
+        bad |= warp_bad[w];
+    }
     if (top < 0 || top > a.num_blocks || s_tokens > a.slots) bad |= SVPA_DEVERR_BAD_VALUE;
     else if (s_pages > top) bad |= SVPA_DEVERR_FREE_OVERFLOW;
     if (bad) {

@@ -31,6 +31,19 @@ __device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d
     return (uint32_t)lo | ((uint32_t)hi << 16);
 }
 
+// v / sc, correctly rounded, from inv = 1 / sc correctly rounded (P. Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor",
+// 1990): the remainder of v * inv is exact in one fused multiply-add, and adding
+// its share rounds once.  Holds for a scale whose significand is not all ones
+// and remainders that do not underflow; a quotient too small for the latter
+// (below 2^-10 for sc >= 2^-89) has the code 0 either way.  Three instructions
+// for the IEEE division's dozen: eight of those per 16 bytes made the kernel
+// bound by instructions.
+__device__ __forceinline__ float over_scale(float v, float sc, float inv) {
+    const float q = __fmul_rn(v, inv);
+    return __fmaf_rn(__fmaf_rn(-q, sc, v), inv, q);
+}
+
 template <bool FP8>
 __global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__ WriteArgs a) {
     const int lane = threadIdx.x & 31;
@@ -74,11 +87,25 @@ __global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__
         for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
         if (w >= wpr) continue;
         const float sc = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
+        const float inv = __frcp_rn(sc);
+        float f[8];
+        const bool plain = sc >= 0x1p-89f && sc < 0x1p127f && (__float_as_uint(sc) & 0x7fffffu) != 0x7fffffu;
+        if (plain) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                f[2 * j] = over_scale(lo_f32(u[j]), sc, inv);
+                f[2 * j + 1] = over_scale(hi_f32(u[j]), sc, inv);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                f[2 * j] = __fdiv_rn(lo_f32(u[j]), sc);
+                f[2 * j + 1] = __fdiv_rn(hi_f32(u[j]), sc);
+            }
+        }
         uint2 codes;
-        codes.x = to_e4m3x4(__fdiv_rn(lo_f32(u[0]), sc), __fdiv_rn(hi_f32(u[0]), sc), __fdiv_rn(lo_f32(u[1]), sc),
-                            __fdiv_rn(hi_f32(u[1]), sc));
-        codes.y = to_e4m3x4(__fdiv_rn(lo_f32(u[2]), sc), __fdiv_rn(hi_f32(u[2]), sc), __fdiv_rn(lo_f32(u[3]), sc),
-                            __fdiv_rn(hi_f32(u[3]), sc));
+        codes.x = to_e4m3x4(f[0], f[1], f[2], f[3]);
+        codes.y = to_e4m3x4(f[4], f[5], f[6], f[7]);
         reinterpret_cast<uint2 *>(pool)[row * wph + c] = codes;
         if ((c & 7) == 0) (kv ? a.v_scale : a.k_scale)[row * (a.D / 64) + c / 8] = sc;
     }

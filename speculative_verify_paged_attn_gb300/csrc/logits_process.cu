@@ -15,8 +15,9 @@
 // all.  The rows are then streamed through with the mask alone, and the listed
 // tokens put right in the output, one a lane, while their lines are in L2: with
 // the rules applied on the way, a warp took the long path for the one token in
-// fifty that needs it (119 to 189 us on 64 x 6 rows of 128256 bf16 logits with
-// histories of 8192).
+// fifty that needs it (64 x 6 rows of 128256 bf16 logits, histories of 8192:
+// 119 us, against 83 us; applying them on the way in slabs with many marks alone
+// gained 1 us there and cost 2 to 5 us on shorter histories).
 #include "admit.h"
 #include "svpa_device.cuh"
 
@@ -39,7 +40,7 @@ struct Shared {
     int bias_n, marked_n;
     int drafts[kMaxDrafts];
 };
-static_assert(sizeof(Shared<8192>) <= 54 * 1024, "four CTAs per SM");
+static_assert(sizeof(Shared<4096>) <= 36 * 1024, "six CTAs per SM");
 
 __device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
     const float4 u = __ldcs(reinterpret_cast<const float4 *>(p)), v = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
@@ -59,16 +60,19 @@ __device__ __forceinline__ float load1(const __nv_bfloat16 *p) {
     return __uint_as_float((unsigned)__ldcs(reinterpret_cast<const unsigned short *>(p)) << 16);
 }
 
-// VEC: eight consecutive tokens a thread (V a multiple of 8, rows 16-byte
-// aligned); else four that lie 32 apart.
+// VEC: eight consecutive tokens a thread, from the row's first one on a 16-byte
+// boundary on (a row of an odd vocabulary starts anywhere; its first few tokens
+// are taken by themselves); else, for arrays off that boundary, four that lie
+// 32 apart.
 template <typename T, bool VEC, int SLAB, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1536 / THREADS) process_kernel(const __grid_constant__ ProcessArgs a) {
     extern __shared__ __align__(16) uint8_t raw[];
     Shared<SLAB> &sm = *reinterpret_cast<Shared<SLAB> *>(raw);
-    const int b = blockIdx.y, v0 = blockIdx.x * SLAB, n = min(SLAB, a.V - v0);
+    // (slabs of the same tokens first: the common ones, with the most marks, start together)
+    const int b = blockIdx.x, v0 = blockIdx.y * SLAB, n = min(SLAB, a.V - v0);
     const int r0 = a.split_rows ? blockIdx.z : 0, r1 = a.split_rows ? r0 + 1 : a.rows;
     const bool marks = a.history || a.drafts || a.bias_tokens;
-    const bool report = blockIdx.x == 0 && blockIdx.z == 0;
+    const bool report = blockIdx.y == 0 && blockIdx.z == 0;
     if (marks) {
         int hn = 0, pn = 0, lo = 0, hi = 0;
         if (a.history) {
@@ -89,27 +93,58 @@ __global__ void __launch_bounds__(THREADS, 1536 / THREADS) process_kernel(const 
             reinterpret_cast<uint4 *>(sm.word)[i] = make_uint4(0u, 0u, 0u, 0u);
         if (threadIdx.x == 0) sm.bias_n = sm.marked_n = 0;
         __syncthreads();
-        // the first mark of a token lists it
+        // the first mark of a token lists it; the lanes that list one here share an add
         auto listed = [&](unsigned before, unsigned x) {
-            if (before == 0u) sm.marked[atomicAdd(&sm.marked_n, 1)] = (uint16_t)x;
+            if (before != 0u) return;
+            const unsigned here = __activemask(), lane = threadIdx.x & 31;
+            int at = 0;
+            if (lane == __ffs(here) - 1) at = atomicAdd(&sm.marked_n, __popc(here));
+            at = __shfl_sync(here, at, __ffs(here) - 1) + __popc(here & ((1u << lane) - 1u));
+            sm.marked[at] = (uint16_t)x;
+        };
+        auto mark = [&](int i, int v) {
+            const unsigned x = (unsigned)(v - v0);
+            if (x < (unsigned)n)
+                listed(i < pn ? atomicOr(&sm.word[x], kInPrompt) : atomicAdd(&sm.word[x], kOnce), x);
         };
         const int32_t *h = a.history + (size_t)b * a.max_hist;
-        constexpr int kAhead = 8;  // history loads in flight per thread
-        for (int i0 = threadIdx.x; i0 < hn; i0 += kAhead * THREADS) {
-            int v[kAhead];
+        // sixteen tokens a thread in flight; few are the slab's
+        const bool quads = ((reinterpret_cast<uintptr_t>(h)) & 15) == 0;
+        int i0 = 0;
+        if (quads) {
+            constexpr int kAhead = 4;
+            for (; i0 + 4 * kAhead * THREADS <= hn; i0 += 4 * kAhead * THREADS) {
+                int4 v[kAhead];
+                const int i1 = i0 + threadIdx.x * 4;
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) v[k] = i0 + k * THREADS < hn ? __ldg(h + i0 + k * THREADS) : v0;
+                for (int k = 0; k < kAhead; ++k) v[k] = __ldg(reinterpret_cast<const int4 *>(h + i1 + k * 4 * THREADS));
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                const int i = i0 + k * THREADS;
-                if (i >= hn) break;
-                const unsigned x = (unsigned)(v[k] - v0);
-                if (x < (unsigned)n) {
-                    listed(i < pn ? atomicOr(&sm.word[x], kInPrompt) : atomicAdd(&sm.word[x], kOnce), x);
-                } else if (report && (v[k] < 0 || v[k] >= a.V)) {
-                    raise_error(a.err, SVPA_DEVERR_BAD_VALUE);
+                for (int k = 0; k < kAhead; ++k) {
+                    const int i = i1 + k * 4 * THREADS;
+                    const bool mine = min(min((unsigned)(v[k].x - v0), (unsigned)(v[k].y - v0)),
+                                          min((unsigned)(v[k].z - v0), (unsigned)(v[k].w - v0))) < (unsigned)n;
+                    if (!mine) continue;
+                    mark(i, v[k].x);
+                    mark(i + 1, v[k].y);
+                    mark(i + 2, v[k].z);
+                    mark(i + 3, v[k].w);
                 }
             }
+        }
+        for (; i0 < hn; i0 += 4 * THREADS) {
+            int v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int i = i0 + threadIdx.x + k * THREADS;
+                v[k] = i < hn ? __ldg(h + i) : -1;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mark(i0 + threadIdx.x + k * THREADS, v[k]);
+        }
+        if (report) {
+            bool bad = false;
+            for (int i = threadIdx.x; i < hn; i += THREADS) bad = bad || (unsigned)__ldg(h + i) >= (unsigned)a.V;
+            if (bad) raise_error(a.err, SVPA_DEVERR_BAD_VALUE);
         }
         if (a.drafts)
             for (int i = threadIdx.x; i < a.draft_stride; i += THREADS) {
@@ -142,41 +177,56 @@ __global__ void __launch_bounds__(THREADS, 1536 / THREADS) process_kernel(const 
     const T *in = static_cast<const T *>(a.in) + ((size_t)b * a.rows + r0) * a.V + v0;
     float *const out = a.out + ((size_t)b * a.rows + r0) * a.V + v0;
     const uint32_t *mask = a.mask ? a.mask + ((size_t)b * a.rows + r0) * words + v0 / 32 : nullptr;
-    constexpr int N = VEC ? 8 : 4;
-    const int at0 = VEC ? threadIdx.x * 8 : (threadIdx.x >> 5) * 128 + (threadIdx.x & 31);
-    for (int i = at0; i < n; i += THREADS * N) {
-        const T *src = in + i;
-        float *dst = out + i;
-        const uint32_t *bits = mask ? mask + i / 32 : nullptr;
+    if constexpr (VEC) {
+        // elements past a multiple of eight of row r0's slab, and of each row after the one before
+        const int off0 = (int)((((size_t)b * a.rows + r0) * a.V + v0) & 7), step = a.V & 7;
+        auto head_of = [&](int j) -> int { return (8 - ((off0 + (j - r0) * step) & 7)) & 7; };
+        auto one = [&](int j, int i) {  // a token by itself
+            const uint32_t bit = mask ? __ldg(mask + (size_t)(j - r0) * words + i / 32) >> (i & 31) : 1u;
+            const size_t at = (size_t)(j - r0) * a.V + i;
+            const float x = load1(in + at);
+            out[at] = bit & 1u ? x : ninf;
+        };
+        if ((off0 | step) != 0)
+            for (int z = threadIdx.x; z < 8 * (r1 - r0); z += THREADS)
+                if ((z & 7) < min(head_of(r0 + z / 8), n)) one(r0 + z / 8, z & 7);
+        for (int c8 = threadIdx.x * 8; c8 < n; c8 += THREADS * 8) {
 #pragma unroll 2
-        for (int j = r0; j < r1; ++j) {
-            float x[N];
-            uint32_t ok = 0xffffffffu;
-            if constexpr (VEC) {
-                load8(src, x);
-                if (mask) ok = __ldg(bits) >> (i & 31);
-            } else {
+            for (int j = r0; j < r1; ++j) {
+                const int i = head_of(j) + c8;
+                const size_t at = (size_t)(j - r0) * a.V + i;
+                if (i + 8 > n) {
+                    for (int k = i; k < n; ++k) one(j, k);
+                    continue;
+                }
+                float x[8];
+                uint32_t ok = 0xffu;
+                load8(in + at, x);
+                if (mask) {
+                    const uint32_t *bits = mask + (size_t)(j - r0) * words + i / 32;
+                    ok = __ldg(bits) >> (i & 31);
+                    if ((i & 31) > 24) ok |= __ldg(bits + 1) << (32 - (i & 31));  // i + 7 < n lies there
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (!((ok >> e) & 1u)) x[e] = ninf;
+                float4 *dst = reinterpret_cast<float4 *>(out + at);
+                dst[0] = make_float4(x[0], x[1], x[2], x[3]);
+                dst[1] = make_float4(x[4], x[5], x[6], x[7]);
+            }
+        }
+    } else {
+        for (int i = (threadIdx.x >> 5) * 128 + (threadIdx.x & 31); i < n; i += THREADS * 4) {
+            for (int j = r0; j < r1; ++j) {
+                const uint32_t *bits = mask ? mask + (size_t)(j - r0) * words + i / 32 : nullptr;
+                const size_t at = (size_t)(j - r0) * a.V + i;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     if (i + e * 32 >= n) continue;
-                    x[e] = load1(src + e * 32);
-                    if (mask && !((__ldg(bits + e) >> (i & 31)) & 1u)) ok &= ~(1u << e);
+                    const float x = load1(in + at + e * 32);
+                    out[at + e * 32] = !mask || (__ldg(bits + e) >> (i & 31)) & 1u ? x : ninf;
                 }
             }
-#pragma unroll
-            for (int e = 0; e < N; ++e)
-                if (!((ok >> e) & 1u)) x[e] = ninf;
-            if constexpr (VEC) {
-                *reinterpret_cast<float4 *>(dst) = make_float4(x[0], x[1], x[2], x[3]);
-                *(reinterpret_cast<float4 *>(dst) + 1) = make_float4(x[4], x[5], x[6], x[7]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (i + e * 32 < n) dst[e * 32] = x[e];
-            }
-            src += a.V;
-            dst += a.V;
-            bits += words;
         }
     }
     if (!marks) return;
@@ -222,9 +272,8 @@ __global__ void __launch_bounds__(THREADS, 1536 / THREADS) process_kernel(const 
 
 template <typename T, int SLAB, int THREADS>
 cudaError_t launch_s(const ProcessArgs &a, cudaStream_t st) {
-    const bool vec = a.V % 8 == 0 && (reinterpret_cast<uintptr_t>(a.in) & 15) == 0 &&
-                     (reinterpret_cast<uintptr_t>(a.out) & 15) == 0;
-    const dim3 grid((a.V + SLAB - 1) / SLAB, a.B, a.split_rows ? a.rows : 1);
+    const bool vec = (reinterpret_cast<uintptr_t>(a.in) & 15) == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15) == 0;
+    const dim3 grid(a.B, (a.V + SLAB - 1) / SLAB, a.split_rows ? a.rows : 1);
     static DeviceMemo<int> attr_set;  // the shared-memory opt-in, once per device
     int done = 0;
     const cudaError_t e = attr_set.get(&done, [](int *v) {
@@ -248,7 +297,7 @@ cudaError_t launch_t(ProcessArgs a, cudaStream_t st) {
     // the largest slab that still leaves every SM a few CTAs; below that, a
     // row a CTA
     const long long tokens = (long long)a.V * a.B;
-    if (tokens >= 8192LL * 152 * 6) return launch_s<T, 8192, 512>(a, st);
+    if (tokens >= 4096LL * 152 * 6) return launch_s<T, 4096, 256>(a, st);
     if (tokens >= 2048LL * 152 * 4) return launch_s<T, 2048, 256>(a, st);
     a.split_rows = 1;
     return launch_s<T, 1024, 128>(a, st);

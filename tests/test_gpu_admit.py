@@ -209,6 +209,29 @@ def test_rows_land_in_their_slots(t, hkv, d, fp8, fused, holes):
         assert s is None or torch.equal(sg, s)
 
 
+def test_every_bf16_value_gets_the_code_of_its_quotient():
+    """All bf16 magnitudes against tiles of many scales: codes at and near the
+    ties of E4M3 included."""
+    vals = torch.arange(0, 0x7F80, device=DEV, dtype=torch.int32).to(torch.int16).view(torch.bfloat16).float()
+    g = torch.Generator(device=DEV)
+    g.manual_seed(3)
+    for top in (1.0, 1.75, 448.0, 3.0e38, 2.0 ** -100, 1.0e-37, 2.0 ** -126):
+        small = vals[vals <= torch.tensor(top, device=DEV).to(torch.bfloat16).float()]
+        # the values a tile of this maximum tells apart, sampled over their whole range
+        pick = small[(torch.rand(64 * 63 * 2, generator=g, device=DEV) ** 0.25 * small.numel()).long().clamp(max=small.numel() - 1)]
+        x = torch.cat([pick.view(-1, 63), torch.full((128, 1), top, device=DEV)], 1).to(torch.bfloat16)
+        x = torch.where(torch.rand(x.shape, generator=g, device=DEV) < 0.5, x, -x).view(64, 2, 64)
+        slots = torch.arange(64, dtype=torch.int32, device=DEV)
+        pools = [torch.zeros((4, 2, BS, 64), dtype=torch.uint8, device=DEV) for _ in range(2)]
+        scales = [torch.zeros((4, 2, BS, 1), device=DEV) for _ in range(2)]
+        want = write_expected(x, slots, pools[0], scales[0], True)
+        err = ints([0])
+        svpa.kv_write(x, x, slots, *pools, error_flag=err, k_scale=scales[0], v_scale=scales[1], scale_tile=64)
+        assert svpa.check_error(err) == 0
+        for p, s in zip(pools, scales):
+            assert torch.equal(p, want[0]) and torch.equal(s, want[1]), top
+
+
 def test_the_scatter_matches_the_append():
     """The same rows written by kv_append (fresh pages) and through a slot map, FP8 tile scales."""
     wl = W.WORKLOADS["fp8_t64"].scaled(num_kv_heads=2, num_q_heads=8)
