@@ -21,13 +21,14 @@
 // tensor cores compute one while the exponentials of the other are taken.
 // Persistent CTAs, one per SM (TMEM 512 columns, 224 KB of shared memory),
 // take units from an atomic counter.  Warps:
-//   0      producer: decodes units, streams K and V blocks (8 pages per
+//   0      producer: streams K and V blocks (8 pages per
 //          block, one TMA copy per page and kv head) through one ring, and
 //          the query tiles;
 //   1, 2   MMA issuers of tile A and tile B (warp 1 owns the TMEM):
 //          O_t += P_t V with P_t read from TMEM over S_t's own columns, then
 //          S_t = Q_t K^T of the next block;
-//   3      reports prefix units whose partials are written;
+//   3      scheduler: decodes units ahead of the producer and reports prefix
+//          units whose partials are written;
 //   4-7    softmax of tile A, one thread per query row: mask, lazy running
 //   8-11   maximum (O_t rescaled only when it grows by more than 2^8), fp32
 //          row sum, P as bf16 (the MMA's input type; the sum is taken before
@@ -75,6 +76,15 @@ struct Unit {
     int32_t prefix;      // a prefix unit: count it when written
 };
 
+// A unit with what its copies need: its table, pages and blocks, and the tokens
+// of one query tile's copy.
+struct Job {
+    Unit w;
+    const int32_t *bt;
+    int32_t page0, npages, nblk, n_tok_load;
+    int32_t once;  // its K/V is read by this unit alone
+};
+
 template <int D>
 struct Smem {
     static constexpr int kTile = kNB * D * 2;
@@ -86,8 +96,12 @@ struct Smem {
     uint64_t s_full[2], p_full[2], o_full[2];
     uint64_t both;  // the two softmax groups meet
     uint64_t drain[2];
-    uint64_t written;  // a prefix unit's partials
+    uint64_t turn[2];  // a pair's tiles issue their MMAs in turn
+    uint64_t job_full, job_want;  // a decoded unit, scheduler -> producer
+    Job job;
+    int32_t job_ids[32];
     Unit unit;
+    int32_t written;  // softmax warps that wrote a prefix unit's partials
     float2 stat[2][128];
     uint32_t tmem_base;
 };
@@ -121,6 +135,24 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
+__device__ __forceinline__ void st_32bytes(void *p, const uint32_t (&v)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+// Sixteen values of a row as bf16 to `dst` (32 bytes: in one store where they may be).
+__device__ __forceinline__ void store_bf16x16(__nv_bfloat16 *dst, const float *f, float scale, bool wide) {
+    uint32_t v[8];
+#pragma unroll
+    for (int x = 0; x < 8; ++x) v[x] = pack_bf16x2(f[2 * x] * scale, f[2 * x + 1] * scale);
+    if (wide) {
+        st_32bytes(dst, v);
+    } else {
+        reinterpret_cast<uint4 *>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<uint4 *>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    }
+}
+
 __device__ __forceinline__ bool elect_one() {
     uint32_t one;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
@@ -136,6 +168,10 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, int32_t
     return mbar_wait(bar, parity, err);
 }
 
+__device__ __forceinline__ bool mbar_wait_all(uint64_t *bar, uint32_t phase, int32_t *err) {
+    return __all_sync(0xffffffffu, bar_wait(bar, phase & 1u, err));
+}
+
 template <int N>
 __device__ __forceinline__ void regs_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
@@ -143,6 +179,24 @@ __device__ __forceinline__ void regs_dec() {
 template <int N>
 __device__ __forceinline__ void regs_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// 16 consecutive fp32 columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
 }
 
 __device__ __forceinline__ int ld_acquire(const int32_t *p) {
@@ -158,6 +212,18 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, i
         "hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar)), "l"(policy)
         : "memory");
+}
+
+// The pool's (page, kv head) tile of the unit's page i; one past the pool (it
+// reads as zeros) behind its last page.
+__device__ __forceinline__ int page_tile(const PackedArgs &a, const Job &d, int i) {
+    if (i >= d.npages) return a.num_blocks * a.Hkv;
+    int blk = __ldg(d.bt + d.page0 + i);
+    if (blk < 0 || blk >= a.num_blocks) {
+        raise_error(a.err, SVPA_DEVERR_BAD_BLOCK);
+        blk = 0;
+    }
+    return blk * a.Hkv + d.w.h;
 }
 
 // Largest b with cu[b] / step + b <= slot (cu[0] = 0), by the whole warp:
@@ -208,23 +274,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     // the first unit is on its way while the CTA sets itself up
-    int next = 0;
+    int next = -1;
+    if (threadIdx.x == 96) next = atomicAdd(&a.sched[0], 1);
     if (threadIdx.x == 0) {
-        next = atomicAdd(&a.sched[0], 1);
         for (int i = 0; i < kRing; ++i) {
             mbar_init(&sm.full[i], 1);
             mbar_init(&sm.empty[i], 2);  // the two MMA issuers
         }
         mbar_init(&sm.both, 8);
-        mbar_init(&sm.written, 8);
+        sm.written = 0;
+        mbar_init(&sm.job_full, 1);
+        mbar_init(&sm.job_want, 1);
         mbar_init(&sm.q_full, 1);
-        // the MMA issuers, the eight softmax warps and the reporter
-        mbar_init(&sm.q_empty, a.p_units > 0 ? 11 : 10);
+        mbar_init(&sm.q_empty, 10);  // the MMA issuers and the eight softmax warps
         for (int t = 0; t < 2; ++t) {
             mbar_init(&sm.s_full[t], 1);
             mbar_init(&sm.p_full[t], 4);
             mbar_init(&sm.o_full[t], 1);
             mbar_init(&sm.drain[t], 1);
+            mbar_init(&sm.turn[t], 1);
         }
         fence_mbar_init();
     }
@@ -253,207 +321,77 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         int tile = 0, units = 0;  // ring tiles issued, units started
         bool ok = true;
-        const int tpt2 = 2 * a.tpt;
-        while (ok) {
-            const int u = __shfl_sync(0xffffffffu, next, 0);
-            if (u >= a.total_units) break;
-            if (lane == 0) next = atomicAdd(&a.sched[0], 1);  // used after this unit
-            // ---- decode
-            Unit w;
-            const int32_t *bt;
-            int n_tok_load, nblk;     // tokens of one query tile's copy, blocks
-            uint64_t pol = keep;
-            w.use_anc = w.merge = w.prefix = 0;
-            w.causal = 0;
-            w.slot = -1;
-            int page0, npages;        // of the unit's kv range
-            if (u < a.p_units) {
-                const int h = u % a.Hkv, x = u / a.Hkv;
-                const int split = x % a.p_splits, pair = x / a.p_splits;
-                w.h = h;
-                w.tok0 = pair * tpt2;
-                w.tok1 = min(w.tok0 + tpt2, a.T);
-                bt = a.prefix_blocks;
-                const int nb = (a.prefix_pages + kPagesPerBlock - 1) / kPagesPerBlock;
-                const int b0 = (int)((long long)nb * split / a.p_splits);
-                const int b1 = (int)((long long)nb * (split + 1) / a.p_splits);
-                page0 = b0 * kPagesPerBlock;
-                npages = min(a.prefix_pages, b1 * kPagesPerBlock) - page0;
-                nblk = b1 - b0;
-                w.kv_end = w.lim0 = a.prefix_pages * kBlockSize;
-                w.kind = w.tok1 - w.tok0 > a.tpt ? kPair : kAlt;
-                w.slot = split;
-                w.prefix = 1;
-                n_tok_load = a.tpt;
-            } else if (a.verify) {
-                const int x = u - a.p_units;
-                const int h = x % a.Hkv, y = x / a.Hkv;
-                const int split = y % a.s_splits, b = y / a.s_splits;
-                const int L = __ldg(a.lens + b);
-                bt = a.block_table + (size_t)b * a.max_blocks;
-                const long long total = (long long)L + a.n_q;
-                if (L < 0 || total > (long long)a.max_blocks * kBlockSize) {
-                    if (lane == 0 && split == 0 && h == 0) raise_error(a.err, SVPA_DEVERR_BAD_VALUE);
-                    continue;
-                }
-                // a sequence whose table begins with the prefix joins it; any
-                // other attends its whole history itself
-                bool mine = L >= a.prefix_pages * kBlockSize;
-                if (mine) {
-                    for (int i0 = 0; i0 < a.prefix_pages && mine; i0 += 256) {
-                        int p[8], q[8];
+        auto issue_q = [&](const Job &d) -> bool {
+            if (units >= 1) {
+                int good = 1;
+                if (lane == 0) good = mbar_wait(&sm.q_empty, (uint32_t)((units - 1) & 1), a.err);
+                if (!__shfl_sync(0xffffffffu, good, 0)) return false;
+            }
+            if (lane == 0) {
+                sm.unit = d.w;
+                const bool two = d.w.kind == kPair;
+                const uint32_t bytes = d.nblk == 0 ? 0u : (uint32_t)(d.n_tok_load * a.G * D * 2) * (two ? 2u : 1u);
+                mbar_arrive_expect_tx(&sm.q_full, bytes);
+                if (bytes) {
+                    const uint64_t pol = d.once ? stream_once : keep;
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const int i = i0 + 32 * k + lane;
-                            const bool in = i < a.prefix_pages;
-                            p[k] = in ? __ldg(bt + i) : 0;
-                            q[k] = in ? __ldg(a.prefix_blocks + i) : 0;
-                        }
-                        bool same = true;
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) same = same && p[k] == q[k];
-                        mine = __all_sync(0xffffffffu, same);
+                    for (int s = 0; s < kSlabs; ++s) {
+                        const CUtensorMap *m = d.w.use_anc ? (s ? &mqs1 : &mqs0) : (s ? &mqt1 : &mqt0);
+                        tma_load_3d(&sm.q[0][s * kQSlab], m, 0, d.w.h * a.G, d.w.tok0, &sm.q_full, pol);
+                        if (two)
+                            tma_load_3d(&sm.q[1][s * kQSlab], m, 0, d.w.h * a.G, d.w.tok0 + a.tpt, &sm.q_full, pol);
                     }
                 }
-                if (a.member && lane == 0 && split == 0 && h == 0) a.member[b] = mine ? 1 : 0;
-                const int first = mine ? a.prefix_pages : 0;
-                const int pages = (int)((total + kBlockSize - 1) / kBlockSize) - first;
-                const int nb = (pages + kPagesPerBlock - 1) / kPagesPerBlock;
-                const int b0 = (int)((long long)nb * split / a.s_splits);
-                const int b1 = (int)((long long)nb * (split + 1) / a.s_splits);
-                page0 = first + b0 * kPagesPerBlock;
-                npages = min(pages, b1 * kPagesPerBlock) - b0 * kPagesPerBlock;
-                nblk = b1 - b0;
-                w.h = h;
-                w.tok0 = b * a.n_q;
-                w.tok1 = w.tok0 + a.n_q;
-                w.kv_end = (int)total;
-                w.lim0 = L;
-                w.use_anc = 1;
-                w.kind = kAlt;
-                w.merge = mine && a.s_splits == 1;
-                w.slot = a.s_splits == 1 ? -1 : a.p_splits + split;
-                n_tok_load = a.n_q;
-                pol = stream_once;
-            } else {
-                // long tiles first: the last tiles of a sequence see the most
-                const int h = u % a.Hkv, y = u / a.Hkv;
-                const int split = y % a.s_splits, slot = a.pairs - 1 - y / a.s_splits;
-                const int b = find_sequence(a.cu, a.B, tpt2, slot, lane);
-                const int c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1);
-                const int kv = __ldg(a.lens + b);
-                const int t0 = c0 + (slot - (c0 / tpt2 + b)) * tpt2;
-                if (t0 >= c1) {
-                    // no tile here; a bad row of offsets is reported with its first slot
-                    if (lane == 0 && (c0 < 0 || c1 < c0 || c1 > a.T)) raise_error(a.err, SVPA_DEVERR_BAD_VALUE);
-                    continue;
-                }
-                if (c0 < 0 || c1 > a.T || t0 < c0 || kv < c1 - c0 || kv > (long long)a.max_blocks * kBlockSize) {
-                    if (lane == 0) raise_error(a.err, SVPA_DEVERR_BAD_VALUE);
-                    continue;
-                }
-                w.h = h;
-                w.tok0 = t0;
-                w.tok1 = min(t0 + tpt2, c1);
-                w.lim0 = kv - (c1 - t0) + 1;
-                w.causal = 1;
-                w.kv_end = kv;
-                bt = a.block_table + (size_t)b * a.max_blocks;
-                const int seen = w.lim0 + (w.tok1 - 1 - t0);  // positions the unit's last token sees
-                const int pages = (seen + kBlockSize - 1) / kBlockSize;
-                const int nb = (seen + kNB - 1) / kNB;
-                const int b0 = (int)((long long)nb * split / a.s_splits);
-                const int b1 = (int)((long long)nb * (split + 1) / a.s_splits);
-                page0 = b0 * kPagesPerBlock;
-                npages = min(pages, b1 * kPagesPerBlock) - page0;
-                nblk = b1 - b0;
-                w.kind = w.tok1 - w.tok0 > a.tpt ? kPair : kAlt;
-                w.slot = a.s_splits == 1 ? -1 : split;
-                n_tok_load = a.tpt;
             }
-            w.pos0 = page0 * kBlockSize;
-            if (w.kind == kPair) {
-                w.nB = nblk;
-                w.nA = nblk;
-                if (w.causal) {
-                    // tile A's last token may end one block or more earlier
-                    const int seenA = w.lim0 + a.tpt - 1;
-                    w.nA = min(nblk, max(0, (seenA - w.pos0 + kNB - 1) / kNB));
-                }
-            } else {
-                w.nA = (nblk + 1) / 2;
-                w.nB = nblk / 2;
+            __syncwarp();
+            return true;
+        };
+        // K and V tiles in the order the MMA issuers take them
+        auto issue_tile = [&](const CUtensorMap *map, int id, uint64_t pol) -> bool {
+            const int s = tile % kRing;
+            if (tile >= kRing) {
+                int good = 1;
+                if (lane == 0) good = mbar_wait(&sm.empty[s], (uint32_t)(((tile / kRing) & 1) ^ 1), a.err);
+                if (!__shfl_sync(0xffffffffu, good, 0)) return false;
             }
-            w.base = tile;
-
-            auto issue_q = [&]() -> bool {
-                if (units >= 1) {
-                    int good = 1;
-                    if (lane == 0) good = mbar_wait(&sm.q_empty, (uint32_t)((units - 1) & 1), a.err);
-                    if (!__shfl_sync(0xffffffffu, good, 0)) return false;
-                }
-                if (lane == 0) {
-                    sm.unit = w;
-                    const bool two = w.kind == kPair;
-                    const uint32_t bytes = nblk == 0 ? 0u : (uint32_t)(n_tok_load * a.G * D * 2) * (two ? 2u : 1u);
-                    mbar_arrive_expect_tx(&sm.q_full, bytes);
-                    if (bytes) {
-                        const bool seq = w.use_anc;
-#pragma unroll
-                        for (int s = 0; s < kSlabs; ++s) {
-                            const CUtensorMap *m = seq ? (s ? &mqs1 : &mqs0) : (s ? &mqt1 : &mqt0);
-                            tma_load_3d(&sm.q[0][s * kQSlab], m, 0, w.h * a.G, w.tok0, &sm.q_full, pol);
-                            if (two)
-                                tma_load_3d(&sm.q[1][s * kQSlab], m, 0, w.h * a.G, w.tok0 + a.tpt, &sm.q_full, pol);
-                        }
-                    }
-                }
-                __syncwarp();
-                return true;
-            };
-            // K and V tiles in the order the MMA issuer takes them
-            auto issue_tile = [&](const CUtensorMap *map, int id) -> bool {
-                const int s = tile % kRing;
-                if (tile >= kRing) {
-                    int good = 1;
-                    if (lane == 0) good = mbar_wait(&sm.empty[s], (uint32_t)(((tile / kRing) & 1) ^ 1), a.err);
-                    if (!__shfl_sync(0xffffffffu, good, 0)) return false;
-                }
-                if (lane == 0) mbar_arrive_expect_tx(&sm.full[s], (uint32_t)SM::kTile);
-                __syncwarp();
-                if (lane < kPagesPerBlock)
-                    tma_load_5d(&sm.kv[s][lane * kPageBytes], map, 0, 0, 0, 0, id, &sm.full[s], pol);
-                ++tile;
-                return true;
-            };
-            const int oob = a.num_blocks * a.Hkv;  // a page that does not exist: zeros
-            int ids = 0;
+            if (lane == 0) mbar_arrive_expect_tx(&sm.full[s], (uint32_t)SM::kTile);
+            __syncwarp();
+            if (lane < kPagesPerBlock)
+                tma_load_5d(&sm.kv[s][lane * kPageBytes], map, 0, 0, 0, 0, id, &sm.full[s], pol);
+            ++tile;
+            return true;
+        };
+        for (; ok; ++units) {
+            ok = mbar_wait_all(&sm.job_full, (uint32_t)units, a.err);
+            if (!ok) break;
+            Job job = sm.job;
+            int ids = sm.job_ids[lane], ids_next = 0;
+            __syncwarp();
+            // the next unit is asked for a few blocks before this one's end: taken
+            // earlier, the last units would wait behind a busy CTA
+            const int ask = max(0, job.nblk - 4);
+            if (job.w.kind == kEnd) break;
+            job.w.base = tile;
+            const uint64_t pol = job.once ? stream_once : keep;
             bool q_out = false;
-            for (int j = 0; j < nblk && ok; ++j) {
+            for (int j = 0; j < job.nblk && ok; ++j) {
                 if ((j & 3) == 0) {
-                    const int i = j * kPagesPerBlock + lane;
-                    ids = oob;
-                    if (i < npages) {
-                        int blk = __ldg(bt + page0 + i);
-                        if (blk < 0 || blk >= a.num_blocks) {
-                            raise_error(a.err, SVPA_DEVERR_BAD_BLOCK);
-                            blk = 0;
-                        }
-                        ids = blk * a.Hkv + w.h;
-                    }
+                    if (j > 0) ids = ids_next;
+                    if (j + 4 < job.nblk) ids_next = page_tile(a, job, (j + 4) * kPagesPerBlock + lane);
                 }
+                if (j == ask && lane == 0) mbar_arrive(&sm.job_want);
                 const int id = __shfl_sync(0xffffffffu, ids, ((j & 3) * kPagesPerBlock + (lane & 7)) & 31);
-                ok = issue_tile(&mk, id);
-                if (ok) ok = issue_tile(&mv, id);
+                ok = issue_tile(&mk, id, pol);
+                if (ok) ok = issue_tile(&mv, id, pol);
                 // the first block of the next unit is on its way before the
                 // query buffers are free
                 if (ok && !q_out) {
-                    ok = issue_q();
+                    ok = issue_q(job);
                     q_out = true;
                 }
             }
-            if (ok && !q_out) ok = issue_q();
-            ++units;
+            if (ok && !q_out) ok = issue_q(job);
+            if (job.nblk == 0 && lane == 0) mbar_arrive(&sm.job_want);
         }
         if (lane == 0) {
             if (ok && units >= 1) ok = mbar_wait(&sm.q_empty, (uint32_t)((units - 1) & 1), a.err);
@@ -498,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 return true;
             };
-            uint32_t np = 0;  // phase of p_full
+            uint32_t np = 0, nt = 0;  // phases of p_full, turn
             bool ok = true;
             for (int unit = 0; ok; ++unit) {
                 if (!wait(&sm.q_full, (uint32_t)unit)) break;
@@ -519,6 +457,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                                          kt > 0 ? 1u : (uint32_t)(j - 1));
                     if (j == n) umma_commit(&sm.o_full[t]);
                 };
+                // A pair's tiles take turns: two queues of MMAs would be served
+                // in alternation, and both tiles' next scores be late.  B's
+                // step j follows A's step j, A's step j + 1 B's step j.
+                auto my_turn = [&](int j) -> bool {
+                    const bool waits = t ? j <= other : j > 1;
+                    return !waits || wait(&sm.turn[t], nt++);
+                };
                 // S_t = Q_t K^T of block j, over the P_t that the MMA before has read
                 auto issue_s = [&](int j, int sk) {
                     const uint64_t kd = k0 + (uint32_t)sk * (SM::kTile / 16);
@@ -537,13 +482,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (pair) {
                         // K (from L2) has landed long before P is ready: wait
                         // for it first, and both MMAs go out together
-                        ok = (j == n || tile_wait(ik)) && (j == 0 || (tile_wait(iv) && wait(&sm.p_full[t], np++)));
+                        ok = (j == n || tile_wait(ik)) && (j == 0 || (tile_wait(iv) && my_turn(j) && wait(&sm.p_full[t], np++)));
                         if (!ok) break;
                         tc_fence_after();
                         if (elect_one()) {
                             if (j > 0) issue_pv(j, sv);
                             if (j < n) issue_s(j, sk);
                             if (j > 0) umma_commit(&sm.empty[sv]);
+                            if (j > 0 && (t == 0 || j < other)) mbar_arrive(&sm.turn[1 - t]);
                         }
                         __syncwarp();
                         continue;
@@ -582,24 +528,182 @@ __global__ void __launch_bounds__(kThreads, 1)
                 wait(&sm.drain[t], 0);
             }
         } else {
-            // ================================================= reporter
-            // A prefix unit's partials are made visible to the other CTAs and
-            // counted here, where the fence holds up no softmax warp.
-            uint32_t done = 0;
-            for (int unit = 0; a.p_units > 0; ++unit) {
-                if (!__all_sync(0xffffffffu, bar_wait(&sm.q_full, (uint32_t)(unit & 1), a.err))) break;
-                const int kind = sm.unit.kind, prefix = sm.unit.prefix;
-                __syncwarp();
-                if (kind == kEnd) break;
-                if (lane == 0) mbar_arrive(&sm.q_empty);
-                if (!prefix) continue;
-                if (!__all_sync(0xffffffffu, bar_wait(&sm.written, done++ & 1u, a.err))) break;
+            // ================================================= scheduler
+            // Decodes the producer's next unit (chains of dependent loads), and makes a prefix unit's partials visible to the other
+            // CTAs and counts it, where the fence holds up no softmax warp.
+            const int tpt2 = 2 * a.tpt;
+        // The next unit that has work; false when there is none.
+        auto decode = [&](Job &d) -> bool {
+            while (true) {
+                if (lane == 0 && next < 0) next = atomicAdd(&a.sched[0], 1);
+                const int u = __shfl_sync(0xffffffffu, next, 0);
+                if (u >= a.total_units) return false;
+                next = -1;
+                Unit &w = d.w;
+                w.use_anc = w.merge = w.prefix = 0;
+                w.causal = 0;
+                w.slot = -1;
+                d.once = false;
+                if (u < a.p_units) {
+                    const int h = u % a.Hkv, x = u / a.Hkv;
+                    const int split = x % a.p_splits, pair = x / a.p_splits;
+                    w.h = h;
+                    w.tok0 = pair * tpt2;
+                    w.tok1 = min(w.tok0 + tpt2, a.T);
+                    d.bt = a.prefix_blocks;
+                    const int nb = (a.prefix_pages + kPagesPerBlock - 1) / kPagesPerBlock;
+                    const int b0 = (int)((long long)nb * split / a.p_splits);
+                    const int b1 = (int)((long long)nb * (split + 1) / a.p_splits);
+                    d.page0 = b0 * kPagesPerBlock;
+                    d.npages = min(a.prefix_pages, b1 * kPagesPerBlock) - d.page0;
+                    d.nblk = b1 - b0;
+                    w.kv_end = w.lim0 = a.prefix_pages * kBlockSize;
+                    w.kind = w.tok1 - w.tok0 > a.tpt ? kPair : kAlt;
+                    w.slot = split;
+                    w.prefix = 1;
+                    d.n_tok_load = a.tpt;
+                } else if (a.verify) {
+                    const int x = u - a.p_units;
+                    const int h = x % a.Hkv, y = x / a.Hkv;
+                    const int split = y % a.s_splits, b = y / a.s_splits;
+                    const int L = __ldg(a.lens + b);
+                    d.bt = a.block_table + (size_t)b * a.max_blocks;
+                    const long long total = (long long)L + a.n_q;
+                    if (L < 0 || total > (long long)a.max_blocks * kBlockSize) {
+                        if (lane == 0 && split == 0 && h == 0) raise_error(a.err, SVPA_DEVERR_BAD_VALUE);
+                        continue;
+                    }
+                    // a sequence whose table begins with the prefix joins it; any
+                    // other attends its whole history itself
+                    bool mine = L >= a.prefix_pages * kBlockSize;
+                    for (int i0 = 0; i0 < a.prefix_pages && mine; i0 += 256) {
+                        int p[8], q[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const int i = i0 + 32 * k + lane;
+                            const bool in = i < a.prefix_pages;
+                            p[k] = in ? __ldg(d.bt + i) : 0;
+                            q[k] = in ? __ldg(a.prefix_blocks + i) : 0;
+                        }
+                        bool same = true;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) same = same && p[k] == q[k];
+                        mine = __all_sync(0xffffffffu, same);
+                    }
+                    if (a.member && lane == 0 && split == 0 && h == 0) a.member[b] = mine ? 1 : 0;
+                    const int first = mine ? a.prefix_pages : 0;
+                    const int pages = (int)((total + kBlockSize - 1) / kBlockSize) - first;
+                    const int nb = (pages + kPagesPerBlock - 1) / kPagesPerBlock;
+                    const int b0 = (int)((long long)nb * split / a.s_splits);
+                    const int b1 = (int)((long long)nb * (split + 1) / a.s_splits);
+                    d.page0 = first + b0 * kPagesPerBlock;
+                    d.npages = min(pages, b1 * kPagesPerBlock) - b0 * kPagesPerBlock;
+                    d.nblk = b1 - b0;
+                    w.h = h;
+                    w.tok0 = b * a.n_q;
+                    w.tok1 = w.tok0 + a.n_q;
+                    w.kv_end = (int)total;
+                    w.lim0 = L;
+                    w.use_anc = 1;
+                    w.kind = kAlt;
+                    w.merge = mine && a.s_splits == 1;
+                    w.slot = a.s_splits == 1 ? -1 : a.p_splits + split;
+                    d.n_tok_load = a.n_q;
+                    d.once = true;
+                } else {
+                    // long tiles first: the last tiles of a sequence see the most
+                    const int h = u % a.Hkv, y = u / a.Hkv;
+                    const int split = y % a.s_splits, slot = a.pairs - 1 - y / a.s_splits;
+                    const int b = find_sequence(a.cu, a.B, tpt2, slot, lane);
+                    const int c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1);
+                    const int kv = __ldg(a.lens + b);
+                    const int t0 = c0 + (slot - (c0 / tpt2 + b)) * tpt2;
+                    if (t0 >= c1) {
+                        // no tile here; a bad row of offsets is reported with its first slot
+                        if (lane == 0 && (c0 < 0 || c1 < c0 || c1 > a.T)) raise_error(a.err, SVPA_DEVERR_BAD_VALUE);
+                        continue;
+                    }
+                    if (c0 < 0 || c1 > a.T || t0 < c0 || kv < c1 - c0 || kv > (long long)a.max_blocks * kBlockSize) {
+                        if (lane == 0) raise_error(a.err, SVPA_DEVERR_BAD_VALUE);
+                        continue;
+                    }
+                    w.h = h;
+                    w.tok0 = t0;
+                    w.tok1 = min(t0 + tpt2, c1);
+                    w.lim0 = kv - (c1 - t0) + 1;
+                    w.causal = 1;
+                    w.kv_end = kv;
+                    d.bt = a.block_table + (size_t)b * a.max_blocks;
+                    const int seen = w.lim0 + (w.tok1 - 1 - t0);  // positions the unit's last token sees
+                    const int pages = (seen + kBlockSize - 1) / kBlockSize;
+                    const int nb = (seen + kNB - 1) / kNB;
+                    const int b0 = (int)((long long)nb * split / a.s_splits);
+                    const int b1 = (int)((long long)nb * (split + 1) / a.s_splits);
+                    d.page0 = b0 * kPagesPerBlock;
+                    d.npages = min(pages, b1 * kPagesPerBlock) - d.page0;
+                    d.nblk = b1 - b0;
+                    w.kind = w.tok1 - w.tok0 > a.tpt ? kPair : kAlt;
+                    w.slot = a.s_splits == 1 ? -1 : split;
+                    d.n_tok_load = a.tpt;
+                }
+                w.pos0 = d.page0 * kBlockSize;
+                if (w.kind == kPair) {
+                    w.nA = w.nB = d.nblk;
+                    if (w.causal) {
+                        // tile A's last token may end one block or more earlier
+                        const int seenA = w.lim0 + a.tpt - 1;
+                        w.nA = min(d.nblk, max(0, (seenA - w.pos0 + kNB - 1) / kNB));
+                    }
+                } else {
+                    w.nA = (d.nblk + 1) / 2;
+                    w.nB = d.nblk / 2;
+                }
+                return true;
+            }
+        };
+            int prefixes = 0, reported = 0;  // prefix units handed on, and counted
+            auto report = [&]() {
+                if (reported >= prefixes) return;
+                const int n = *reinterpret_cast<volatile int *>(&sm.written);
+                if (__shfl_sync(0xffffffffu, n, 0) < 8 * (reported + 1)) return;
                 if (lane == 0) {
                     __threadfence();
                     atomicAdd(a.sched + 2, 1);
                 }
                 __syncwarp();
+                ++reported;
+            };
+            // bounded, reporting meanwhile
+            auto until = [&](auto done) -> bool {
+                unsigned long long start = 0;
+                while (!done()) {
+                    report();
+                    __nanosleep(100);
+                    const unsigned long long now = global_ns();
+                    if (start == 0) start = now;
+                    if (__any_sync(0xffffffffu, now - start > kWaitLimitNs)) {
+                        if (lane == 0) raise_error(a.err, SVPA_DEVERR_TIMEOUT);
+                        return false;
+                    }
+                }
+                return true;
+            };
+            for (int jobs = 0;; ++jobs) {
+                Job d;
+                const bool more = decode(d);
+                if (!more) d.w.kind = kEnd;
+                const int ids = more ? page_tile(a, d, lane) : 0;
+                if (lane == 0) sm.job = d;
+                sm.job_ids[lane] = ids;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.job_full);
+                if (!more) break;
+                prefixes += d.w.prefix;
+                // the producer has this one and is near its end
+                if (!until([&]() -> bool { return __all_sync(0xffffffffu, mbar_test(&sm.job_want, (uint32_t)(jobs & 1))); }))
+                    break;
             }
+            until([&]() -> bool { return reported >= prefixes; });
         }
     } else {
         // ================================================= softmax and epilogue
@@ -615,6 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float sc = a.scale_log2;
         uint32_t ns = 0, no[2] = {0, 0};  // phases of s_full[t], o_full[0], o_full[1]
         bool ready = false;               // every prefix partial is written
+        const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
         uint32_t nb2 = 0;                 // phases of both
         bool ok = true;
         // bounded waits of the whole warp: one outcome for all lanes
@@ -694,16 +799,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint64_t sc2 = pack2(sc, sc), neg2 = pack2(neg_m, neg_m);
                 uint64_t ls[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-                for (int c = 0; c < kNB / 64; ++c) {
-                    uint32_t p[32];
+                for (int c = 0; c < kNB / 32; ++c) {
+                    uint32_t p[16];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const float2 x = unpack2(fma2(pack2(s[c * 64 + 2 * e], s[c * 64 + 2 * e + 1]), sc2, neg2));
+                    for (int e = 0; e < 16; ++e) {
+                        const float2 x = unpack2(fma2(pack2(s[c * 32 + 2 * e], s[c * 32 + 2 * e + 1]), sc2, neg2));
                         const float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
                         ls[e & 3] = add2(ls[e & 3], pack2(p0, p1));
                         p[e] = pack_bf16x2(p0, p1);
                     }
-                    tmem_st32(tS + c * 32, p);
+                    tmem_st16(tS + c * 16, p);
                 }
                 const float2 lsum = unpack2(add2(add2(ls[0], ls[1]), add2(ls[2], ls[3])));
                 l_run += lsum.x + lsum.y;
@@ -763,13 +868,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_ld_wait();
                         if (!live) continue;
                         if (w.slot < 0) {
-                            uint4 *o = reinterpret_cast<uint4 *>(a.out + row * D + c * 32);
-#pragma unroll
-                            for (int x = 0; x < 4; ++x) {
-                                const float *f = reinterpret_cast<const float *>(&raw[8 * x]);
-                                o[x] = make_uint4(pack_bf16x2(f[0] * inv, f[1] * inv), pack_bf16x2(f[2] * inv, f[3] * inv),
-                                                  pack_bf16x2(f[4] * inv, f[5] * inv), pack_bf16x2(f[6] * inv, f[7] * inv));
-                            }
+                            const float *f = reinterpret_cast<const float *>(raw);
+                            store_bf16x16(a.out + row * D + c * 32, f, inv, wide);
+                            store_bf16x16(a.out + row * D + c * 32 + 16, f + 16, inv, wide);
                         } else {
                             float4 *o = part_cols<D>(a, prow) + c * 8 * 32;
 #pragma unroll
@@ -810,6 +911,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int np = live && w.merge ? a.p_splits : 0;
                 m = fmaxf(sA.x, sB.x);
                 l = 0.f;
+#pragma unroll 4
                 for (int p = 0; p < np; ++p) {
                     const float2 ml = __ldcg(&a.part_ml[p * pslot + prow]);
                     const float mn = fmaxf(m, ml.x);
@@ -863,12 +965,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (live) {
                     if (w.slot < 0) {
-                        uint4 *d = reinterpret_cast<uint4 *>(a.out + row * D + t * kHalf);
 #pragma unroll
-                        for (int x = 0; x < kHalf / 8; ++x)
-                            d[x] = make_uint4(pack_bf16x2(o[8 * x], o[8 * x + 1]), pack_bf16x2(o[8 * x + 2], o[8 * x + 3]),
-                                              pack_bf16x2(o[8 * x + 4], o[8 * x + 5]),
-                                              pack_bf16x2(o[8 * x + 6], o[8 * x + 7]));
+                        for (int x = 0; x < kHalf / 16; ++x)
+                            store_bf16x16(a.out + row * D + t * kHalf + x * 16, o + x * 16, 1.f, wide);
                         if (t == 0 && a.lse) a.lse[row] = (m + __log2f(l)) * kLn2;
                     } else {
                         float4 *d = part_cols<D>(a, prow) + t * (kHalf / 4) * 32;
@@ -884,7 +983,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             no[1] += w.nB > 0;
             if (w.prefix) {
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.written);
+                if (lane == 0) {
+                    __threadfence_block();
+                    atomicAdd(&sm.written, 1);
+                }
             }
         }
     }
