@@ -359,10 +359,14 @@ svpa_status svpa_prefix_verify_attn_workspace_size(const svpa_attn_params *p,
  * tables: a sequence joins the shared prefix when context_lens[b] >=
  * prefix_len and its table begins with prefix_blocks, and attends its whole
  * history by itself otherwise, so the result never depends on the prefix
- * given.  bf16 pages; FP8 pages and variant 1 are refused
- * (SVPA_ERR_UNSUPPORTED); split_pages is not used.  One kernel on `stream`,
- * two when the own parts are split over idle SMs (small batches).  K/V values
- * of every position below context_lens[b] + n_q must be finite.
+ * given.  Where sharing would not pay (short prefixes, or few of them beside
+ * query rows that fill a tile) the call is svpa_paged_verify_attn.  bf16 pages;
+ * FP8 pages and variant 1 are refused (SVPA_ERR_UNSUPPORTED); split_pages is
+ * not used where the prefix is shared.  A block of prefix_blocks outside the
+ * pool raises SVPA_DEVERR_BAD_BLOCK there.  One kernel on `stream`, two when
+ * sequences are first ranked longest first or the own parts are split over
+ * idle SMs (small batches).  K/V values of every position below
+ * context_lens[b] + n_q must be finite.
  */
 svpa_status svpa_prefix_verify_attn(const svpa_attn_params *p, const void *q,
                                     const void *k_pool, const void *v_pool,

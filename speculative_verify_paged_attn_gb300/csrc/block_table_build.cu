@@ -22,7 +22,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kChunk = 512;  // entries a warp writes at a time
-constexpr int kMaxCtas = 152 * 8;  // resident at once for batches of up to about 3500
+constexpr int kMaxCtas = 152 * 4;  // resident at once for batches of up to about 7000
 
 // Exclusive sums of two values per thread over the CTA; totals returned too.
 __device__ __forceinline__ void scan2(int &x, int &y, int &tx, int &ty, int2 *warp_sums) {
@@ -225,6 +225,10 @@ __global__ void __launch_bounds__(kThreads) build_kernel(const __grid_constant__
     // *free_top is lowered once every CTA has read it
     __syncthreads();
     if (threadIdx.x == 0) {
+        if (gridDim.x == 1) {
+            *a.free_top = top - tp;
+            return;
+        }
         __threadfence();
         if (atomicAdd(a.ticket, 1) == (int)gridDim.x - 1) {
             *a.ticket = 0;

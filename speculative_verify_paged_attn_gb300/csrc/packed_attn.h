@@ -13,6 +13,7 @@ struct PackedArgs {
     const int32_t *cu;             // [B + 1] packed query offsets (prompt)
     const int32_t *lens;           // [B] kv lengths (prompt) or committed histories (verify)
     const int32_t *prefix_blocks;  // [prefix_pages] (verify)
+    const int32_t *order;          // [B] sequences, longest first, or null (verify)
     __nv_bfloat16 *out;            // [T, Hq, D]
     float *lse;                    // [T, Hq] or null
     // partials, one row for each (slot, kv head, 128-row query tile, row of the

@@ -565,7 +565,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else if (a.verify) {
                     const int x = u - a.p_units;
                     const int h = x % a.Hkv, y = x / a.Hkv;
-                    const int split = y % a.s_splits, b = y / a.s_splits;
+                    const int split = y % a.s_splits;
+                    const int b = a.order ? __ldg(a.order + y / a.s_splits) : y / a.s_splits;
                     const int L = __ldg(a.lens + b);
                     d.bt = a.block_table + (size_t)b * a.max_blocks;
                     const long long total = (long long)L + a.n_q;

@@ -87,10 +87,11 @@ bool encode_queries(EncodeTiledFn enc, CUtensorMap m[2], const void *q, int D, i
 
 struct Plan {
     int tpt, tiles, pairs, p_units, p_splits, s_splits, total_units;
+    bool shared, ordered;
     size_t off_member, off_ml, off_o, bytes;
 };
 
-// Workspace: [counters][member][partial (max, sum)][partial outputs], one
+// Workspace: [counters][member or order][partial (max, sum)][partial outputs], one
 // partial slot for each KV split of the prefix units and, when split, of the others.
 svpa_status layout(Plan *pl, long long units, long long T, int Hkv, int D, int members) {
     if (units > 0x7fffffff) return SVPA_ERR_UNSUPPORTED;
@@ -134,8 +135,8 @@ svpa_status plan_prompt(const svpa_prompt_params *p, Plan *pl) {
 }
 
 svpa_status plan_prefix(const svpa_attn_params *p, int32_t prefix_len, Plan *pl) {
-    size_t dummy;
-    const svpa_status s = svpa_attn_workspace_size(p, &dummy);
+    size_t alone_bytes;
+    const svpa_status s = svpa_attn_workspace_size(p, &alone_bytes);
     if (s != SVPA_OK) return s;
     if (prefix_len < 0 || prefix_len % kBlockSize != 0 || prefix_len / kBlockSize > p->num_blocks)
         return SVPA_ERR_INVALID_ARG;
@@ -148,31 +149,45 @@ svpa_status plan_prefix(const svpa_attn_params *p, int32_t prefix_len, Plan *pl)
     pl->tpt = kMaxRows / G;
     pl->pairs = ceil_div(T, 2 * pl->tpt);
     const int slots = sm_count();
+    const long long own = (long long)p->batch * p->num_kv_heads;
     const int pb = ceil_div(prefix_len, 8 * kBlockSize);
+    const int sb = std::max(1, ceil_div(p->max_blocks_per_seq, 8) - pb);  // own blocks at most
     const long long tiles = (long long)pl->pairs * p->num_kv_heads;
-    // Splits of the prefix: rounds of units over the SMs times a unit's length,
-    // in blocks; a unit costs about three blocks beside its own (filling the
-    // pipeline and storing its partials), a split one block of every own part
-    // (joining them).
+    // Sharing pays when reading the prefix for each sequence costs more than
+    // reading it for 256 query rows at a time and joining the two parts.  Per
+    // sequence and kv head, in thousands of cycles (traces of small and large
+    // cases): 1.75 a block alone, against its share of a prefix unit (3 a block
+    // and 8 besides) and 2 for joining.  Measured both ways: 64 x 1 tokens behind
+    // 64: 25.6 us alone, 32.0 shared; behind 1024: 58.2 and 39.8; draft trees of
+    // 29 nodes x 4 heads, 116 rows of a 128-row tile as it is, behind 800: 465
+    // and 475; 6 nodes x 4 heads behind 256: 231 and 220.
+    const double rows = (double)p->n_q * G;
+    pl->shared = rows / 256. * (3. * pb + 8.) + 2. < 1.75 * pb;
+    if (!pl->shared) {
+        pl->bytes = alone_bytes;
+        return SVPA_OK;
+    }
+    // Splits of the prefix: rounds of units over the SMs times a unit's length
+    // (3 a block for a pair of tiles, 1.5 for one; 8 besides), and one more for
+    // each split that an own unit joins.
+    const double block = T > pl->tpt ? 3.0 : 1.5;
+    double best = 0.;
     pl->p_splits = 0;
-    if (pb > 0 && tiles > 0) {
-        long long best = 0;
-        for (int sp = 1; sp <= std::min(kMaxSplits, std::max(1, pb / 2)); ++sp) {
-            const long long cost = ceil_div(tiles * sp, slots) * (long long)(ceil_div(pb, sp) + 3) +
-                                   ceil_div((long long)p->batch * p->num_kv_heads, slots) * (long long)sp;
-            if (pl->p_splits == 0 || cost < best) {
-                best = cost;
-                pl->p_splits = sp;
-            }
+    for (int sp = 1; sp <= std::min(kMaxSplits, std::max(1, pb / 2)); ++sp) {
+        const double cost = ceil_div(tiles * sp, slots) * (ceil_div(pb, sp) * block + 8.) +
+                            (double)ceil_div(own, slots) * sp;
+        if (pl->p_splits == 0 || cost < best) {
+            best = cost;
+            pl->p_splits = sp;
         }
     }
     pl->p_units = (int)(tiles * pl->p_splits);
     // the sequences' own parts: split when they alone leave SMs idle
-    const long long own = (long long)p->batch * p->num_kv_heads;
-    const int sb = ceil_div(std::max(0, p->max_blocks_per_seq - prefix_len / kBlockSize), 8);
     pl->s_splits = 1;
     if (own > 0 && own < slots)
         pl->s_splits = (int)std::max<long long>(1, std::min<long long>({slots / own, sb / 8, (long long)kMaxSplits}));
+    // units of different lengths on every SM: longest first
+    pl->ordered = pl->s_splits == 1 && p->batch > 1 && p->batch <= kMaxOrderedSeqs && own > slots;
     return layout(pl, pl->p_units + own * pl->s_splits, T, p->num_kv_heads, p->head_dim, p->batch);
 }
 
@@ -274,6 +289,9 @@ svpa_status svpa_prefix_verify_attn(const svpa_attn_params *p, const void *q, co
                         error_flag);
     if (s != SVPA_OK) return s;
     if (prefix_len > 0 && !prefix_blocks) return SVPA_ERR_INVALID_ARG;
+    if (!pl.shared)  // not worth sharing: every sequence reads its whole history itself
+        return svpa_paged_verify_attn(p, q, k_pool, v_pool, nullptr, nullptr, block_table, context_lens, ancestor_mask,
+                                      out, lse, workspace, workspace_bytes, error_flag, stream);
     if (!workspace || workspace_bytes < pl.bytes || !aligned16(workspace)) return SVPA_ERR_WORKSPACE;
     EncodeTiledFn enc = encode_fn();
     if (!enc) return SVPA_ERR_CUDA;
@@ -307,7 +325,14 @@ svpa_status svpa_prefix_verify_attn(const svpa_attn_params *p, const void *q, co
     a.scale_log2 = p->sm_scale * 1.4426950408889634f;
     for (int j = 0; j < p->n_q; ++j)
         a.anc[j] = ancestor_mask ? ancestor_mask[j] : ((j == 63) ? ~0ull : ((1ull << (j + 1)) - 1ull));
-    return launch(maps, a, D, static_cast<cudaStream_t>(stream));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (pl.ordered) {
+        int32_t *order = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(workspace) + pl.off_member);
+        const cudaError_t e = launch_seq_order(context_lens, p->batch, order, st);
+        if (e != cudaSuccess) return from_cuda(e);
+        a.order = order;
+    }
+    return launch(maps, a, D, st);
 }
 
 }  // extern "C"
