@@ -20,11 +20,15 @@ namespace svpa {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kChunk = 512;  // entries a warp writes at a time
-constexpr int kMaxCtas = 152 * 4;  // resident at once for batches of up to about 7000
+// Small admissions are one CTA of 1024 threads, whose warps take 128 entries
+// at a time (nothing to wait for at the end; 8 requests of some hundred tokens:
+// about 6 us); others CTAs of 256, 256 entries a warp (256 requests of up to
+// 32768 tokens, 4 million slots: about 13 us).
+constexpr int kOneCta = 32768;     // entries and slots
+constexpr int kMaxCtas = 152 * 5;  // resident at once for batches of up to about 5500
 
 // Exclusive sums of two values per thread over the CTA; totals returned too.
+template <int kThreads>
 __device__ __forceinline__ void scan2(int &x, int &y, int &tx, int &ty, int2 *warp_sums) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int ix = x, iy = y;
@@ -54,6 +58,7 @@ __device__ __forceinline__ void scan2(int &x, int &y, int &tx, int &ty, int2 *wa
     y = by + iy - y;
 }
 
+template <int kThreads, int kChunk>
 __global__ void __launch_bounds__(kThreads) build_kernel(const __grid_constant__ BuildArgs a) {
     extern __shared__ int32_t sh[];
     int32_t *first = sh;               // [B + 1] own pages of the requests before
@@ -120,7 +125,7 @@ __global__ void __launch_bounds__(kThreads) build_kernel(const __grid_constant__
     }
     // the sums fit: at most num_blocks pages and `slots` tokens
     int x = (int)lp, y = (int)lt, tp, tt;
-    scan2(x, y, tp, tt, warp_sums);
+    scan2<kThreads>(x, y, tp, tt, warp_sums);
     for (int b = b0; b < b1; ++b) {
         first[b] = x;
         cu[b] = y;
@@ -149,13 +154,17 @@ __global__ void __launch_bounds__(kThreads) build_kernel(const __grid_constant__
     const long long warps = (long long)gridDim.x * (kThreads / 32);
     const long long w0 = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
     const long long entries = (long long)a.B * a.max_blocks;
-    for (long long c = w0; c * kChunk < entries; c += warps) {
+    const long long table_chunks = (entries + kChunk - 1) / kChunk;
+    const long long all_chunks = table_chunks + (a.slots + kChunk - 1) / kChunk;
+    // the table's chunks, then the slot map's, over all warps
+    long long c = w0;
+    for (; c < table_chunks; c += warps) {
         const long long e0 = c * kChunk;
         const int row0 = (int)(e0 / a.max_blocks);
         const unsigned col0 = (unsigned)(e0 - (long long)row0 * a.max_blocks);
-#pragma unroll 4
+#pragma unroll 8
         for (int k = lane; k < kChunk; k += 32) {
-            if (e0 + k >= entries) break;
+            if (e0 + k >= entries) continue;
             const unsigned q = (col0 + k) / (unsigned)a.max_blocks;
             const int b = row0 + (int)q, i = (int)(col0 + k - q * a.max_blocks);
             const int own = first[b + 1] - first[b];
@@ -178,8 +187,8 @@ __global__ void __launch_bounds__(kThreads) build_kernel(const __grid_constant__
     }
     const int total = cu[a.B];
     const bool vec = (reinterpret_cast<uintptr_t>(a.slot_map) & 15) == 0;
-    for (long long c = w0; c * kChunk < a.slots; c += warps) {
-        const int s0 = (int)(c * kChunk), s1 = min(s0 + kChunk, a.slots);
+    for (; c < all_chunks; c += warps) {
+        const int s0 = (int)((c - table_chunks) * kChunk), s1 = min(s0 + kChunk, a.slots);
         // the requests of the chunk's first and last rows
         auto request_of = [&](int t, int lo, int hi) -> int {  // in [lo, hi)
             while (hi - lo > 1) {
@@ -196,7 +205,19 @@ __global__ void __launch_bounds__(kThreads) build_kernel(const __grid_constant__
             const int t0 = s0 + k * 128 + lane * 4;
             if (t0 >= s1) break;
             int b = t0 < total ? request_of(t0, lo, hi) : 0;
-            int page = -1, row = -1, id = -1, slot[4];
+            int slot[4];
+            if (t0 < total && t0 + 3 < cu[b + 1]) {
+                // four rows of one request: of one page, or of two that follow
+                const int pos = prefix_len + t0 - cu[b], page = pos / kBlockSize, last = (pos + 3) / kBlockSize;
+                const int id0 = block_of(b, page), id1 = last == page ? id0 : block_of(b, last);
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    const int id = (pos + z) / kBlockSize == page ? id0 : id1;
+                    // (one outside the pool is raised with the table)
+                    slot[z] = (unsigned)id < (unsigned)a.num_blocks ? id * kBlockSize + (pos + z) % kBlockSize : -1;
+                }
+            } else {
+            int page = -1, row = -1, id = -1;
 #pragma unroll
             for (int z = 0; z < 4; ++z) {
                 const int t = t0 + z;
@@ -212,6 +233,7 @@ __global__ void __launch_bounds__(kThreads) build_kernel(const __grid_constant__
                     }
                     if (id >= 0) slot[z] = id * kBlockSize + pos % kBlockSize;
                 }
+            }
             }
             if (vec && t0 + 4 <= a.slots) {
                 *reinterpret_cast<int4 *>(a.slot_map + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
@@ -239,23 +261,32 @@ __global__ void __launch_bounds__(kThreads) build_kernel(const __grid_constant__
 
 }  // namespace
 
-cudaError_t launch_block_table_build(const BuildArgs &a, cudaStream_t stream) {
-    const long long entries = (long long)a.B * a.max_blocks + a.slots;
-    const long long ctas = (entries + kChunk * (kThreads / 32) - 1) / (kChunk * (kThreads / 32));
-    const int grid = (int)(ctas < 1 ? 1 : ctas > kMaxCtas ? kMaxCtas : ctas);
+namespace {
+
+template <int kThreads, int kChunk>
+cudaError_t launch_t(const BuildArgs &a, int grid, cudaStream_t stream) {
     const size_t smem = (size_t)2 * (a.B + 1) * sizeof(int32_t);
-    if (smem > 48 * 1024) {
+    if (smem > 40 * 1024) {  // (a few hundred bytes are static)
         static DeviceMemo<int> attr_set;
         int done = 0;
         const cudaError_t e = attr_set.get(&done, [](int *v) {
             *v = 1;
-            return cudaFuncSetAttribute(build_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            return cudaFuncSetAttribute(build_kernel<kThreads, kChunk>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         (int)(2 * (kMaxBuildBatch + 1) * sizeof(int32_t)));
         });
         if (e != cudaSuccess) return e;
     }
-    build_kernel<<<grid, kThreads, smem, stream>>>(a);
+    build_kernel<kThreads, kChunk><<<grid, kThreads, smem, stream>>>(a);
     return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_block_table_build(const BuildArgs &a, cudaStream_t stream) {
+    const long long entries = (long long)a.B * a.max_blocks + a.slots;
+    if (entries <= kOneCta) return launch_t<1024, 128>(a, 1, stream);
+    const long long ctas = (entries + 256 * 8 - 1) / (256 * 8);
+    return launch_t<256, 256>(a, (int)(ctas > kMaxCtas ? kMaxCtas : ctas), stream);
 }
 
 }  // namespace svpa
