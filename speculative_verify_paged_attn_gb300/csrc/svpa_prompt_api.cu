@@ -54,7 +54,7 @@ int sm_count() {
     return e == cudaSuccess ? n : 152;
 }
 
-int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
+long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
 bool encode_bf16(EncodeTiledFn enc, CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims,
                  const cuuint64_t *strides, const cuuint32_t *box) {
@@ -97,7 +97,7 @@ svpa_status layout(Plan *pl, long long units, long long T, int Hkv, int D, int m
     if (units > 0x7fffffff) return SVPA_ERR_UNSUPPORTED;
     pl->total_units = (int)units;
     const size_t slots = (size_t)pl->p_splits + (pl->s_splits > 1 ? pl->s_splits : 0);
-    pl->tiles = ceil_div(T, pl->tpt);
+    pl->tiles = (int)ceil_div(T, pl->tpt);
     const size_t rows = (size_t)Hkv * pl->tiles * kMaxRows;
     pl->off_member = kAlign;
     pl->off_ml = pl->off_member + align_up((size_t)members * sizeof(int32_t));
@@ -125,7 +125,7 @@ svpa_status plan_prompt(const svpa_prompt_params *p, Plan *pl) {
     pl->p_units = 0;
     pl->p_splits = 0;
     const long long units = (long long)pl->pairs * p->num_kv_heads;
-    const int blocks = ceil_div(p->max_blocks_per_seq, 8);
+    const int blocks = (int)ceil_div(p->max_blocks_per_seq, 8);
     // few tiles against long histories (a chunk or single tokens behind a long
     // cache): split the kv range until every SM has a unit
     pl->s_splits = 1;
@@ -147,11 +147,11 @@ svpa_status plan_prefix(const svpa_attn_params *p, int32_t prefix_len, Plan *pl)
     const int G = p->num_q_heads / p->num_kv_heads;
     const long long T = (long long)p->batch * p->n_q;
     pl->tpt = kMaxRows / G;
-    pl->pairs = ceil_div(T, 2 * pl->tpt);
+    pl->pairs = (int)ceil_div(T, 2 * pl->tpt);
     const int slots = sm_count();
     const long long own = (long long)p->batch * p->num_kv_heads;
-    const int pb = ceil_div(prefix_len, 8 * kBlockSize);
-    const int sb = std::max(1, ceil_div(p->max_blocks_per_seq, 8) - pb);  // own blocks at most
+    const int pb = (int)ceil_div(prefix_len, 8 * kBlockSize);
+    const int sb = std::max(1, (int)ceil_div(p->max_blocks_per_seq, 8) - pb);  // own blocks at most
     const long long tiles = (long long)pl->pairs * p->num_kv_heads;
     // Sharing pays when reading the prefix for each sequence costs more than
     // reading it for 256 query rows at a time and joining the two parts.  Per
@@ -174,13 +174,14 @@ svpa_status plan_prefix(const svpa_attn_params *p, int32_t prefix_len, Plan *pl)
     double best = 0.;
     pl->p_splits = 0;
     for (int sp = 1; sp <= std::min(kMaxSplits, std::max(1, pb / 2)); ++sp) {
-        const double cost = ceil_div(tiles * sp, slots) * (ceil_div(pb, sp) * block + 8.) +
+        const double cost = (double)ceil_div(tiles * sp, slots) * ((double)ceil_div(pb, sp) * block + 8.) +
                             (double)ceil_div(own, slots) * sp;
         if (pl->p_splits == 0 || cost < best) {
             best = cost;
             pl->p_splits = sp;
         }
     }
+    if (tiles * pl->p_splits > 0x7fffffff) return SVPA_ERR_UNSUPPORTED;
     pl->p_units = (int)(tiles * pl->p_splits);
     // the sequences' own parts: split when they alone leave SMs idle
     pl->s_splits = 1;

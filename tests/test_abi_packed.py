@@ -63,11 +63,24 @@ def test_prompt_call_arguments(lib):
         assert call(ctypes.byref(q), *([None] * 9), 0, None, None) == 0
 
 
+def test_prompt_binding_refuses_rows_other_than_its_stride(lib):
+    import torch
+
+    from speculative_verify_paged_attn_gb300 import svpa
+    p = svpa.prompt_params(1, 5, 2, 2, 64, 4, 4)
+    q = torch.zeros(5, 6, 64, dtype=torch.bfloat16)[:, :2]  # sliced, but q_stride not said
+    x = torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(svpa.SvpaError):
+        svpa.paged_prompt_attn(p, q, x, x, x, x, x, q, workspace=x, error_flag=x, stream=0)
+
+
 @pytest.mark.parametrize("prefix,kw,status", [
     (0, {}, 0), (512, {}, 0), (-16, {}, 1), (100, {}, 1), (16 * 71, {}, 1), (16 * 70, {}, 0),
     (512, dict(kv_fp8=True), 2), (512, dict(variant=1), 2), (512, dict(variant=2), 0), (512, dict(n_q=40), 2),
     (512, dict(head_dim=96), 2), (512, dict(num_kv_heads=3), 1), (512, dict(n_q=0), 1), (512, dict(n_q=65), 1),
     (512, dict(batch=65536), 2),
+    # more units than 31 bits count
+    (512, dict(batch=65535, n_q=8, num_q_heads=131070, num_kv_heads=65535), 2),
 ])
 def test_prefix_shapes(lib, prefix, kw, status):
     from speculative_verify_paged_attn_gb300 import svpa

@@ -78,6 +78,7 @@ class Build:
     ([48, 33, 32], 32, dict(spare=1)), ([0, 100, 0], 96, dict(width=31)), ([800, 800], 800, dict(spare=5)),
     ([5000, 1, 333, 4096], 0, dict(width=400)), (list(range(1, 600)), 0, {}), ([40] * 1000, 16, dict(width=3)),
     ([20000, 7, 20000], 0, dict(width=1251, spare=50)), ([3] * 8192, 0, dict(width=1)),
+    ([20 + i % 3 for i in range(8192)], 16, dict(width=5, spare=3)),
 ])
 def test_tables_and_slots(lens, prefix, kw):
     c = Build(lens, prefix, **kw)

@@ -106,7 +106,7 @@ def test_draft_tree(own):
     c.check()
 
 
-@pytest.mark.parametrize("own,hkv", [([30, 200, 77, 5] * 50, 4), ([900, 30, 77], 1)])
+@pytest.mark.parametrize("own,hkv", [([30, 200, 77, 5] * 50, 4), ([900, 30, 77], 1), ([3000, 2500, 77], 1)])
 def test_sequences_without_the_prefix(own, hkv):
     """Rows whose table does not begin with the shared blocks, and rows shorter
     than the prefix, attend their own history: the result is that of
