@@ -273,9 +273,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kPageBytes = kBlockSize * D * 2;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    // the first unit is on its way while the CTA sets itself up
+    // A prompt's first units go by CTA.  Units of a verification are all taken
+    // from the counter, so that every prefix unit is a running CTA's before any
+    // unit that waits for it is taken (the first, while the CTA sets itself up).
     int next = -1;
-    if (threadIdx.x == 96) next = atomicAdd(&a.sched[0], 1);
+    if (threadIdx.x == 96) next = a.verify ? atomicAdd(&a.sched[0], 1) : (int)blockIdx.x;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kRing; ++i) {
             mbar_init(&sm.full[i], 1);
@@ -535,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // The next unit that has work; false when there is none.
         auto decode = [&](Job &d) -> bool {
             while (true) {
-                if (lane == 0 && next < 0) next = atomicAdd(&a.sched[0], 1);
+                if (lane == 0 && next < 0) next = atomicAdd(&a.sched[0], 1) + (a.verify ? 0 : (int)gridDim.x);
                 const int u = __shfl_sync(0xffffffffu, next, 0);
                 if (u >= a.total_units) return false;
                 next = -1;
@@ -615,9 +617,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // long tiles first: the last tiles of a sequence see the most
                     const int h = u % a.Hkv, y = u / a.Hkv;
                     const int split = y % a.s_splits, slot = a.pairs - 1 - y / a.s_splits;
-                    const int b = find_sequence(a.cu, a.B, tpt2, slot, lane);
-                    const int c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1);
-                    const int kv = __ldg(a.lens + b);
+                    int b, c0, c1, kv;
+                    if (a.B <= 32) {  // the whole batch in one round of loads
+                        const bool in = lane < a.B;
+                        c0 = in ? __ldg(a.cu + lane) : 0;
+                        c1 = in ? __ldg(a.cu + lane + 1) : 0;
+                        kv = in ? __ldg(a.lens + lane) : 0;
+                        const unsigned m = __ballot_sync(0xffffffffu, in && c0 / tpt2 + lane <= slot);
+                        b = m ? 31 - __clz((int)m) : 0;
+                        c0 = __shfl_sync(0xffffffffu, c0, b);
+                        c1 = __shfl_sync(0xffffffffu, c1, b);
+                        kv = __shfl_sync(0xffffffffu, kv, b);
+                    } else {
+                        b = find_sequence(a.cu, a.B, tpt2, slot, lane);
+                        c0 = __ldg(a.cu + b);
+                        c1 = __ldg(a.cu + b + 1);
+                        kv = __ldg(a.lens + b);
+                    }
                     const int t0 = c0 + (slot - (c0 / tpt2 + b)) * tpt2;
                     if (t0 >= c1) {
                         // no tile here; a bad row of offsets is reported with its first slot
