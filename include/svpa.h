@@ -23,6 +23,19 @@
  *   svpa_gamma_update        acceptance moving averages and the draft length
  *                            of the next step (with E[K] / speed-up telemetry).
  *
+ * Before it, for requests that are admitted, and beside it:
+ *
+ *   svpa_block_table_build   block tables and slot maps of new requests from
+ *                            their lengths, behind an optional shared prefix.
+ *   svpa_kv_write            the prompts' K/V rows into their pages through the
+ *                            slot map.
+ *   svpa_paged_prompt_attn   causal attention of packed prompts (or chunks)
+ *                            over their pages.
+ *   svpa_prefix_verify_attn  svpa_paged_verify_attn for a batch that shares a
+ *                            long prefix, attended once for all sequences.
+ *   svpa_logits_process      penalties, biases and grammar masks on the target's
+ *                            logits, before a sampler fed by logits.
+ *
  * Conventions shared by every entry point
  *  - Every pointer argument is a DEVICE pointer unless its comment says HOST.
  *    The caller owns and allocates all memory; no entry point calls an
@@ -37,6 +50,8 @@
  *    bits; kernels never trap.  svpa_check_error() synchronises the stream,
  *    reads the word and maps it to a status.
  *  - Calls that share buffers are not thread safe; order them on one stream.
+ *    That holds for workspaces too: one belongs to one call at a time, also
+ *    where the calls are in different captured graphs.
  *  - Output of an operation whose error_flag came back non-zero is undefined.
  */
 #ifndef SVPA_H
