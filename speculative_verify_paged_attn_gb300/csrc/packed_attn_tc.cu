@@ -719,6 +719,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // the producer has this one and is near its end
                 if (!until([&]() -> bool { return __all_sync(0xffffffffu, mbar_test(&sm.job_want, (uint32_t)(jobs & 1))); }))
                     break;
+                // a unit that waits for the prefix holds no second one back: the CTAs
+                // that end their prefix units take the rest (2 x 1 tokens of 32
+                // heads behind 4096: the third own unit of a CTA ended at 36 us)
+                if (d.w.merge && !until([&]() -> bool {
+                        return __all_sync(0xffffffffu, ld_acquire(a.sched + 2) >= a.p_units);
+                    }))
+                    break;
             }
             until([&]() -> bool { return reported >= prefixes; });
         }
