@@ -116,7 +116,8 @@ svpa_status svpa_logits_process(const svpa_logits_params *p, const void *logits,
     if (!p || p->batch < 0 || p->rows < 1 || p->rows > kMaxNq || p->vocab < 1 || p->max_history < 0 ||
         (p->logits_dtype != SVPA_LOGITS_FP32 && p->logits_dtype != SVPA_LOGITS_BF16))
         return SVPA_ERR_INVALID_ARG;
-    if (p->vocab > (1 << 24) || p->batch > 65535) return SVPA_ERR_UNSUPPORTED;
+    // a token's count has 29 bits, and the history's index runs a CTA's step past its end
+    if (p->vocab > (1 << 24) || p->batch > 65535 || p->max_history > (1 << 28)) return SVPA_ERR_UNSUPPORTED;
     ProcessArgs a;
     memset(&a, 0, sizeof a);
     for (int j = 0; j < p->rows; ++j) {

@@ -118,3 +118,9 @@ def logits_status(lib, ptrs=(), logits=NZ, out=NZ, err=NZ, parent=None, history=
 ])
 def test_logits_arguments(lib, kw, status):
     assert logits_status(lib, **kw) == status
+
+
+@pytest.mark.parametrize("n,status", [((1 << 28) + 1, 2), (0x7fffffff, 2)])
+def test_logits_history_limit(lib, n, status):
+    # a count has 29 bits and the history's index runs a step past its end: neither may wrap
+    assert logits_status(lib, max_history=n) == status
