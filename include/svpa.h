@@ -52,6 +52,8 @@
  *  - Calls that share buffers are not thread safe; order them on one stream.
  *    That holds for workspaces too: one belongs to one call at a time, also
  *    where the calls are in different captured graphs.
+ *  - A call runs on the calling thread's current device; its pointers and its
+ *    stream belong to that device.
  *  - Output of an operation whose error_flag came back non-zero is undefined.
  */
 #ifndef SVPA_H
@@ -250,7 +252,8 @@ svpa_status svpa_block_table_build_workspace_size(int32_t batch, size_t *bytes);
  * SVPA_DEVERR_BAD_BLOCK; tables, counts and the stack are then unchanged.  A
  * free-stack entry outside the pool raises SVPA_DEVERR_BAD_BLOCK; its page is
  * -1.  Limits: batch <= 8192, num_blocks < 2^27, num_slots <= 2^30, else
- * SVPA_ERR_UNSUPPORTED.
+ * SVPA_ERR_UNSUPPORTED.  With batch 0 nothing is written, slot_map and
+ * cu_seqlens included.
  * One kernel on `stream`.
  */
 svpa_status svpa_block_table_build(int32_t batch, int32_t block_size,
@@ -272,9 +275,9 @@ svpa_status svpa_block_table_build(int32_t batch, int32_t block_size,
  *
  * Row t goes to page slot_map[t] / 16, row slot_map[t] % 16 of every kv head's
  * tile; a negative slot is a padding row and is skipped, one past the pool
- * raises SVPA_DEVERR_BAD_BLOCK.  Two rows with the same slot: one of them is
- * stored in each 16-byte word, which one is unspecified.  Other slots are left
- * as they were.  FP8 pages take one scale per 64 consecutive elements
+ * raises SVPA_DEVERR_BAD_BLOCK.  Two rows with the same slot: what that slot
+ * holds is unspecified (words of either row; in FP8 pages a scale of one may
+ * stand beside codes of the other).  Other slots are left as they were.  FP8 pages take one scale per 64 consecutive elements
  * (scale_tile 64): scale = amax / 448 of the tile (1 when amax is 0), codes
  * e4m3(value / scale), as svpa_kv_append.
  *
@@ -402,7 +405,7 @@ typedef struct svpa_logits_params {
     int32_t rows;         /* logit rows per sequence, 1..64 (gamma + 1, or the
                              nodes of a draft tree)                           */
     int32_t vocab;        /* V, up to 2^24                                    */
-    int32_t max_history;  /* row stride of history                            */
+    int32_t max_history;  /* row stride of history, up to 2^28                */
     int32_t logits_dtype; /* SVPA_LOGITS_FP32 or SVPA_LOGITS_BF16             */
 } svpa_logits_params;
 

@@ -21,9 +21,10 @@ namespace svpa {
 namespace {
 
 // Small admissions are one CTA of 1024 threads, whose warps take 128 entries
-// at a time (nothing to wait for at the end; 8 requests of some hundred tokens:
-// about 6 us); others CTAs of 256, 256 entries a warp (256 requests of up to
-// 32768 tokens, 4 million slots: about 13 us).
+// at a time (nothing to wait for at the end); others CTAs of 256, 256 entries a
+// warp.  With a 4-byte copy before each call (0.9 us alone): 8 requests of some
+// hundred tokens 7.8 us, 256 requests of up to 32768 tokens, 4 million slots,
+// 15.1 us.  Bound by dependent loads: lengths, counts, stack, then the ticket.
 constexpr int kOneCta = 32768;     // entries and slots
 constexpr int kMaxCtas = 152 * 5;  // resident at once for batches of up to about 5500
 
@@ -217,23 +218,23 @@ __global__ void __launch_bounds__(kThreads) build_kernel(const __grid_constant__
                     slot[z] = (unsigned)id < (unsigned)a.num_blocks ? id * kBlockSize + (pos + z) % kBlockSize : -1;
                 }
             } else {
-            int page = -1, row = -1, id = -1;
+                int page = -1, row = -1, id = -1;
 #pragma unroll
-            for (int z = 0; z < 4; ++z) {
-                const int t = t0 + z;
-                slot[z] = -1;
-                if (t < total) {
-                    while (cu[b + 1] <= t) ++b;
-                    const int pos = prefix_len + t - cu[b];
-                    if (b != row || pos / kBlockSize != page) {
-                        row = b;
-                        page = pos / kBlockSize;
-                        id = block_of(b, page);
-                        if (id < 0 || id >= a.num_blocks) id = -1;  // raised with the table
+                for (int z = 0; z < 4; ++z) {
+                    const int t = t0 + z;
+                    slot[z] = -1;
+                    if (t < total) {
+                        while (cu[b + 1] <= t) ++b;
+                        const int pos = prefix_len + t - cu[b];
+                        if (b != row || pos / kBlockSize != page) {
+                            row = b;
+                            page = pos / kBlockSize;
+                            id = block_of(b, page);
+                            if (id < 0 || id >= a.num_blocks) id = -1;  // raised with the table
+                        }
+                        if (id >= 0) slot[z] = id * kBlockSize + pos % kBlockSize;
                     }
-                    if (id >= 0) slot[z] = id * kBlockSize + pos % kBlockSize;
                 }
-            }
             }
             if (vec && t0 + 4 <= a.slots) {
                 *reinterpret_cast<int4 *>(a.slot_map + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);

@@ -9,7 +9,9 @@
 // 16-byte words of one row, four per lane, so that its loads are in flight
 // together; consecutive rows fill consecutive rows of a page.  FP8: eight lanes
 // hold a 64-value tile, its scale is amax / 448 (1 for a tile of zeros) and its
-// codes the values over the scale, each rounded once.
+// codes the values over the scale, each rounded once.  32768 rows of 8 x 128:
+// bf16 42 us, 95% of the measured copy rate; FP8 54 us against a floor of 31,
+// bound by the instructions of the quotients and conversions.
 #include "admit.h"
 #include "svpa_device.cuh"
 

@@ -16,8 +16,10 @@
 // tokens put right in the output, one a lane, while their lines are in L2: with
 // the rules applied on the way, a warp took the long path for the one token in
 // fifty that needs it (64 x 6 rows of 128256 bf16 logits, histories of 8192:
-// 119 us, against 83 us; applying them on the way in slabs with many marks alone
-// gained 1 us there and cost 2 to 5 us on shorter histories).
+// 119 us, against 84; applying them on the way in slabs with many marks alone
+// gained 1.5 us there and cost 0.4 to 6 elsewhere).  Listing the marked tokens in
+// order gained 5 us there and cost 0.9 to 3.5 on short histories and odd rows.  84 us is 54% of the bytes'
+// floor: without histories the same rows take 59 us.
 #include "admit.h"
 #include "svpa_device.cuh"
 

@@ -157,10 +157,14 @@ svpa_status plan_prefix(const svpa_attn_params *p, int32_t prefix_len, Plan *pl)
     // reading it for 256 query rows at a time and joining the two parts.  Per
     // sequence and kv head, in thousands of cycles (traces of small and large
     // cases): 1.75 a block alone, against its share of a prefix unit (3 a block
-    // and 8 besides) and 2 for joining.  Measured both ways: 64 x 1 tokens behind
-    // 64: 25.6 us alone, 32.0 shared; behind 1024: 58.2 and 39.8; draft trees of
-    // 29 nodes x 4 heads, 116 rows of a 128-row tile as it is, behind 800: 465
-    // and 475; 6 nodes x 4 heads behind 256: 231 and 220.
+    // and 8 besides) and 2 for joining.  Against svpa_paged_verify_attn, 64
+    // sequences of up to 400 tokens more, 32/8 heads: 1 token behind 64: 23.4 us
+    // alone, 33.7 shared; behind 1024: 66.9 and 40.8; 6 drafts behind 256: 34.5
+    // and 36.6; behind 512: 44.5 and 40.4; trees of 29 nodes, 116 rows of a
+    // 128-row tile as they are, behind 800: 61.6 and 64.6; behind 2048: 112 and
+    // 90.  Over 138 such cases the rule is 4% behind the better side on average
+    // and 1.65 times at worst (8 x 1 tokens of 64/8 heads behind 128: 22.6 us
+    // alone, 13.7 shared).
     const double rows = (double)p->n_q * G;
     pl->shared = rows / 256. * (3. * pb + 8.) + 2. < 1.75 * pb;
     if (!pl->shared) {

@@ -118,7 +118,7 @@ def _p(t) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        # the current stream's handle without a Stream object around it (0.2 us against 3)
+        # the current stream's handle without a Stream object around it (0.3 us against 3)
         return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
