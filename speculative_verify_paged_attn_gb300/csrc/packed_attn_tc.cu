@@ -103,6 +103,7 @@ struct Smem {
     uint64_t drain[2];
     uint64_t turn[2];  // a pair's tiles issue their MMAs in turn
     uint64_t job_full, job_want;  // a decoded unit, scheduler -> producer
+    uint64_t prefix_done;         // every prefix unit's partials are written
     Job job;
     int32_t job_ids[32];
     Unit unit;
@@ -292,6 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         sm.written = 0;
         mbar_init(&sm.job_full, 1);
         mbar_init(&sm.job_want, 1);
+        mbar_init(&sm.prefix_done, 1);
         mbar_init(&sm.q_full, 1);
         mbar_init(&sm.q_empty, 10);  // the MMA issuers and the eight softmax warps
         for (int t = 0; t < 2; ++t) {
@@ -711,6 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 return true;
             };
+            bool told = false;  // that the prefix is complete
             for (int jobs = 0;; ++jobs) {
                 Job d;
                 const bool more = decode(d);
@@ -728,10 +731,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // a CTA whose unit waits for the prefix takes no second one: the CTAs
                 // that end their prefix units take the rest (2 x 1 tokens of 32 heads
                 // behind 4096: 27 us; with up to three units queued behind the wait 42)
-                if (d.w.merge && !until([&]() -> bool {
-                        return __all_sync(0xffffffffu, ld_acquire(a.sched + 2) >= a.p_units);
-                    }))
-                    break;
+                if (d.w.merge && !told) {
+                    // every prefix unit was taken by a running CTA before this unit
+                    // was: they end without waiting for anything of this one
+                    if (!until([&]() -> bool {
+                            return __all_sync(0xffffffffu, ld_acquire(a.sched + 2) >= a.p_units);
+                        }))
+                        break;
+                    told = true;
+                    if (lane == 0) mbar_arrive(&sm.prefix_done);
+                }
             }
             until([&]() -> bool { return reported >= prefixes; });
         }
@@ -748,7 +757,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int G = a.G, jq = r / G, gi = r - jq * G;
         const float sc = a.scale_log2;
         uint32_t ns = 0, no[2] = {0, 0};  // phases of s_full[t], o_full[0], o_full[1]
-        bool ready = false;               // every prefix partial is written
         const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
         uint32_t nb2 = 0;                 // phases of both
         bool ok = true;
@@ -917,20 +925,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             } else {
                 sm.stat[t][r] = make_float2(m_ref, l_run);
-                if (w.merge && !ready && threadIdx.x == 128) {
-                    // every prefix unit was taken by a running CTA before this
-                    // unit was: they end without waiting for anything of this one
-                    const unsigned long long start = global_ns();
-                    while (ld_acquire(a.sched + 2) < a.p_units) {
-                        __nanosleep(200);
-                        if (global_ns() - start > kWaitLimitNs) {
-                            raise_error(a.err, SVPA_DEVERR_TIMEOUT);
-                            break;
-                        }
-                    }
-                    __threadfence();
-                }
-                ready = ready || w.merge;
+                if (w.merge) ok = wait(&sm.prefix_done, 0);
+                if (!ok) break;
                 ok = meet();
                 if (!ok) break;
                 const float2 sA = sm.stat[0][r], sB = sm.stat[1][r];
@@ -940,20 +936,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 const int np = live && w.merge ? a.p_splits : 0;
                 m = fmaxf(sA.x, sB.x);
-                l = 0.f;
-#pragma unroll 4
-                for (int p = 0; p < np; ++p) {
-                    const float2 ml = __ldcg(&a.part_ml[p * pslot + prow]);
-                    const float mn = fmaxf(m, ml.x);
-                    l = (l > 0.f ? l * ex2_approx(m - mn) : 0.f) + (ml.y > 0.f ? ml.y * ex2_approx(ml.x - mn) : 0.f);
-                    m = mn;
-                }
                 float fA = sA.x == -CUDART_INF_F ? 0.f : ex2_approx(sA.x - m);
                 float fB = sB.x == -CUDART_INF_F ? 0.f : ex2_approx(sB.x - m);
-                l += sA.y * fA + sB.y * fB;
-                const float inv = w.slot >= 0 ? 1.f : l > 0.f ? 1.f / l : 0.f;
-                fA *= inv;
-                fB *= inv;
+                l = sA.y * fA + sB.y * fB;
+                if (np == 0 && w.slot < 0) {
+                    const float inv = l > 0.f ? 1.f / l : 0.f;
+                    fA *= inv;
+                    fB *= inv;
+                }
                 // group t takes half of the columns of both accumulators
                 constexpr int kHalf = D / 2, kC = D / 64;  // columns, pieces of 32
                 float o[kHalf];
@@ -983,15 +973,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float4 v[kHalf / 4];
 #pragma unroll
                     for (int x = 0; x < kHalf / 4; ++x) v[x] = __ldcg(src + x * 32);
-                    const float f = ml.y > 0.f ? ex2_approx(ml.x - m) * inv : 0.f;
-                    if (f == 0.f) continue;  // nothing there: not even zeros
+                    if (!(ml.y > 0.f)) continue;  // nothing there: not even zeros
+                    const float mn = fmaxf(m, ml.x);
+                    const float fo = l > 0.f ? ex2_approx(m - mn) : 0.f, fp = ex2_approx(ml.x - mn);
+                    l = l * fo + ml.y * fp;
+                    m = mn;
 #pragma unroll
                     for (int x = 0; x < kHalf / 4; ++x) {
-                        o[4 * x] = fmaf(v[x].x, f, o[4 * x]);
-                        o[4 * x + 1] = fmaf(v[x].y, f, o[4 * x + 1]);
-                        o[4 * x + 2] = fmaf(v[x].z, f, o[4 * x + 2]);
-                        o[4 * x + 3] = fmaf(v[x].w, f, o[4 * x + 3]);
+                        o[4 * x] = fmaf(v[x].x, fp, o[4 * x] * fo);
+                        o[4 * x + 1] = fmaf(v[x].y, fp, o[4 * x + 1] * fo);
+                        o[4 * x + 2] = fmaf(v[x].z, fp, o[4 * x + 2] * fo);
+                        o[4 * x + 3] = fmaf(v[x].w, fp, o[4 * x + 3] * fo);
                     }
+                }
+                if (np > 0) {
+                    const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+                    for (int x = 0; x < kHalf; ++x) o[x] *= inv;
                 }
                 if (live) {
                     if (w.slot < 0) {
