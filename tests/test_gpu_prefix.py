@@ -197,3 +197,44 @@ def test_bad_inputs_raise_and_the_next_call_is_right():
     c.err.zero_()
     c.call()
     c.check()
+
+
+@pytest.mark.parametrize("own,prefix,n_q,hq,hkv,loners", [
+    ([200, 33], 4096, 1, 32, 32, ()), ([100 + 29 * i for i in range(8)], 2048, 1, 32, 32, (3,)),
+    ([300, 7, 64, 1000, 0, 450], 3200, 5, 16, 8, (0, 5)),
+])
+def test_few_ctas_wait_for_a_long_prefix(own, prefix, n_q, hq, hkv, loners):
+    """CTAs without a prefix unit wait most of the call: what they hold back, and
+    what the others take, does not change the result."""
+    c = Case(own, prefix, n_q, hq, hkv, 128, loners=loners)
+    c.call()
+    c.check()
+    first, lse = c.out.clone(), c.lse.clone()
+    flush = torch.empty(64 << 20, device=DEV)
+    for i in range(6):
+        c.out.zero_()
+        c.lse.zero_()
+        if i % 2:
+            flush.fill_(float(i))
+        c.call()
+        assert torch.equal(c.out, first) and torch.equal(c.lse, lse), i
+    c.check()
+
+
+def test_two_calls_at_once_with_their_own_workspaces():
+    cases = [Case([90, 260, 140, 33] * 5, 1024, 4, 16, 4, 128, seed=3), Case([12, 700], 4096, 1, 16, 16, 128, seed=4)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    for c in cases:
+        c.call()
+        c.check()
+    want = [c.out.clone() for c in cases]
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for c, s in zip(cases, streams):
+            with torch.cuda.stream(s):
+                c.out.zero_()
+                c.call(stream=s)
+    torch.cuda.synchronize()
+    for c, w in zip(cases, want):
+        c.check()
+        assert torch.equal(c.out, w)
