@@ -18,7 +18,8 @@
 // fifty that needs it (64 x 6 rows of 128256 bf16 logits, histories of 8192:
 // 119 us, against 84; applying them on the way in slabs with many marks alone
 // gained 1.5 us there and cost 0.4 to 6 elsewhere).  Listing the marked tokens in
-// order gained 5 us there and cost 0.9 to 3.5 on short histories and odd rows.  84 us is 54% of the bytes'
+// order gained 5 us there and cost 0.6 to 3.5 on short histories and odd rows,
+// and 19 on long ones of fp32 rows.  84 us is 54% of the bytes'
 // floor: without histories the same rows take 59 us.
 #include "admit.h"
 #include "svpa_device.cuh"
