@@ -52,6 +52,12 @@
  *  - Calls that share buffers are not thread safe; order them on one stream.
  *    That holds for workspaces too: one belongs to one call at a time, also
  *    where the calls are in different captured graphs.
+ *  - One buffer, zero-filled once and large enough for each, may be the
+ *    workspace of svpa_paged_verify_attn, svpa_paged_prompt_attn,
+ *    svpa_prefix_verify_attn and svpa_block_table_build in turn, whatever
+ *    their batch, draft length, prefix and heads: every completed call leaves
+ *    its first 65792 bytes (counters and tickets) at zero.  The samplers'
+ *    workspace is another buffer.  After SVPA_DEVERR_TIMEOUT zero-fill again.
  *  - A call runs on the calling thread's current device; its pointers and its
  *    stream belong to that device.
  *  - Output of an operation whose error_flag came back non-zero is undefined.
@@ -141,7 +147,8 @@ svpa_status svpa_attn_launches(const svpa_attn_params *p, int32_t *launches);
  * results, per-(sequence, kv head) tickets and, for unsplit work, the order
  * in which sequences are handed out: longest first).  The workspace must be
  * zero-filled once before its first use; every completed call leaves its
- * ticket words at zero again. */
+ * ticket words at zero again.  A call that splits more than 16384 (sequence,
+ * kv head) pairs clears their tickets itself, in a memset before its kernel. */
 svpa_status svpa_attn_workspace_size(const svpa_attn_params *p, size_t *bytes);
 
 /*

@@ -62,7 +62,7 @@ struct AttnPlan {
     size_t off_order, off_prefix, off_ml, off_acc, bytes;
 };
 
-svpa_status plan_attn(const svpa_attn_params *p, AttnPlan *pl) {
+svpa_status plan_attn(const svpa_attn_params *p, AttnPlan *pl, size_t ticket_bytes = kTicketBytes) {
     if (!p) return SVPA_ERR_INVALID_ARG;
     if (p->batch < 0 || p->n_q < 1 || p->n_q > kMaxNq || p->num_q_heads < 1 || p->num_kv_heads < 1 ||
         p->num_q_heads % p->num_kv_heads != 0 || p->block_size != kBlockSize || p->max_blocks_per_seq < 1 ||
@@ -116,7 +116,7 @@ svpa_status plan_attn(const svpa_attn_params *p, AttnPlan *pl) {
     pl->max_splits = (p->max_blocks_per_seq + sp - 1) / sp;
     const size_t units = (size_t)p->batch * p->num_kv_heads;
     // [scheduler counters][tickets][split (max, sum)][split accumulators]
-    size_t off = kAlign + align_up(units * sizeof(int32_t));
+    size_t off = kWorkspaceCounterBytes + std::max(align_up(units * sizeof(int32_t)), ticket_bytes);
     // unsplit units vary most in length: hand out the longest first (a
     // greedy longest-first order; the draft-tree workload's 1024 unsplit
     // units on 152 SMs: about 12% above the ideal finish in index order,
@@ -188,65 +188,26 @@ svpa_status check_attn_call(const svpa_attn_params *p, const void *q, const void
     return SVPA_OK;
 }
 
-}  // namespace svpa
-
-extern "C" {
-
-const char *svpa_status_string(svpa_status s) {
-    switch (s) {
-        case SVPA_OK: return "ok";
-        case SVPA_ERR_INVALID_ARG: return "invalid argument";
-        case SVPA_ERR_UNSUPPORTED: return "unsupported configuration";
-        case SVPA_ERR_CUDA: return "CUDA error";
-        case SVPA_ERR_OUT_OF_BLOCKS: return "free block stack overflow";
-        case SVPA_ERR_BAD_BLOCK: return "block id outside the pool";
-        case SVPA_ERR_WORKSPACE: return "workspace missing or too small";
-        case SVPA_ERR_TIMEOUT: return "device wait timed out";
-    }
-    return "unknown status";
-}
-
-int32_t svpa_version(void) { return 100; }
-
-svpa_status svpa_attn_kernel(const svpa_attn_params *p, int32_t *kernel) {
-    if (!kernel) return SVPA_ERR_INVALID_ARG;
-    AttnPlan pl;
-    const svpa_status s = plan_attn(p, &pl);
-    if (s != SVPA_OK) return s;
-    *kernel = pl.use_tc ? 2 : 1;
-    return SVPA_OK;
-}
-
-svpa_status svpa_attn_launches(const svpa_attn_params *p, int32_t *launches) {
-    if (!launches) return SVPA_ERR_INVALID_ARG;
-    AttnPlan pl;
-    const svpa_status s = plan_attn(p, &pl);
-    if (s != SVPA_OK) return s;
-    *launches = p->batch == 0 ? 0 : (pl.ordered || pl.streamk ? 2 : 1);
-    return SVPA_OK;
-}
-
-svpa_status svpa_attn_workspace_size(const svpa_attn_params *p, size_t *bytes) {
+svpa_status attn_workspace_bytes(const svpa_attn_params *p, size_t ticket_bytes, size_t *bytes) {
     if (!bytes) return SVPA_ERR_INVALID_ARG;
     AttnPlan pl;
-    const svpa_status s = plan_attn(p, &pl);
+    const svpa_status s = plan_attn(p, &pl, ticket_bytes);
     if (s != SVPA_OK) return s;
     *bytes = pl.bytes;
     return SVPA_OK;
 }
 
-svpa_status svpa_paged_verify_attn(const svpa_attn_params *p, const void *q, const void *k_pool,
-                                   const void *v_pool, const float *k_scale, const float *v_scale,
-                                   const int32_t *block_table, const int32_t *context_lens,
-                                   const uint64_t *ancestor_mask, void *out, float *lse, void *workspace,
-                                   size_t workspace_bytes, int32_t *error_flag, void *stream) {
-    svpa::NvtxRange nvtx_range("svpa_paged_verify_attn");
+svpa_status verify_attn(const svpa_attn_params *p, const void *q, const void *k_pool, const void *v_pool,
+                        const float *k_scale, const float *v_scale, const int32_t *block_table,
+                        const int32_t *context_lens, const uint64_t *ancestor_mask, void *out, float *lse,
+                        void *workspace, size_t workspace_bytes, size_t ticket_bytes, int32_t *error_flag,
+                        void *stream) {
     AttnPlan pl;
-    svpa_status s = plan_attn(p, &pl);
+    svpa_status s = plan_attn(p, &pl, ticket_bytes);
     if (s != SVPA_OK) return s;
     if (p->batch == 0) return SVPA_OK;
-    s = svpa::check_attn_call(p, q, k_pool, v_pool, k_scale, v_scale, block_table, context_lens, ancestor_mask,
-                              out, error_flag);
+    s = check_attn_call(p, q, k_pool, v_pool, k_scale, v_scale, block_table, context_lens, ancestor_mask, out,
+                        error_flag);
     if (s != SVPA_OK) return s;
     const bool fp8 = p->kv_dtype == SVPA_KV_FP8_E4M3;
     if (!workspace || workspace_bytes < pl.bytes || !aligned16(workspace)) return SVPA_ERR_WORKSPACE;
@@ -342,7 +303,7 @@ svpa_status svpa_paged_verify_attn(const svpa_attn_params *p, const void *q, con
     a.lse = lse;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     a.sched = reinterpret_cast<int32_t *>(ws);
-    a.tickets = reinterpret_cast<int32_t *>(ws + kAlign);
+    a.tickets = reinterpret_cast<int32_t *>(ws + kWorkspaceCounterBytes);
     a.order = pl.ordered ? reinterpret_cast<const int32_t *>(ws + pl.off_order) : nullptr;
     a.part_ml = reinterpret_cast<float *>(ws + pl.off_ml);
     a.part_acc = reinterpret_cast<float *>(ws + pl.off_acc);
@@ -362,6 +323,11 @@ svpa_status svpa_paged_verify_attn(const svpa_attn_params *p, const void *q, con
     for (int j = 0; j < p->n_q; ++j)
         a.anc[j] = ancestor_mask ? ancestor_mask[j] : ((j == 63) ? ~0ull : ((1ull << (j + 1)) - 1ull));
     a.total_units = p->batch * p->num_kv_heads * pl.max_splits;
+    const size_t tickets = (size_t)p->batch * p->num_kv_heads * sizeof(int32_t);
+    if ((pl.max_splits > 1 || pl.streamk) && ticket_bytes > 0 && tickets > ticket_bytes) {
+        const cudaError_t e = cudaMemsetAsync(a.tickets, 0, tickets, static_cast<cudaStream_t>(stream));
+        if (e != cudaSuccess) return from_cuda(e);
+    }
     if (pl.ordered) {
         cudaError_t e = launch_seq_order(context_lens, p->batch, reinterpret_cast<int32_t *>(ws + pl.off_order),
                                          static_cast<cudaStream_t>(stream));
@@ -387,6 +353,58 @@ svpa_status svpa_paged_verify_attn(const svpa_attn_params *p, const void *q, con
     a.n_stages = lp.n_stages;
     const int grid = std::max(1, std::min(lp.ctas_per_sm * sm_count(), a.total_units));
     return from_cuda(launch_paged_verify_attn(maps, a, D, fp8, grid, lp.smem, static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace svpa
+
+extern "C" {
+
+const char *svpa_status_string(svpa_status s) {
+    switch (s) {
+        case SVPA_OK: return "ok";
+        case SVPA_ERR_INVALID_ARG: return "invalid argument";
+        case SVPA_ERR_UNSUPPORTED: return "unsupported configuration";
+        case SVPA_ERR_CUDA: return "CUDA error";
+        case SVPA_ERR_OUT_OF_BLOCKS: return "free block stack overflow";
+        case SVPA_ERR_BAD_BLOCK: return "block id outside the pool";
+        case SVPA_ERR_WORKSPACE: return "workspace missing or too small";
+        case SVPA_ERR_TIMEOUT: return "device wait timed out";
+    }
+    return "unknown status";
+}
+
+int32_t svpa_version(void) { return 100; }
+
+svpa_status svpa_attn_kernel(const svpa_attn_params *p, int32_t *kernel) {
+    if (!kernel) return SVPA_ERR_INVALID_ARG;
+    AttnPlan pl;
+    const svpa_status s = plan_attn(p, &pl);
+    if (s != SVPA_OK) return s;
+    *kernel = pl.use_tc ? 2 : 1;
+    return SVPA_OK;
+}
+
+svpa_status svpa_attn_launches(const svpa_attn_params *p, int32_t *launches) {
+    if (!launches) return SVPA_ERR_INVALID_ARG;
+    AttnPlan pl;
+    const svpa_status s = plan_attn(p, &pl);
+    if (s != SVPA_OK) return s;
+    *launches = p->batch == 0 ? 0 : (pl.ordered || pl.streamk ? 2 : 1);
+    return SVPA_OK;
+}
+
+svpa_status svpa_attn_workspace_size(const svpa_attn_params *p, size_t *bytes) {
+    return svpa::attn_workspace_bytes(p, kTicketBytes, bytes);
+}
+
+svpa_status svpa_paged_verify_attn(const svpa_attn_params *p, const void *q, const void *k_pool,
+                                   const void *v_pool, const float *k_scale, const float *v_scale,
+                                   const int32_t *block_table, const int32_t *context_lens,
+                                   const uint64_t *ancestor_mask, void *out, float *lse, void *workspace,
+                                   size_t workspace_bytes, int32_t *error_flag, void *stream) {
+    svpa::NvtxRange nvtx_range("svpa_paged_verify_attn");
+    return svpa::verify_attn(p, q, k_pool, v_pool, k_scale, v_scale, block_table, context_lens, ancestor_mask, out,
+                             lse, workspace, workspace_bytes, kTicketBytes, error_flag, stream);
 }
 
 svpa_status svpa_check_error(const int32_t *error_flag, void *stream) {

@@ -54,6 +54,15 @@ constexpr int kBlockSize = 16;   // tokens per page
 constexpr int kMaxNq = 64;       // queries per sequence (one 64-bit mask row each)
 constexpr int kMaxRows = 128;    // GQA group size x queries handled by one CTA
 
+// The head of every attention call's workspace: counters, then the tickets of
+// split units ([B * Hkv], used by the verification kernels).  Nothing else is
+// ever written there and every completed call leaves both at zero, so that one
+// buffer may serve calls of any kind, batch, draft length and prefix in turn.
+// A batch with more tickets clears them itself (the rest of its array lies
+// where other calls keep partial results).
+constexpr size_t kWorkspaceCounterBytes = 256;
+constexpr size_t kTicketBytes = 64 << 10;  // 16384 (sequence, kv head) pairs
+
 // Arguments of the paged verification attention kernel (passed by value).
 struct AttnArgs {
     const __nv_bfloat16 *q;
@@ -105,6 +114,16 @@ svpa_status check_attn_call(const svpa_attn_params *p, const void *q, const void
                             const float *k_scale, const float *v_scale, const int32_t *block_table,
                             const int32_t *context_lens, const uint64_t *ancestor_mask, const void *out,
                             const int32_t *error_flag);
+
+// svpa_attn_workspace_size and svpa_paged_verify_attn with `ticket_bytes` kept
+// for tickets (kTicketBytes; 0: the workspace's tickets are known to be zero,
+// and the rest follows them at once).
+svpa_status attn_workspace_bytes(const svpa_attn_params *p, size_t ticket_bytes, size_t *bytes);
+svpa_status verify_attn(const svpa_attn_params *p, const void *q, const void *k_pool, const void *v_pool,
+                        const float *k_scale, const float *v_scale, const int32_t *block_table,
+                        const int32_t *context_lens, const uint64_t *ancestor_mask, void *out, float *lse,
+                        void *workspace, size_t workspace_bytes, size_t ticket_bytes, int32_t *error_flag,
+                        void *stream);
 
 // Launch the attention kernel matching (head_dim, fp8, row tiles).
 cudaError_t launch_paged_verify_attn(const AttnMaps &maps, const AttnArgs &a, int head_dim,

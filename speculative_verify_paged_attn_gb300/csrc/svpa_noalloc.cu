@@ -63,7 +63,7 @@ svpa_status svpa_paged_verify_attn_noalloc(const svpa_attn_params *p, const void
                                            int32_t *error_flag, void *stream) {
     svpa::NvtxRange nvtx_range("svpa_paged_verify_attn_noalloc");
     size_t need = 0;
-    svpa_status s = svpa_attn_workspace_size(p, &need);
+    svpa_status s = svpa::attn_workspace_bytes(p, 0, &need);
     if (s != SVPA_OK) return s;
     if (need > kScratchBytes) return SVPA_ERR_WORKSPACE;  // the shape needs more than the fixed array
     if (p->batch == 0) return SVPA_OK;
@@ -82,8 +82,8 @@ svpa_status svpa_paged_verify_attn_noalloc(const svpa_attn_params *p, const void
     const size_t head = 256 + tickets;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (cudaMemsetAsync(ws, 0, head < need ? head : need, st) != cudaSuccess) return SVPA_ERR_CUDA;
-    return svpa_paged_verify_attn(p, q, k_pool, v_pool, k_scale, v_scale, block_table, context_lens,
-                                  ancestor_mask, out, lse, ws, kScratchBytes, error_flag, stream);
+    return svpa::verify_attn(p, q, k_pool, v_pool, k_scale, v_scale, block_table, context_lens, ancestor_mask, out, lse,
+                             ws, kScratchBytes, 0, error_flag, stream);
 }
 
 }  // extern "C"

@@ -91,15 +91,16 @@ struct Plan {
     size_t off_member, off_ml, off_o, bytes;
 };
 
-// Workspace: [counters][member or order][partial (max, sum)][partial outputs], one
-// partial slot for each KV split of the prefix units and, when split, of the others.
+// Workspace: [counters][tickets of the verification kernels, never written here]
+// [member or order][partial (max, sum)][partial outputs], one partial slot for
+// each KV split of the prefix units and, when split, of the others.
 svpa_status layout(Plan *pl, long long units, long long T, int Hkv, int D, int members) {
     if (units > 0x7fffffff) return SVPA_ERR_UNSUPPORTED;
     pl->total_units = (int)units;
     const size_t slots = (size_t)pl->p_splits + (pl->s_splits > 1 ? pl->s_splits : 0);
     pl->tiles = (int)ceil_div(T, pl->tpt);
     const size_t rows = (size_t)Hkv * pl->tiles * kMaxRows;
-    pl->off_member = kAlign;
+    pl->off_member = kWorkspaceCounterBytes + kTicketBytes;
     pl->off_ml = pl->off_member + align_up((size_t)members * sizeof(int32_t));
     pl->off_o = pl->off_ml + align_up(slots * rows * sizeof(float2));
     pl->bytes = pl->off_o + align_up(slots * rows * D * sizeof(float));

@@ -119,3 +119,24 @@ def test_prefix_call_arguments(lib):
     assert run(good, mask=ctypes.cast(blind, ctypes.c_void_p)) == 1
     p0 = svpa.attn_params(0, 5, 8, 2, 128, 60, 70)
     assert call(ctypes.byref(p0), None, None, None, None, 0, None, None, None, None, None, None, 0, None, None) == 0
+
+
+def test_workspaces_keep_room_for_tickets(lib):
+    """Counters and 64 KB of tickets head every attention workspace; the
+    allocation-free call, whose array is its own, takes what it took without them."""
+    from speculative_verify_paged_attn_gb300 import svpa
+    head = 256 + (64 << 10)
+    assert svpa.attn_workspace_size(svpa.attn_params(1, 1, 8, 8, 128, 4, 16)) >= head
+    assert svpa.paged_prompt_attn_workspace_size(svpa.prompt_params(**PROMPT)) >= head
+    for prefix in (0, 512):
+        assert svpa.prefix_verify_attn_workspace_size(svpa.attn_params(3, 5, 8, 2, 128, 60, 70), prefix) >= head
+
+    def needs(b):  # 2 heads, 25 splits of 20 rows: partials behind the head
+        return svpa.attn_workspace_size(svpa.attn_params(b, 5, 8, 2, 128, 500, 16, split_pages=20)) - head
+
+    # the largest batch that 32 MiB hold with 8 bytes of tickets a sequence in the head's place
+    batch = max(b for b in range(1, 200) if needs(b) + 256 + (b * 8 + 255) // 256 * 256 <= 32 << 20)
+    for b, status in ((batch, 1), (batch + 1, 6)):  # null arrays, or too large
+        p = svpa.attn_params(b, 5, 8, 2, 128, 500, 16, split_pages=20)
+        assert svpa.paged_verify_attn_noalloc(p, None, None, None, None, None, None, error_flag=None, stream=0,
+                                              check=False) == status, b
