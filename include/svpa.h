@@ -349,8 +349,9 @@ svpa_status svpa_paged_prompt_attn_workspace_size(const svpa_prompt_params *p, s
  *  out          bf16 [T, Hq, D] (written); rows from cu_seqlens[B] on are left
  *               as they were
  *  lse          fp32 [T, Hq] natural-log sum of exp(scores), or NULL
- * A sequence with bad offsets or a bad length raises SVPA_DEVERR_BAD_VALUE, a
- * block id outside the pool SVPA_DEVERR_BAD_BLOCK.  Scores and sums are fp32;
+ * Offsets that do not start at 0, that fall or that pass T, and a bad length of
+ * a sequence with query tokens raise SVPA_DEVERR_BAD_VALUE, a block id outside
+ * the pool SVPA_DEVERR_BAD_BLOCK.  Scores and sums are fp32;
  * the weights of a row are rounded to bf16 for their product with V.  K/V
  * values of every position below kv_lens[b] must be finite (the weight of a
  * position that a token does not see is an exact zero).

@@ -642,13 +642,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         c1 = __ldg(a.cu + b + 1);
                         kv = __ldg(a.lens + b);
                     }
-                    const int t0 = c0 + (slot - (c0 / tpt2 + b)) * tpt2;
-                    if (t0 >= c1) {
-                        // no tile here; a bad row of offsets is reported with its first slot
-                        if (lane == 0 && (c0 < 0 || c1 < c0 || c1 > a.T)) raise_error(a.err, SVPA_DEVERR_BAD_VALUE);
+                    if (c0 < 0 || c1 < c0 || c1 > a.T) {
+                        if (lane == 0) raise_error(a.err, SVPA_DEVERR_BAD_VALUE);
                         continue;
                     }
-                    if (c0 < 0 || c1 > a.T || t0 < c0 || kv < c1 - c0 || kv > (long long)a.max_blocks * kBlockSize) {
+                    const int t0 = c0 + (slot - (c0 / tpt2 + b)) * tpt2;
+                    if (t0 >= c1) continue;  // no tile here
+                    if (t0 < c0 || kv < c1 - c0 || kv > (long long)a.max_blocks * kBlockSize) {
                         if (lane == 0) raise_error(a.err, SVPA_DEVERR_BAD_VALUE);
                         continue;
                     }
@@ -686,6 +686,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return true;
             }
         };
+            // A prompt's offsets, a share for each CTA: decoding sees a sequence only
+            // in the slots that it finds, and one whose offsets fall may own none.
+            auto check_offsets = [&]() {
+                const int per = (a.B + (int)gridDim.x - 1) / (int)gridDim.x;
+                const int b0 = (int)blockIdx.x * per, b1 = min(b0 + per, a.B);
+                bool bad = blockIdx.x == 0 && __ldg(a.cu) != 0;
+                for (int b = b0 + lane; b < b1; b += 32) {
+                    const int end = __ldg(a.cu + b + 1);
+                    bad = bad || end < __ldg(a.cu + b) || end > a.T;
+                }
+                if (bad) raise_error(a.err, SVPA_DEVERR_BAD_VALUE);
+                __syncwarp();
+            };
             int prefixes = 0, reported = 0;  // prefix units handed on, and counted
             auto report = [&]() {
                 if (reported >= prefixes) return;
@@ -723,6 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 sm.job_ids[lane] = ids;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.job_full);
+                if (jobs == 0 && !a.verify) check_offsets();
                 if (!more) break;
                 prefixes += d.w.prefix;
                 // the producer has this one and is near its end

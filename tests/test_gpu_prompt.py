@@ -231,3 +231,30 @@ def test_bad_block_raises():
     c.err.zero_()
     c.call()
     c.check()
+
+
+@pytest.mark.parametrize("new,cached,hq,hkv,cu", [
+    # the falling row owns no tile: 0 -> 1000 -> 500 -> 1200 with 256 tokens a unit
+    ([1000, 500, 700], [0, 0, 0], 2, 2, {1: 1000, 2: 500, 3: 1200}),
+    # every length fits its (wrong) row
+    ([600, 300, 600], [0, 0, 0], 8, 1, {1: 600, 2: 300, 3: 900}),
+    # rows before the first sequence
+    ([40, 20], [0, 0], 2, 2, {0: 5}),
+    ([40, 20], [0, 0], 2, 2, {0: -5}),
+    # more sequences than one round of loads finds
+    ([300] * 50, [3000 if b == 20 else 0 for b in range(50)], 16, 2, {20: 3100}),
+    ([300] * 50, [0] * 50, 16, 2, {49: -2 ** 31}),
+    ([3] * 700, [0] * 700, 2, 2, {650: 40}),
+])
+def test_offsets_that_fall_or_start_late_raise(new, cached, hq, hkv, cu):
+    c = Case(new, cached, hq, hkv, 64)
+    keep = c.cu.clone()
+    for i, v in cu.items():
+        c.cu[i] = v
+    c.call()
+    assert svpa.STATUS[svpa.check_error(c.err)] == "SVPA_ERR_INVALID_ARG"
+    c.cu.copy_(keep)
+    c.err.zero_()
+    c.out.fill_(77.0)
+    c.call()
+    c.check()
