@@ -119,3 +119,70 @@ def test_a_bias_for_every_token():
     c.offsets = torch.tensor([0, 2 * c.v, 2 * c.v + 1], dtype=torch.int32, device=DEV)
     c.call()
     c.check()
+
+
+TREE = W.tree_parents((3, 2))
+
+# the batch of each slab's smallest call, to the sequence, and odd vocabularies
+@pytest.mark.parametrize("kw", [
+    dict(b=25, rows=3, v=50257), dict(b=25, rows=3, v=50257, bf16=True), dict(b=24, rows=3, v=50257),
+    dict(b=75, rows=2, v=50257, bf16=True), dict(b=75, rows=3, v=50257), dict(b=74, rows=2, v=50257),
+    dict(b=10, rows=4, v=128256), dict(b=30, rows=3, v=128256, bf16=True), dict(b=30, rows=2, v=128255),
+    dict(b=30, rows=len(TREE), v=128256, parent=TREE), dict(b=75, rows=len(TREE), v=50257, parent=TREE, bf16=True),
+    dict(b=75, rows=1, v=50257), dict(b=30, rows=3, v=128256, masked=False, biases=0),
+    dict(b=75, rows=2, v=50257, hist=5001), dict(b=30, rows=2, v=128256, hist=9000, bf16=True),
+    dict(b=10, rows=2, v=128256, hist=4096), dict(b=25, rows=2, v=50257, hist=8191), dict(b=2, rows=3, v=32000, hist=6001),
+    dict(b=3, rows=2, v=50257, hist=2048), dict(b=25, rows=64, v=50257, hist=30),
+], ids=lambda k: "-".join(str(k[x]) for x in ("b", "rows", "v")) + ("-bf16" if k.get("bf16") else ""))
+def test_full_batches_against_64_bits(kw):
+    c = Case(**kw)
+    c.call()
+    c.check()
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("b,v", [(25, 50257), (75, 50257), (30, 128256)])
+def test_full_batches_off_every_vector_boundary(b, v, bf16):
+    c = Case(b, 2, v, bf16=bf16, hist=700)
+    wide = torch.zeros(c.x.numel() + 1, dtype=c.x.dtype, device=DEV)
+    wide[1:] = c.x.reshape(-1)
+    c.x = wide[1:].view(c.x.shape)
+    out = torch.full((c.out.numel() + 1,), 5.0, device=DEV)
+    c.call(out=out[1:].view(c.out.shape))
+    c.check(out[1:].view(c.out.shape))
+    assert float(out[0]) == 5.0
+
+
+@pytest.mark.parametrize("b,v", [(25, 50257), (30, 128256)])
+def test_full_batches_in_place(b, v):
+    c = Case(b, 3, v, hist=5000)
+    keep = c.x.clone()
+    c.call(out=c.x)
+    got, c.x = c.x, keep
+    c.check(got)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("b,v", [(2, 5000), (25, 50257), (30, 128256)])
+def test_special_logits_of_marked_tokens(b, v, bf16):
+    """NaN and infinities among prompt, generated, drafted and biased tokens, in
+    allowed and masked places."""
+    c = Case(b, 4, v, bf16=bf16, hist=400, biases=400, span=3000)
+    low = c.x[:, :, :3000]
+    pick = torch.arange(3000, device=DEV) % 7
+    for k, value in enumerate((math.nan, math.inf, -math.inf)):
+        low[:, :, pick == k] = value
+    c.call()
+    c.check()
+
+
+def test_the_same_bits_every_time():
+    """Marks are listed in any order and counted by atomics: the result is the same."""
+    c = Case(30, 3, 128256, hist=9000, biases=300, span=4096, bf16=True)
+    c.call()
+    c.check()
+    first = c.out.clone()
+    for _ in range(4):
+        c.out.zero_()
+        c.call()
+        assert torch.equal(c.out, first)

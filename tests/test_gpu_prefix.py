@@ -238,3 +238,16 @@ def test_two_calls_at_once_with_their_own_workspaces():
     for c, w in zip(cases, want):
         c.check()
         assert torch.equal(c.out, w)
+
+
+@pytest.mark.parametrize("own,prefix,n_q,hq,hkv", [
+    ([100, 17, 260, 1], 800, 6, 16, 2), ([70, 20, 0], 16, 4, 4, 2), ([33, 12] * 20, 480, 5, 8, 4),
+])
+def test_outputs_on_a_16_byte_boundary(own, prefix, n_q, hq, hkv):
+    """Results stored in pieces of 16 bytes, not of 32."""
+    c = Case(own, prefix, n_q, hq, hkv, 128)
+    wide = torch.full((c.out.numel() + 16,), 5.0, dtype=torch.bfloat16, device=DEV)
+    c.out = wide[8:-8].view(c.out.shape)
+    c.call()
+    c.check()
+    assert bool((wide[:8] == 5.0).all()) and bool((wide[-8:] == 5.0).all())

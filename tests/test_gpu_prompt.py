@@ -258,3 +258,16 @@ def test_offsets_that_fall_or_start_late_raise(new, cached, hq, hkv, cu):
     c.out.fill_(77.0)
     c.call()
     c.check()
+
+
+@pytest.mark.parametrize("new,cached,hq,hkv,d", [
+    ([300, 1, 0, 5, 700], [0, 0, 0, 0, 0], 4, 4, 128), ([64, 1, 130], [100, 129, 1], 4, 1, 64), ([20], [5000], 8, 2, 128),
+])
+def test_outputs_on_a_16_byte_boundary(new, cached, hq, hkv, d):
+    """Results stored in pieces of 16 bytes, not of 32."""
+    c = Case(new, cached, hq, hkv, d, pad=2)
+    wide = torch.full((c.out.numel() + 16,), 77.0, dtype=torch.bfloat16, device=DEV)
+    c.out = wide[8:-8].view(c.out.shape)
+    c.call()
+    c.check()
+    assert bool((wide[:8] == 77.0).all()) and bool((wide[-8:] == 77.0).all())
