@@ -65,6 +65,8 @@ class LogitsParams(ctypes.Structure):
                 ("max_history", ctypes.c_int32), ("logits_dtype", ctypes.c_int32)]
 
 
+_BF16, _F32, _I32, _U32 = torch.bfloat16, torch.float32, torch.int32, torch.uint32
+
 _lib = None
 
 
@@ -114,6 +116,15 @@ def load(path: str = LIB_PATH):
 
 def _p(t) -> Optional[int]:
     return None if t is None else t.data_ptr()
+
+
+def _arr(t, dtype, n: int, what: str) -> Optional[int]:
+    """The pointer of a contiguous array of at least n values of dtype, or of None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.numel() < n or not t.is_contiguous():
+        raise SvpaError(1, f"{what}: {n} contiguous values of {dtype} expected, not {tuple(t.shape)} of {t.dtype}")
+    return t.data_ptr()
 
 
 def _stream(stream) -> Optional[int]:
@@ -205,6 +216,11 @@ def paged_verify_attn_noalloc(params: AttnParams, q, k_pool, v_pool, block_table
     return st
 
 
+def _pool_type(params, pool):
+    """bf16, or for FP8 pages (which the packed attention calls refuse) the pool's own type."""
+    return _BF16 if params.kv_dtype == SVPA_KV_BF16 else pool.dtype
+
+
 def prompt_params(batch, total_q, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, num_blocks, *,
                   sm_scale=None, q_stride=0, block_size=16, kv_fp8=False) -> PromptParams:
     """q_stride: elements from one token of q to the next (q.stride(0)); 0 = contiguous."""
@@ -224,12 +240,19 @@ def paged_prompt_attn(params: PromptParams, q, k_pool, v_pool, block_table, cu_s
                       workspace, error_flag, lse=None, stream=None, check=True) -> int:
     """svpa_paged_prompt_attn: causal attention of packed prompts (or chunks) over
     their pages; q [T, Hq, D], its tokens params.q_stride elements apart."""
-    if q.shape[0] > 1 and _row_stride(q, "q") != (params.q_stride or params.num_q_heads * params.head_dim):
+    b, rows, d = params.batch, params.total_q * params.num_q_heads, params.head_dim
+    if q.dtype is not _BF16 or q.dim() != 3 or q.shape[0] < params.total_q or \
+            q.shape[1] != params.num_q_heads or q.shape[2] != d:
+        raise SvpaError(1, "q: bf16 [total_q, num_q_heads, head_dim] expected")
+    if _row_stride(q, "q") != (params.q_stride or params.num_q_heads * d) and q.shape[0] > 1:
         raise SvpaError(1, "q: its tokens are not q_stride elements apart")
+    page, pool = params.num_blocks * params.num_kv_heads * params.block_size * d, _pool_type(params, k_pool)
     st = load().svpa_paged_prompt_attn(
-        ctypes.byref(params), _p(q), _p(k_pool), _p(v_pool), _p(block_table), _p(cu_seqlens), _p(kv_lens),
-        _p(out), _p(lse), _p(workspace), workspace.numel() * workspace.element_size(), _p(error_flag),
-        _stream(stream))
+        ctypes.byref(params), _p(q), _arr(k_pool, pool, page, "k_pool"), _arr(v_pool, pool, page, "v_pool"),
+        _arr(block_table, _I32, b * params.max_blocks_per_seq, "block_table"),
+        _arr(cu_seqlens, _I32, b + 1, "cu_seqlens"), _arr(kv_lens, _I32, b, "kv_lens"),
+        _arr(out, _BF16, rows * d, "out"), _arr(lse, _F32, rows, "lse"), _p(workspace),
+        workspace.numel() * workspace.element_size(), _arr(error_flag, _I32, 1, "error_flag"), _stream(stream))
     if check:
         _check(st, "svpa_paged_prompt_attn")
     return st
@@ -247,11 +270,21 @@ def prefix_verify_attn(params: AttnParams, q, k_pool, v_pool, prefix_blocks, blo
     """svpa_prefix_verify_attn: paged_verify_attn with the attention over the
     blocks of prefix_blocks (int32, or None) formed once for all sequences."""
     m = _mask_array(ancestor_mask)
+    if m is not None and len(m) < params.n_q:
+        raise SvpaError(1, "svpa_prefix_verify_attn: one ancestor mask per query")
+    b, d = params.batch, params.head_dim
+    rows = b * params.n_q * params.num_q_heads
+    page, pool = params.num_blocks * params.num_kv_heads * params.block_size * d, _pool_type(params, k_pool)
     st = load().svpa_prefix_verify_attn(
-        ctypes.byref(params), _p(q), _p(k_pool), _p(v_pool), _p(prefix_blocks),
-        0 if prefix_blocks is None else prefix_blocks.shape[0] * params.block_size, _p(block_table),
-        _p(context_lens), None if m is None else ctypes.cast(m, ctypes.c_void_p), _p(out), _p(lse), _p(workspace),
-        workspace.numel() * workspace.element_size(), _p(error_flag), _stream(stream))
+        ctypes.byref(params), _arr(q, _BF16, rows * d, "q"), _arr(k_pool, pool, page, "k_pool"),
+        _arr(v_pool, pool, page, "v_pool"),
+        _arr(prefix_blocks, _I32, 0, "prefix_blocks"),
+        0 if prefix_blocks is None else prefix_blocks.shape[0] * params.block_size,
+        _arr(block_table, _I32, b * params.max_blocks_per_seq, "block_table"),
+        _arr(context_lens, _I32, b, "context_lens"),
+        None if m is None else ctypes.cast(m, ctypes.c_void_p),
+        _arr(out, _BF16, rows * d, "out"), _arr(lse, _F32, rows, "lse"), _p(workspace),
+        workspace.numel() * workspace.element_size(), _arr(error_flag, _I32, 1, "error_flag"), _stream(stream))
     if check:
         _check(st, "svpa_prefix_verify_attn")
     return st
@@ -374,11 +407,14 @@ def block_table_build(seq_lens, block_table, cu_seqlens, slot_map, refcount, fre
     slots of the new tokens of requests with seq_lens [B] tokens, the first of
     them in the shared blocks of prefix_blocks (int32, or None)."""
     B, max_blocks = block_table.shape
+    blocks = refcount.shape[0]
     st = load().svpa_block_table_build(
-        B, 16, max_blocks, refcount.shape[0], slot_map.shape[0], _p(seq_lens), _p(prefix_blocks),
-        0 if prefix_blocks is None else prefix_blocks.shape[0] * 16, _p(block_table), _p(cu_seqlens), _p(slot_map),
-        _p(refcount), _p(free_stack), _p(free_top), _p(workspace), workspace.numel() * workspace.element_size(),
-        _p(error_flag), _stream(stream))
+        B, 16, max_blocks, blocks, slot_map.shape[0], _arr(seq_lens, _I32, B, "seq_lens"),
+        _arr(prefix_blocks, _I32, 0, "prefix_blocks"), 0 if prefix_blocks is None else prefix_blocks.shape[0] * 16,
+        _arr(block_table, _I32, 0, "block_table"), _arr(cu_seqlens, _I32, B + 1, "cu_seqlens"),
+        _arr(slot_map, _I32, 0, "slot_map"), _arr(refcount, _I32, 0, "refcount"),
+        _arr(free_stack, _I32, blocks, "free_stack"), _arr(free_top, _I32, 1, "free_top"), _p(workspace),
+        workspace.numel() * workspace.element_size(), _arr(error_flag, _I32, 1, "error_flag"), _stream(stream))
     if check:
         _check(st, "svpa_block_table_build")
     return st
@@ -397,10 +433,17 @@ def kv_write(new_k, new_v, slot_map, k_pool, v_pool, *, error_flag, k_scale=None
     along the heads are taken as they are) to the slots of slot_map [T]; the
     pools are bf16 or float8_e4m3fn/uint8 [num_blocks, Hkv, 16, D]."""
     T, Hkv, D = new_k.shape
+    blocks, fp8 = k_pool.shape[0], k_pool.element_size() == 1
+    if new_k.dtype is not _BF16 or new_v.dtype is not _BF16 or new_v.shape != new_k.shape:
+        raise SvpaError(1, "new_k, new_v: bf16 rows of one shape expected")
+    page, scales = blocks * Hkv * 16 * D, blocks * Hkv * 16 * (D // 64) if fp8 else 0
+    pool = k_pool.dtype if fp8 else _BF16
     st = load().svpa_kv_write(
-        T, Hkv, D, 16, k_pool.shape[0], SVPA_KV_FP8_E4M3 if k_pool.element_size() == 1 else SVPA_KV_BF16, scale_tile,
-        _p(new_k), _p(new_v), _row_stride(new_k, "new_k"), _row_stride(new_v, "new_v"), _p(slot_map), _p(k_pool),
-        _p(v_pool), _p(k_scale), _p(v_scale), _p(error_flag), _stream(stream))
+        T, Hkv, D, 16, blocks, SVPA_KV_FP8_E4M3 if fp8 else SVPA_KV_BF16, scale_tile, _p(new_k), _p(new_v),
+        _row_stride(new_k, "new_k"), _row_stride(new_v, "new_v"), _arr(slot_map, _I32, T, "slot_map"),
+        _arr(k_pool, pool, page, "k_pool"), _arr(v_pool, pool, page, "v_pool"),
+        _arr(k_scale, _F32, scales, "k_scale"), _arr(v_scale, _F32, scales, "v_scale"),
+        _arr(error_flag, _I32, 1, "error_flag"), _stream(stream))
     if check:
         _check(st, "svpa_kv_write")
     return st
@@ -410,21 +453,26 @@ def logits_process(logits, out, *, error_flag, history=None, prompt_lens=None, h
                    parent: Optional[Sequence[int]] = None, repetition=None, presence=None, frequency=None,
                    bias_offsets=None, bias_tokens=None, bias_values=None, mask=None, stream=None, check=True) -> int:
     """svpa_logits_process: penalties, biases and grammar masks on logits [B,
-    rows, V] (fp32 or bf16) into out (fp32, may be logits); parent: host
-    sequence of the draft tree (parent[0] = -1) or None for a chain."""
+    rows, V] (fp32 or bf16, contiguous) into out (fp32, may be logits); parent:
+    host sequence of the draft tree (parent[0] = -1) or None for a chain."""
     B, rows, V = logits.shape
-    p = LogitsParams(B, rows, V, 0 if history is None else history.shape[1],
-                     SVPA_LOGITS_BF16 if logits.element_size() == 2 else SVPA_LOGITS_FP32)
+    bf16, hist = logits.dtype is _BF16, 0 if history is None else history.shape[1]
+    p = LogitsParams(B, rows, V, hist, SVPA_LOGITS_BF16 if bf16 else SVPA_LOGITS_FP32)
     arr = None
     if parent is not None:
         par = [int(x) for x in (parent.tolist() if hasattr(parent, "tolist") else parent)]
         if len(par) != rows:
             raise SvpaError(1, "svpa_logits_process: one parent per row")
         arr = (ctypes.c_int32 * rows)(*par)
+    # (the arrays of one value a sequence are taken as they are)
     st = load().svpa_logits_process(
-        ctypes.byref(p), _p(logits), _p(history), _p(prompt_lens), _p(hist_lens), _p(draft_tokens),
+        ctypes.byref(p), _arr(logits, _BF16 if bf16 else _F32, 0, "logits"),
+        _arr(history, _I32, B * hist, "history"), _p(prompt_lens), _p(hist_lens),
+        _arr(draft_tokens, _I32, B * (rows - 1 if arr is None else rows), "draft_tokens"),
         None if arr is None else ctypes.cast(arr, ctypes.c_void_p), _p(repetition), _p(presence), _p(frequency),
-        _p(bias_offsets), _p(bias_tokens), _p(bias_values), _p(mask), _p(out), _p(error_flag), _stream(stream))
+        _p(bias_offsets), _p(bias_tokens), _p(bias_values),
+        None if mask is None else _arr(mask, _U32 if mask.dtype is _U32 else _I32, B * rows * ((V + 31) // 32), "mask"),
+        _arr(out, _F32, B * rows * V, "out"), _p(error_flag), _stream(stream))
     if check:
         _check(st, "svpa_logits_process")
     return st
