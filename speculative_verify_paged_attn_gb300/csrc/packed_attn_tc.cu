@@ -107,7 +107,7 @@ struct Smem {
     Job job;
     int32_t job_ids[32];
     Unit unit;
-    int32_t written;  // softmax warps that wrote a prefix unit's partials
+    int32_t written[2];  // each group's warps that wrote a prefix unit's partials
     float2 stat[2][128];
     uint32_t tmem_base;
 };
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sm.empty[i], 2);  // the two MMA issuers
         }
         mbar_init(&sm.both, 8);
-        sm.written = 0;
+        sm.written[0] = sm.written[1] = 0;
         mbar_init(&sm.job_full, 1);
         mbar_init(&sm.job_want, 1);
         mbar_init(&sm.prefix_done, 1);
@@ -701,9 +701,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             int prefixes = 0, reported = 0;  // prefix units handed on, and counted
             auto report = [&]() {
+                // A unit is written when both groups have written it, four warps
+                // each.  Counted together, one group's next unit could stand for
+                // the other's; a group's own warps cannot be a unit apart (each
+                // block's P is all four's, and each prefix unit has a block).
                 if (reported >= prefixes) return;
-                const int n = *reinterpret_cast<volatile int *>(&sm.written);
-                if (__shfl_sync(0xffffffffu, n, 0) < 8 * (reported + 1)) return;
+                const volatile int32_t *w = sm.written;
+                const int n = min(w[0], w[1]);
+                if (__shfl_sync(0xffffffffu, n, 0) < 4 * (reported + 1)) return;
                 if (lane == 0) {
                     __threadfence();
                     atomicAdd(a.sched + 2, 1);
@@ -1027,7 +1032,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) {
                     __threadfence_block();
-                    atomicAdd(&sm.written, 1);
+                    atomicAdd(&sm.written[t], 1);
                 }
             }
         }
