@@ -95,7 +95,8 @@ struct Plan {
 // [member or order][partial (max, sum)][partial outputs], one partial slot for
 // each KV split of the prefix units and, when split, of the others.
 svpa_status layout(Plan *pl, long long units, long long T, int Hkv, int D, int members) {
-    if (units > 0x7fffffff) return SVPA_ERR_UNSUPPORTED;
+    // the kernels' counter runs up to a CTA count past the last unit
+    if (units > 0x7fffffff - 65536) return SVPA_ERR_UNSUPPORTED;
     pl->total_units = (int)units;
     const size_t slots = (size_t)pl->p_splits + (pl->s_splits > 1 ? pl->s_splits : 0);
     pl->tiles = (int)ceil_div(T, pl->tpt);

@@ -140,3 +140,11 @@ def test_workspaces_keep_room_for_tickets(lib):
         p = svpa.attn_params(b, 5, 8, 2, 128, 500, 16, split_pages=20)
         assert svpa.paged_verify_attn_noalloc(p, None, None, None, None, None, None, error_flag=None, stream=0,
                                               check=False) == status, b
+
+
+def test_units_leave_room_for_the_counter(lib):
+    # 1038435 sequences of 2068 kv heads: 67 units below 2^31, and the kernel's
+    # counter goes up to one for each CTA past the last unit
+    heads = dict(total_q=1, num_q_heads=2068, num_kv_heads=2068, head_dim=64, num_blocks=5)
+    assert prompt_status(lib, batch=1038435, **heads) == 2
+    assert prompt_status(lib, batch=1038435 - 64, **heads) == 0
