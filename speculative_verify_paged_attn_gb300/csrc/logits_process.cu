@@ -79,9 +79,8 @@ __global__ void __launch_bounds__(THREADS, 1536 / THREADS) process_kernel(const 
     const int r0 = a.split_rows ? blockIdx.z : 0, r1 = a.split_rows ? r0 + 1 : a.rows;
     const bool marks = a.history || a.drafts || a.bias_tokens;
     const bool report = blockIdx.y == 0 && blockIdx.z == 0;
-    int lo = 0, hi = 0;  // the sequence's biases
     if (marks) {
-        int hn = 0, pn = 0;
+        int hn = 0, pn = 0, lo = 0, hi = 0;
         if (a.history) {
             hn = a.hist_lens[b];
             pn = a.prompt_lens ? a.prompt_lens[b] : 0;
@@ -244,53 +243,57 @@ __global__ void __launch_bounds__(THREADS, 1536 / THREADS) process_kernel(const 
     const float rep = a.repetition ? a.repetition[b] : 1.f;
     const float pres = a.presence ? a.presence[b] : 0.f;
     const float freq = a.frequency ? a.frequency[b] : 0.f;
-    auto put = [&](int i, unsigned w, int entry) {
-        const float bias = w & kBiased ? a.bias_values[entry] : 0.f;
-        float *dst = out + i;
-#pragma unroll 4
-        for (int j = r0; j < r1; ++j, dst += a.V) {
-            float x = *dst;
-            unsigned count = w / kOnce;
-            if (w & kDrafted)
-                for (unsigned long long path = a.path[j]; path; path &= path - 1)
-                    count += sm.drafts[__ffsll((long long)path) - 1] == v0 + i;
-            if ((w & kInPrompt) || count) x = x > 0.f ? __fdiv_rn(x, rep) : __fmul_rn(x, rep);
-            if (count) x = __fadd_rn(__fadd_rn(x, -__fmul_rn(freq, (float)count)), -pres);
-            if (w & kBiased) x = __fadd_rn(x, bias);
-            if (*dst != ninf) *dst = x;
-        }
-    };
-    const int c = sm.bias_n;
-    if (c <= kBiasList) {
-        const int m = sm.marked_n;
-        for (int z = threadIdx.x; z < m; z += THREADS) {
-            const int i = sm.marked[z];
-            const unsigned w = sm.word[i];
-            int entry = -1;  // the last entry of the list that names the token
-            if (w & kBiased)
-                for (int k = 0; k < c; ++k)
-                    if (sm.bias_at[k] == i) entry = max(entry, sm.bias_entry[k]);
-            put(i, w, entry);
-        }
-        return;
-    }
-    // more biased tokens than the list holds: the sequence's biases are read
-    // twice more, each time keeping the last entry of half the slab's tokens
-    // where the marked ones were listed (64 x 6 rows of 128256 fp32 logits: 97 us
-    // without biases, 105 with lists of up to 300 among the first 4096 tokens,
-    // 115 with up to 4096, 445 with up to 128256 of the whole vocabulary)
+    // Where the slab has more biased tokens than the list holds, the sequence's
+    // biases are read twice more, each time keeping the last entry of half the
+    // slab's tokens where the marked ones were listed.  64 x 6 rows of 128256
+    // fp32 logits: 76 us without biases, 97 with lists of up to 300 among the
+    // first 4096 tokens, 112 with up to 4096, 490 with up to 128256 of the whole
+    // vocabulary.  One loop for both: with a copy of the rules for each, the rows
+    // above took 97 us without any biases (and 114 for 95 with histories of 8192).
+    const int m = sm.marked_n, c = sm.bias_n;
+    const bool many = c > kBiasList;
 #pragma unroll 1
-    for (int x0 = 0; x0 < n; x0 += SLAB / 2) {
-        __syncthreads();
-        for (int i = threadIdx.x; i < SLAB / 2; i += THREADS) sm.last[i] = 0;
-        __syncthreads();
-        for (int i = lo + threadIdx.x; i < hi; i += THREADS) {
-            const unsigned x = (unsigned)a.bias_tokens[i] - (unsigned)(v0 + x0);
-            if (x < (unsigned)min(SLAB / 2, n - x0)) atomicMax(&sm.last[x], i + 1);
+    for (int x0 = 0; x0 < (many ? n : 1); x0 += SLAB / 2) {
+        const int end = many ? min(SLAB / 2, n - x0) : m;
+        if (many) {
+            __syncthreads();
+            for (int i = threadIdx.x; i < SLAB / 2; i += THREADS) sm.last[i] = 0;
+            __syncthreads();
+            const int hi = a.bias_offsets[b + 1];
+#pragma unroll 4
+            for (int i = a.bias_offsets[b] + threadIdx.x; i < hi; i += THREADS) {
+                const unsigned x = (unsigned)a.bias_tokens[i] - (unsigned)(v0 + x0);
+                if (x < (unsigned)end) atomicMax(&sm.last[x], i + 1);
+            }
+            __syncthreads();
         }
-        __syncthreads();
-        for (int i = x0 + threadIdx.x; i < min(x0 + SLAB / 2, n); i += THREADS)
-            if (const unsigned w = sm.word[i]) put(i, w, sm.last[i - x0] - 1);
+        for (int z = threadIdx.x; z < end; z += THREADS) {
+            const int i = many ? x0 + z : sm.marked[z];
+            const unsigned w = sm.word[i];
+            if (many && w == 0u) continue;
+            float bias = 0.f;
+            if (w & kBiased) {  // the last entry of the list that names the token
+                int entry = -1;
+                if (many) entry = sm.last[z] - 1;
+                else
+                    for (int k = 0; k < c; ++k)
+                        if (sm.bias_at[k] == i) entry = max(entry, sm.bias_entry[k]);
+                bias = a.bias_values[entry];
+            }
+            float *dst = out + i;
+#pragma unroll 4
+            for (int j = r0; j < r1; ++j, dst += a.V) {
+                float x = *dst;
+                unsigned count = w / kOnce;
+                if (w & kDrafted)
+                    for (unsigned long long path = a.path[j]; path; path &= path - 1)
+                        count += sm.drafts[__ffsll((long long)path) - 1] == v0 + i;
+                if ((w & kInPrompt) || count) x = x > 0.f ? __fdiv_rn(x, rep) : __fmul_rn(x, rep);
+                if (count) x = __fadd_rn(__fadd_rn(x, -__fmul_rn(freq, (float)count)), -pres);
+                if (w & kBiased) x = __fadd_rn(x, bias);
+                if (*dst != ninf) *dst = x;
+            }
+        }
     }
 }
 
