@@ -76,8 +76,9 @@ __global__ void __launch_bounds__(kThreads) build_kernel(const __grid_constant__
     long long lp = 0, lt = 0;
     for (int b = b0; b < b1; ++b) {
         const int n = a.seq_lens[b];
-        if (n < 0 || n > (long long)a.max_blocks * kBlockSize || (n > 0 && n < prefix_len)) bad |= SVPA_DEVERR_BAD_VALUE;
-        else if (n > 0) {
+        if (n < 0 || n > (long long)a.max_blocks * kBlockSize || (n > 0 && n < prefix_len)) {
+            bad |= SVPA_DEVERR_BAD_VALUE;
+        } else if (n > 0) {
             ++live;
             lp += (n + kBlockSize - 1) / kBlockSize - P;
             lt += n - prefix_len;

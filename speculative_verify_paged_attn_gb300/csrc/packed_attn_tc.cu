@@ -483,7 +483,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (pair) {
                         // K (from L2) has landed long before P is ready: wait
                         // for it first, and both MMAs go out together
-                        ok = (j == n || tile_wait(ik)) && (j == 0 || (tile_wait(iv) && my_turn(j) && wait(&sm.p_full[t], np++)));
+                        ok = (j == n || tile_wait(ik)) &&
+                             (j == 0 || (tile_wait(iv) && my_turn(j) && wait(&sm.p_full[t], np++)));
                         if (!ok) break;
                         tc_fence_after();
                         if (elect_one()) {
@@ -737,7 +738,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!more) break;
                 prefixes += d.w.prefix;
                 // the producer has this one and is near its end
-                if (!until([&]() -> bool { return __all_sync(0xffffffffu, mbar_test(&sm.job_want, (uint32_t)(jobs & 1))); }))
+                if (!until([&]() -> bool {
+                        return __all_sync(0xffffffffu, mbar_test(&sm.job_want, (uint32_t)(jobs & 1)));
+                    }))
                     break;
                 // a CTA whose unit waits for the prefix takes no second one: the CTAs
                 // that end their prefix units take the rest (2 x 1 tokens of 32 heads
@@ -924,8 +927,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                             float4 *o = part_cols<D>(a, prow) + c * 8 * 32;
 #pragma unroll
                             for (int x = 0; x < 8; ++x)
-                                o[x * 32] = make_float4(__uint_as_float(raw[4 * x]), __uint_as_float(raw[4 * x + 1]),
-                                                        __uint_as_float(raw[4 * x + 2]), __uint_as_float(raw[4 * x + 3]));
+                                o[x * 32] =
+                                    make_float4(__uint_as_float(raw[4 * x]), __uint_as_float(raw[4 * x + 1]),
+                                                __uint_as_float(raw[4 * x + 2]), __uint_as_float(raw[4 * x + 3]));
                         }
                     }
                     tc_fence_before();

@@ -17,15 +17,7 @@
 
 using namespace svpa;
 
-namespace {
-
-constexpr size_t kAlign = 256;
-inline size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
-                                  CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
-                                  CUtensorMapFloatOOBfill);
+namespace svpa {
 
 EncodeTiledFn encode_fn() {
     static EncodeTiledFn fn = nullptr;
@@ -50,8 +42,15 @@ int sm_count() {
         if (r == cudaSuccess) r = cudaDeviceGetAttribute(v, cudaDevAttrMultiProcessorCount, dev);
         return r == cudaSuccess && *v <= 0 ? cudaErrorInvalidValue : r;
     });
-    return e == cudaSuccess ? n : 148;
+    return e == cudaSuccess ? n : 152;
 }
+
+}  // namespace svpa
+
+namespace {
+
+constexpr size_t kAlign = 256;
+inline size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 struct AttnPlan {
     int M, split_pages, max_splits;

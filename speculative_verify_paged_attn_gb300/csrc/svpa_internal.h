@@ -50,6 +50,15 @@ struct DeviceMemo {
     }
 };
 
+// The current device's SM count, and cuTensorMapEncodeTiled (null where the
+// driver has none), each looked up once.
+int sm_count();
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
+                                  CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                                  CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn();
+
 constexpr int kBlockSize = 16;   // tokens per page
 constexpr int kMaxNq = 64;       // queries per sequence (one 64-bit mask row each)
 constexpr int kMaxRows = 128;    // GQA group size x queries handled by one CTA

@@ -2,14 +2,12 @@
 // attention over pages and verification behind a shared prefix.  Host-side
 // validation, split choice, workspace layout, tensor maps and the launches;
 // no function here allocates device memory.
-#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 #include <string.h>
 
 #include <algorithm>
 #include <cmath>
-#include <mutex>
 
 #include "../../include/svpa.h"
 #include "packed_attn.h"
@@ -23,36 +21,6 @@ constexpr int kMaxSplits = 32;
 inline size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 svpa_status from_cuda(cudaError_t e) { return e == cudaSuccess ? SVPA_OK : SVPA_ERR_CUDA; }
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    });
-    return fn;
-}
-
-int sm_count() {
-    static DeviceMemo<int> memo;
-    int n = 0;
-    const cudaError_t e = memo.get(&n, [](int *v) {
-        int dev = 0;
-        cudaError_t r = cudaGetDevice(&dev);
-        if (r == cudaSuccess) r = cudaDeviceGetAttribute(v, cudaDevAttrMultiProcessorCount, dev);
-        return r == cudaSuccess && *v <= 0 ? cudaErrorInvalidValue : r;
-    });
-    return e == cudaSuccess ? n : 152;
-}
 
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
@@ -120,7 +88,8 @@ svpa_status plan_prompt(const svpa_prompt_params *p, Plan *pl) {
     const int G = p->num_q_heads / p->num_kv_heads;
     if ((p->head_dim != 64 && p->head_dim != 128) || p->kv_dtype != SVPA_KV_BF16 || G > kMaxRows ||
         p->max_blocks_per_seq > (0x7fffffff - 4096) / kBlockSize ||
-        (long long)p->num_blocks * p->num_kv_heads > 0x7fffffff || p->num_kv_heads > 65535 || p->batch > (1 << 20) || p->total_q > (1 << 28))
+        (long long)p->num_blocks * p->num_kv_heads > 0x7fffffff || p->num_kv_heads > 65535 ||
+        p->batch > (1 << 20) || p->total_q > (1 << 28))
         return SVPA_ERR_UNSUPPORTED;
     pl->tpt = kMaxRows / G;
     pl->pairs = p->total_q / (2 * pl->tpt) + p->batch;
