@@ -988,7 +988,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float4 v[kHalf / 4];
 #pragma unroll
                     for (int x = 0; x < kHalf / 4; ++x) v[x] = __ldcg(src + x * 32);
-                    if (!(ml.y > 0.f)) continue;  // nothing there: not even zeros
+                    if (ml.y == 0.f) continue;  // nothing there: not even zeros (a NaN stays)
                     const float mn = fmaxf(m, ml.x);
                     const float fo = l > 0.f ? ex2_approx(m - mn) : 0.f, fp = ex2_approx(ml.x - mn);
                     l = l * fo + ml.y * fp;
@@ -1079,7 +1079,7 @@ __global__ void __launch_bounds__(256) packed_combine_kernel(const __grid_consta
 #pragma unroll 2
     for (int s = first; s < slots; ++s) {
         const float2 ml = a.part_ml[s * pslot + prow];
-        if (!(ml.y > 0.f)) continue;
+        if (ml.y == 0.f) continue;  // nothing there (a NaN is, and stays)
         const float mn = fmaxf(m, ml.x);
         const float fo = ex2_approx(m - mn), fn = ex2_approx(ml.x - mn);
         const float4 *src = part_cols<D>(a, s * pslot + prow) + warp * kPer * 32;

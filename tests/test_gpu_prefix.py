@@ -251,3 +251,22 @@ def test_outputs_on_a_16_byte_boundary(own, prefix, n_q, hq, hkv):
     c.call()
     c.check()
     assert bool((wide[:8] == 5.0).all()) and bool((wide[-8:] == 5.0).all())
+
+
+@pytest.mark.parametrize("own,prefix,n_q,hq,hkv", [
+    ([100, 17, 260, 1], 800, 6, 16, 2), ([33, 12] * 40, 480, 5, 16, 4), ([3000, 10], 512, 2, 8, 1),
+])
+def test_a_nan_query_stays_in_its_row(own, prefix, n_q, hq, hkv):
+    """Behind a shared prefix, joined at once or from split parts: the row's
+    result is NaN, every other row is as it was."""
+    c = Case(own, prefix, n_q, hq, hkv, 128)
+    c.call()
+    c.check()
+    out, lse = c.out.clone(), c.lse.clone()
+    c.q[1, n_q - 1, 3, 7] = float("nan")
+    c.call()
+    assert svpa.check_error(c.err) == 0
+    spot = (1, n_q - 1, 3)
+    assert bool(torch.isnan(c.out[spot]).all()) and bool(torch.isnan(c.lse[spot]))
+    c.out[spot], c.lse[spot] = out[spot], lse[spot]
+    assert torch.equal(c.out, out) and torch.equal(c.lse, lse)

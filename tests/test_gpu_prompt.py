@@ -271,3 +271,23 @@ def test_outputs_on_a_16_byte_boundary(new, cached, hq, hkv, d):
     c.call()
     c.check()
     assert bool((wide[:8] == 77.0).all()) and bool((wide[-8:] == 77.0).all())
+
+
+@pytest.mark.parametrize("new,cached,hq,hkv,d", [
+    ([300, 40], [0, 0], 4, 4, 128),      # pairs of tiles
+    ([37, 5], [0, 600], 8, 2, 64),       # single tiles
+    ([20], [5000], 8, 2, 128), ([300], [3000], 2, 1, 64),  # split over the kv range
+])
+def test_a_nan_query_stays_in_its_row(new, cached, hq, hkv, d):
+    """The row's result is NaN, not zeros; every other row is as it was."""
+    c = Case(new, cached, hq, hkv, d)
+    c.call()
+    c.check()
+    out, lse = c.out.clone(), c.lse.clone()
+    t, h = new[0] - 3, hq - 1
+    c.q[t, h, 5] = float("nan")
+    c.call()
+    assert svpa.check_error(c.err) == 0
+    assert bool(torch.isnan(c.out[t, h]).all()) and bool(torch.isnan(c.lse[t, h]))
+    c.out[t, h], c.lse[t, h] = out[t, h], lse[t, h]
+    assert torch.equal(c.out, out) and torch.equal(c.lse, lse)
