@@ -284,9 +284,10 @@ svpa_status svpa_block_table_build(int32_t batch, int32_t block_size,
  * tile; a negative slot is a padding row and is skipped, one past the pool
  * raises SVPA_DEVERR_BAD_BLOCK.  Two rows with the same slot: what that slot
  * holds is unspecified (words of either row; in FP8 pages a scale of one may
- * stand beside codes of the other).  Other slots are left as they were.  FP8 pages take one scale per 64 consecutive elements
- * (scale_tile 64): scale = amax / 448 of the tile (1 when amax is 0), codes
- * e4m3(value / scale), as svpa_kv_append.
+ * stand beside codes of the other).  Other slots are left as they were.  FP8
+ * pages take one scale per 64 consecutive elements (scale_tile 64): scale =
+ * amax / 448 of the tile (1 when amax is 0), codes e4m3(value / scale), as
+ * svpa_kv_append.
  *
  *  new_k, new_v  bf16 [T, Hkv, D], tokens k_stride / v_stride elements apart
  *                (at least Hkv * D, multiples of 8), 16-byte aligned
@@ -354,7 +355,8 @@ svpa_status svpa_paged_prompt_attn_workspace_size(const svpa_prompt_params *p, s
  * the pool SVPA_DEVERR_BAD_BLOCK.  Scores and sums are fp32;
  * the weights of a row are rounded to bf16 for their product with V.  K/V
  * values of every position below kv_lens[b] must be finite (the weight of a
- * position that a token does not see is an exact zero).
+ * position that a token does not see is an exact zero); a NaN in a query gives
+ * NaN in its row alone.
  */
 svpa_status svpa_paged_prompt_attn(const svpa_prompt_params *p, const void *q,
                                    const void *k_pool, const void *v_pool,
@@ -830,9 +832,9 @@ svpa_status svpa_gamma_update(int32_t batch, int32_t gamma,
  * Same arguments and result as svpa_paged_verify_attn minus the workspace.
  * Its scratch is a fixed 32 MiB array inside the library, present on every
  * GPU that loads it until the process exits; a shape whose workspace
- * (svpa_attn_workspace_size) exceeds 32 MiB is rejected with
- * SVPA_ERR_WORKSPACE before anything is enqueued, as is any call that
- * svpa_paged_verify_attn would reject.  No call makes an allocation: no
+ * (svpa_attn_workspace_size, less the room it keeps for other calls' tickets)
+ * exceeds 32 MiB is rejected with SVPA_ERR_WORKSPACE before anything is
+ * enqueued, as is any call that svpa_paged_verify_attn would reject.  No call makes an allocation: no
  * cudaMalloc, cudaFree or allocating library call.
  *  - The first call on a device looks up the array's device address (once per
  *    device, with that device current).  Under CUDA's lazy module loading

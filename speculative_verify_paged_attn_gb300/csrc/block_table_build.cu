@@ -23,8 +23,10 @@ namespace {
 // Small admissions are one CTA of 1024 threads, whose warps take 128 entries
 // at a time (nothing to wait for at the end); others CTAs of 256, 256 entries a
 // warp.  With a 4-byte copy before each call (0.9 us alone): 8 requests of some
-// hundred tokens 7.8 us, 256 requests of up to 32768 tokens, 4 million slots,
-// 15.1 us.  Bound by dependent loads: lengths, counts, stack, then the ticket.
+// hundred tokens 7.9 us, bound by the launch and dependent loads (lengths,
+// counts, stack); 256 requests of up to 32768 tokens, 4 million slots, 15.1 us,
+// the rest of it instructions (searches and index arithmetic: 59% of the issue
+// slots; stalls an issue: fixed latencies 2.9, loads 2.4, barriers 2.3).
 constexpr int kOneCta = 32768;     // entries and slots
 constexpr int kMaxCtas = 152 * 5;  // resident at once for batches of up to about 5500
 

@@ -10,8 +10,9 @@
 // together; consecutive rows fill consecutive rows of a page.  FP8: eight lanes
 // hold a 64-value tile, its scale is amax / 448 (1 for a tile of zeros) and its
 // codes the values over the scale, each rounded once.  32768 rows of 8 x 128:
-// bf16 42 us, 95% of the measured copy rate; FP8 54 us against a floor of 31,
-// bound by the instructions of the quotients and conversions.
+// bf16 42 us, 95% of the measured copy rate; FP8 55 us against a floor of 31,
+// bound by the instructions of the quotients and conversions (75% of the issue
+// slots taken, the ALU pipe 62% busy, DRAM 34%).
 #include "admit.h"
 #include "svpa_device.cuh"
 
@@ -35,10 +36,13 @@ __device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d
 
 // v / sc, correctly rounded, from inv = 1 / sc correctly rounded (P. Markstein,
 // "Computation of elementary functions on the IBM RISC System/6000 processor",
-// 1990): the remainder of v * inv is exact in one fused multiply-add, and adding
-// its share rounds once.  Holds for a scale whose significand is not all ones
-// and remainders that do not underflow; a quotient too small for the latter
-// (below 2^-10 for sc >= 2^-89) has the code 0 either way.  Three instructions
+// 1990): the remainder of v * inv comes from one fused multiply-add, and adding
+// its share rounds once.  Of the 128 x 128 pairs of significands (v, and the
+// scale of a maximum), the remainder is rounded itself in 35, and the result is
+// the correctly rounded quotient in all (enumerated in rationals).  Holds for a
+// scale whose significand is not all ones and remainders that do not underflow;
+// a quotient too small for the latter (below 2^-10 for sc >= 2^-89) has the code
+// 0 either way.  Three instructions
 // for the IEEE division's dozen: eight of those per 16 bytes made the kernel
 // bound by instructions.
 __device__ __forceinline__ float over_scale(float v, float sc, float inv) {

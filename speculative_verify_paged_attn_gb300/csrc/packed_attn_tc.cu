@@ -32,8 +32,9 @@
 //   8-11   maximum (O_t rescaled only when it grows by more than 2^8), fp32
 //          row sum, P as bf16 (the MMA's input type; the sum is taken before
 //          that rounding); then the unit's epilogue.
-// 8192 tokens, 64/8 heads, D 128: 692 us, 1.59 PFLOP/s.  Bound by one tile's
-// chain from scores to the next scores: a pair's block takes about 3000 cycles,
+// 8192 tokens, 64/8 heads, D 128: 693 us, 1.59 PFLOP/s, in a burst at 2070 MHz;
+// 746 us, 1.47 PFLOP/s, sustained at the power limit (1927 MHz).  Bound by one
+// tile's chain from scores to the next scores: a pair's block takes about 3000 cycles,
 // 2048 of them MMAs (the exponentials of both tiles about 1000, the rest waits
 // and fences of some 100 to 250 each).  40 x 6 queries behind 8192 shared
 // tokens: 84 to 91 us by process (247 with every sequence reading the prefix).

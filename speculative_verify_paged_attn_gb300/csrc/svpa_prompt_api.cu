@@ -135,7 +135,9 @@ svpa_status plan_prefix(const svpa_attn_params *p, int32_t prefix_len, Plan *pl)
     // 128-row tile as they are, behind 800: 61.6 and 64.6; behind 2048: 112 and
     // 90.  Over 138 such cases the rule is 4% behind the better side on average
     // and 1.65 times at worst (8 x 1 tokens of 64/8 heads behind 128: 22.6 us
-    // alone, 13.7 shared).
+    // alone, 13.7 shared).  The batch has no part in it: for one sequence sharing
+    // splits the prefix over SMs (32/8 heads, 1 token behind 1024: 27.3 us alone,
+    // 15.6 shared; 32/32 heads: 15.4 and 17.9).
     const double rows = (double)p->n_q * G;
     pl->shared = rows / 256. * (3. * pb + 8.) + 2. < 1.75 * pb;
     if (!pl->shared) {
