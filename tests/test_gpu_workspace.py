@@ -4,9 +4,11 @@ batch, draft length and prefix."""
 import pytest
 import torch
 
+import gpu_util as G
 import test_gpu_prefix as P
 import test_gpu_prompt as Q
 from speculative_verify_paged_attn_gb300 import svpa
+from speculative_verify_paged_attn_gb300 import workloads as W
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -79,3 +81,35 @@ def test_more_tickets_than_the_workspace_keeps(make):
         assert svpa.check_error(c.err) == 0
         assert torch.equal(c.out, out) and torch.equal(c.lse, lse)
         assert int(c.ws[:HEAD].view(torch.int32).abs().sum()) == 0
+
+
+@pytest.mark.parametrize("name", ["fp8", "fp8_t64"])
+def test_fp8_pages_on_the_same_workspace(name):
+    """FP8 pages, whose blocks are split over all SMs, between calls of the other kinds."""
+    wl = W.WORKLOADS[name].scaled(num_q_heads=16, num_kv_heads=2)
+    inp = G.to_dev(W.make_attention(wl, 3, contexts=(3000, 17, 900, 5000)))
+    b, n_q, hq, d = inp.q.shape
+    p = svpa.attn_params(b, n_q, hq, 2, d, inp.block_table.shape[1], inp.num_blocks, kv_fp8=True,
+                         sm_scale=wl.sm_scale, scale_tile=wl.scale_tile)
+    out, err = torch.zeros((b, n_q, hq, d), dtype=torch.bfloat16, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+
+    def call(ws):
+        out.zero_()
+        svpa.paged_verify_attn(p, inp.q, inp.k_pool.view(torch.uint8), inp.v_pool.view(torch.uint8), inp.block_table,
+                               inp.context_lens, out, workspace=ws, error_flag=err, k_scale=inp.k_scale,
+                               v_scale=inp.v_scale, ancestor_mask=G.mask_list(inp))
+        assert svpa.check_error(err) == 0
+        return out.clone()
+
+    size = svpa.attn_workspace_size(p)
+    want = call(torch.zeros(size, dtype=torch.uint8, device=DEV))
+    others = [CALLS[k]() for k in ("shared, split", "unshared, split", "prompt chunks, split")]
+    ws = torch.zeros(max([size] + [c.ws.numel() for c in others]), dtype=torch.uint8, device=DEV)
+    for c in others:
+        c.ws = ws
+        c.call()
+        c.check()
+        assert torch.equal(call(ws), want)
+        c.call()
+        c.check()
+    assert int(ws[:HEAD].view(torch.int32).abs().sum()) == 0
