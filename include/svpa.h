@@ -36,6 +36,16 @@
  *   svpa_logits_process      penalties, biases and grammar masks on the target's
  *                            logits, before a sampler fed by logits.
  *
+ * Between the projections and the cache, and for a cache held in 4 bits:
+ *
+ *   svpa_qk_norm_rope        norms of queries and keys for each head and the
+ *                            position rotation, in one pass.
+ *   svpa_rope_kv_write       the same on the way into the pages (bf16, FP8 or
+ *                            4 bits) through a slot map.
+ *   svpa_kv_append_fp4       svpa_kv_append for 4-bit pages.
+ *   svpa_paged_verify_attn_fp4  svpa_paged_verify_attn over 4-bit pages.
+ *   svpa_kv_read             rows of pages back as bf16 through a slot map.
+ *
  * Conventions shared by every entry point
  *  - Every pointer argument is a DEVICE pointer unless its comment says HOST.
  *    The caller owns and allocates all memory; no entry point calls an
@@ -53,9 +63,10 @@
  *    That holds for workspaces too: one belongs to one call at a time, also
  *    where the calls are in different captured graphs.
  *  - One buffer, zero-filled once and large enough for each, may be the
- *    workspace of svpa_paged_verify_attn, svpa_paged_prompt_attn,
- *    svpa_prefix_verify_attn and svpa_block_table_build in turn, whatever
- *    their batch, draft length, prefix and heads: every completed call leaves
+ *    workspace of svpa_paged_verify_attn, svpa_paged_verify_attn_fp4,
+ *    svpa_paged_prompt_attn, svpa_prefix_verify_attn and
+ *    svpa_block_table_build in turn, whatever their batch, draft length,
+ *    prefix and heads: every completed call leaves
  *    its first 65792 bytes (counters and tickets) at zero.  The samplers'
  *    workspace is another buffer.  After SVPA_DEVERR_TIMEOUT zero-fill again.
  *  - A call runs on the calling thread's current device; its pointers and its
@@ -93,6 +104,25 @@ typedef enum svpa_status {
 /* K/V page element types */
 #define SVPA_KV_BF16 0
 #define SVPA_KV_FP8_E4M3 1
+/*
+ * 4 bits: E2M1 codes with one E4M3 scale for each 16 consecutive elements of a
+ * row, and one fp32 factor per kv head beside the pool.  A pool is uint8
+ * [num_blocks, Hkv, 9 D]: for each (page, kv head) 16 rows of D / 2 code bytes
+ * (element 2 i in the low half of byte i), then 16 rows of D / 16 scale bytes.
+ * Element d of a row stands for
+ *     e2m1(code) * e4m3(scale[d / 16]) * factor[head],
+ * codes 0..7 being 0, 0.5, 1, 1.5, 2, 3, 4, 6 and 8..15 their negatives.
+ * Rows are encoded one by one (history keeps its codes):
+ *     scale = e4m3(amax / (6 factor)), amax the largest magnitude of the 16,
+ *     code  = e2m1(x / (e4m3(scale) * factor)), 0 where the scale is 0,
+ * each quotient and product rounded to fp32 once, the conversions to nearest
+ * even, saturating at 448 and at 6.  Factors are fp32 [Hkv], device, in
+ * [2^-60, 2^60] (else SVPA_DEVERR_BAD_VALUE), or NULL (1); the largest value
+ * a head can hold is 2688 factor, and rows keep 3 to 4 significant bits of
+ * their scales while amax > 0.1 factor.  Values that are not finite cannot be
+ * held and raise SVPA_DEVERR_BAD_VALUE.
+ */
+#define SVPA_KV_FP4_E2M1 2
 
 /*
  * Geometry of one paged-attention call.
@@ -114,7 +144,8 @@ typedef struct svpa_attn_params {
     int32_t block_size;         /* tokens per page: 16                        */
     int32_t max_blocks_per_seq; /* row stride of block_table                  */
     int32_t num_blocks;         /* physical pages in the pool                 */
-    int32_t kv_dtype;           /* SVPA_KV_BF16 or SVPA_KV_FP8_E4M3           */
+    int32_t kv_dtype;           /* SVPA_KV_BF16 or SVPA_KV_FP8_E4M3 (4 bits:
+                                   svpa_paged_verify_attn_fp4 alone)           */
     float sm_scale;             /* softmax scale, normally 1/sqrt(D)          */
     int32_t split_pages;        /* pages per KV split; 0 = chosen by library
                                    (not used by the tcgen05 kernel for FP8
@@ -683,7 +714,8 @@ svpa_status svpa_spec_accept_tree_logits(int32_t batch, int32_t n_nodes, int32_t
  *  refcount     int32 [num_blocks] (in/out)
  *  free_stack   int32 [num_blocks] (in/out), free_top int32 [1] (in/out)
  *  path_nodes   int32 [B, path_width] or NULL (linear)
- *  k_pool, v_pool  the pools (only read/written for a tree; bf16 only)
+ *  k_pool, v_pool  the pools (only read/written for a tree; bf16 pages, or 4
+ *               bits, whose rows move as they are stored)
  */
 svpa_status svpa_block_table_commit(int32_t batch, int32_t n_q,
                                     int32_t block_size,
@@ -857,6 +889,153 @@ svpa_status svpa_paged_verify_attn_noalloc(const svpa_attn_params *p, const void
                                            const uint64_t *ancestor_mask, void *out,
                                            float *lse, int32_t *error_flag,
                                            void *stream);
+
+/*
+ * Geometry of svpa_qk_norm_rope and svpa_rope_kv_write.
+ */
+typedef struct svpa_rope_params {
+    int32_t num_tokens;   /* T, 0..2^28                                       */
+    int32_t num_q_heads;  /* Hq, 0..4096; 0 = no queries (q, q_out unused)    */
+    int32_t num_kv_heads; /* Hkv, 1..4096                                     */
+    int32_t head_dim;     /* D: 64, 128 or 256                                */
+    int32_t rotary_dim;   /* R, the first elements of a head that turn: 0 (no
+                             rotation) or a multiple of 16 up to D            */
+    int32_t interleaved;  /* the pairs that turn: 0 = elements (i, i + R / 2),
+                             1 = elements (2 i, 2 i + 1)                      */
+    int32_t max_position; /* rows of cos_sin                                  */
+    int32_t block_size;   /* tokens per page: 16   (rope_kv_write, as below)  */
+    int32_t num_blocks;   /* physical pages in the pools, below 2^27          */
+    int32_t kv_dtype;     /* SVPA_KV_BF16, _FP8_E4M3 or _FP4_E2M1             */
+    int32_t scale_tile;   /* 64 for FP8 pages, else 0                         */
+    float eps;            /* of the norms, >= 0                               */
+    int64_t q_stride;     /* elements from one token to the next, multiples of */
+    int64_t k_stride;     /* 8, at least the token's own (slices of a fused    */
+    int64_t v_stride;     /* projection are taken as they are)                 */
+    int64_t q_out_stride;
+    int64_t k_out_stride;
+} svpa_rope_params;
+
+/*
+ * Norms of queries and keys for each head and the position rotation, in one
+ * pass.  The pages this library follows have no counterpart of these two entry
+ * points; they stand between the projections and svpa_kv_append,
+ * svpa_paged_verify_attn and svpa_paged_prompt_attn.
+ *
+ * For each head x of token t:
+ *   n = x / sqrt(mean(x^2) + eps) * weight       (x itself without a weight)
+ *   (a, b) -> (a cos - b sin, b cos + a sin)     for its R / 2 pairs, with the
+ *                                                 angles of positions[t]
+ * in fp32, rounded to bf16 once.
+ *
+ *  q, k         bf16 [T, Hq, D], [T, Hkv, D], tokens q_stride, k_stride apart
+ *  positions    int32 [T], 0..max_position - 1 (not read when R is 0); another
+ *               one raises SVPA_DEVERR_BAD_VALUE
+ *  cos_sin      fp32 [max_position, R]: R / 2 cosines, then R / 2 sines
+ *  q_weight,
+ *  k_weight     bf16 [D], or NULL: no norm
+ *  q_out, k_out bf16, as q and k with their own strides; may be q and k
+ *               themselves (in place), else they overlap nothing
+ * Pointers are 16-byte aligned (positions 4).  A token's values do not depend
+ * on the other tokens.  One kernel on `stream`.
+ */
+svpa_status svpa_qk_norm_rope(const svpa_rope_params *p, const void *q, const void *k,
+                              const int32_t *positions, const float *cos_sin,
+                              const void *q_weight, const void *k_weight, void *q_out,
+                              void *k_out, int32_t *error_flag, void *stream);
+
+/*
+ * svpa_qk_norm_rope with the keys, and the values as they are, written into
+ * their pages through a slot map, as svpa_kv_write does with finished rows:
+ * the pages hold what they would hold after svpa_qk_norm_rope and a write of
+ * its bf16 rows.
+ *
+ *  v            bf16 [T, Hkv, D], tokens v_stride apart
+ *  slot_map     int32 [T]: row t goes to page slot_map[t] / 16, row
+ *               slot_map[t] % 16; negative: a padding row, of which nothing is
+ *               read or written, its query included; past the pool:
+ *               SVPA_DEVERR_BAD_BLOCK.  Two rows with the same slot: what that
+ *               slot holds is unspecified.  Other slots are left as they were.
+ *  k_pool, v_pool  bf16 or E4M3 [num_blocks, Hkv, 16, D], or 4-bit pages
+ *  k_scale, v_scale  FP8: fp32 [num_blocks, Hkv, 16, D / 64], as svpa_kv_write;
+ *               else NULL
+ *  k_factor, v_factor  4 bits: fp32 [Hkv] or NULL; else not used
+ * q may be NULL with num_q_heads 0.  One kernel on `stream`.
+ */
+svpa_status svpa_rope_kv_write(const svpa_rope_params *p, const void *q, const void *k,
+                               const void *v, const int32_t *positions,
+                               const int32_t *slot_map, const float *cos_sin,
+                               const void *q_weight, const void *k_weight, void *q_out,
+                               void *k_pool, void *v_pool, float *k_scale, float *v_scale,
+                               const float *k_factor, const float *v_factor,
+                               int32_t *error_flag, void *stream);
+
+/*
+ * Rows of pages back as bf16, through a slot map: the inverse of the writes
+ * (an FP8 or 4-bit value rounded to bf16 once).  A prompt whose first part is
+ * held in 4 bits goes on over bf16 pages with it.
+ *
+ *  slot_map     int32 [T]: row t is read from page slot_map[t] / 16, row
+ *               slot_map[t] % 16; negative: row t of the outputs is left as it
+ *               was; past the pool: SVPA_DEVERR_BAD_BLOCK
+ *  k_pool, v_pool, k_scale, v_scale, k_factor, v_factor  as svpa_rope_kv_write
+ *  k_out, v_out bf16 [T, Hkv, D], tokens k_stride / v_stride elements apart (at
+ *               least Hkv * D, multiples of 8), 16-byte aligned
+ * Limits: 1 <= num_kv_heads <= 4096; head_dim a multiple of 8 up to 1024 (4
+ * bits: of 16; FP8: of 64, scale_tile 64); num_tokens <= 2^28, num_blocks below
+ * 2^27.  One kernel on `stream`.
+ */
+svpa_status svpa_kv_read(int32_t num_tokens, int32_t num_kv_heads, int32_t head_dim,
+                         int32_t block_size, int32_t num_blocks, int32_t kv_dtype,
+                         int32_t scale_tile, const int32_t *slot_map, const void *k_pool,
+                         const void *v_pool, const float *k_scale, const float *v_scale,
+                         const float *k_factor, const float *v_factor, void *k_out,
+                         void *v_out, int64_t k_stride, int64_t v_stride,
+                         int32_t *error_flag, void *stream);
+
+/*
+ * svpa_kv_append for 4-bit pages: the same allocation, copy-on-write and
+ * errors; each new row is encoded by itself, history rows keep their codes and
+ * slots past the last row are left as they were.  k_factor, v_factor: fp32
+ * [Hkv] or NULL.  head_dim a multiple of 16 up to 1024.  Two kernels.
+ */
+svpa_status svpa_kv_append_fp4(int32_t batch, int32_t n_new, int32_t num_kv_heads,
+                               int32_t head_dim, int32_t block_size,
+                               int32_t max_blocks_per_seq, int32_t num_blocks,
+                               const void *new_k, const void *new_v, int32_t *block_table,
+                               const int32_t *context_lens, int32_t *refcount,
+                               int32_t *free_stack, int32_t *free_top, void *k_pool,
+                               void *v_pool, const float *k_factor, const float *v_factor,
+                               int32_t *error_flag, void *stream);
+
+/* Bytes of workspace svpa_paged_verify_attn_fp4 needs for `p`; zero-filled once
+ * before its first use (every completed call leaves its counters zero). */
+svpa_status svpa_paged_verify_attn_fp4_workspace_size(const svpa_attn_params *p, size_t *bytes);
+
+/*
+ * svpa_paged_verify_attn over 4-bit pages (p->kv_dtype SVPA_KV_FP4_E2M1; the
+ * field split_pages is not used, variant and scale_tile are 0).  Head
+ * dimensions 64 and 128, up to 128 query rows per kv head; one token a sequence
+ * (n_q 1) is plain decoding.
+ *
+ *  k_pool, v_pool  uint8 [num_blocks, Hkv, 9 D], 16-byte aligned
+ *  k_factor, v_factor  fp32 [Hkv] or NULL (1)
+ * The other arguments, the masks, `out`, `lse` and the errors are those of
+ * svpa_paged_verify_attn; num_blocks * num_kv_heads below 2^31.
+ * Codes times scales are exact; the queries are taken in f16 at one power of
+ * two per (sequence, kv head) (what that drops is below 2^-39 of its largest
+ * query value), the weights of the softmax are rounded to f16, scores and sums
+ * are fp32.  Scale bytes of positions that a query sees are those that the
+ * writes store (0 to 0x7e).  A query that is not finite raises
+ * SVPA_DEVERR_BAD_VALUE.
+ */
+svpa_status svpa_paged_verify_attn_fp4(const svpa_attn_params *p, const void *q,
+                                       const void *k_pool, const void *v_pool,
+                                       const float *k_factor, const float *v_factor,
+                                       const int32_t *block_table,
+                                       const int32_t *context_lens,
+                                       const uint64_t *ancestor_mask, void *out, float *lse,
+                                       void *workspace, size_t workspace_bytes,
+                                       int32_t *error_flag, void *stream);
 
 /* Synchronise `stream`, read the device error word and map it to a status
  * (SVPA_OK when it is zero).  Does not clear the word. */

@@ -38,6 +38,9 @@ SOURCES = {
     "kv_write.cu": ["-fmad=false"],
     "logits_process.cu": ["-fmad=false"],
     "svpa_admit_api.cu": [],
+    "rope_kv.cu": [],
+    "paged_verify_attn_fp4.cu": [],
+    "svpa_fp4_api.cu": [],
 }
 
 

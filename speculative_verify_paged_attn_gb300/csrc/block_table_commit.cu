@@ -70,9 +70,16 @@ __global__ void __launch_bounds__(128) commit_kernel(const __grid_constant__ Com
                 const int rem = w - which * a.Hkv * words;
                 const int g = rem / words, x = rem - g * words;
                 uint8_t *pool = which ? a.v_pool : a.k_pool;
-                const size_t so = (((size_t)sb * a.Hkv + g) * kBlockSize + src % kBlockSize) * a.row_bytes;
-                const size_t dof = (((size_t)db * a.Hkv + g) * kBlockSize + dst % kBlockSize) * a.row_bytes;
-                reinterpret_cast<uint4 *>(pool + dof)[x] = reinterpret_cast<const uint4 *>(pool + so)[x];
+                const size_t tile = (size_t)kBlockSize * (a.row_bytes + a.scale_bytes);
+                uint8_t *st = pool + ((size_t)sb * a.Hkv + g) * tile, *dt = pool + ((size_t)db * a.Hkv + g) * tile;
+                reinterpret_cast<uint4 *>(dt + (size_t)(dst % kBlockSize) * a.row_bytes)[x] =
+                    reinterpret_cast<const uint4 *>(st + (size_t)(src % kBlockSize) * a.row_bytes)[x];
+                // a 4-bit row's scales: four bytes beside every two words of codes
+                if (x * 4 < a.scale_bytes) {
+                    const size_t at = (size_t)kBlockSize * a.row_bytes + 4 * x;
+                    *reinterpret_cast<uint32_t *>(dt + at + (size_t)(dst % kBlockSize) * a.scale_bytes) =
+                        *reinterpret_cast<const uint32_t *>(st + at + (size_t)(src % kBlockSize) * a.scale_bytes);
+                }
             }
             __syncthreads();
         }

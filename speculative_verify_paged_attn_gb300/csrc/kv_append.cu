@@ -13,6 +13,8 @@
 //   scale per 64-element tile of a row (the implementation checklist's
 //   per-64-element block scales), where each new row's tiles are quantised
 //   on their own and the history is left as it is.
+//   4-bit pages (E2M1 codes, an E4M3 scale for each 16 elements): each new
+//   row's groups are encoded on their own too.
 //
 // Two launches on the caller's stream:
 //   1. append_alloc_kernel, one CTA per sequence: maps, allocates and clones
@@ -29,7 +31,7 @@
 // every access is a 16-byte vector, and each thread issues all its loads
 // (4 per thread per round; an FP8 lane holds its whole share of the tile in
 // registers) before its stores, so one call costs a few memory round trips.
-#include "svpa_device.cuh"
+#include "fp4.cuh"
 #include "svpa_internal.h"
 
 namespace svpa {
@@ -399,6 +401,74 @@ __global__ void __launch_bounds__(kWriteThreads) append_write_kernel(const __gri
     }
 }
 
+// 4-bit pages: the bf16 form's rounds of 16-byte chunks (eight elements), each
+// encoded before its store; a scale's two chunks are neighbouring lanes'.
+__global__ void __launch_bounds__(kWriteThreads) append_write_fp4_kernel(const __grid_constant__ AppendArgs a) {
+    const int b = blockIdx.x;
+    const int L = a.context_lens[b];
+    const long long end = (long long)L + a.n_new;
+    if (L < 0 || (end + kBlockSize - 1) / kBlockSize > a.max_blocks) return;
+    const int i = L / kBlockSize + (int)blockIdx.y;
+    const long long ps = (long long)i * kBlockSize;
+    if (ps >= end) return;
+    const int s0 = L > ps ? (int)(L - ps) : 0;                               // the page's first new slot
+    const int s1 = end - ps < kBlockSize ? (int)(end - ps) : kBlockSize;     // behind its last
+    const int D = a.D, Hkv = a.Hkv;
+    const int u0 = (int)blockIdx.z * kUnitsBf16;
+    const int units = min(kUnitsBf16, 2 * Hkv - u0);
+    const int cpr = D / 8;  // chunks per row
+    const int per_unit = (s1 - s0) * cpr;
+    const int total = units * per_unit;
+    auto where = [&](int w, int &kv, int &h, int &s, int &c) {
+        const int uu = w / per_unit, r = w - uu * per_unit;
+        s = s0 + r / cpr;
+        c = r - (r / cpr) * cpr;
+        kv = u0 + uu >= Hkv;
+        h = u0 + uu - kv * Hkv;
+    };
+    auto load_round = [&](int w0, uint4 (&x)[kLoads]) {
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k) {
+            const int w = w0 + k * kWriteThreads;
+            x[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (w < total) {
+                int kv, h, s, c;
+                where(w, kv, h, s, c);
+                const uint16_t *row = (kv ? a.new_v : a.new_k) +
+                                      (((size_t)b * a.n_new + (size_t)(ps + s - L)) * Hkv + h) * D;
+                x[k] = reinterpret_cast<const uint4 *>(row)[c];
+            }
+        }
+    };
+    // (a warp leaves as a whole: its lanes exchange maxima)
+    if ((int)(threadIdx.x & ~31u) >= total) return;
+    uint4 x[kLoads];
+    load_round(threadIdx.x, x);  // the first round overlaps the allocation kernel
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (*reinterpret_cast<volatile int32_t *>(a.err) != 0) return;
+    const int blk = a.block_table[(size_t)b * a.max_blocks + i];
+    if (blk < 0 || blk >= a.num_blocks) return;
+    for (int w0 = threadIdx.x; (w0 & ~31) < total; w0 += kLoads * kWriteThreads) {
+        if (w0 != (int)threadIdx.x) load_round(w0, x);
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k) {
+            const int w = w0 + k * kWriteThreads;
+            uint32_t amax = bf16_amax8(x[k]);
+            amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            if (w >= total) continue;
+            if (amax > 0x7f7fu) raise_error(a.err, SVPA_DEVERR_BAD_VALUE);
+            int kv, h, s, c;
+            where(w, kv, h, s, c);
+            uint32_t scale;
+            const uint32_t codes =
+                fp4_encode8(x[k], amax, fp4_factor(kv ? a.v_factor : a.k_factor, h, a.err), scale);
+            uint8_t *page = (kv ? a.v_pool : a.k_pool) + ((size_t)blk * Hkv + h) * fp4_tile_bytes(D);
+            reinterpret_cast<uint32_t *>(page + s * (D / 2))[c] = codes;
+            if ((c & 1) == 0) page[fp4_code_bytes(D) + s * (D / 16) + c / 2] = (uint8_t)scale;
+        }
+    }
+}
+
 }  // namespace
 
 cudaError_t launch_kv_append(const AppendArgs &a, cudaStream_t stream) {
@@ -418,6 +488,7 @@ cudaError_t launch_kv_append(const AppendArgs &a, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    if (a.fp4) return cudaLaunchKernelEx(&cfg, append_write_fp4_kernel, a);
     if (a.fp8) return cudaLaunchKernelEx(&cfg, append_write_kernel<true>, a);
     return cudaLaunchKernelEx(&cfg, append_write_kernel<false>, a);
 }

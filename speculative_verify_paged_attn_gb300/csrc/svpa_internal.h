@@ -221,6 +221,7 @@ struct CommitArgs {
     uint8_t *v_pool;
     int32_t *err;
     int32_t B, n_q, max_blocks, num_blocks, path_width, Hkv, row_bytes;
+    int32_t scale_bytes;  // of a row, behind the tile's 16 rows (4-bit pages; else 0)
 };
 cudaError_t launch_block_table_commit(const CommitArgs &a, cudaStream_t stream);
 
@@ -242,7 +243,9 @@ struct AppendArgs {
     int32_t *err;
     size_t page_bytes;      // one block, all kv heads
     int32_t scales_per_block;  // FP8: Hkv (per page) or Hkv * 16 * D / 64 (per 64-element tile)
-    int32_t B, n_new, Hkv, D, max_blocks, num_blocks, fp8, scale_tile;
+    const float *k_factor;     // 4-bit pages: [Hkv] or null
+    const float *v_factor;
+    int32_t B, n_new, Hkv, D, max_blocks, num_blocks, fp8, scale_tile, fp4;
 };
 cudaError_t launch_kv_append(const AppendArgs &a, cudaStream_t stream);
 

@@ -134,11 +134,13 @@ svpa_status svpa_block_table_commit(int32_t batch, int32_t n_q, int32_t block_si
     CommitArgs a;
     memset(&a, 0, sizeof a);
     if (path_nodes) {
-        if (kv_dtype != SVPA_KV_BF16) return SVPA_ERR_UNSUPPORTED;  // per-page FP8 scales differ
+        // (per-page FP8 scales differ)
+        if (kv_dtype != SVPA_KV_BF16 && kv_dtype != SVPA_KV_FP4_E2M1) return SVPA_ERR_UNSUPPORTED;
         if (!k_pool || !v_pool || path_width < 1 || num_kv_heads < 1 || (head_dim != 64 && head_dim != 128))
             return SVPA_ERR_INVALID_ARG;
         if (!aligned16(k_pool) || !aligned16(v_pool)) return SVPA_ERR_INVALID_ARG;
-        a.row_bytes = head_dim * 2;
+        a.row_bytes = kv_dtype == SVPA_KV_BF16 ? head_dim * 2 : head_dim / 2;
+        a.scale_bytes = kv_dtype == SVPA_KV_BF16 ? 0 : head_dim / 16;
     }
     a.block_table = block_table;
     a.context_lens = context_lens;

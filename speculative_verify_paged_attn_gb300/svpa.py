@@ -22,6 +22,7 @@ LIB_PATH = os.path.join(_HERE, "libsvpa.so")
 
 SVPA_KV_BF16 = 0
 SVPA_KV_FP8_E4M3 = 1
+SVPA_KV_FP4_E2M1 = 2
 SVPA_LOGITS_FP32 = 0
 SVPA_LOGITS_BF16 = 1
 STATUS = {0: "SVPA_OK", 1: "SVPA_ERR_INVALID_ARG", 2: "SVPA_ERR_UNSUPPORTED", 3: "SVPA_ERR_CUDA",
@@ -34,7 +35,9 @@ EXPORTS = ("svpa_attn_workspace_size", "svpa_attn_kernel", "svpa_paged_verify_at
            "svpa_spec_accept_logits_workspace_size", "svpa_wait_selftest", "svpa_spec_accept_tree_logits",
            "svpa_paged_prompt_attn_workspace_size", "svpa_paged_prompt_attn",
            "svpa_prefix_verify_attn_workspace_size", "svpa_prefix_verify_attn",
-           "svpa_block_table_build_workspace_size", "svpa_block_table_build", "svpa_kv_write", "svpa_logits_process")
+           "svpa_block_table_build_workspace_size", "svpa_block_table_build", "svpa_kv_write", "svpa_logits_process",
+           "svpa_qk_norm_rope", "svpa_rope_kv_write", "svpa_kv_read", "svpa_kv_append_fp4",
+           "svpa_paged_verify_attn_fp4_workspace_size", "svpa_paged_verify_attn_fp4")
 
 
 class SvpaError(RuntimeError):
@@ -65,7 +68,14 @@ class LogitsParams(ctypes.Structure):
                 ("max_history", ctypes.c_int32), ("logits_dtype", ctypes.c_int32)]
 
 
-_BF16, _F32, _I32, _U32 = torch.bfloat16, torch.float32, torch.int32, torch.uint32
+class RopeParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("num_tokens", "num_q_heads", "num_kv_heads", "head_dim", "rotary_dim", "interleaved", "max_position",
+                 "block_size", "num_blocks", "kv_dtype", "scale_tile")] + [("eps", ctypes.c_float)] + \
+               [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride", "q_out_stride", "k_out_stride")]
+
+
+_BF16, _F32, _I32, _U32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint32, torch.uint8
 
 _lib = None
 
@@ -102,6 +112,12 @@ def load(path: str = LIB_PATH):
     L.svpa_block_table_build.argtypes = [I] * 5 + [P, P, I] + [P] * 7 + [U, P, P]
     L.svpa_kv_write.argtypes = [I] * 7 + [P, P, ctypes.c_int64, ctypes.c_int64] + [P] * 7
     L.svpa_logits_process.argtypes = [ctypes.POINTER(LogitsParams)] + [P] * 16
+    L.svpa_qk_norm_rope.argtypes = [ctypes.POINTER(RopeParams)] + [P] * 10
+    L.svpa_rope_kv_write.argtypes = [ctypes.POINTER(RopeParams)] + [P] * 17
+    L.svpa_kv_read.argtypes = [I] * 7 + [P] * 9 + [ctypes.c_int64, ctypes.c_int64, P, P]
+    L.svpa_kv_append_fp4.argtypes = [I] * 7 + [P] * 13
+    L.svpa_paged_verify_attn_fp4_workspace_size.argtypes = [ctypes.POINTER(AttnParams), ctypes.POINTER(U)]
+    L.svpa_paged_verify_attn_fp4.argtypes = [ctypes.POINTER(AttnParams)] + [P] * 11 + [U, P, P]
     L.svpa_check_error.argtypes = [P, P]
     L.svpa_wait_selftest.argtypes = [ctypes.c_uint64, P, P, P]
     L.svpa_status_string.argtypes = [I]
@@ -151,9 +167,11 @@ VARIANT_AUTO, VARIANT_MMA, VARIANT_TCGEN05 = 0, 1, 2
 
 def attn_params(batch, n_q, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, num_blocks,
                 kv_fp8=False, sm_scale=None, split_pages=0, block_size=16, variant=0,
-                scale_tile=0) -> AttnParams:
+                scale_tile=0, kv_fp4=False) -> AttnParams:
+    """kv_fp4: 4-bit pages (paged_verify_attn_fp4)."""
+    kv = SVPA_KV_FP4_E2M1 if kv_fp4 else SVPA_KV_FP8_E4M3 if kv_fp8 else SVPA_KV_BF16
     return AttnParams(batch, n_q, num_q_heads, num_kv_heads, head_dim, block_size,
-                      max_blocks_per_seq, num_blocks, SVPA_KV_FP8_E4M3 if kv_fp8 else SVPA_KV_BF16,
+                      max_blocks_per_seq, num_blocks, kv,
                       1.0 / math.sqrt(head_dim) if sm_scale is None else sm_scale, split_pages,
                       variant, scale_tile)
 
@@ -372,13 +390,14 @@ def spec_accept_tree_logits(parent: Sequence[int], target_logits, draft_logits, 
 
 def block_table_commit(n_q, block_table, context_lens, accepted_len, refcount, free_stack, free_top,
                        *, error_flag, path_nodes=None, k_pool=None, v_pool=None, num_kv_heads=0,
-                       head_dim=0, kv_fp8=False, stream=None, check=True) -> int:
+                       head_dim=0, kv_fp8=False, kv_fp4=False, stream=None, check=True) -> int:
     B, max_blocks = block_table.shape
     st = load().svpa_block_table_commit(
         B, n_q, 16, max_blocks, refcount.shape[0], _p(block_table), _p(context_lens),
         _p(accepted_len), _p(refcount), _p(free_stack), _p(free_top), _p(path_nodes),
         0 if path_nodes is None else path_nodes.shape[1], _p(k_pool), _p(v_pool), num_kv_heads,
-        head_dim, SVPA_KV_FP8_E4M3 if kv_fp8 else SVPA_KV_BF16, _p(error_flag), _stream(stream))
+        head_dim, SVPA_KV_FP4_E2M1 if kv_fp4 else SVPA_KV_FP8_E4M3 if kv_fp8 else SVPA_KV_BF16, _p(error_flag),
+        _stream(stream))
     if check:
         _check(st, "svpa_block_table_commit")
     return st
@@ -453,6 +472,153 @@ def kv_write(new_k, new_v, slot_map, k_pool, v_pool, *, error_flag, k_scale=None
         _arr(error_flag, _I32, 1, "error_flag"), _stream(stream))
     if check:
         _check(st, "svpa_kv_write")
+    return st
+
+
+def fp4_page_bytes(head_dim: int) -> int:
+    """Bytes of one kv head's 16 rows in a 4-bit page: the last dimension of a pool [num_blocks, Hkv, 9 D]."""
+    return 9 * head_dim
+
+
+def _page_kind(pool, fp4: bool):
+    """(kv_dtype, the element type a pool of that kind has)."""
+    if fp4:
+        return SVPA_KV_FP4_E2M1, _U8
+    return (SVPA_KV_FP8_E4M3, pool.dtype) if pool.element_size() == 1 else (SVPA_KV_BF16, _BF16)
+
+
+def _page_args(k_pool, v_pool, k_scale, v_scale, k_factor, v_factor, Hkv: int, D: int, fp4: bool):
+    """The pool, scale and factor pointers of a call on pages of any kind, and its kv_dtype."""
+    kind, pool = _page_kind(k_pool, fp4)
+    blocks = k_pool.shape[0]
+    page = blocks * Hkv * (9 * D if fp4 else 16 * D)
+    scales = blocks * Hkv * 16 * (D // 64) if kind == SVPA_KV_FP8_E4M3 else 0
+    return kind, [_arr(k_pool, pool, page, "k_pool"), _arr(v_pool, pool, page, "v_pool"),
+                  _arr(k_scale, _F32, scales, "k_scale"), _arr(v_scale, _F32, scales, "v_scale"),
+                  _arr(k_factor, _F32, Hkv, "k_factor"), _arr(v_factor, _F32, Hkv, "v_factor")]
+
+
+def _rows(t, like, what: str) -> int:
+    """The token stride of bf16 rows t [T, H, D] of `like`'s shape."""
+    if t.dtype is not _BF16 or t.dim() != 3 or t.shape != like.shape:
+        raise SvpaError(1, f"{what}: bf16 [tokens, heads, head_dim] of {tuple(like.shape)} expected")
+    return _row_stride(t, what)
+
+
+def _rope_params(q, k, v, q_out, k_out, cos_sin, eps, interleaved, kind=SVPA_KV_BF16, num_blocks=1,
+                 scale_tile=0) -> RopeParams:
+    T, Hkv, D = k.shape
+    if cos_sin is not None and cos_sin.dim() != 2:
+        raise SvpaError(1, "cos_sin: [max_position, rotary_dim] expected")
+    if (q is None) != (q_out is None):
+        raise SvpaError(1, "q and q_out: both or neither")
+    ks = _rows(k, k, "k")
+    if q is not None and (q.shape[0] != T or q.shape[2] != D):
+        raise SvpaError(1, "q: the tokens and head dimension of k expected")
+    return RopeParams(T, 0 if q is None else q.shape[1], Hkv, D, 0 if cos_sin is None else cos_sin.shape[1],
+                      int(interleaved), 1 if cos_sin is None else cos_sin.shape[0], 16, num_blocks, kind, scale_tile,
+                      float(eps), 0 if q is None else _rows(q, q, "q"), ks, ks if v is None else _rows(v, k, "v"),
+                      0 if q is None else _rows(q_out, q, "q_out"), ks if k_out is None else _rows(k_out, k, "k_out"))
+
+
+def qk_norm_rope(q, k, positions, cos_sin, q_out, k_out, *, error_flag, q_weight=None, k_weight=None, eps=1e-6,
+                 interleaved=False, stream=None, check=True) -> int:
+    """svpa_qk_norm_rope: q [T, Hq, D] and k [T, Hkv, D] (bf16; slices of a fused
+    projection along the heads are taken as they are) normed with q_weight /
+    k_weight [D] (None: not) and rotated at positions [T] by cos_sin
+    [max_position, R] (None: not), into q_out and k_out (may be q and k)."""
+    p = _rope_params(q, k, None, q_out, k_out, cos_sin, eps, interleaved)
+    if k_out is None:
+        raise SvpaError(1, "k_out: rows expected")
+    st = load().svpa_qk_norm_rope(
+        ctypes.byref(p), _p(q), _p(k), _arr(positions, _I32, p.num_tokens, "positions"),
+        _arr(cos_sin, _F32, 0, "cos_sin"), _arr(q_weight, _BF16, p.head_dim, "q_weight"),
+        _arr(k_weight, _BF16, p.head_dim, "k_weight"), _p(q_out), _p(k_out), _arr(error_flag, _I32, 1, "error_flag"),
+        _stream(stream))
+    if check:
+        _check(st, "svpa_qk_norm_rope")
+    return st
+
+
+def rope_kv_write(k, v, positions, slot_map, cos_sin, k_pool, v_pool, *, error_flag, q=None, q_out=None,
+                  q_weight=None, k_weight=None, eps=1e-6, interleaved=False, k_scale=None, v_scale=None, scale_tile=0,
+                  fp4=False, k_factor=None, v_factor=None, stream=None, check=True) -> int:
+    """svpa_rope_kv_write: qk_norm_rope with the keys, and v [T, Hkv, D] as it is,
+    written to the slots of slot_map [T] of bf16, FP8 (scale_tile 64) or 4-bit
+    (fp4: uint8 [num_blocks, Hkv, 9 D]) pages."""
+    T, Hkv, D = k.shape
+    kind, pages = _page_args(k_pool, v_pool, k_scale, v_scale, k_factor, v_factor, Hkv, D, fp4)
+    p = _rope_params(q, k, v, q_out, None, cos_sin, eps, interleaved, kind, k_pool.shape[0], scale_tile)
+    st = load().svpa_rope_kv_write(
+        ctypes.byref(p), _p(q), _p(k), _p(v), _arr(positions, _I32, T, "positions"),
+        _arr(slot_map, _I32, T, "slot_map"), _arr(cos_sin, _F32, 0, "cos_sin"), _arr(q_weight, _BF16, D, "q_weight"),
+        _arr(k_weight, _BF16, D, "k_weight"), _p(q_out), *pages, _arr(error_flag, _I32, 1, "error_flag"),
+        _stream(stream))
+    if check:
+        _check(st, "svpa_rope_kv_write")
+    return st
+
+
+def kv_read(slot_map, k_pool, v_pool, k_out, v_out, *, error_flag, k_scale=None, v_scale=None, scale_tile=0, fp4=False,
+            k_factor=None, v_factor=None, stream=None, check=True) -> int:
+    """svpa_kv_read: the rows of slot_map [T] of bf16, FP8 (scale_tile 64) or 4-bit
+    pages as bf16 rows k_out, v_out [T, Hkv, D]."""
+    T, Hkv, D = k_out.shape
+    kind, pages = _page_args(k_pool, v_pool, k_scale, v_scale, k_factor, v_factor, Hkv, D, fp4)
+    ks, vs = _rows(k_out, k_out, "k_out"), _rows(v_out, k_out, "v_out")
+    st = load().svpa_kv_read(T, Hkv, D, 16, k_pool.shape[0], kind, scale_tile, _arr(slot_map, _I32, T, "slot_map"),
+                             *pages, _p(k_out), _p(v_out), ks, vs, _arr(error_flag, _I32, 1, "error_flag"),
+                             _stream(stream))
+    if check:
+        _check(st, "svpa_kv_read")
+    return st
+
+
+def kv_append_fp4(new_k, new_v, block_table, context_lens, refcount, free_stack, free_top, k_pool, v_pool, *,
+                  error_flag, k_factor=None, v_factor=None, stream=None, check=True) -> int:
+    """svpa_kv_append_fp4: kv_append of new_k/new_v [B, n_new, Hkv, D] into 4-bit
+    pages uint8 [num_blocks, Hkv, 9 D]."""
+    B, n_new, Hkv, D = new_k.shape
+    blocks, n = k_pool.shape[0], B * n_new * Hkv * D
+    page = blocks * Hkv * 9 * D
+    st = load().svpa_kv_append_fp4(
+        B, n_new, Hkv, D, 16, block_table.shape[1], blocks, _arr(new_k, _BF16, n, "new_k"),
+        _arr(new_v, _BF16, n, "new_v"), _arr(block_table, _I32, B * block_table.shape[1], "block_table"),
+        _arr(context_lens, _I32, B, "context_lens"), _arr(refcount, _I32, blocks, "refcount"),
+        _arr(free_stack, _I32, blocks, "free_stack"), _arr(free_top, _I32, 1, "free_top"),
+        _arr(k_pool, _U8, page, "k_pool"), _arr(v_pool, _U8, page, "v_pool"), _arr(k_factor, _F32, Hkv, "k_factor"),
+        _arr(v_factor, _F32, Hkv, "v_factor"), _arr(error_flag, _I32, 1, "error_flag"), _stream(stream))
+    if check:
+        _check(st, "svpa_kv_append_fp4")
+    return st
+
+
+def paged_verify_attn_fp4_workspace_size(params: AttnParams) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().svpa_paged_verify_attn_fp4_workspace_size(ctypes.byref(params), ctypes.byref(n)),
+           "svpa_paged_verify_attn_fp4_workspace_size")
+    return n.value
+
+
+def paged_verify_attn_fp4(params: AttnParams, q, k_pool, v_pool, block_table, context_lens, out, *, workspace,
+                          error_flag, k_factor=None, v_factor=None, ancestor_mask=None, lse=None, stream=None,
+                          check=True) -> int:
+    """svpa_paged_verify_attn_fp4: paged_verify_attn over 4-bit pages uint8
+    [num_blocks, Hkv, 9 D]; params from attn_params(..., kv_fp4=True)."""
+    m = _mask_array(ancestor_mask)
+    if m is not None and len(m) < params.n_q:
+        raise SvpaError(1, "svpa_paged_verify_attn_fp4: one ancestor mask per query")
+    b, d, h = params.batch, params.head_dim, params.num_kv_heads
+    rows, page = b * params.n_q * params.num_q_heads, params.num_blocks * h * 9 * d
+    st = load().svpa_paged_verify_attn_fp4(
+        ctypes.byref(params), _arr(q, _BF16, rows * d, "q"), _arr(k_pool, _U8, page, "k_pool"),
+        _arr(v_pool, _U8, page, "v_pool"), _arr(k_factor, _F32, h, "k_factor"), _arr(v_factor, _F32, h, "v_factor"),
+        _arr(block_table, _I32, b * params.max_blocks_per_seq, "block_table"),
+        _arr(context_lens, _I32, b, "context_lens"), None if m is None else ctypes.cast(m, ctypes.c_void_p),
+        _arr(out, _BF16, rows * d, "out"), _arr(lse, _F32, rows, "lse"), _p(workspace),
+        workspace.numel() * workspace.element_size(), _arr(error_flag, _I32, 1, "error_flag"), _stream(stream))
+    if check:
+        _check(st, "svpa_paged_verify_attn_fp4")
     return st
 
 
