@@ -38,7 +38,7 @@ SOURCES = {
     "kv_write.cu": ["-fmad=false"],
     "logits_process.cu": ["-fmad=false"],
     "svpa_admit_api.cu": [],
-    "rope_kv.cu": [],
+    "rope_kv.cu": ["-fmad=false"],
     "paged_verify_attn_fp4.cu": [],
     "svpa_fp4_api.cu": [],
 }

@@ -1,9 +1,37 @@
-// paged_verify_attn_fp4.cu -- paged verification attention over 4-bit pages.
+// paged_verify_attn_fp4.cu -- paged verification attention over 4-bit pages, on
+// the 5th-generation tensor cores (tcgen05 + TMEM) for sm_103a.
 //
-// One CTA per (sequence, kv head): the pages in turn decoded into shared
-// memory, scores and the running maximum and sum of each query row in fp32,
-// the output in registers.
+// out = softmax(Q K^T * scale + mask) V with K and V decoded on the way: a code
+// times its scale is exact in f16, so both products are f16 MMAs whose only
+// rounded operand is the softmax's weights; the heads' factors go into the
+// scores' scale and the output's.
+//
+// Both products are formed transposed.  S^T = K Q^T: the 128 tokens of a block
+// are the rows of the MMA and the query rows (heads of the group x queries) its
+// columns, padded to 16, 32, 64 or 128; O^T += V^T P^T: the head dimensions are
+// the rows.  A token's row of codes is what one thread decodes: for K into its
+// TMEM lane, which the MMA reads as its A operand, for V into shared memory.  In
+// the other orientation the query rows would be padded to 128 and both decoded
+// tiles would pass through shared memory twice, whose bandwidth is what bounds
+// this kernel.
+//
+// The softmax has a token a thread, so that a column's maximum lies across
+// threads: it is taken in a unit's first block, and after that only when some
+// score exceeds its column's reference by 2^8 (a vote a block).
+//
+// Work: the 128-token blocks of all (sequence, kv head) pairs, in that order,
+// split evenly over one persistent CTA per SM; the parts of a pair that is cut
+// are merged by the CTA that writes the last of them.
+// Warps: 0-3 decode K and turn the queries to f16; 4-11 softmax and epilogue
+// (4-7 the first half of the columns, 8-11 the second); 12-15 decode V (with 128
+// columns warps 0-3 do, to leave the softmax its registers); then one warp of
+// TMA copies and one that issues the MMAs.  A warp reads the TMEM lanes of
+// quadrant warp % 4.  Every role walks the same list of blocks.
+// All waits are bounded: a role whose wait ran out goes on without waiting.
 #include <math_constants.h>
+
+#include <algorithm>
+#include <cstddef>
 
 #include "fp4.cuh"
 #include "fp4_attn.h"
@@ -12,115 +40,921 @@ namespace svpa {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kPB = 8;                        // pages per block
+constexpr int kNB = kPB * kBlockSize;         // tokens per block
+constexpr float kRescaleLog2 = 8.f;           // a weight may be up to 2^8
+constexpr uint32_t kTmemCols = 512, kTmemS = 0, kTmemO = 256, kTmemK = 384;
+constexpr int kSlab = kNB * 128;              // 64 f16 columns of 128 rows
+constexpr float kLn2 = 0.69314718055994530942f;
+enum { kBarHalf0 = 1, kBarSoft = 3, kBarPrep = 4 };  // named barriers
 
-template <int D>
-__global__ void __launch_bounds__(kThreads) fp4_attn_kernel(const __grid_constant__ Fp4AttnArgs a) {
-    extern __shared__ float sm[];
-    const int M = a.M, tid = threadIdx.x, b = blockIdx.y, h = blockIdx.x;
-    float *sq = sm, *sk = sq + M * (D + 1), *sv = sk + 16 * (D + 1), *sp = sv + 16 * (D + 1);
-    float *mx = sp + M * 17, *sum = mx + M, *alpha = sum + M;
-    const int L = a.context_lens[b];
-    const long long end = (long long)L + a.n_q;
-    const int pages = (int)((end + 15) / 16);
-    if (L < 0 || pages > a.max_blocks) {
-        if (tid == 0) raise_error(a.err, SVPA_DEVERR_BAD_VALUE);
-        return;
+template <int D, int NP>
+struct Cfg {
+    static constexpr bool kBoth = NP == 128;  // warps 0-3 decode K and V
+    static constexpr int kProducerWarp = kBoth ? 12 : 16, kMmaWarp = kProducerWarp + 1;
+    static constexpr int kThreads = 32 * (kProducerWarp + 4);  // (two warps idle)
+    // registers a thread, from the 96 (128 with 16 warps) at launch: their sum
+    // over the warps of a scheduler stays within 5 * 96 (4 * 128)
+    static constexpr int kRegsDecode = kBoth ? 112 : 80, kRegsIssue = 64, kRegsSoftmax = kBoth ? 168 : 128;
+    static_assert((kBoth ? 1 : 2) * kRegsDecode + kRegsIssue + 2 * kRegsSoftmax <= (kBoth ? 4 * 128 : 5 * 96),
+                  "registers handed over");
+    static constexpr int kNH = NP / 2;              // columns of a softmax half
+    static constexpr int kCH = kNH < 32 ? kNH : 32; // ... taken at a time
+    static constexpr int kPBufs = NP == 128 ? 1 : 2;
+    static constexpr int kQ = NP * D * 2, kP = kNB * NP * 2;
+    static constexpr int kCodes = kNB * D / 2, kScales = kPB * 128;
+    static constexpr int kStage = 2 * (kCodes + kScales);
+    static constexpr int kRoom = (232448 - 8192 - 2 * kQ - kPBufs * kP - 4 * kSlab) / kStage;
+    static constexpr int kStages = kRoom < 8 ? kRoom : 8;
+};
+
+template <int D, int NP>
+struct Smem {
+    using C = Cfg<D, NP>;
+    uint8_t q[2][C::kQ];              // [slab][NP rows][128 B], 128-byte swizzle
+    uint8_t v[2][2 * kSlab];          // decoded V: [slab][128 tokens][128 B] (D 64: one slab)
+    uint8_t p[C::kPBufs][C::kP];      // weights: [token][NP columns]
+    uint8_t kc[C::kStages][C::kCodes], vc[C::kStages][C::kCodes];
+    uint8_t ks[C::kStages][C::kScales], vs[C::kStages][C::kScales];
+    float negm[2][64];                // minus the columns' reference maxima (0: none yet)
+    float m[2][64];
+    float fac[2][64];                 // what a raised maximum leaves of the sums
+    float inv[2][64];
+    float warp_col[2][4][64];         // a column's maximum or sum in each quadrant
+    float mult[4];                    // score -> log2 units, per unit in flight
+    int32_t row_off[128];             // query row -> row of out behind the unit's first
+    uint64_t raw_full[C::kStages], raw_empty[C::kStages];
+    uint64_t k_full[2], k_empty[2], v_full[2];
+    uint64_t q_full[2], q_ready[2], q_empty[2];
+    uint64_t s_full[2], s_empty[2], p_full[2], pv_done[2];
+    uint64_t o_full, o_empty;
+    long long scan[32];
+    long long work, first_x;          // all blocks; this CTA's first
+    int32_t b0, h0, f0;
+    uint32_t tmem_base;
+    uint32_t qmax[4];
+    int32_t last;
+};
+
+// ---------------------------------------------------------------- small pieces
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+// A wait that a role whose earlier wait ran out passes over.
+__device__ __forceinline__ void wait(bool &ok, uint64_t *bar, int phase, int32_t *err) {
+    if (!ok) return;
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+        if (mbar_try_wait(bar, (uint32_t)(phase & 1))) return;
+    ok = mbar_wait(bar, (uint32_t)(phase & 1), err);
+}
+__device__ __forceinline__ void warp_arrive(uint64_t *bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+// Whether `v` holds for any of the `threads` threads of a named barrier.
+__device__ __forceinline__ bool barrier_any(int id, int threads, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+        "barrier.cta.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(id), "r"(threads), "r"((uint32_t)v)
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ float warp_max(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+__device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, int c0, int c1, uint64_t *bar,
+                                            uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_"
+        "hint [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int c0, int c1, int c2, uint64_t *bar,
+                                            uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_"
+        "hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
+}
+
+// N consecutive columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(at));
+}
+__device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(at));
+}
+__device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[32]) { tmem_ld32(at, r); }
+__device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(at), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};" ::"r"(at),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t (&r)[32]) { tmem_st32(at, r); }
+
+// The sums over a warp's lanes of N columns: v[0] of lane l is column l % N's.
+template <int N>
+__device__ __forceinline__ void column_sums(float (&v)[N], int lane) {
+#pragma unroll
+    for (int h = N / 2; h >= 1; h /= 2) {
+        const bool upper = lane & h;
+#pragma unroll
+        for (int i = 0; i < h; ++i) {
+            const float send = upper ? v[i] : v[i + h], keep = upper ? v[i + h] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, h);
+        }
     }
-    for (int i = tid; i < M * D; i += kThreads) {
-        const int r = i / D, d = i % D;
-        const float x =
-            __bfloat162float(a.q[(((size_t)b * a.n_q + r / a.G) * a.Hq + (size_t)h * a.G + r % a.G) * D + d]);
-        if (!(fabsf(x) <= 3.4e38f)) raise_error(a.err, SVPA_DEVERR_BAD_VALUE);
-        sq[r * (D + 1) + d] = x;
+#pragma unroll
+    for (int h = N; h < 32; h *= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], h);
+}
+
+// Byte of column chunk c (eight columns) of token t in the weights' tile, whose
+// rows of NP columns (64 a slab) have the swizzle as wide as they are.
+template <int NP>
+__device__ __forceinline__ uint32_t p_at(int t, int c) {
+    if constexpr (NP == 16) return (uint32_t)(t * 32 + ((c ^ ((t >> 2) & 1)) << 4));
+    else if constexpr (NP == 32) return (uint32_t)(t * 64 + ((c ^ ((t >> 1) & 3)) << 4));
+    else return (uint32_t)((c >> 3) * kSlab + t * 128 + (((c & 7) ^ (t & 7)) << 4));
+}
+// Its descriptor (MN-major, the tokens are K), from its first byte.
+template <int NP>
+__device__ __forceinline__ uint64_t p_desc(uint32_t at) {
+    constexpr uint32_t row = NP < 64 ? 2 * NP : 128;
+    constexpr uint64_t layout = NP == 16 ? 6 : NP == 32 ? 4 : 2;
+    return (umma_desc_sw128(at, kSlab, 8 * row) & ~(7ull << 61)) | layout << 61;
+}
+
+// f16 A and B, fp32 D, 128 rows; A and B as they lie (1: MN-major).
+__host__ __device__ constexpr uint32_t idesc(int N, int a_mn, int b_mn) {
+    return (1u << 4) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
+}
+
+// ---------------------------------------------------------------- the work list
+struct Piece {
+    int b, h, f, n, nb, L;  // sequence, kv head, first block, blocks, the pair's blocks, history
+    long long x;            // the first block's place in the list
+};
+
+__device__ __forceinline__ int blocks_of(const Fp4AttnArgs &a, int L) {
+    const long long pages = ((long long)L + a.n_q + kBlockSize - 1) / kBlockSize;
+    return L < 0 || pages > a.max_blocks ? 0 : (int)((pages + kPB - 1) / kPB);
+}
+
+struct Walk {
+    int b, h, f, nb, L;
+    long long x, left;
+    __device__ __forceinline__ bool next(const Fp4AttnArgs &a, Piece &p) {
+        if (left <= 0) return false;
+        while (nb == 0) {
+            L = __ldg(a.context_lens + b);
+            nb = blocks_of(a, L);
+            if (nb == 0) ++b;  // (counts no blocks)
+        }
+        p.b = b, p.h = h, p.f = f, p.nb = nb, p.L = L, p.x = x;
+        p.n = (int)min((long long)(nb - f), left);
+        left -= p.n, x += p.n, f += p.n;
+        if (f == nb) {
+            f = 0;
+            if (++h == a.Hkv) h = 0, ++b, nb = 0;
+        }
+        return true;
     }
-    for (int r = tid; r < M; r += kThreads) mx[r] = -CUDART_INF_F, sum[r] = 0.f;
-    const float fk = fp4_factor(a.k_factor, h, a.err), fv = fp4_factor(a.v_factor, h, a.err);
-    constexpr int kAcc = 128 * D / kThreads;
-    float acc[kAcc];
+};
+
+// ---------------------------------------------------------------- decoding
+// 32 codes and their two scales to 16 f16 pairs.
+__device__ __forceinline__ void decode32(const uint4 &w, uint32_t two_scales, uint32_t *out) {
+    const uint32_t s = e4m3x2_to_f16x2(two_scales & 0xffffu);
+    const uint32_t lo = __byte_perm(s, s, 0x1010), hi = __byte_perm(s, s, 0x3232);
+    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int i = 0; i < kAcc; ++i) acc[i] = 0.f;
-    for (int p = 0; p < pages; ++p) {
-        int blk = a.block_table[(size_t)b * a.max_blocks + p];
-        if (blk < 0 || blk >= a.num_blocks) {
-            if (tid == 0) raise_error(a.err, SVPA_DEVERR_BAD_BLOCK);
-            blk = 0;
-        }
-        __syncthreads();
-        const size_t tile = ((size_t)blk * a.Hkv + h) * fp4_tile_bytes(D);
-        for (int i = tid; i < 2 * 16 * D / 8; i += kThreads) {
-            const int kv = i / (16 * D / 8), w = i % (16 * D / 8), s = w / (D / 8), c = w % (D / 8);
-            const uint8_t *page = (kv ? a.v_pool : a.k_pool) + tile;
-            uint32_t e[4];
-            e2m1x8_to_f16(reinterpret_cast<const uint32_t *>(page + s * (D / 2))[c], e);
-            const float sc = e4m3_value(page[fp4_code_bytes(D) + s * (D / 16) + c / 2]);
-            float *dst = (kv ? sv : sk) + s * (D + 1) + 8 * c;
-            const bool in = p * 16 + s < end;
+    for (int i = 0; i < 4; ++i) {
+        uint32_t h[4];
+        e2m1x8_to_f16(in[i], h);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 f = f16x2_to_float2(e[j]);
-                dst[2 * j] = in ? f.x * sc : 0.f;
-                dst[2 * j + 1] = in ? f.y * sc : 0.f;
-            }
-        }
-        __syncthreads();
-        for (int i = tid; i < M * 16; i += kThreads) {
-            const int r = i / 16, s = i % 16, at = p * 16 + s - L;
-            float dot = 0.f;
-            for (int d = 0; d < D; ++d) dot = fmaf(sq[r * (D + 1) + d], sk[s * (D + 1) + d], dot);
-            const bool seen = at < 0 || (at < a.n_q && (a.anc[r / a.G] >> at & 1));
-            sp[r * 17 + s] = seen ? dot * (a.scale_log2 * fk) : -CUDART_INF_F;
-        }
-        __syncthreads();
-        for (int r = tid; r < M; r += kThreads) {
-            float top = mx[r];
-            for (int s = 0; s < 16; ++s) top = fmaxf(top, sp[r * 17 + s]);
-            const float ref = top == -CUDART_INF_F ? 0.f : top;
-            alpha[r] = ex2_approx(mx[r] - ref);
-            float l = sum[r] * alpha[r];
-            for (int s = 0; s < 16; ++s) {
-                const float e = ex2_approx(sp[r * 17 + s] - ref);
-                sp[r * 17 + s] = e;
-                l += e;
-            }
-            mx[r] = top;
-            sum[r] = l;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kAcc; ++i) {
-            const int r = (tid + i * kThreads) / D, d = tid % D;
-            if (r >= M) break;
-            float v = acc[i] * alpha[r];
-            for (int s = 0; s < 16; ++s) v = fmaf(sp[r * 17 + s], sv[s * (D + 1) + d], v);
-            acc[i] = v;
-        }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kAcc; ++i) {
-        const int r = (tid + i * kThreads) / D, d = tid % D;
-        if (r >= M) break;
-        const size_t o = ((size_t)b * a.n_q + r / a.G) * a.Hq + (size_t)h * a.G + r % a.G;
-        a.out[o * D + d] = __float2bfloat16_rn(acc[i] * fv / sum[r]);
-        if (d == 0 && a.lse) a.lse[o] = (mx[r] + __log2f(sum[r])) * 0.69314718055994530942f;
+        for (int j = 0; j < 4; ++j) out[4 * i + j] = mul_f16x2(h[j], i < 2 ? lo : hi);
     }
 }
 
+// Chunk c (32 codes) of token t of a landed block, and all of its scales.
 template <int D>
-cudaError_t launch(const Fp4AttnArgs &a, cudaStream_t st) {
-    const int smem = (a.M * (D + 1) + 32 * (D + 1) + a.M * 20) * 4;
-    const cudaError_t e =
-        cudaFuncSetAttribute(fp4_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 << 10);
+__device__ __forceinline__ uint4 codes_at(const uint8_t *codes, int t, int c) {
+    // (rows of 64 or 32 bytes, with the swizzle as wide)
+    const int sw = D == 128 ? (t >> 1) & 3 : (t >> 2) & 1;
+    return *reinterpret_cast<const uint4 *>(codes + t * (D / 2) + ((c ^ sw) << 4));
+}
+template <int D>
+__device__ __forceinline__ uint2 scales_at(const uint8_t *scales, int t) {
+    const uint8_t *at = scales + (t >> 4) * 128 + (t & 15) * (D / 16);
+    if constexpr (D == 128) return *reinterpret_cast<const uint2 *>(at);
+    else return make_uint2(*reinterpret_cast<const uint32_t *>(at), 0u);
+}
+
+template <int D, int NP>
+__device__ __forceinline__ void decode_k(Smem<D, NP> &sm, int stage, uint32_t lane_base, int buf, int t) {
+    const uint2 sc = scales_at<D>(sm.ks[stage], t);
+#pragma unroll
+    for (int c = 0; c < D / 32; c += 2) {
+        uint32_t r[32];
+        const uint32_t s = c ? sc.y : sc.x;
+        decode32(codes_at<D>(sm.kc[stage], t, c), s, r);
+        decode32(codes_at<D>(sm.kc[stage], t, c + 1), s >> 16, r + 16);
+        tmem_st32(lane_base + kTmemK + 64 * buf + 16 * c, r);
+    }
+}
+
+template <int D, int NP>
+__device__ __forceinline__ void decode_v(Smem<D, NP> &sm, int stage, int buf, int t, bool held) {
+    const uint2 sc = scales_at<D>(sm.vs[stage], t);
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+        uint32_t r[16];
+        const uint32_t s = c < 2 ? sc.x : sc.y;
+        decode32(codes_at<D>(sm.vc[stage], t, c), c & 1 ? s >> 16 : s, r);
+        uint8_t *row = sm.v[buf] + (c >> 1) * kSlab + t * 128;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            // (a slot behind the sequence's last: what it holds is anything)
+            const uint4 x = held ? make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3])
+                                 : make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4 *>(row + (((4 * (c & 1) + k) ^ (t & 7)) << 4)) = x;
+        }
+    }
+}
+
+// The unit's queries, bf16 as they landed, to f16 in place at one power of two
+// that puts the largest of them in [2^14, 2^15); what falls below f16's smallest
+// value there is less than 2^-39 of it.  Sets the scores' multiplier.
+template <int D, int NP>
+__device__ __forceinline__ void prepare_queries(Smem<D, NP> &sm, const Fp4AttnArgs &a, int slot, int unit, float kf,
+                                                int tid) {
+    constexpr int kRow = 8, kSlabs = D / 64;  // 16-byte chunks of a row of a slab
+    uint4 *q = reinterpret_cast<uint4 *>(sm.q[slot]);
+    const int per = a.M * kRow;
+    uint32_t top = 0u;
+#pragma unroll 1
+    for (int s = 0; s < kSlabs; ++s)
+        for (int i = tid; i < per; i += 128) top = max(top, bf16_amax8(q[s * NP * kRow + i]));
+    top = __reduce_max_sync(0xffffffffu, top);
+    if ((tid & 31) == 0) sm.qmax[tid >> 5] = top;
+    named_barrier_sync(kBarPrep, 128);
+    top = max(max(sm.qmax[0], sm.qmax[1]), max(sm.qmax[2], sm.qmax[3]));
+    int e = 0;
+    if (top > 0x7f7fu) {
+        if (tid == 0) raise_error(a.err, SVPA_DEVERR_BAD_VALUE);
+    } else if (top != 0u) {
+        e = min(max(141 - (int)(top >> 7), -126), 126);
+    }
+    const float scale = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll 1
+    for (int s = 0; s < kSlabs; ++s)
+#pragma unroll 2
+        for (int i = tid; i < per; i += 128) {
+            const uint4 x = q[s * NP * kRow + i];
+            uint4 y;
+            y.x = pack_f16x2(bf16_lo(x.x) * scale, bf16_hi(x.x) * scale);
+            y.y = pack_f16x2(bf16_lo(x.y) * scale, bf16_hi(x.y) * scale);
+            y.z = pack_f16x2(bf16_lo(x.z) * scale, bf16_hi(x.z) * scale);
+            y.w = pack_f16x2(bf16_lo(x.w) * scale, bf16_hi(x.w) * scale);
+            q[s * NP * kRow + i] = y;
+        }
+    // (positive, so that a masked score stays -inf)
+    if (tid == 0)
+        sm.mult[unit & 3] = fmaxf(a.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23) * kf, 1e-30f);
+    named_barrier_sync(kBarPrep, 128);  // (qmax is free again)
+}
+
+// ---------------------------------------------------------------- the softmax
+template <int D, int NP>
+__device__ __forceinline__ void softmax_role(Smem<D, NP> &sm, const Fp4AttnArgs &a, Walk w, uint32_t tmem) {
+    using C = Cfg<D, NP>;
+    constexpr int NH = C::kNH, CH = C::kCH, NCH = NH / CH;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int quad = warp & 3, half = (warp - 4) >> 2, t = 32 * quad + lane, c0 = half * NH;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
+    const int live = min(max(a.M - c0, 0), NH);  // columns with a query row
+    const long long W = sm.work, first_x = w.x;
+    const int nsh = (int)min((long long)gridDim.x, W);
+    auto cta_of = [&](long long x) { return (int)(((x + 1) * nsh - 1) / W); };
+    bool ok = true;
+    int j = 0, unit = 0;
+    Piece p;
+    uint64_t sum[NH / 2];
+#pragma unroll 1
+    for (; w.next(a, p); ++unit) {
+#pragma unroll
+        for (int i = 0; i < NH / 2; ++i) sum[i] = 0ull;
+        float mult = 1.f;
+#pragma unroll 1
+        for (int i = 0; i < p.n; ++i, ++j) {
+            wait(ok, &sm.s_full[j & 1], j >> 1, a.err);
+            tc_fence_after();
+            if (i == 0) mult = sm.mult[unit & 3];
+            const uint64_t mult2 = pack2(mult, mult);
+            const uint32_t sa = lanes + kTmemS + (uint32_t)((j & 1) * NP + c0);
+            // which columns see this thread's token
+            const int at = (p.f + i) * kNB + t - p.L;  // >= 0: a speculative slot
+            const bool edge = (p.f + i + 1) * kNB > p.L;
+            unsigned long long vis = ~0ull;
+            if (edge && at >= 0)
+                vis = at >= a.n_q ? 0ull : NP == 128 ? a.slots[at][half] : a.slots[at][0] >> c0;
+            uint32_t s[CH];
+            auto load = [&](int ch) {
+                tmem_ld(sa + (uint32_t)(ch * CH), s);
+                tmem_ld_wait();
+                if (edge) {
+                    const uint32_t v = (uint32_t)(vis >> (ch * CH));
+#pragma unroll
+                    for (int c = 0; c < CH; ++c)
+                        if (!(v >> c & 1u)) s[c] = 0xff800000u;
+                }
+            };
+            auto shift = [&](int ch) {  // scores to log2 units below their reference
+                const float4 *nm = reinterpret_cast<const float4 *>(&sm.negm[half][ch * CH]);
+#pragma unroll
+                for (int c = 0; c < CH; c += 4) {
+                    const float4 n = nm[c / 4];
+                    const float2 u = unpack2(fma2(pack2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), mult2,
+                                                  pack2(n.x, n.y)));
+                    const float2 v = unpack2(fma2(pack2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), mult2,
+                                                  pack2(n.z, n.w)));
+                    s[c] = __float_as_uint(u.x), s[c + 1] = __float_as_uint(u.y);
+                    s[c + 2] = __float_as_uint(v.x), s[c + 3] = __float_as_uint(v.y);
+                }
+            };
+            bool raise = i == 0;
+            if (!raise) {
+                float top = -CUDART_INF_F;
+#pragma unroll
+                for (int ch = 0; ch < NCH; ++ch) {
+                    load(ch);
+                    shift(ch);
+#pragma unroll
+                    for (int c = 0; c < CH; c += 2) top = max3(top, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+                }
+                raise = barrier_any(kBarHalf0 + half, 128, top > kRescaleLog2);
+            }
+            if (raise) {
+                // the columns' maxima over the block's tokens, and new references
+#pragma unroll
+                for (int ch = 0; ch < NCH; ++ch) {
+                    load(ch);
+                    float mine = -CUDART_INF_F;
+#pragma unroll
+                    for (int c = 0; c < CH; ++c) {
+                        const float v = warp_max(__uint_as_float(s[c]));
+                        if (lane == c) mine = v;
+                    }
+                    if (lane < CH) sm.warp_col[half][quad][ch * CH + lane] = mine;
+                }
+                named_barrier_sync(kBarHalf0 + half, 128);
+                float m_new[NCH], fac[NCH];
+#pragma unroll
+                for (int ch = 0; ch < NCH; ++ch) {
+                    const int c = ch * CH + (lane & (CH - 1));
+                    const float top = fmaxf(fmaxf(sm.warp_col[half][0][c], sm.warp_col[half][1][c]),
+                                            fmaxf(sm.warp_col[half][2][c], sm.warp_col[half][3][c])) *
+                                      mult;
+                    const float old = i == 0 ? -CUDART_INF_F : sm.m[half][c];
+                    m_new[ch] = fmaxf(old, top);
+                    fac[ch] = old == m_new[ch] ? 1.f : ex2_approx(old - m_new[ch]);
+                }
+                named_barrier_sync(kBarHalf0 + half, 128);
+                if (quad == 0 && lane < CH) {
+#pragma unroll
+                    for (int ch = 0; ch < NCH; ++ch) {
+                        sm.m[half][ch * CH + lane] = m_new[ch];
+                        sm.negm[half][ch * CH + lane] = m_new[ch] == -CUDART_INF_F ? 0.f : -m_new[ch];
+                        sm.fac[half][ch * CH + lane] = fac[ch];
+                    }
+                }
+                named_barrier_sync(kBarHalf0 + half, 128);
+                if (i > 0) {
+                    // what was summed so far, here and in O, once the last block's P V is there
+                    wait(ok, &sm.pv_done[(j - 1) & 1], (j - 1) >> 1, a.err);
+                    tc_fence_after();
+#pragma unroll
+                    for (int ch = 0; ch < NCH; ++ch) {
+                        const float2 *fc = reinterpret_cast<const float2 *>(&sm.fac[half][ch * CH]);
+                        uint32_t o[CH];
+                        tmem_ld(lanes + kTmemO + (uint32_t)(c0 + ch * CH), o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int c = 0; c < CH; c += 2) {
+                            const float2 f = fc[c / 2];
+                            sum[(ch * CH + c) / 2] = mul2(sum[(ch * CH + c) / 2], pack2(f.x, f.y));
+                            o[c] = __float_as_uint(__uint_as_float(o[c]) * f.x);
+                            o[c + 1] = __float_as_uint(__uint_as_float(o[c + 1]) * f.y);
+                        }
+                        tmem_st(lanes + kTmemO + (uint32_t)(c0 + ch * CH), o);
+                    }
+                    tmem_st_wait();
+                    tc_fence_before();
+                }
+            }
+            // the weights of block j, once the products that read their place are done
+            const int before = j - C::kPBufs;
+            if (before >= 0) wait(ok, &sm.pv_done[before & 1], before >> 1, a.err);
+            uint8_t *pt = sm.p[j % C::kPBufs];
+#pragma unroll
+            for (int ch = 0; ch < NCH; ++ch) {
+                if (NCH > 1 || raise) {
+                    load(ch);
+                    shift(ch);
+                }
+                if (ch == NCH - 1) {  // S is in registers
+                    tc_fence_before();
+                    warp_arrive(&sm.s_empty[j & 1]);
+                }
+#pragma unroll
+                for (int c = 0; c < CH; c += 8) {
+                    if (ch * CH + c >= live) break;  // the same for the whole warp
+                    uint32_t pk[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float u = ex2_approx(__uint_as_float(s[c + 2 * k]));
+                        const float v = ex2_approx(__uint_as_float(s[c + 2 * k + 1]));
+                        sum[(ch * CH + c) / 2 + k] = add2(sum[(ch * CH + c) / 2 + k], pack2(u, v));
+                        pk[k] = pack_f16x2(u, v);  // a weight keeps 11 bits, as many as f16 pages would
+                    }
+                    *reinterpret_cast<uint4 *>(pt + p_at<NP>(t, (c0 + ch * CH + c) / 8)) =
+                        make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                }
+            }
+            fence_proxy_async_smem();
+            warp_arrive(&sm.p_full[j & 1]);
+        }
+        // ------------------------------------------------ the unit's epilogue
+        const long long px = p.x - p.f;
+        const int c_first = cta_of(px), parts = cta_of(px + p.nb - 1) - c_first + 1;
+        const int slot = 2 * (int)blockIdx.x + (p.x == first_x ? 0 : 1);
+        const float fv = fp4_factor(a.v_factor, p.h, a.err);
+        const size_t row0 = (size_t)p.b * a.n_q * a.Hq + (size_t)p.h * a.G;
+#pragma unroll
+        for (int ch = 0; ch < NCH; ++ch) {
+            float v[CH];
+#pragma unroll
+            for (int c = 0; c < CH; c += 2) {
+                const float2 f = unpack2(sum[(ch * CH + c) / 2]);
+                v[c] = f.x, v[c + 1] = f.y;
+            }
+            column_sums<CH>(v, lane);
+            if (lane < CH) sm.warp_col[half][quad][ch * CH + lane] = v[0];
+        }
+        named_barrier_sync(kBarHalf0 + half, 128);
+        if (quad == 0 && lane < CH) {
+#pragma unroll
+            for (int ch = 0; ch < NCH; ++ch) {
+                const int c = ch * CH + lane;
+                const float l = (sm.warp_col[half][0][c] + sm.warp_col[half][1][c]) +
+                                (sm.warp_col[half][2][c] + sm.warp_col[half][3][c]);
+                sm.inv[half][c] = parts == 1 ? (l > 0.f ? fv / l : 0.f) : 1.f;
+                const int r = c0 + c;
+                if (r < a.M) {
+                    if (parts > 1)
+                        reinterpret_cast<float2 *>(a.part_ml)[(size_t)slot * a.M + r] = make_float2(sm.m[half][c], l);
+                    else if (a.lse)
+                        a.lse[row0 + sm.row_off[r]] = (sm.m[half][c] + __log2f(l)) * kLn2;
+                }
+            }
+        }
+        named_barrier_sync(kBarHalf0 + half, 128);
+        wait(ok, &sm.o_full, unit, a.err);
+        tc_fence_after();
+#pragma unroll
+        for (int ch = 0; ch < NCH; ++ch) {
+            if (ch * CH >= live) break;
+            uint32_t o[CH];
+            tmem_ld(lanes + kTmemO + (uint32_t)(c0 + ch * CH), o);
+            tmem_ld_wait();
+            if (t < D) {
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    const int r = c0 + ch * CH + c;
+                    if (r >= a.M) break;
+                    const float v = __uint_as_float(o[c]) * sm.inv[half][ch * CH + c];
+                    if (parts == 1) a.out[(row0 + sm.row_off[r]) * D + t] = __float2bfloat16_rn(v);
+                    else a.part_acc[((size_t)slot * a.M + r) * D + t] = v;
+                }
+            }
+        }
+        tc_fence_before();
+        warp_arrive(&sm.o_empty);
+        if (parts == 1) continue;
+        // every part of the pair is written: the last one's CTA joins them
+        __threadfence();
+        named_barrier_sync(kBarSoft, 256);
+        if (warp == 4 && lane == 0) {
+            const int pair = p.b * a.Hkv + p.h;
+            sm.last = atomicAdd(&a.tickets[pair], 1) == parts - 1;
+            if (sm.last) a.tickets[pair] = 0;
+        }
+        named_barrier_sync(kBarSoft, 256);
+        if (!sm.last) continue;
+        __threadfence();
+        // (the first part is its CTA's last piece unless the pair begins that CTA's share)
+        const int second = (long long)c_first * W / nsh == px ? 0 : 1;
+#pragma unroll 1
+        for (int r = warp - 4; r < a.M; r += 8) {
+            float m = -CUDART_INF_F, l = 0.f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+            for (int k = 0; k < parts; ++k) {
+                const size_t row = (size_t)(2 * (c_first + k) + (k == 0 ? second : 0)) * a.M + r;
+                const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.part_ml) + row);
+                const float4 v = lane < D / 4 ? __ldcg(reinterpret_cast<const float4 *>(a.part_acc + row * D) + lane) : o;
+                if (ml.x == -CUDART_INF_F) continue;  // a part without a visible token
+                const float mn = fmaxf(m, ml.x), fo = ex2_approx(m - mn), fn = ex2_approx(ml.x - mn);
+                l = l * fo + ml.y * fn;
+                o.x = o.x * fo + v.x * fn, o.y = o.y * fo + v.y * fn;
+                o.z = o.z * fo + v.z * fn, o.w = o.w * fo + v.w * fn;
+                m = mn;
+            }
+            const float inv = l > 0.f ? fv / l : 0.f;
+            const size_t row = row0 + sm.row_off[r];
+            if (lane < D / 4)
+                reinterpret_cast<uint2 *>(a.out + row * D)[lane] =
+                    make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+            if (lane == 0 && a.lse) a.lse[row] = (m + __log2f(l)) * kLn2;
+        }
+    }
+}
+
+template <int D, int NP>
+__global__ void __launch_bounds__(Cfg<D, NP>::kThreads, 1)
+    fp4_attn_kernel(const __grid_constant__ CUtensorMap mkc, const __grid_constant__ CUtensorMap mvc,
+                    const __grid_constant__ CUtensorMap mks, const __grid_constant__ CUtensorMap mvs,
+                    const __grid_constant__ CUtensorMap mq0, const __grid_constant__ CUtensorMap mq1,
+                    const __grid_constant__ Fp4AttnArgs a) {
+    using C = Cfg<D, NP>;
+    constexpr int kStages = C::kStages;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    Smem<D, NP> &sm =
+        *reinterpret_cast<Smem<D, NP> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
+
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&sm.raw_full[i], 1);
+            mbar_init(&sm.raw_empty[i], C::kBoth ? 4 : 8);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.k_full[i], 4);
+            mbar_init(&sm.k_empty[i], 1);
+            mbar_init(&sm.v_full[i], 4);
+            mbar_init(&sm.q_full[i], 1);
+            mbar_init(&sm.q_ready[i], 4);
+            mbar_init(&sm.q_empty[i], 1);
+            mbar_init(&sm.s_full[i], 1);
+            mbar_init(&sm.s_empty[i], 8);
+            mbar_init(&sm.p_full[i], 8);
+            mbar_init(&sm.pv_done[i], 1);
+        }
+        mbar_init(&sm.o_full, 1);
+        mbar_init(&sm.o_empty, 8);
+        fence_mbar_init();
+    }
+    if (warp == C::kProducerWarp && lane == 0) {
+        prefetch_tensormap(&mkc);
+        prefetch_tensormap(&mvc);
+        prefetch_tensormap(&mks);
+        prefetch_tensormap(&mvs);
+        prefetch_tensormap(&mq0);
+        prefetch_tensormap(&mq1);
+    }
+    // query rows past M are never copied: zeros
+    for (int i = tid; i < 2 * C::kQ / 16; i += C::kThreads)
+        reinterpret_cast<uint4 *>(sm.q[0])[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (tid < a.M) sm.row_off[tid] = tid / a.G * a.Hq + tid % a.G;
+    fence_proxy_async_smem();
+    if (warp == C::kMmaWarp) {
+        tmem_alloc(&sm.tmem_base, kTmemCols);
+        tmem_relinquish();
+    }
+    // the number of blocks, and where this CTA's share of them begins
+    const int per = (a.B + C::kThreads - 1) / C::kThreads;
+    const int lo = min(tid * per, a.B), hi = min(lo + per, a.B);
+    long long mine = 0;
+    for (int b = lo; b < hi; ++b) {
+        const int n = blocks_of(a, __ldg(a.context_lens + b));
+        if (n == 0 && blockIdx.x == 0) raise_error(a.err, SVPA_DEVERR_BAD_VALUE);
+        mine += (long long)n * a.Hkv;
+    }
+    long long incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += v;
+    }
+    if (lane == 31) sm.scan[warp] = incl;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    long long W = 0, before = 0;
+    for (int i = 0; i < C::kThreads / 32; ++i) {
+        if (i == warp) before = W;
+        W += sm.scan[i];
+    }
+    const int nsh = (int)min((long long)gridDim.x, W);
+    const long long xs = (int)blockIdx.x < nsh ? (long long)blockIdx.x * W / nsh : W;
+    const long long xe = (int)blockIdx.x < nsh ? (long long)(blockIdx.x + 1) * W / nsh : W;
+    before += incl - mine;
+    if (xs < xe && xs >= before && xs < before + mine) {
+        long long x = before;
+        int b = lo;
+        while (true) {
+            const int nb = blocks_of(a, __ldg(a.context_lens + b));
+            if (xs < x + (long long)nb * a.Hkv) {
+                sm.b0 = b, sm.h0 = (int)((xs - x) / nb), sm.f0 = (int)((xs - x) % nb);
+                break;
+            }
+            x += (long long)nb * a.Hkv;
+            ++b;
+        }
+    }
+    if (tid == 0) sm.work = W;
+    __syncthreads();
+    const uint32_t tmem = sm.tmem_base;
+    Walk w;
+    w.b = w.h = w.f = w.nb = w.L = 0;
+    w.x = xs, w.left = xe - xs;
+    if (xs < xe) w.b = sm.b0, w.h = sm.h0, w.f = sm.f0;
+    Piece p;
+    bool ok = true;
+
+    if (warp < 4) {
+        regs_dec<C::kRegsDecode>();
+        // ============================================ queries, K (and V) decoded
+        const uint32_t lanes = tmem + ((uint32_t)(32 * warp) << 16);
+        int j = 0, unit = 0;
+#pragma unroll 1
+        for (; w.next(a, p); ++unit) {
+            const float kf = fp4_factor(a.k_factor, p.h, a.err);
+            wait(ok, &sm.q_full[unit & 1], unit >> 1, a.err);
+            prepare_queries<D, NP>(sm, a, unit & 1, unit, kf, tid);
+            fence_proxy_async_smem();
+            warp_arrive(&sm.q_ready[unit & 1]);
+#pragma unroll 1
+            for (int i = 0; i < p.n; ++i, ++j) {
+                const int st = j % kStages;
+                wait(ok, &sm.raw_full[st], j / kStages, a.err);
+                if (j >= 2) wait(ok, &sm.k_empty[j & 1], (j - 2) >> 1, a.err);
+                tc_fence_after();
+                decode_k<D, NP>(sm, st, lanes, j & 1, tid);
+                if (!C::kBoth) warp_arrive(&sm.raw_empty[st]);
+                tmem_st_wait();
+                tc_fence_before();
+                warp_arrive(&sm.k_full[j & 1]);
+                if (C::kBoth) {
+                    if (j >= 2) wait(ok, &sm.pv_done[j & 1], (j - 2) >> 1, a.err);
+                    decode_v<D, NP>(sm, st, j & 1, tid, (p.f + i) * kNB + tid < p.L + a.n_q);
+                    warp_arrive(&sm.raw_empty[st]);
+                    fence_proxy_async_smem();
+                    warp_arrive(&sm.v_full[j & 1]);
+                }
+            }
+        }
+    } else if (warp < 12) {
+        regs_inc<C::kRegsSoftmax>();
+        softmax_role<D, NP>(sm, a, w, tmem);
+    } else if (!C::kBoth && warp < 16) {
+        regs_dec<C::kRegsDecode>();
+        // ============================================ V decoded
+        const int t = 32 * (warp - 12) + lane;
+        int j = 0;
+#pragma unroll 1
+        while (w.next(a, p)) {
+#pragma unroll 1
+            for (int i = 0; i < p.n; ++i, ++j) {
+                const int st = j % kStages;
+                wait(ok, &sm.raw_full[st], j / kStages, a.err);
+                if (j >= 2) wait(ok, &sm.pv_done[j & 1], (j - 2) >> 1, a.err);
+                decode_v<D, NP>(sm, st, j & 1, t, (p.f + i) * kNB + t < p.L + a.n_q);
+                warp_arrive(&sm.raw_empty[st]);
+                fence_proxy_async_smem();
+                warp_arrive(&sm.v_full[j & 1]);
+            }
+        }
+    } else {
+    regs_dec<C::kRegsIssue>();
+    if (warp == C::kProducerWarp) {
+        // ============================================ copies
+        const uint64_t pol = policy_evict_first();
+        const int none = a.num_blocks * a.Hkv;  // behind the pool: zeros
+        const int kind = lane >> 3, pg = lane & 7;
+        const CUtensorMap *map = kind == 0 ? &mkc : kind == 1 ? &mvc : kind == 2 ? &mks : &mvs;
+        int j = 0, unit = 0;
+#pragma unroll 1
+        for (; w.next(a, p) && ok; ++unit) {
+            if (unit >= 2) wait(ok, &sm.q_empty[unit & 1], (unit - 2) >> 1, a.err);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&sm.q_full[unit & 1], (uint32_t)(a.M * D * 2));
+                tma_load_4d(sm.q[unit & 1], &mq0, 0, p.h * a.G, 0, p.b, &sm.q_full[unit & 1], pol);
+                if (D == 128)
+                    tma_load_4d(sm.q[unit & 1] + NP * 128, &mq1, 0, p.h * a.G, 0, p.b, &sm.q_full[unit & 1], pol);
+            }
+            __syncwarp();
+            const int pages = (p.L + a.n_q + kBlockSize - 1) / kBlockSize - p.f * kPB;  // from the first block on
+            const int32_t *table = a.block_table + (size_t)p.b * a.max_blocks + (size_t)p.f * kPB;
+            int ids = 0;
+#pragma unroll 1
+            for (int i = 0; i < p.n; ++i, ++j) {
+                if ((i & 3) == 0) {  // 32 pages at a time
+                    const int at = i * kPB + lane;
+                    ids = none;
+                    if (at < pages) {
+                        const int blk = __ldg(table + at);
+                        if (blk >= 0 && blk < a.num_blocks) ids = blk * a.Hkv + p.h;
+                        else if (at < p.n * kPB) raise_error(a.err, SVPA_DEVERR_BAD_BLOCK);
+                    }
+                }
+                const int id = __shfl_sync(0xffffffffu, ids, (i & 3) * kPB + pg);
+                const int st = j % kStages;
+                if (j >= kStages) wait(ok, &sm.raw_empty[st], j / kStages - 1, a.err);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(&sm.raw_full[st], kNB * D + 2 * kNB * D / 16);
+                __syncwarp();
+                if (kind < 2)
+                    tma_load_3d((kind ? sm.vc[st] : sm.kc[st]) + pg * (kBlockSize * D / 2), map, 0, 0, id,
+                                &sm.raw_full[st], pol);
+                else
+                    tma_load_2d((kind == 3 ? sm.vs[st] : sm.ks[st]) + pg * 128, map, 0, id, &sm.raw_full[st], pol);
+            }
+        }
+        if (!ok) {  // copies in flight land before the CTA's memory is given up
+            bool still = true;
+            for (int i = max(0, j - kStages); i < j; ++i) wait(still, &sm.raw_full[i % kStages], i / kStages, a.err);
+            for (int i = max(0, unit - 1); i <= unit; ++i)
+                if (i >= 0) wait(still, &sm.q_full[i & 1], i >> 1, a.err);
+        }
+    } else if (warp == C::kMmaWarp) {
+        // ============================================ MMAs
+        const uint32_t idS = idesc(NP, 0, 0), idO = idesc(NP, 1, 1);
+        int j = 0, unit = 0, pj = 0, punit = 0;
+        bool pfirst = true;
+        auto products = [&](int jj, bool first, bool last, int u) {  // O^T (+)= V^T P^T of block jj
+            wait(ok, &sm.p_full[jj & 1], jj >> 1, a.err);
+            if (first && u > 0) wait(ok, &sm.o_empty, u - 1, a.err);
+            wait(ok, &sm.v_full[jj & 1], jj >> 1, a.err);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) return;
+            tc_fence_after();
+            const uint32_t va = smem_u32(sm.v[jj & 1]), pa = smem_u32(sm.p[jj % C::kPBufs]);
+            constexpr uint32_t row = NP < 64 ? 2 * NP : 128;
+            if (elect_one()) {
+#pragma unroll
+                for (int k = 0; k < kNB / 16; ++k)
+                    umma_bf16(tmem + kTmemO, umma_desc_sw128(va + k * 2048, kSlab, 1024), p_desc<NP>(pa + k * 16 * row),
+                              idO, first && k == 0 ? 0u : 1u);
+                umma_commit(&sm.pv_done[jj & 1]);
+                if (last) umma_commit(&sm.o_full);
+            }
+            __syncwarp();
+        };
+        bool plast = false;
+#pragma unroll 1
+        for (; ok && w.next(a, p); ++unit) {
+#pragma unroll 1
+            for (int i = 0; i < p.n && ok; ++i, ++j) {
+                // S^T of block j, ahead of the block before's products
+                wait(ok, &sm.k_full[j & 1], j >> 1, a.err);
+                if (i == 0) wait(ok, &sm.q_ready[unit & 1], unit >> 1, a.err);
+                if (j >= 2) wait(ok, &sm.s_empty[j & 1], (j - 2) >> 1, a.err);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t qa = smem_u32(sm.q[unit & 1]);
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+                        umma_bf16_tmem_a(tmem + kTmemS + (uint32_t)((j & 1) * NP), tmem + kTmemK + 64 * (j & 1) + 8 * k,
+                                         umma_desc_sw128(qa + (k >> 2) * NP * 128 + (k & 3) * 32, 16, 1024), idS,
+                                         k == 0 ? 0u : 1u);
+                    umma_commit(&sm.k_empty[j & 1]);
+                    umma_commit(&sm.s_full[j & 1]);
+                    if (i == p.n - 1) umma_commit(&sm.q_empty[unit & 1]);
+                }
+                __syncwarp();
+                if (j > 0) products(pj, pfirst, plast, punit);
+                pj = j, pfirst = i == 0, plast = i == p.n - 1, punit = unit;
+            }
+        }
+        if (ok && j > 0) {
+            products(pj, pfirst, plast, punit);
+            // the last arrivals land before the barriers are given up
+            wait(ok, &sm.pv_done[pj & 1], pj >> 1, a.err);
+            wait(ok, &sm.q_empty[punit & 1], punit >> 1, a.err);
+            wait(ok, &sm.o_full, punit, a.err);
+        }
+    }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == C::kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+}
+
+template <int D, int NP>
+cudaError_t launch(const Fp4AttnMaps &m, const Fp4AttnArgs &a, cudaStream_t st) {
+    using C = Cfg<D, NP>;
+    using S = Smem<D, NP>;
+    static_assert(C::kStages >= 2 && sizeof(S) + 1024 <= 232448, "fp4_attn_kernel shared memory");
+    static_assert(offsetof(S, negm) % 16 == 0 && offsetof(S, ks) % 128 == 0 && offsetof(S, kc) % 1024 == 0 &&
+                      offsetof(S, v) % 1024 == 0 && offsetof(S, p) % 1024 == 0,
+                  "tiles start on their swizzle's boundary");
+    const size_t smem = sizeof(S) + 1024;
+    static DeviceMemo<int> attr_set;  // the shared-memory opt-in, once per device
+    int done = 0;
+    const cudaError_t e = attr_set.get(&done, [&](int *v) {
+        *v = 1;
+        return cudaFuncSetAttribute(fp4_attn_kernel<D, NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    });
     if (e != cudaSuccess) return e;
-    fp4_attn_kernel<D><<<dim3(a.Hkv, a.B), kThreads, smem, st>>>(a);
+    fp4_attn_kernel<D, NP><<<fp4_attn_grid(), C::kThreads, smem, st>>>(m.kc, m.vc, m.ks, m.vs, m.q[0], m.q[1], a);
     return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_d(const Fp4AttnMaps &m, const Fp4AttnArgs &a, cudaStream_t st) {
+    if (a.M <= 16) return launch<D, 16>(m, a, st);
+    if (a.M <= 32) return launch<D, 32>(m, a, st);
+    if (a.M <= 64) return launch<D, 64>(m, a, st);
+    return launch<D, 128>(m, a, st);
 }
 
 }  // namespace
 
-cudaError_t launch_paged_verify_attn_fp4(const Fp4AttnArgs &a, int D, cudaStream_t st) {
-    return D == 64 ? launch<64>(a, st) : launch<128>(a, st);
+int fp4_attn_grid() { return sm_count(); }
+
+cudaError_t launch_paged_verify_attn_fp4(const Fp4AttnMaps &m, const Fp4AttnArgs &a, int D, cudaStream_t st) {
+    return D == 64 ? launch_d<64>(m, a, st) : launch_d<128>(m, a, st);
 }
 
 }  // namespace svpa

@@ -7,7 +7,11 @@
 //   or (2i, 2i + 1) of the first R elements, t = the angle of (position, i)
 // All of it in fp32, one rounding to bf16; FP8 and 4-bit pages encode that bf16
 // value, so that a row has the same codes whether it is rotated on the way into
-// the pages or before.
+// the pages or before.  Each operation on a key is rounded by itself and its sum
+// of squares has one order (ordered_squares): a value next to the border of two
+// codes moves by up to half of itself when its last fp32 bit does, so a key's
+// codes are made reproducible by plain fp32 operations.  (This file is compiled
+// without fused multiply-adds.)
 //
 // Bytes only: each row is read once and written once.  A lane holds eight
 // elements (16 bytes), a head is D / 8 lanes, and a warp takes four words a
@@ -31,6 +35,25 @@ __device__ __forceinline__ void unpack8(const uint4 &x, float (&f)[8]) {
 __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
     return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
                       pack_bf16x2(f[6], f[7]));
+}
+
+// The sum of a head's squares in one fixed order: 32 partial sums, of the
+// elements i, i + 32, i + 64, ... in turn, added in pairs of neighbours.
+template <int D>
+__device__ __forceinline__ float ordered_squares(const float (&f)[8], int lane) {
+    float s[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float sq = f[j] * f[j];
+        s[j] = sq;
+        // (complete in a head's first four lanes)
+#pragma unroll
+        for (int m = 1; m < D / 32; ++m) s[j] += __shfl_down_sync(0xffffffffu, sq, 4 * m);
+    }
+    float sum = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    return __shfl_sync(0xffffffffu, sum, lane & ~(D / 8 - 1));
 }
 
 // One lane's eight bf16 values of head h, chunk c, into slot `slot` of the pages.
@@ -144,10 +167,14 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
             unpack8(x[i], f);
             if (weight) {
                 float sum = 0.f;
+                if (kind == 1) {
+                    sum = ordered_squares<D>(f, lane);
+                } else {  // any order: queries are rounded to bf16 alone
 #pragma unroll
-                for (int j = 0; j < 8; ++j) sum = fmaf(f[j], f[j], sum);
+                    for (int j = 0; j < 8; ++j) sum = fmaf(f[j], f[j], sum);
 #pragma unroll
-                for (int o = 1; o < kLanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                    for (int o = 1; o < kLanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                }
                 const float r = rsqrtf(sum * (1.f / D) + a.eps);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) f[j] = f[j] * r * wt[j];

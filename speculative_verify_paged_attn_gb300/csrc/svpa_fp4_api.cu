@@ -6,6 +6,7 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "../../include/svpa.h"
@@ -99,6 +100,24 @@ svpa_status check_attn(const svpa_attn_params *p) {
         p->num_kv_heads > 65535 || (long long)p->num_blocks * p->num_kv_heads > 0x7fffffffLL ||
         p->max_blocks_per_seq > kMaxPoolBlocks)
         return SVPA_ERR_UNSUPPORTED;
+    return SVPA_OK;
+}
+
+constexpr size_t fp4_tile(int D) { return 9 * (size_t)D; }
+
+// The attention's workspace: [counters][tickets][parts' (max, sum)][parts' accumulators].
+struct AttnSpace {
+    size_t tickets, off_ml, off_acc, bytes;
+};
+svpa_status attn_space(const svpa_attn_params *p, AttnSpace *sp) {
+    const svpa_status s = check_attn(p);
+    if (s != SVPA_OK) return s;
+    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    const size_t rows = (size_t)2 * fp4_attn_grid() * (p->num_q_heads / p->num_kv_heads) * p->n_q;
+    sp->tickets = (size_t)p->batch * p->num_kv_heads * sizeof(int32_t);
+    sp->off_ml = kWorkspaceCounterBytes + up(std::max(sp->tickets, kTicketBytes));
+    sp->off_acc = sp->off_ml + up(rows * 2 * sizeof(float));
+    sp->bytes = sp->off_acc + up(rows * p->head_dim * sizeof(float));
     return SVPA_OK;
 }
 
@@ -242,10 +261,11 @@ svpa_status svpa_kv_append_fp4(int32_t batch, int32_t n_new, int32_t num_kv_head
 }
 
 svpa_status svpa_paged_verify_attn_fp4_workspace_size(const svpa_attn_params *p, size_t *bytes) {
-    const svpa_status s = check_attn(p);
+    AttnSpace sp;
+    const svpa_status s = attn_space(p, &sp);
     if (s != SVPA_OK) return s;
     if (!bytes) return SVPA_ERR_INVALID_ARG;
-    *bytes = kWorkspaceCounterBytes + kTicketBytes;
+    *bytes = sp.bytes;
     return SVPA_OK;
 }
 
@@ -255,19 +275,53 @@ svpa_status svpa_paged_verify_attn_fp4(const svpa_attn_params *p, const void *q,
                                        const uint64_t *ancestor_mask, void *out, float *lse, void *workspace,
                                        size_t workspace_bytes, int32_t *error_flag, void *stream) {
     svpa::NvtxRange nvtx_range("svpa_paged_verify_attn_fp4");
-    size_t need;
-    svpa_status s = svpa_paged_verify_attn_fp4_workspace_size(p, &need);
+    AttnSpace sp;
+    svpa_status s = attn_space(p, &sp);
     if (s != SVPA_OK) return s;
     if (p->batch == 0) return SVPA_OK;
     s = check_attn_call(p, q, k_pool, v_pool, nullptr, nullptr, block_table, context_lens, ancestor_mask, out,
                         error_flag);
     if (s != SVPA_OK) return s;
-    if (!workspace || workspace_bytes < need || !aligned(workspace, 16)) return SVPA_ERR_WORKSPACE;
+    if (!workspace || workspace_bytes < sp.bytes || !aligned(workspace, 16)) return SVPA_ERR_WORKSPACE;
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return SVPA_ERR_CUDA;
+
+    const int D = p->head_dim, G = p->num_q_heads / p->num_kv_heads;
+    Fp4AttnMaps maps;
+    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    auto encode = [&](CUtensorMap *m, CUtensorMapDataType type, int dims, const void *base, const cuuint64_t *size,
+                      const cuuint64_t *stride, const cuuint32_t *box, CUtensorMapSwizzle swizzle) {
+        return enc(m, type, (cuuint32_t)dims, const_cast<void *>(base), size, stride, box, ones,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    const cuuint64_t tiles = (cuuint64_t)p->num_blocks * p->num_kv_heads, tile = (cuuint64_t)fp4_tile(D);
+    for (int kv = 0; kv < 2; ++kv) {
+        const uint8_t *pool = static_cast<const uint8_t *>(kv ? v_pool : k_pool);
+        const cuuint64_t cd[3] = {(cuuint64_t)D / 2, kBlockSize, tiles}, cs[2] = {(cuuint64_t)D / 2, tile};
+        const cuuint32_t cb[3] = {(cuuint32_t)D / 2, kBlockSize, 1};
+        const cuuint64_t sd[2] = {(cuuint64_t)D, tiles}, ss[1] = {tile};
+        const cuuint32_t sb[2] = {(cuuint32_t)D, 1};
+        if (!encode(kv ? &maps.vc : &maps.kc, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, pool, cd, cs, cb,
+                    D == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B) ||
+            !encode(kv ? &maps.vs : &maps.ks, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, pool + 8 * D, sd, ss, sb,
+                    CU_TENSOR_MAP_SWIZZLE_NONE))
+            return SVPA_ERR_CUDA;
+    }
+    // queries [B, n_q, Hq, D]: (64 columns, G heads, n_q queries) of a sequence at a time
+    const cuuint64_t qd[4] = {64, (cuuint64_t)p->num_q_heads, (cuuint64_t)p->n_q, (cuuint64_t)p->batch};
+    const cuuint64_t qs[3] = {(cuuint64_t)D * 2, (cuuint64_t)p->num_q_heads * D * 2,
+                              (cuuint64_t)p->n_q * p->num_q_heads * D * 2};
+    const cuuint32_t qb[4] = {64, (cuuint32_t)G, (cuuint32_t)p->n_q, 1};
+    for (int i = 0; i < 2; ++i)
+        if (!encode(&maps.q[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                    static_cast<const uint8_t *>(q) + (D == 128 ? 128 * i : 0), qd, qs, qb,
+                    CU_TENSOR_MAP_SWIZZLE_128B))
+            return SVPA_ERR_CUDA;
+
     Fp4AttnArgs a;
     memset(&a, 0, sizeof a);
-    a.q = static_cast<const __nv_bfloat16 *>(q);
-    a.k_pool = static_cast<const uint8_t *>(k_pool);
-    a.v_pool = static_cast<const uint8_t *>(v_pool);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
     a.k_factor = k_factor;
     a.v_factor = v_factor;
     a.block_table = block_table;
@@ -275,18 +329,31 @@ svpa_status svpa_paged_verify_attn_fp4(const svpa_attn_params *p, const void *q,
     a.out = static_cast<__nv_bfloat16 *>(out);
     a.lse = lse;
     a.err = error_flag;
+    a.tickets = reinterpret_cast<int32_t *>(ws + kWorkspaceCounterBytes);
+    a.part_ml = reinterpret_cast<float *>(ws + sp.off_ml);
+    a.part_acc = reinterpret_cast<float *>(ws + sp.off_acc);
     a.B = p->batch;
     a.n_q = p->n_q;
     a.Hq = p->num_q_heads;
     a.Hkv = p->num_kv_heads;
-    a.G = p->num_q_heads / p->num_kv_heads;
-    a.M = a.G * p->n_q;
+    a.G = G;
+    a.M = G * p->n_q;
     a.max_blocks = p->max_blocks_per_seq;
     a.num_blocks = p->num_blocks;
     a.scale_log2 = p->sm_scale * 1.4426950408889634f;
-    for (int j = 0; j < p->n_q; ++j)
-        a.anc[j] = ancestor_mask ? ancestor_mask[j] : ((j == 63) ? ~0ull : ((1ull << (j + 1)) - 1ull));
-    return from_cuda(launch_paged_verify_attn_fp4(a, p->head_dim, static_cast<cudaStream_t>(stream)));
+    for (int j = 0; j < p->n_q; ++j) {
+        const uint64_t sees = ancestor_mask ? ancestor_mask[j] : ~0ull >> (63 - j);
+        for (int i = 0; i <= j; ++i) {
+            if (!(sees >> i & 1)) continue;
+            for (int c = j * G; c < (j + 1) * G; ++c) a.slots[i][c >> 6] |= 1ull << (c & 63);
+        }
+    }
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (sp.tickets > kTicketBytes) {  // where other calls keep partial results
+        const cudaError_t e = cudaMemsetAsync(a.tickets, 0, sp.tickets, st);
+        if (e != cudaSuccess) return from_cuda(e);
+    }
+    return from_cuda(launch_paged_verify_attn_fp4(maps, a, D, st));
 }
 
 }  // extern "C"
