@@ -6,6 +6,8 @@
 namespace svpa {
 
 struct Fp4AttnArgs {
+    const uint8_t *k_pool;
+    const uint8_t *v_pool;
     const float *k_factor;  // [Hkv] or null
     const float *v_factor;
     const int32_t *block_table;
@@ -22,14 +24,9 @@ struct Fp4AttnArgs {
     unsigned long long slots[kMaxNq][2];
 };
 
-struct Fp4AttnMaps {
-    CUtensorMap kc, vc;  // codes: [(page, kv head)][16 rows][D / 2 bytes]
-    CUtensorMap ks, vs;  // scales: [(page, kv head)][16 * D / 16 bytes]
-    CUtensorMap q[2];    // 64-column slabs of one (sequence, kv head)'s queries
-};
-
 // CTAs of a launch; each has two part slots.
 int fp4_attn_grid();
-cudaError_t launch_paged_verify_attn_fp4(const Fp4AttnMaps &maps, const Fp4AttnArgs &a, int D, cudaStream_t stream);
+// mq: the maps of the two 64-column slabs of one (sequence, kv head)'s queries (D 64: one).
+cudaError_t launch_paged_verify_attn_fp4(const CUtensorMap *mq, const Fp4AttnArgs &a, int D, cudaStream_t stream);
 
 }  // namespace svpa

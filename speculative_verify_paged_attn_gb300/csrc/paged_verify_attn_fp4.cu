@@ -16,17 +16,20 @@
 // this kernel.
 //
 // The softmax has a token a thread, so that a column's maximum lies across
-// threads: it is taken in a unit's first block, and after that only when some
-// score exceeds its column's reference by 2^8 (a vote a block).
+// threads: it is taken in a group's first block of a unit, and after that only
+// when some score exceeds its column's reference by 15 in log2 units (a vote a
+// block).
 //
 // Work: the 128-token blocks of all (sequence, kv head) pairs, in that order,
 // split evenly over one persistent CTA per SM; the parts of a pair that is cut
 // are merged by the CTA that writes the last of them.
-// Warps: 0-3 decode K and turn the queries to f16; 4-11 softmax and epilogue
-// (4-7 the first half of the columns, 8-11 the second); 12-15 decode V (with 128
-// columns warps 0-3 do, to leave the softmax its registers); then one warp of
-// TMA copies and one that issues the MMAs.  A warp reads the TMEM lanes of
-// quadrant warp % 4.  Every role walks the same list of blocks.
+// Warps: 0-3 decode K and turn the queries to f16; 4-7 and 8-11 are the softmax
+// and the epilogue; 12-15 decode V; then a warp that copies K's pages, one for
+// V's, and one each that issues the MMAs of either product (with 128 columns
+// there are no warps for V: Cfg).  The pages are copied 16 bytes a lane
+// (cp.async): by bulk copies of each page's codes and scales, 32 a block at some
+// 95 cycles each, the copies were what bound the kernel.  A warp reads the TMEM
+// lanes of quadrant warp % 4.  Every role walks the same list of blocks.
 // All waits are bounded: a role whose wait ran out goes on without waiting.
 #include <math_constants.h>
 
@@ -42,58 +45,100 @@ namespace {
 
 constexpr int kPB = 8;                        // pages per block
 constexpr int kNB = kPB * kBlockSize;         // tokens per block
-constexpr float kRescaleLog2 = 8.f;           // a weight may be up to 2^8
+constexpr float kMaxWeight = 0x1p15f;
 constexpr uint32_t kTmemCols = 512, kTmemS = 0, kTmemO = 256, kTmemK = 384;
 constexpr int kSlab = kNB * 128;              // 64 f16 columns of 128 rows
 constexpr float kLn2 = 0.69314718055994530942f;
 enum { kBarHalf0 = 1, kBarSoft = 3, kBarPrep = 4 };  // named barriers
 
+// ---------------------------------------------------------------- the work list
+struct Piece {
+    int b, h, f, n, nb, L;  // sequence, kv head, first block, blocks, the pair's blocks, history
+    long long x;            // the first block's place in the list
+};
+
+__device__ __forceinline__ int blocks_of(const Fp4AttnArgs &a, int L) {
+    const long long pages = ((long long)L + a.n_q + kBlockSize - 1) / kBlockSize;
+    return L < 0 || pages > a.max_blocks ? 0 : (int)((pages + kPB - 1) / kPB);
+}
+
+struct Walk {
+    int b, h, f, nb, L;
+    long long x, left;
+    __device__ __forceinline__ bool next(const Fp4AttnArgs &a, Piece &p) {
+        if (left <= 0) return false;
+        while (nb == 0) {
+            L = __ldg(a.context_lens + b);
+            nb = blocks_of(a, L);
+            if (nb == 0) ++b;  // (counts no blocks)
+        }
+        p.b = b, p.h = h, p.f = f, p.nb = nb, p.L = L, p.x = x;
+        p.n = (int)min((long long)(nb - f), left);
+        left -= p.n, x += p.n, f += p.n;
+        if (f == nb) {
+            f = 0;
+            if (++h == a.Hkv) h = 0, ++b, nb = 0;
+        }
+        return true;
+    }
+};
+
 template <int D, int NP>
 struct Cfg {
-    static constexpr bool kBoth = NP == 128;  // warps 0-3 decode K and V
-    static constexpr int kProducerWarp = kBoth ? 12 : 16, kMmaWarp = kProducerWarp + 1;
-    static constexpr int kThreads = 32 * (kProducerWarp + 4);  // (two warps idle)
+    // Up to 64 columns: the two softmax groups take the blocks in turn, each with
+    // a reference, sums and an O of its own, so that one block's chain of waits
+    // runs beside the other's.  128: each takes half of every block's columns (two
+    // O do not fit TMEM), and warps 0-3 decode V too.
+    static constexpr bool kAlt = NP < 128;
+    static constexpr int kCopyWarp = kAlt ? 16 : 12;  // K's and V's copies, then the MMAs: P V, S
+    static constexpr int kPvWarp = kCopyWarp + 2, kScoreWarp = kCopyWarp + 3;
+    static constexpr int kThreads = 32 * (kCopyWarp + 4);
     // registers a thread, from the 96 (128 with 16 warps) at launch: their sum
     // over the warps of a scheduler stays within 5 * 96 (4 * 128)
-    static constexpr int kRegsDecode = kBoth ? 112 : 80, kRegsIssue = 64, kRegsSoftmax = kBoth ? 168 : 128;
-    static_assert((kBoth ? 1 : 2) * kRegsDecode + kRegsIssue + 2 * kRegsSoftmax <= (kBoth ? 4 * 128 : 5 * 96),
+    static constexpr int kRegsDecode = kAlt ? 80 : 112, kRegsIssue = 64, kRegsSoftmax = kAlt ? 128 : 160;
+    static_assert((kAlt ? 2 : 1) * kRegsDecode + kRegsIssue + 2 * kRegsSoftmax <= (kAlt ? 5 * 96 : 4 * 128),
                   "registers handed over");
-    static constexpr int kNH = NP / 2;              // columns of a softmax half
-    static constexpr int kCH = kNH < 32 ? kNH : 32; // ... taken at a time
-    static constexpr int kPBufs = NP == 128 ? 1 : 2;
+    static constexpr int kNH = kAlt ? NP : 64;        // columns of a softmax thread
+    static constexpr int kCH = kNH < 32 ? kNH : 32;   // ... taken at a time
+    static constexpr int kEC = NP / 2;                // columns of a group in the epilogue
+    static constexpr int kSBufs = kAlt ? 4 : 2, kPBufs = kAlt ? 2 : 1, kVBufs = kAlt ? 3 : 2;
     static constexpr int kQ = NP * D * 2, kP = kNB * NP * 2;
     static constexpr int kCodes = kNB * D / 2, kScales = kPB * 128;
     static constexpr int kStage = 2 * (kCodes + kScales);
-    static constexpr int kRoom = (232448 - 8192 - 2 * kQ - kPBufs * kP - 4 * kSlab) / kStage;
+    static constexpr int kRoom = (232448 - 12288 - 2 * kQ - kPBufs * kP - kVBufs * 2 * kSlab) / kStage;
     static constexpr int kStages = kRoom < 8 ? kRoom : 8;
 };
 
 template <int D, int NP>
 struct Smem {
     using C = Cfg<D, NP>;
-    uint8_t q[2][C::kQ];              // [slab][NP rows][128 B], 128-byte swizzle
-    uint8_t v[2][2 * kSlab];          // decoded V: [slab][128 tokens][128 B] (D 64: one slab)
-    uint8_t p[C::kPBufs][C::kP];      // weights: [token][NP columns]
+    uint8_t q[2][C::kQ];               // [slab][NP rows][128 B], 128-byte swizzle
+    uint8_t v[C::kVBufs][2 * kSlab];   // decoded V: [slab][128 tokens][128 B] (D 64: one slab)
+    uint8_t p[C::kPBufs][C::kP];       // weights: [token][NP columns]
     uint8_t kc[C::kStages][C::kCodes], vc[C::kStages][C::kCodes];
     uint8_t ks[C::kStages][C::kScales], vs[C::kStages][C::kScales];
-    float negm[2][64];                // minus the columns' reference maxima (0: none yet)
-    float m[2][64];
-    float fac[2][64];                 // what a raised maximum leaves of the sums
-    float inv[2][64];
-    float warp_col[2][4][64];         // a column's maximum or sum in each quadrant
-    float mult[4];                    // score -> log2 units, per unit in flight
-    int32_t row_off[128];             // query row -> row of out behind the unit's first
-    uint64_t raw_full[C::kStages], raw_empty[C::kStages];
-    uint64_t k_full[2], k_empty[2], v_full[2];
+    float negm[2][64];                 // a group's columns: minus the reference maxima (0: none yet)
+    float fac[2][64];                  // what a raised maximum leaves of the sums
+    float top[2][4][64];               // a column's maximum in each quadrant
+    float m[2][2][64];                 // [unit parity][group]: the reference maxima
+    float sums[2][2][4][64];           // ... and each quadrant's sums
+    // score -> log2 units, of the units in flight: one is written once S of the unit
+    // two before is there, whose buffer the softmax has read four blocks earlier
+    float mult[8];
+    int32_t row_off[128];              // query row -> row of out behind the unit's first
+    uint64_t raw_full[2][C::kStages], raw_empty[2][C::kStages];  // K's and V's
+    uint64_t k_full[2], k_empty[2], v_full[C::kVBufs], v_empty[C::kVBufs];
     uint64_t q_full[2], q_ready[2], q_empty[2];
-    uint64_t s_full[2], s_empty[2], p_full[2], pv_done[2];
+    uint64_t s_full[C::kSBufs], s_empty[C::kSBufs], p_full[2], pv_done[2];
     uint64_t o_full, o_empty;
     long long scan[32];
-    long long work, first_x;          // all blocks; this CTA's first
-    int32_t b0, h0, f0;
+    long long work;                    // all blocks
+    int32_t b0, h0, f0;                // this CTA's first
     uint32_t tmem_base;
     uint32_t qmax[4];
     int32_t last;
+    Walk walk[8];  // a softmax warp's place in the list, and its unit (registers are for scores and sums)
+    Piece piece[8];
 };
 
 // ---------------------------------------------------------------- small pieces
@@ -169,21 +214,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
-__device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, int c0, int c1, uint64_t *bar,
-                                            uint64_t policy) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_"
-        "hint [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_u32(bar)), "l"(policy)
-        : "memory");
-}
-__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int c0, int c1, int c2, uint64_t *bar,
-                                            uint64_t policy) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_"
-        "hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar)), "l"(policy)
-        : "memory");
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
 // N consecutive columns of this thread's TMEM lane.
@@ -253,38 +285,6 @@ __host__ __device__ constexpr uint32_t idesc(int N, int a_mn, int b_mn) {
     return (1u << 4) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
 }
 
-// ---------------------------------------------------------------- the work list
-struct Piece {
-    int b, h, f, n, nb, L;  // sequence, kv head, first block, blocks, the pair's blocks, history
-    long long x;            // the first block's place in the list
-};
-
-__device__ __forceinline__ int blocks_of(const Fp4AttnArgs &a, int L) {
-    const long long pages = ((long long)L + a.n_q + kBlockSize - 1) / kBlockSize;
-    return L < 0 || pages > a.max_blocks ? 0 : (int)((pages + kPB - 1) / kPB);
-}
-
-struct Walk {
-    int b, h, f, nb, L;
-    long long x, left;
-    __device__ __forceinline__ bool next(const Fp4AttnArgs &a, Piece &p) {
-        if (left <= 0) return false;
-        while (nb == 0) {
-            L = __ldg(a.context_lens + b);
-            nb = blocks_of(a, L);
-            if (nb == 0) ++b;  // (counts no blocks)
-        }
-        p.b = b, p.h = h, p.f = f, p.nb = nb, p.L = L, p.x = x;
-        p.n = (int)min((long long)(nb - f), left);
-        left -= p.n, x += p.n, f += p.n;
-        if (f == nb) {
-            f = 0;
-            if (++h == a.Hkv) h = 0, ++b, nb = 0;
-        }
-        return true;
-    }
-};
-
 // ---------------------------------------------------------------- decoding
 // 32 codes and their two scales to 16 f16 pairs.
 __device__ __forceinline__ void decode32(const uint4 &w, uint32_t two_scales, uint32_t *out) {
@@ -314,10 +314,11 @@ __device__ __forceinline__ uint2 scales_at(const uint8_t *scales, int t) {
     else return make_uint2(*reinterpret_cast<const uint32_t *>(at), 0u);
 }
 
+// (Rolled loops: the roles' loops share an instruction cache.)
 template <int D, int NP>
 __device__ __forceinline__ void decode_k(Smem<D, NP> &sm, int stage, uint32_t lane_base, int buf, int t) {
     const uint2 sc = scales_at<D>(sm.ks[stage], t);
-#pragma unroll
+#pragma unroll 1
     for (int c = 0; c < D / 32; c += 2) {
         uint32_t r[32];
         const uint32_t s = c ? sc.y : sc.x;
@@ -329,20 +330,19 @@ __device__ __forceinline__ void decode_k(Smem<D, NP> &sm, int stage, uint32_t la
 
 template <int D, int NP>
 __device__ __forceinline__ void decode_v(Smem<D, NP> &sm, int stage, int buf, int t, bool held) {
-    const uint2 sc = scales_at<D>(sm.vs[stage], t);
-#pragma unroll
-    for (int c = 0; c < D / 32; ++c) {
-        uint32_t r[16];
-        const uint32_t s = c < 2 ? sc.x : sc.y;
-        decode32(codes_at<D>(sm.vc[stage], t, c), c & 1 ? s >> 16 : s, r);
+    uint2 sc = scales_at<D>(sm.vs[stage], t);
+    if (!held) sc = make_uint2(0u, 0u);  // a slot behind the sequence's last: what it holds is anything
+#pragma unroll 1
+    for (int c = 0; c < D / 32; c += 2) {
+        uint32_t r[32];
+        const uint32_t s = c ? sc.y : sc.x;
+        decode32(codes_at<D>(sm.vc[stage], t, c), s, r);
+        decode32(codes_at<D>(sm.vc[stage], t, c + 1), s >> 16, r + 16);
         uint8_t *row = sm.v[buf] + (c >> 1) * kSlab + t * 128;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            // (a slot behind the sequence's last: what it holds is anything)
-            const uint4 x = held ? make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3])
-                                 : make_uint4(0u, 0u, 0u, 0u);
-            *reinterpret_cast<uint4 *>(row + (((4 * (c & 1) + k) ^ (t & 7)) << 4)) = x;
-        }
+        for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<uint4 *>(row + ((k ^ (t & 7)) << 4)) =
+                make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
     }
 }
 
@@ -384,7 +384,7 @@ __device__ __forceinline__ void prepare_queries(Smem<D, NP> &sm, const Fp4AttnAr
         }
     // (positive, so that a masked score stays -inf)
     if (tid == 0)
-        sm.mult[unit & 3] = fmaxf(a.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23) * kf, 1e-30f);
+        sm.mult[unit & 7] = fmaxf(a.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23) * kf, 1e-30f);
     named_barrier_sync(kBarPrep, 128);  // (qmax is free again)
 }
 
@@ -392,36 +392,50 @@ __device__ __forceinline__ void prepare_queries(Smem<D, NP> &sm, const Fp4AttnAr
 template <int D, int NP>
 __device__ __forceinline__ void softmax_role(Smem<D, NP> &sm, const Fp4AttnArgs &a, Walk w, uint32_t tmem) {
     using C = Cfg<D, NP>;
-    constexpr int NH = C::kNH, CH = C::kCH, NCH = NH / CH;
+    constexpr bool kAlt = C::kAlt;
+    constexpr int NH = C::kNH, CH = C::kCH, NCH = NH / CH, kStep = kAlt ? 2 : 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int quad = warp & 3, half = (warp - 4) >> 2, t = 32 * quad + lane, c0 = half * NH;
+    const int quad = warp & 3, g = (warp - 4) >> 2, t = 32 * quad + lane, c0 = kAlt ? 0 : g * NH;
     const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
+    const uint32_t o_at = lanes + kTmemO + (kAlt ? g * NP : c0);  // this group's columns of O
     const int live = min(max(a.M - c0, 0), NH);  // columns with a query row
-    const long long W = sm.work, first_x = w.x;
-    const int nsh = (int)min((long long)gridDim.x, W);
-    auto cta_of = [&](long long x) { return (int)(((x + 1) * nsh - 1) / W); };
+    Walk &walk = sm.walk[warp - 4];
+    const Piece &p = sm.piece[warp - 4];
+    auto next_unit = [&]() -> bool {
+        int more = 0;
+        __syncwarp();
+        if (lane == 0) {
+            Walk u = walk;
+            more = u.next(a, sm.piece[warp - 4]);
+            walk = u;
+        }
+        return __shfl_sync(0xffffffffu, more, 0) != 0;
+    };
+    if (lane == 0) walk = w;
     bool ok = true;
-    int j = 0, unit = 0;
-    Piece p;
+    int j0 = 0, unit = 0;  // the unit's first block
     uint64_t sum[NH / 2];
 #pragma unroll 1
-    for (; w.next(a, p); ++unit) {
+    for (; next_unit(); ++unit) {
 #pragma unroll
         for (int i = 0; i < NH / 2; ++i) sum[i] = 0ull;
+        float *m_unit = sm.m[unit & 1][g];
         float mult = 1.f;
 #pragma unroll 1
-        for (int i = 0; i < p.n; ++i, ++j) {
-            wait(ok, &sm.s_full[j & 1], j >> 1, a.err);
+        for (int i = kAlt ? (g - j0) & 1 : 0; i < p.n; i += kStep) {
+            const int j = j0 + i, sb = j % C::kSBufs;
+            const bool first = i < kStep;
+            wait(ok, &sm.s_full[sb], j / C::kSBufs, a.err);
             tc_fence_after();
-            if (i == 0) mult = sm.mult[unit & 3];
+            if (first) mult = sm.mult[unit & 7];
             const uint64_t mult2 = pack2(mult, mult);
-            const uint32_t sa = lanes + kTmemS + (uint32_t)((j & 1) * NP + c0);
+            const uint32_t sa = lanes + kTmemS + (uint32_t)(sb * NP + c0);
             // which columns see this thread's token
             const int at = (p.f + i) * kNB + t - p.L;  // >= 0: a speculative slot
             const bool edge = (p.f + i + 1) * kNB > p.L;
             unsigned long long vis = ~0ull;
-            if (edge && at >= 0)
-                vis = at >= a.n_q ? 0ull : NP == 128 ? a.slots[at][half] : a.slots[at][0] >> c0;
+            if (edge && at >= 0) vis = at >= a.n_q ? 0ull : a.slots[at][kAlt ? 0 : g];
+            uint8_t *pt = sm.p[kAlt ? g : 0];
             uint32_t s[CH];
             auto load = [&](int ch) {
                 tmem_ld(sa + (uint32_t)(ch * CH), s);
@@ -433,127 +447,132 @@ __device__ __forceinline__ void softmax_role(Smem<D, NP> &sm, const Fp4AttnArgs 
                         if (!(v >> c & 1u)) s[c] = 0xff800000u;
                 }
             };
-            auto shift = [&](int ch) {  // scores to log2 units below their reference
-                const float4 *nm = reinterpret_cast<const float4 *>(&sm.negm[half][ch * CH]);
-#pragma unroll
-                for (int c = 0; c < CH; c += 4) {
-                    const float4 n = nm[c / 4];
-                    const float2 u = unpack2(fma2(pack2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), mult2,
-                                                  pack2(n.x, n.y)));
-                    const float2 v = unpack2(fma2(pack2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), mult2,
-                                                  pack2(n.z, n.w)));
-                    s[c] = __float_as_uint(u.x), s[c + 1] = __float_as_uint(u.y);
-                    s[c + 2] = __float_as_uint(v.x), s[c + 3] = __float_as_uint(v.y);
-                }
-            };
-            bool raise = i == 0;
-            if (!raise) {
-                float top = -CUDART_INF_F;
-#pragma unroll
-                for (int ch = 0; ch < NCH; ++ch) {
-                    load(ch);
-                    shift(ch);
-#pragma unroll
-                    for (int c = 0; c < CH; c += 2) top = max3(top, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-                }
-                raise = barrier_any(kBarHalf0 + half, 128, top > kRescaleLog2);
-            }
-            if (raise) {
-                // the columns' maxima over the block's tokens, and new references
-#pragma unroll
-                for (int ch = 0; ch < NCH; ++ch) {
-                    load(ch);
-                    float mine = -CUDART_INF_F;
-#pragma unroll
-                    for (int c = 0; c < CH; ++c) {
-                        const float v = warp_max(__uint_as_float(s[c]));
-                        if (lane == c) mine = v;
-                    }
-                    if (lane < CH) sm.warp_col[half][quad][ch * CH + lane] = mine;
-                }
-                named_barrier_sync(kBarHalf0 + half, 128);
-                float m_new[NCH], fac[NCH];
-#pragma unroll
-                for (int ch = 0; ch < NCH; ++ch) {
-                    const int c = ch * CH + (lane & (CH - 1));
-                    const float top = fmaxf(fmaxf(sm.warp_col[half][0][c], sm.warp_col[half][1][c]),
-                                            fmaxf(sm.warp_col[half][2][c], sm.warp_col[half][3][c])) *
-                                      mult;
-                    const float old = i == 0 ? -CUDART_INF_F : sm.m[half][c];
-                    m_new[ch] = fmaxf(old, top);
-                    fac[ch] = old == m_new[ch] ? 1.f : ex2_approx(old - m_new[ch]);
-                }
-                named_barrier_sync(kBarHalf0 + half, 128);
-                if (quad == 0 && lane < CH) {
-#pragma unroll
+            // A weight may be up to 2^15 (f16's limit is 2^16).  Beyond that the block
+            // is taken back, what cancels being below 2^-24 of the sums to come, and
+            // done again under new references.
+            bool raise = first;
+            float sign = 1.f;
+#pragma unroll 1
+            while (true) {
+                if (raise) {
+                    // the columns' maxima over the block's tokens, and new references
+#pragma unroll 1
                     for (int ch = 0; ch < NCH; ++ch) {
-                        sm.m[half][ch * CH + lane] = m_new[ch];
-                        sm.negm[half][ch * CH + lane] = m_new[ch] == -CUDART_INF_F ? 0.f : -m_new[ch];
-                        sm.fac[half][ch * CH + lane] = fac[ch];
-                    }
-                }
-                named_barrier_sync(kBarHalf0 + half, 128);
-                if (i > 0) {
-                    // what was summed so far, here and in O, once the last block's P V is there
-                    wait(ok, &sm.pv_done[(j - 1) & 1], (j - 1) >> 1, a.err);
-                    tc_fence_after();
+                        load(ch);
+                        float mine = -CUDART_INF_F;
 #pragma unroll
-                    for (int ch = 0; ch < NCH; ++ch) {
-                        const float2 *fc = reinterpret_cast<const float2 *>(&sm.fac[half][ch * CH]);
-                        uint32_t o[CH];
-                        tmem_ld(lanes + kTmemO + (uint32_t)(c0 + ch * CH), o);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int c = 0; c < CH; c += 2) {
-                            const float2 f = fc[c / 2];
-                            sum[(ch * CH + c) / 2] = mul2(sum[(ch * CH + c) / 2], pack2(f.x, f.y));
-                            o[c] = __float_as_uint(__uint_as_float(o[c]) * f.x);
-                            o[c + 1] = __float_as_uint(__uint_as_float(o[c + 1]) * f.y);
+                        for (int c = 0; c < CH; ++c) {
+                            const float v = warp_max(__uint_as_float(s[c]));
+                            if (lane == c) mine = v;
                         }
-                        tmem_st(lanes + kTmemO + (uint32_t)(c0 + ch * CH), o);
+                        if (lane < CH) sm.top[g][quad][ch * CH + lane] = mine;
                     }
-                    tmem_st_wait();
-                    tc_fence_before();
-                }
-            }
-            // the weights of block j, once the products that read their place are done
-            const int before = j - C::kPBufs;
-            if (before >= 0) wait(ok, &sm.pv_done[before & 1], before >> 1, a.err);
-            uint8_t *pt = sm.p[j % C::kPBufs];
+                    named_barrier_sync(kBarHalf0 + g, 128);
+                    // (a column a thread)
+                    const int c = threadIdx.x & 127;
+                    float m_new = 0.f, fac = 0.f;
+                    if (c < NH) {
+                        const float top = fmaxf(fmaxf(sm.top[g][0][c], sm.top[g][1][c]),
+                                                fmaxf(sm.top[g][2][c], sm.top[g][3][c])) *
+                                          mult;
+                        const float old = first ? -CUDART_INF_F : m_unit[c];
+                        m_new = fmaxf(old, top);
+                        fac = old == m_new ? 1.f : ex2_approx(old - m_new);
+                        m_unit[c] = m_new;
+                        sm.negm[g][c] = m_new == -CUDART_INF_F ? 0.f : -m_new;
+                        sm.fac[g][c] = fac;
+                    }
+                    named_barrier_sync(kBarHalf0 + g, 128);
+                    if (!first) {
+                        // what was summed so far, here and in O, once the last block's P V is there
+                        // (a weight that overflowed leaves a sum that is none, and a factor 0)
+                        const float4 *fc = reinterpret_cast<const float4 *>(sm.fac[g]);
 #pragma unroll
-            for (int ch = 0; ch < NCH; ++ch) {
-                if (NCH > 1 || raise) {
+                        for (int x = 0; x < NH / 2; ++x) {
+                            const float2 f = reinterpret_cast<const float2 *>(fc)[x], v = unpack2(sum[x]);
+                            sum[x] = pack2(f.x > 0.f ? v.x * f.x : 0.f, f.y > 0.f ? v.y * f.y : 0.f);
+                        }
+                        wait(ok, &sm.pv_done[(j - kStep) & 1], (j - kStep) >> 1, a.err);
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int ch = 0; ch < NCH; ++ch) {
+                            tmem_ld(o_at + (uint32_t)(ch * CH), s);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int x = 0; x < CH; x += 4) {
+                                const float4 f = fc[(ch * CH + x) / 4];
+                                s[x] = __float_as_uint(__uint_as_float(s[x]) * f.x);
+                                s[x + 1] = __float_as_uint(__uint_as_float(s[x + 1]) * f.y);
+                                s[x + 2] = __float_as_uint(__uint_as_float(s[x + 2]) * f.z);
+                                s[x + 3] = __float_as_uint(__uint_as_float(s[x + 3]) * f.w);
+                            }
+                            tmem_st(o_at + (uint32_t)(ch * CH), s);
+                        }
+                        tmem_st_wait();
+                        tc_fence_before();
+                    }
+                }
+                // the weights of block j, once the products that read their place are done
+                const int before = j - C::kPBufs;
+                if (before >= 0) wait(ok, &sm.pv_done[before & 1], before >> 1, a.err);
+                const uint64_t sign2 = pack2(sign, sign);
+                float top = 0.f;
+#pragma unroll
+                for (int ch = 0; ch < NCH; ++ch) {
+                    if (ch * CH >= live) break;  // (the same for the whole warp)
                     load(ch);
-                    shift(ch);
-                }
-                if (ch == NCH - 1) {  // S is in registers
-                    tc_fence_before();
-                    warp_arrive(&sm.s_empty[j & 1]);
-                }
+                    const float4 *nm = reinterpret_cast<const float4 *>(&sm.negm[g][ch * CH]);
 #pragma unroll
-                for (int c = 0; c < CH; c += 8) {
-                    if (ch * CH + c >= live) break;  // the same for the whole warp
-                    uint32_t pk[4];
+                    for (int c = 0; c < CH; c += 8) {
+                        if (ch * CH + c >= live) break;
+                        uint32_t pk[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float u = ex2_approx(__uint_as_float(s[c + 2 * k]));
-                        const float v = ex2_approx(__uint_as_float(s[c + 2 * k + 1]));
-                        sum[(ch * CH + c) / 2 + k] = add2(sum[(ch * CH + c) / 2 + k], pack2(u, v));
-                        pk[k] = pack_f16x2(u, v);  // a weight keeps 11 bits, as many as f16 pages would
+                        for (int k = 0; k < 4; k += 2) {
+                            const float4 n = nm[c / 4 + k / 2];
+                            const float2 x0 = unpack2(fma2(
+                                pack2(__uint_as_float(s[c + 2 * k]), __uint_as_float(s[c + 2 * k + 1])), mult2,
+                                pack2(n.x, n.y)));
+                            const float2 x1 = unpack2(fma2(
+                                pack2(__uint_as_float(s[c + 2 * k + 2]), __uint_as_float(s[c + 2 * k + 3])), mult2,
+                                pack2(n.z, n.w)));
+                            const float u0 = ex2_approx(x0.x), v0 = ex2_approx(x0.y);
+                            const float u1 = ex2_approx(x1.x), v1 = ex2_approx(x1.y);
+                            const int at2 = (ch * CH + c) / 2 + k;
+                            sum[at2] = fma2(pack2(u0, v0), sign2, sum[at2]);
+                            sum[at2 + 1] = fma2(pack2(u1, v1), sign2, sum[at2 + 1]);
+                            top = max3(max3(top, u0, v0), u1, v1);
+                            pk[k] = pack_f16x2(u0, v0);  // a weight keeps 11 bits
+                            pk[k + 1] = pack_f16x2(u1, v1);
+                        }
+                        *reinterpret_cast<uint4 *>(pt + p_at<NP>(t, (c0 + ch * CH + c) / 8)) =
+                            make_uint4(pk[0], pk[1], pk[2], pk[3]);
                     }
-                    *reinterpret_cast<uint4 *>(pt + p_at<NP>(t, (c0 + ch * CH + c) / 8)) =
-                        make_uint4(pk[0], pk[1], pk[2], pk[3]);
                 }
+                if (raise) break;  // (no weight is above 1)
+                if (sign < 0.f) {
+                    sign = 1.f, raise = true;
+                    continue;
+                }
+                if (!barrier_any(kBarHalf0 + g, 128, top > kMaxWeight)) break;
+                sign = -1.f;
             }
+            tc_fence_before();
+            warp_arrive(&sm.s_empty[sb]);
             fence_proxy_async_smem();
             warp_arrive(&sm.p_full[j & 1]);
         }
         // ------------------------------------------------ the unit's epilogue
-        const long long px = p.x - p.f;
+        const long long W = sm.work, px = p.x - p.f;
+        const int nsh = (int)min((long long)gridDim.x, W);
+        const long long first_x = (long long)blockIdx.x * W / nsh;
+        auto cta_of = [&](long long x) { return (int)(((x + 1) * nsh - 1) / W); };
         const int c_first = cta_of(px), parts = cta_of(px + p.nb - 1) - c_first + 1;
         const int slot = 2 * (int)blockIdx.x + (p.x == first_x ? 0 : 1);
         const float fv = fp4_factor(a.v_factor, p.h, a.err);
         const size_t row0 = (size_t)p.b * a.n_q * a.Hq + (size_t)p.h * a.G;
+        // the groups with a block of this unit (their O hold something)
+        const bool has0 = !kAlt || p.n > 1 || (j0 & 1) == 0, has1 = kAlt && (p.n > 1 || (j0 & 1) == 1);
+        j0 += p.n;
 #pragma unroll
         for (int ch = 0; ch < NCH; ++ch) {
             float v[CH];
@@ -563,47 +582,88 @@ __device__ __forceinline__ void softmax_role(Smem<D, NP> &sm, const Fp4AttnArgs 
                 v[c] = f.x, v[c + 1] = f.y;
             }
             column_sums<CH>(v, lane);
-            if (lane < CH) sm.warp_col[half][quad][ch * CH + lane] = v[0];
+            if (lane < CH) sm.sums[unit & 1][g][quad][ch * CH + lane] = v[0];
         }
-        named_barrier_sync(kBarHalf0 + half, 128);
-        if (quad == 0 && lane < CH) {
+        if (kAlt) named_barrier_sync(kBarSoft, 256);
+        else named_barrier_sync(kBarHalf0 + g, 128);
+        // the columns g * kEC .. of both groups' results, a column a lane: their
+        // common maximum and sum, and what each O is multiplied by
+        constexpr int EC = C::kEC, CE = EC < 32 ? EC : 32, NE = EC / CE;
+        const int e0 = g * EC;
+        float w0[NE], w1[NE];
 #pragma unroll
-            for (int ch = 0; ch < NCH; ++ch) {
-                const int c = ch * CH + lane;
-                const float l = (sm.warp_col[half][0][c] + sm.warp_col[half][1][c]) +
-                                (sm.warp_col[half][2][c] + sm.warp_col[half][3][c]);
-                sm.inv[half][c] = parts == 1 ? (l > 0.f ? fv / l : 0.f) : 1.f;
-                const int r = c0 + c;
-                if (r < a.M) {
-                    if (parts > 1)
-                        reinterpret_cast<float2 *>(a.part_ml)[(size_t)slot * a.M + r] = make_float2(sm.m[half][c], l);
-                    else if (a.lse)
-                        a.lse[row0 + sm.row_off[r]] = (sm.m[half][c] + __log2f(l)) * kLn2;
-                }
+        for (int ch = 0; ch < NE; ++ch) {
+            const int r = e0 + ch * CE + (lane & (CE - 1)), c = kAlt ? r : r - e0, ga = kAlt ? 0 : g;
+            auto total = [&](int gg) {
+                const float(*q)[64] = sm.sums[unit & 1][gg];
+                return (q[0][c] + q[1][c]) + (q[2][c] + q[3][c]);
+            };
+            float m0 = has0 ? sm.m[unit & 1][ga][c] : -CUDART_INF_F, l0 = has0 ? total(ga) : 0.f;
+            const float m1 = has1 ? sm.m[unit & 1][1][c] : -CUDART_INF_F, l1 = has1 ? total(1) : 0.f;
+            const float m = fmaxf(m0, m1);
+            w0[ch] = m0 == m ? 1.f : ex2_approx(m0 - m);
+            w1[ch] = m1 == m ? 1.f : ex2_approx(m1 - m);
+            const float l = l0 * w0[ch] + l1 * w1[ch];
+            if (parts == 1) {
+                const float inv = l > 0.f ? fv / l : 0.f;
+                w0[ch] *= inv, w1[ch] *= inv;
+            }
+            if (quad == 0 && lane < CE && r < a.M) {
+                if (parts > 1) reinterpret_cast<float2 *>(a.part_ml)[(size_t)slot * a.M + r] = make_float2(m, l);
+                else if (a.lse) a.lse[row0 + sm.row_off[r]] = (m + __log2f(l)) * kLn2;
             }
         }
-        named_barrier_sync(kBarHalf0 + half, 128);
         wait(ok, &sm.o_full, unit, a.err);
         tc_fence_after();
+        // turned in this group's part of the weights' place, whose products are all
+        // done (the next unit's first weights wait for a barrier of the group)
+        float *turn = reinterpret_cast<float *>(kAlt ? sm.p[g] : sm.p[0] + g * kSlab);
 #pragma unroll
-        for (int ch = 0; ch < NCH; ++ch) {
-            if (ch * CH >= live) break;
-            uint32_t o[CH];
-            tmem_ld(lanes + kTmemO + (uint32_t)(c0 + ch * CH), o);
+        for (int ch = 0; ch < NE; ++ch) {
+            if (e0 + ch * CE >= a.M) break;
+            uint32_t o[CE];
+            tmem_ld(lanes + kTmemO + (uint32_t)((has0 ? 0 : NP) + e0 + ch * CE), o);
             tmem_ld_wait();
+            const float wa = has0 ? w0[ch] : w1[ch];
+#pragma unroll
+            for (int c = 0; c < CE; ++c)
+                o[c] = __float_as_uint(__uint_as_float(o[c]) * __shfl_sync(0xffffffffu, wa, c));
+            if (has0 && has1) {
+                uint32_t o1[CE];
+                tmem_ld(lanes + kTmemO + (uint32_t)(NP + e0 + ch * CE), o1);
+                tmem_ld_wait();
+#pragma unroll
+                for (int c = 0; c < CE; ++c)
+                    o[c] = __float_as_uint(fmaf(__uint_as_float(o1[c]), __shfl_sync(0xffffffffu, w1[ch], c),
+                                                __uint_as_float(o[c])));
+            }
+            if (NE == 1) {  // O is in registers
+                tc_fence_before();
+                warp_arrive(&sm.o_empty);
+            }
+            if (ch > 0) named_barrier_sync(kBarHalf0 + g, 128);
             if (t < D) {
 #pragma unroll
-                for (int c = 0; c < CH; ++c) {
-                    const int r = c0 + ch * CH + c;
-                    if (r >= a.M) break;
-                    const float v = __uint_as_float(o[c]) * sm.inv[half][ch * CH + c];
-                    if (parts == 1) a.out[(row0 + sm.row_off[r]) * D + t] = __float2bfloat16_rn(v);
-                    else a.part_acc[((size_t)slot * a.M + r) * D + t] = v;
-                }
+                for (int c = 0; c < CE; ++c) turn[c * D + t] = __uint_as_float(o[c]);
+            }
+            named_barrier_sync(kBarHalf0 + g, 128);
+            const int rows = min(CE, a.M - e0 - ch * CE);
+#pragma unroll 1
+            for (int c = quad; c < rows; c += 4) {
+                if (lane >= D / 4) break;
+                const int r = e0 + ch * CE + c;
+                const float4 v = reinterpret_cast<const float4 *>(turn + c * D)[lane];
+                if (parts == 1)
+                    reinterpret_cast<uint2 *>(a.out + (row0 + sm.row_off[r]) * D)[lane] =
+                        make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+                else
+                    reinterpret_cast<float4 *>(a.part_acc + ((size_t)slot * a.M + r) * D)[lane] = v;
             }
         }
-        tc_fence_before();
-        warp_arrive(&sm.o_empty);
+        if (NE > 1 || e0 >= a.M) {
+            tc_fence_before();
+            warp_arrive(&sm.o_empty);
+        }
         if (parts == 1) continue;
         // every part of the pair is written: the last one's CTA joins them
         __threadfence();
@@ -646,9 +706,7 @@ __device__ __forceinline__ void softmax_role(Smem<D, NP> &sm, const Fp4AttnArgs 
 
 template <int D, int NP>
 __global__ void __launch_bounds__(Cfg<D, NP>::kThreads, 1)
-    fp4_attn_kernel(const __grid_constant__ CUtensorMap mkc, const __grid_constant__ CUtensorMap mvc,
-                    const __grid_constant__ CUtensorMap mks, const __grid_constant__ CUtensorMap mvs,
-                    const __grid_constant__ CUtensorMap mq0, const __grid_constant__ CUtensorMap mq1,
+    fp4_attn_kernel(const __grid_constant__ CUtensorMap mq0, const __grid_constant__ CUtensorMap mq1,
                     const __grid_constant__ Fp4AttnArgs a) {
     using C = Cfg<D, NP>;
     constexpr int kStages = C::kStages;
@@ -658,31 +716,33 @@ __global__ void __launch_bounds__(Cfg<D, NP>::kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
 
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) {
-            mbar_init(&sm.raw_full[i], 1);
-            mbar_init(&sm.raw_empty[i], C::kBoth ? 4 : 8);
-        }
+        for (int i = 0; i < kStages; ++i)
+            for (int kv = 0; kv < 2; ++kv) {
+                mbar_init(&sm.raw_full[kv][i], 32);
+                mbar_init(&sm.raw_empty[kv][i], 4);
+            }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.k_full[i], 4);
             mbar_init(&sm.k_empty[i], 1);
-            mbar_init(&sm.v_full[i], 4);
             mbar_init(&sm.q_full[i], 1);
             mbar_init(&sm.q_ready[i], 4);
             mbar_init(&sm.q_empty[i], 1);
-            mbar_init(&sm.s_full[i], 1);
-            mbar_init(&sm.s_empty[i], 8);
-            mbar_init(&sm.p_full[i], 8);
+            mbar_init(&sm.p_full[i], C::kAlt ? 4 : 8);
             mbar_init(&sm.pv_done[i], 1);
+        }
+        for (int i = 0; i < C::kVBufs; ++i) {
+            mbar_init(&sm.v_full[i], 4);
+            mbar_init(&sm.v_empty[i], 1);
+        }
+        for (int i = 0; i < C::kSBufs; ++i) {
+            mbar_init(&sm.s_full[i], 1);
+            mbar_init(&sm.s_empty[i], C::kAlt ? 4 : 8);
         }
         mbar_init(&sm.o_full, 1);
         mbar_init(&sm.o_empty, 8);
         fence_mbar_init();
     }
-    if (warp == C::kProducerWarp && lane == 0) {
-        prefetch_tensormap(&mkc);
-        prefetch_tensormap(&mvc);
-        prefetch_tensormap(&mks);
-        prefetch_tensormap(&mvs);
+    if (warp == C::kCopyWarp && lane == 0) {
         prefetch_tensormap(&mq0);
         prefetch_tensormap(&mq1);
     }
@@ -691,7 +751,7 @@ __global__ void __launch_bounds__(Cfg<D, NP>::kThreads, 1)
         reinterpret_cast<uint4 *>(sm.q[0])[i] = make_uint4(0u, 0u, 0u, 0u);
     if (tid < a.M) sm.row_off[tid] = tid / a.G * a.Hq + tid % a.G;
     fence_proxy_async_smem();
-    if (warp == C::kMmaWarp) {
+    if (warp == C::kPvWarp) {
         tmem_alloc(&sm.tmem_base, kTmemCols);
         tmem_relinquish();
     }
@@ -761,27 +821,29 @@ __global__ void __launch_bounds__(Cfg<D, NP>::kThreads, 1)
 #pragma unroll 1
             for (int i = 0; i < p.n; ++i, ++j) {
                 const int st = j % kStages;
-                wait(ok, &sm.raw_full[st], j / kStages, a.err);
+                wait(ok, &sm.raw_full[0][st], j / kStages, a.err);
                 if (j >= 2) wait(ok, &sm.k_empty[j & 1], (j - 2) >> 1, a.err);
                 tc_fence_after();
                 decode_k<D, NP>(sm, st, lanes, j & 1, tid);
-                if (!C::kBoth) warp_arrive(&sm.raw_empty[st]);
+                warp_arrive(&sm.raw_empty[0][st]);
                 tmem_st_wait();
                 tc_fence_before();
                 warp_arrive(&sm.k_full[j & 1]);
-                if (C::kBoth) {
-                    if (j >= 2) wait(ok, &sm.pv_done[j & 1], (j - 2) >> 1, a.err);
-                    decode_v<D, NP>(sm, st, j & 1, tid, (p.f + i) * kNB + tid < p.L + a.n_q);
-                    warp_arrive(&sm.raw_empty[st]);
+                if (!C::kAlt) {
+                    wait(ok, &sm.raw_full[1][st], j / kStages, a.err);
+                    const int vb = j % C::kVBufs;
+                    if (j >= C::kVBufs) wait(ok, &sm.v_empty[vb], j / C::kVBufs - 1, a.err);
+                    decode_v<D, NP>(sm, st, vb, tid, (p.f + i) * kNB + tid < p.L + a.n_q);
+                    warp_arrive(&sm.raw_empty[1][st]);
                     fence_proxy_async_smem();
-                    warp_arrive(&sm.v_full[j & 1]);
+                    warp_arrive(&sm.v_full[vb]);
                 }
             }
         }
     } else if (warp < 12) {
         regs_inc<C::kRegsSoftmax>();
         softmax_role<D, NP>(sm, a, w, tmem);
-    } else if (!C::kBoth && warp < 16) {
+    } else if (C::kAlt && warp < 16) {
         regs_dec<C::kRegsDecode>();
         // ============================================ V decoded
         const int t = 32 * (warp - 12) + lane;
@@ -791,35 +853,44 @@ __global__ void __launch_bounds__(Cfg<D, NP>::kThreads, 1)
 #pragma unroll 1
             for (int i = 0; i < p.n; ++i, ++j) {
                 const int st = j % kStages;
-                wait(ok, &sm.raw_full[st], j / kStages, a.err);
-                if (j >= 2) wait(ok, &sm.pv_done[j & 1], (j - 2) >> 1, a.err);
-                decode_v<D, NP>(sm, st, j & 1, t, (p.f + i) * kNB + t < p.L + a.n_q);
-                warp_arrive(&sm.raw_empty[st]);
+                wait(ok, &sm.raw_full[1][st], j / kStages, a.err);
+                const int vb = j % C::kVBufs;
+                if (j >= C::kVBufs) wait(ok, &sm.v_empty[vb], j / C::kVBufs - 1, a.err);
+                decode_v<D, NP>(sm, st, vb, t, (p.f + i) * kNB + t < p.L + a.n_q);
+                warp_arrive(&sm.raw_empty[1][st]);
                 fence_proxy_async_smem();
-                warp_arrive(&sm.v_full[j & 1]);
+                warp_arrive(&sm.v_full[vb]);
             }
         }
     } else {
     regs_dec<C::kRegsIssue>();
-    if (warp == C::kProducerWarp) {
-        // ============================================ copies
-        const uint64_t pol = policy_evict_first();
-        const int none = a.num_blocks * a.Hkv;  // behind the pool: zeros
-        const int kind = lane >> 3, pg = lane & 7;
-        const CUtensorMap *map = kind == 0 ? &mkc : kind == 1 ? &mvc : kind == 2 ? &mks : &mvs;
+    if (warp < C::kPvWarp) {
+        // ============================================ copies: K's, V's
+        const int kv = warp - C::kCopyWarp;
+        const uint8_t *pool = kv ? a.v_pool : a.k_pool;
+        // a lane's 16 bytes of 32 lanes' codes, where they go, and of the scales
+        constexpr int kRowChunks = D / 32, kSweeps = D / 64, kScaleLanes = D / 16;
+        const int row = lane / kRowChunks, sw = D == 128 ? (row >> 1) & 3 : (row >> 2) & 1;
+        const uint32_t code_dst = (uint32_t)(row * (D / 2) + (((lane % kRowChunks) ^ sw) << 4));
+        const uint32_t codes0 = smem_u32(kv ? sm.vc[0] : sm.kc[0]) + code_dst;
+        const uint32_t scales0 = smem_u32(kv ? sm.vs[0] : sm.ks[0]) + (lane / kScaleLanes) * 128 +
+                                 (lane % kScaleLanes) * 16;
         int j = 0, unit = 0;
 #pragma unroll 1
-        for (; w.next(a, p) && ok; ++unit) {
-            if (unit >= 2) wait(ok, &sm.q_empty[unit & 1], (unit - 2) >> 1, a.err);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&sm.q_full[unit & 1], (uint32_t)(a.M * D * 2));
-                tma_load_4d(sm.q[unit & 1], &mq0, 0, p.h * a.G, 0, p.b, &sm.q_full[unit & 1], pol);
-                if (D == 128)
-                    tma_load_4d(sm.q[unit & 1] + NP * 128, &mq1, 0, p.h * a.G, 0, p.b, &sm.q_full[unit & 1], pol);
+        for (; ok && w.next(a, p); ++unit) {
+            if (kv == 0) {
+                if (unit >= 2) wait(ok, &sm.q_empty[unit & 1], (unit - 2) >> 1, a.err);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (lane == 0) {
+                    uint64_t *bar = &sm.q_full[unit & 1];
+                    const uint64_t pol = policy_evict_first();
+                    mbar_arrive_expect_tx(bar, (uint32_t)(a.M * D * 2));
+                    tma_load_4d(sm.q[unit & 1], &mq0, 0, p.h * a.G, 0, p.b, bar, pol);
+                    if (D == 128) tma_load_4d(sm.q[unit & 1] + NP * 128, &mq1, 0, p.h * a.G, 0, p.b, bar, pol);
+                }
+                __syncwarp();
             }
-            __syncwarp();
             const int pages = (p.L + a.n_q + kBlockSize - 1) / kBlockSize - p.f * kPB;  // from the first block on
             const int32_t *table = a.block_table + (size_t)p.b * a.max_blocks + (size_t)p.f * kPB;
             int ids = 0;
@@ -827,66 +898,59 @@ __global__ void __launch_bounds__(Cfg<D, NP>::kThreads, 1)
             for (int i = 0; i < p.n; ++i, ++j) {
                 if ((i & 3) == 0) {  // 32 pages at a time
                     const int at = i * kPB + lane;
-                    ids = none;
-                    if (at < pages) {
-                        const int blk = __ldg(table + at);
-                        if (blk >= 0 && blk < a.num_blocks) ids = blk * a.Hkv + p.h;
-                        else if (at < p.n * kPB) raise_error(a.err, SVPA_DEVERR_BAD_BLOCK);
+                    ids = -1;
+                    if (at < pages && at < p.n * kPB) {
+                        ids = __ldg(table + at);
+                        if (ids < 0 || ids >= a.num_blocks) {
+                            if (kv == 0) raise_error(a.err, SVPA_DEVERR_BAD_BLOCK);
+                            ids = -1;
+                        }
                     }
                 }
-                const int id = __shfl_sync(0xffffffffu, ids, (i & 3) * kPB + pg);
                 const int st = j % kStages;
-                if (j >= kStages) wait(ok, &sm.raw_empty[st], j / kStages - 1, a.err);
+                if (j >= kStages) wait(ok, &sm.raw_empty[kv][st], j / kStages - 1, a.err);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                if (lane == 0) mbar_arrive_expect_tx(&sm.raw_full[st], kNB * D + 2 * kNB * D / 16);
-                __syncwarp();
-                if (kind < 2)
-                    tma_load_3d((kind ? sm.vc[st] : sm.kc[st]) + pg * (kBlockSize * D / 2), map, 0, 0, id,
-                                &sm.raw_full[st], pol);
-                else
-                    tma_load_2d((kind == 3 ? sm.vs[st] : sm.ks[st]) + pg * 128, map, 0, id, &sm.raw_full[st], pol);
-            }
-        }
-        if (!ok) {  // copies in flight land before the CTA's memory is given up
-            bool still = true;
-            for (int i = max(0, j - kStages); i < j; ++i) wait(still, &sm.raw_full[i % kStages], i / kStages, a.err);
-            for (int i = max(0, unit - 1); i <= unit; ++i)
-                if (i >= 0) wait(still, &sm.q_full[i & 1], i >> 1, a.err);
-        }
-    } else if (warp == C::kMmaWarp) {
-        // ============================================ MMAs
-        const uint32_t idS = idesc(NP, 0, 0), idO = idesc(NP, 1, 1);
-        int j = 0, unit = 0, pj = 0, punit = 0;
-        bool pfirst = true;
-        auto products = [&](int jj, bool first, bool last, int u) {  // O^T (+)= V^T P^T of block jj
-            wait(ok, &sm.p_full[jj & 1], jj >> 1, a.err);
-            if (first && u > 0) wait(ok, &sm.o_empty, u - 1, a.err);
-            wait(ok, &sm.v_full[jj & 1], jj >> 1, a.err);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) return;
-            tc_fence_after();
-            const uint32_t va = smem_u32(sm.v[jj & 1]), pa = smem_u32(sm.p[jj % C::kPBufs]);
-            constexpr uint32_t row = NP < 64 ? 2 * NP : 128;
-            if (elect_one()) {
+                // (a page that is not there stays as it was: its tokens are masked, its V rows zeroed)
+#pragma unroll 2
+                for (int pg = 0; pg < kPB; ++pg) {
+                    const int id = __shfl_sync(0xffffffffu, ids, (i & 3) * kPB + pg);
+                    if (id >= 0) {
+                        const uint8_t *src = pool + ((size_t)id * a.Hkv + p.h) * fp4_tile_bytes(D) + lane * 16;
+                        const uint32_t dst = codes0 + st * C::kCodes + pg * (kBlockSize * D / 2);
 #pragma unroll
-                for (int k = 0; k < kNB / 16; ++k)
-                    umma_bf16(tmem + kTmemO, umma_desc_sw128(va + k * 2048, kSlab, 1024), p_desc<NP>(pa + k * 16 * row),
-                              idO, first && k == 0 ? 0u : 1u);
-                umma_commit(&sm.pv_done[jj & 1]);
-                if (last) umma_commit(&sm.o_full);
+                        for (int x = 0; x < kSweeps; ++x) cp_async_16(dst + 512 * x, src + 512 * x);
+                    }
+                }
+#pragma unroll
+                for (int pg = 0; pg < kPB; pg += 32 / kScaleLanes) {
+                    const int id = __shfl_sync(0xffffffffu, ids, (i & 3) * kPB + pg + lane / kScaleLanes);
+                    if (id >= 0)
+                        cp_async_16(scales0 + st * C::kScales + pg * 128,
+                                    pool + ((size_t)id * a.Hkv + p.h) * fp4_tile_bytes(D) + fp4_code_bytes(D) +
+                                        (lane % kScaleLanes) * 16);
+                }
+                cp_async_mbar_arrive_noinc(&sm.raw_full[kv][st]);
             }
-            __syncwarp();
-        };
-        bool plast = false;
+        }
+        // (copies in flight land before the CTA's memory is given up)
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        if (!ok && kv == 0) {
+            bool still = true;
+            for (int i = max(0, unit - 1); i <= unit; ++i) wait(still, &sm.q_full[i & 1], i >> 1, a.err);
+        }
+    } else if (warp == C::kScoreWarp) {
+        // ============================================ S^T = K Q^T
+        const uint32_t id = idesc(NP, 0, 0);
+        int j = 0, unit = 0;
 #pragma unroll 1
         for (; ok && w.next(a, p); ++unit) {
 #pragma unroll 1
-            for (int i = 0; i < p.n && ok; ++i, ++j) {
-                // S^T of block j, ahead of the block before's products
-                wait(ok, &sm.k_full[j & 1], j >> 1, a.err);
+            for (int i = 0; i < p.n; ++i, ++j) {
+                const int sb = j % C::kSBufs;
                 if (i == 0) wait(ok, &sm.q_ready[unit & 1], unit >> 1, a.err);
-                if (j >= 2) wait(ok, &sm.s_empty[j & 1], (j - 2) >> 1, a.err);
+                if (j >= C::kSBufs) wait(ok, &sm.s_empty[sb], j / C::kSBufs - 1, a.err);
+                wait(ok, &sm.k_full[j & 1], j >> 1, a.err);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
@@ -894,35 +958,67 @@ __global__ void __launch_bounds__(Cfg<D, NP>::kThreads, 1)
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
-                        umma_bf16_tmem_a(tmem + kTmemS + (uint32_t)((j & 1) * NP), tmem + kTmemK + 64 * (j & 1) + 8 * k,
-                                         umma_desc_sw128(qa + (k >> 2) * NP * 128 + (k & 3) * 32, 16, 1024), idS,
+                        umma_bf16_tmem_a(tmem + kTmemS + (uint32_t)(sb * NP), tmem + kTmemK + 64 * (j & 1) + 8 * k,
+                                         umma_desc_sw128(qa + (k >> 2) * NP * 128 + (k & 3) * 32, 16, 1024), id,
                                          k == 0 ? 0u : 1u);
                     umma_commit(&sm.k_empty[j & 1]);
-                    umma_commit(&sm.s_full[j & 1]);
+                    umma_commit(&sm.s_full[sb]);
                     if (i == p.n - 1) umma_commit(&sm.q_empty[unit & 1]);
                 }
                 __syncwarp();
-                if (j > 0) products(pj, pfirst, plast, punit);
-                pj = j, pfirst = i == 0, plast = i == p.n - 1, punit = unit;
+            }
+        }
+        // the last arrivals land before the barriers are given up
+        if (ok && j > 0) {
+            wait(ok, &sm.k_empty[(j - 1) & 1], (j - 1) >> 1, a.err);
+            wait(ok, &sm.q_empty[(unit - 1) & 1], (unit - 1) >> 1, a.err);
+        }
+    } else {
+        // ============================================ O^T += V^T P^T
+        const uint32_t id = idesc(NP, 1, 1);
+        constexpr uint32_t row = NP < 64 ? 2 * NP : 128;  // bytes of a token's weights
+        int j = 0, unit = 0;
+#pragma unroll 1
+        for (; ok && w.next(a, p); ++unit) {
+#pragma unroll 1
+            for (int i = 0; i < p.n; ++i, ++j) {
+                const int vb = j % C::kVBufs;
+                if (i == 0 && unit > 0) wait(ok, &sm.o_empty, unit - 1, a.err);
+                wait(ok, &sm.v_full[vb], j / C::kVBufs, a.err);
+                wait(ok, &sm.p_full[j & 1], j >> 1, a.err);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t va = smem_u32(sm.v[vb]), pa = smem_u32(sm.p[j % C::kPBufs]);
+                const uint32_t o = tmem + kTmemO + (C::kAlt ? (j & 1) * NP : 0);
+                const bool first = i < (C::kAlt ? 2 : 1);
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < kNB / 16; ++k)
+                        umma_bf16(o, umma_desc_sw128(va + k * 2048, kSlab, 1024), p_desc<NP>(pa + k * 16 * row), id,
+                                  first && k == 0 ? 0u : 1u);
+                    umma_commit(&sm.pv_done[j & 1]);
+                    umma_commit(&sm.v_empty[vb]);
+                    if (i == p.n - 1) umma_commit(&sm.o_full);
+                }
+                __syncwarp();
             }
         }
         if (ok && j > 0) {
-            products(pj, pfirst, plast, punit);
-            // the last arrivals land before the barriers are given up
-            wait(ok, &sm.pv_done[pj & 1], pj >> 1, a.err);
-            wait(ok, &sm.q_empty[punit & 1], punit >> 1, a.err);
-            wait(ok, &sm.o_full, punit, a.err);
+            wait(ok, &sm.pv_done[(j - 1) & 1], (j - 1) >> 1, a.err);
+            wait(ok, &sm.v_empty[(j - 1) % C::kVBufs], (j - 1) / C::kVBufs, a.err);
+            wait(ok, &sm.o_full, unit - 1, a.err);
         }
     }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == C::kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+    if (warp == C::kPvWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
 template <int D, int NP>
-cudaError_t launch(const Fp4AttnMaps &m, const Fp4AttnArgs &a, cudaStream_t st) {
+cudaError_t launch(const CUtensorMap *mq, const Fp4AttnArgs &a, cudaStream_t st) {
     using C = Cfg<D, NP>;
     using S = Smem<D, NP>;
     static_assert(C::kStages >= 2 && sizeof(S) + 1024 <= 232448, "fp4_attn_kernel shared memory");
@@ -937,24 +1033,24 @@ cudaError_t launch(const Fp4AttnMaps &m, const Fp4AttnArgs &a, cudaStream_t st) 
         return cudaFuncSetAttribute(fp4_attn_kernel<D, NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     });
     if (e != cudaSuccess) return e;
-    fp4_attn_kernel<D, NP><<<fp4_attn_grid(), C::kThreads, smem, st>>>(m.kc, m.vc, m.ks, m.vs, m.q[0], m.q[1], a);
+    fp4_attn_kernel<D, NP><<<fp4_attn_grid(), C::kThreads, smem, st>>>(mq[0], mq[1], a);
     return cudaGetLastError();
 }
 
 template <int D>
-cudaError_t launch_d(const Fp4AttnMaps &m, const Fp4AttnArgs &a, cudaStream_t st) {
-    if (a.M <= 16) return launch<D, 16>(m, a, st);
-    if (a.M <= 32) return launch<D, 32>(m, a, st);
-    if (a.M <= 64) return launch<D, 64>(m, a, st);
-    return launch<D, 128>(m, a, st);
+cudaError_t launch_d(const CUtensorMap *mq, const Fp4AttnArgs &a, cudaStream_t st) {
+    if (a.M <= 16) return launch<D, 16>(mq, a, st);
+    if (a.M <= 32) return launch<D, 32>(mq, a, st);
+    if (a.M <= 64) return launch<D, 64>(mq, a, st);
+    return launch<D, 128>(mq, a, st);
 }
 
 }  // namespace
 
 int fp4_attn_grid() { return sm_count(); }
 
-cudaError_t launch_paged_verify_attn_fp4(const Fp4AttnMaps &m, const Fp4AttnArgs &a, int D, cudaStream_t st) {
-    return D == 64 ? launch_d<64>(m, a, st) : launch_d<128>(m, a, st);
+cudaError_t launch_paged_verify_attn_fp4(const CUtensorMap *mq, const Fp4AttnArgs &a, int D, cudaStream_t st) {
+    return D == 64 ? launch_d<64>(mq, a, st) : launch_d<128>(mq, a, st);
 }
 
 }  // namespace svpa

@@ -103,8 +103,6 @@ svpa_status check_attn(const svpa_attn_params *p) {
     return SVPA_OK;
 }
 
-constexpr size_t fp4_tile(int D) { return 9 * (size_t)D; }
-
 // The attention's workspace: [counters][tickets][parts' (max, sum)][parts' accumulators].
 struct AttnSpace {
     size_t tickets, off_ml, off_acc, bytes;
@@ -287,41 +285,26 @@ svpa_status svpa_paged_verify_attn_fp4(const svpa_attn_params *p, const void *q,
     if (!enc) return SVPA_ERR_CUDA;
 
     const int D = p->head_dim, G = p->num_q_heads / p->num_kv_heads;
-    Fp4AttnMaps maps;
+    CUtensorMap mq[2];
     const cuuint32_t ones[4] = {1, 1, 1, 1};
-    auto encode = [&](CUtensorMap *m, CUtensorMapDataType type, int dims, const void *base, const cuuint64_t *size,
-                      const cuuint64_t *stride, const cuuint32_t *box, CUtensorMapSwizzle swizzle) {
-        return enc(m, type, (cuuint32_t)dims, const_cast<void *>(base), size, stride, box, ones,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-    };
-    const cuuint64_t tiles = (cuuint64_t)p->num_blocks * p->num_kv_heads, tile = (cuuint64_t)fp4_tile(D);
-    for (int kv = 0; kv < 2; ++kv) {
-        const uint8_t *pool = static_cast<const uint8_t *>(kv ? v_pool : k_pool);
-        const cuuint64_t cd[3] = {(cuuint64_t)D / 2, kBlockSize, tiles}, cs[2] = {(cuuint64_t)D / 2, tile};
-        const cuuint32_t cb[3] = {(cuuint32_t)D / 2, kBlockSize, 1};
-        const cuuint64_t sd[2] = {(cuuint64_t)D, tiles}, ss[1] = {tile};
-        const cuuint32_t sb[2] = {(cuuint32_t)D, 1};
-        if (!encode(kv ? &maps.vc : &maps.kc, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, pool, cd, cs, cb,
-                    D == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B) ||
-            !encode(kv ? &maps.vs : &maps.ks, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, pool + 8 * D, sd, ss, sb,
-                    CU_TENSOR_MAP_SWIZZLE_NONE))
-            return SVPA_ERR_CUDA;
-    }
     // queries [B, n_q, Hq, D]: (64 columns, G heads, n_q queries) of a sequence at a time
     const cuuint64_t qd[4] = {64, (cuuint64_t)p->num_q_heads, (cuuint64_t)p->n_q, (cuuint64_t)p->batch};
     const cuuint64_t qs[3] = {(cuuint64_t)D * 2, (cuuint64_t)p->num_q_heads * D * 2,
                               (cuuint64_t)p->n_q * p->num_q_heads * D * 2};
     const cuuint32_t qb[4] = {64, (cuuint32_t)G, (cuuint32_t)p->n_q, 1};
-    for (int i = 0; i < 2; ++i)
-        if (!encode(&maps.q[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
-                    static_cast<const uint8_t *>(q) + (D == 128 ? 128 * i : 0), qd, qs, qb,
-                    CU_TENSOR_MAP_SWIZZLE_128B))
+    for (int i = 0; i < 2; ++i) {
+        uint8_t *base = static_cast<uint8_t *>(const_cast<void *>(q)) + (D == 128 ? 128 * i : 0);
+        if (enc(&mq[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, qd, qs, qb, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return SVPA_ERR_CUDA;
+    }
 
     Fp4AttnArgs a;
     memset(&a, 0, sizeof a);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
+    a.k_pool = static_cast<const uint8_t *>(k_pool);
+    a.v_pool = static_cast<const uint8_t *>(v_pool);
     a.k_factor = k_factor;
     a.v_factor = v_factor;
     a.block_table = block_table;
@@ -353,7 +336,7 @@ svpa_status svpa_paged_verify_attn_fp4(const svpa_attn_params *p, const void *q,
         const cudaError_t e = cudaMemsetAsync(a.tickets, 0, sp.tickets, st);
         if (e != cudaSuccess) return from_cuda(e);
     }
-    return from_cuda(launch_paged_verify_attn_fp4(maps, a, D, st));
+    return from_cuda(launch_paged_verify_attn_fp4(mq, a, D, st));
 }
 
 }  // extern "C"
