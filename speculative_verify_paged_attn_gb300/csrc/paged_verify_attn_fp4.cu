@@ -24,12 +24,14 @@
 // split evenly over one persistent CTA per SM; the parts of a pair that is cut
 // are merged by the CTA that writes the last of them.
 // Warps: 0-3 decode K and turn the queries to f16; 4-7 and 8-11 are the softmax
-// and the epilogue; 12-15 decode V; then a warp that copies K's pages, one for
-// V's, and one each that issues the MMAs of either product (with 128 columns
-// there are no warps for V: Cfg).  The pages are copied 16 bytes a lane
-// (cp.async): by bulk copies of each page's codes and scales, 32 a block at some
-// 95 cycles each, the copies were what bound the kernel.  A warp reads the TMEM
-// lanes of quadrant warp % 4.  Every role walks the same list of blocks.
+// and the epilogue; 12-15 decode V; then a warp that copies the queries and one
+// each that issues the MMAs of either product (with 128 columns warps 0-3 decode
+// V too: Cfg).  A decoding warp copies the pages of its own tokens ahead of
+// itself (cp.async), so that no other warp is waited for: by bulk copies of each
+// page's codes and scales, 32 a block at some 95 cycles each, the copies bound
+// the kernel (855 us against the 625 of a copying warp each for K and V, 64 x 1
+// queries of 64 / 8 heads behind 8K to 32K tokens).  A warp reads the TMEM lanes
+// of quadrant warp % 4.  Every role walks the same list of blocks.
 // All waits are bounded: a role whose wait ran out goes on without waiting.
 #include <math_constants.h>
 
@@ -83,6 +85,26 @@ struct Walk {
     }
 };
 
+// A warp's place in the list and its unit, kept in shared memory: the registers
+// are for scores, sums and codes.
+struct Cursor {
+    Walk w;
+    Piece p;
+    __device__ __forceinline__ void begin(const Walk &at) {
+        if ((threadIdx.x & 31) == 0) w = at;
+    }
+    __device__ __forceinline__ bool next(const Fp4AttnArgs &a) {
+        int more = 0;
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) {
+            Walk u = w;
+            more = u.next(a, p);
+            w = u;
+        }
+        return __shfl_sync(0xffffffffu, more, 0) != 0;
+    }
+};
+
 template <int D, int NP>
 struct Cfg {
     // Up to 64 columns: the two softmax groups take the blocks in turn, each with
@@ -90,9 +112,9 @@ struct Cfg {
     // runs beside the other's.  128: each takes half of every block's columns (two
     // O do not fit TMEM), and warps 0-3 decode V too.
     static constexpr bool kAlt = NP < 128;
-    static constexpr int kCopyWarp = kAlt ? 16 : 12;  // K's and V's copies, then the MMAs: P V, S
-    static constexpr int kPvWarp = kCopyWarp + 2, kScoreWarp = kCopyWarp + 3;
-    static constexpr int kThreads = 32 * (kCopyWarp + 4);
+    static constexpr int kQueryWarp = kAlt ? 16 : 12;  // the queries' copies; then the MMAs: P V, S; one idle
+    static constexpr int kPvWarp = kQueryWarp + 1, kScoreWarp = kQueryWarp + 2;
+    static constexpr int kThreads = 32 * (kQueryWarp + 4);
     // registers a thread, from the 96 (128 with 16 warps) at launch: their sum
     // over the warps of a scheduler stays within 5 * 96 (4 * 128)
     static constexpr int kRegsDecode = kAlt ? 80 : 112, kRegsIssue = 64, kRegsSoftmax = kAlt ? 128 : 160;
@@ -126,7 +148,6 @@ struct Smem {
     // two before is there, whose buffer the softmax has read four blocks earlier
     float mult[8];
     int32_t row_off[128];              // query row -> row of out behind the unit's first
-    uint64_t raw_full[2][C::kStages], raw_empty[2][C::kStages];  // K's and V's
     uint64_t k_full[2], k_empty[2], v_full[C::kVBufs], v_empty[C::kVBufs];
     uint64_t q_full[2], q_ready[2], q_empty[2];
     uint64_t s_full[C::kSBufs], s_empty[C::kSBufs], p_full[2], pv_done[2];
@@ -137,8 +158,7 @@ struct Smem {
     uint32_t tmem_base;
     uint32_t qmax[4];
     int32_t last;
-    Walk walk[8];  // a softmax warp's place in the list, and its unit (registers are for scores and sums)
-    Piece piece[8];
+    Cursor cursor[2][16];  // the warps' places in the list: [.][0..15] where they work, [1][.] where they copy
 };
 
 // ---------------------------------------------------------------- small pieces
@@ -314,35 +334,28 @@ __device__ __forceinline__ uint2 scales_at(const uint8_t *scales, int t) {
     else return make_uint2(*reinterpret_cast<const uint32_t *>(at), 0u);
 }
 
-// (Rolled loops: the roles' loops share an instruction cache.)
-template <int D, int NP>
-__device__ __forceinline__ void decode_k(Smem<D, NP> &sm, int stage, uint32_t lane_base, int buf, int t) {
-    const uint2 sc = scales_at<D>(sm.ks[stage], t);
+// Row t of the staged block to its place as an MMA operand: K's into the TMEM
+// lane, V's into shared memory.  (One rolled loop for both: the roles' loops
+// share an instruction cache.)
+template <int D>
+__device__ __forceinline__ void decode_row(const uint8_t *codes, uint2 scales, bool is_v, uint32_t k_at, uint8_t *v_row,
+                                           int t) {
 #pragma unroll 1
     for (int c = 0; c < D / 32; c += 2) {
         uint32_t r[32];
-        const uint32_t s = c ? sc.y : sc.x;
-        decode32(codes_at<D>(sm.kc[stage], t, c), s, r);
-        decode32(codes_at<D>(sm.kc[stage], t, c + 1), s >> 16, r + 16);
-        tmem_st32(lane_base + kTmemK + 64 * buf + 16 * c, r);
-    }
-}
-
-template <int D, int NP>
-__device__ __forceinline__ void decode_v(Smem<D, NP> &sm, int stage, int buf, int t, bool held) {
-    uint2 sc = scales_at<D>(sm.vs[stage], t);
-    if (!held) sc = make_uint2(0u, 0u);  // a slot behind the sequence's last: what it holds is anything
-#pragma unroll 1
-    for (int c = 0; c < D / 32; c += 2) {
-        uint32_t r[32];
-        const uint32_t s = c ? sc.y : sc.x;
-        decode32(codes_at<D>(sm.vc[stage], t, c), s, r);
-        decode32(codes_at<D>(sm.vc[stage], t, c + 1), s >> 16, r + 16);
-        uint8_t *row = sm.v[buf] + (c >> 1) * kSlab + t * 128;
+        const uint32_t s = c ? scales.y : scales.x;
+        decode32(codes_at<D>(codes, t, c), s, r);
+        decode32(codes_at<D>(codes, t, c + 1), s >> 16, r + 16);
+        if (is_v) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            *reinterpret_cast<uint4 *>(row + ((k ^ (t & 7)) << 4)) =
-                make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+            for (int k = 0; k < 8; ++k)
+                *reinterpret_cast<uint4 *>(v_row + ((k ^ (t & 7)) << 4)) =
+                    make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+            v_row += kSlab;
+        } else {
+            tmem_st32(k_at, r);
+            k_at += 32;
+        }
     }
 }
 
@@ -388,9 +401,121 @@ __device__ __forceinline__ void prepare_queries(Smem<D, NP> &sm, const Fp4AttnAr
     named_barrier_sync(kBarPrep, 128);  // (qmax is free again)
 }
 
+// A decoding warp: the pages of its own 32 tokens of every block, copied 16
+// bytes a lane (cp.async) kStages - 1 blocks ahead, K's (kv 0), V's (1) or both.
+template <int D, int NP>
+__device__ __forceinline__ void decode_role(Smem<D, NP> &sm, const Fp4AttnArgs &a, const Walk &w, uint32_t tmem,
+                                            int kv0, int kv1) {
+    using C = Cfg<D, NP>;
+    constexpr int kStages = C::kStages, kCodePage = kBlockSize * D / 2;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp & 3, t = 32 * part + lane;
+    const uint32_t k_at = tmem + ((uint32_t)(32 * part) << 16) + kTmemK;
+    Cursor &cur = sm.cursor[0][warp], &ahead = sm.cursor[1][warp];
+    cur.begin(w);
+    ahead.begin(w);
+    // where a lane's 16 bytes of a page's codes go (in the swizzle that makes the
+    // rows' reads free of conflicts), and of two pages' scales
+    constexpr int kRowChunks = D / 32, kScaleLanes = D / 16;
+    const int row = lane / kRowChunks, sw = D == 128 ? (row >> 1) & 3 : (row >> 2) & 1;
+    const uint32_t code_dst = (uint32_t)(2 * part * kCodePage + row * (D / 2) + (((lane % kRowChunks) ^ sw) << 4));
+    const uint32_t scale_dst = (uint32_t)(2 * part * 128 + (lane / kScaleLanes) * 128 + (lane % kScaleLanes) * 16);
+    int ids = -1, ci = 0, cn = 0, cst = 0;  // copies: pages, block in the piece, its blocks, stage
+    bool more = true;
+    auto copy_block = [&]() {
+        if (more && ci == cn) {
+            more = ahead.next(a);
+            ci = 0, cn = more ? ahead.p.n : 0;
+        }
+        if (more) {
+            const Piece &p = ahead.p;
+            if ((ci & 15) == 0) {  // the pages of 16 blocks, two a block
+                const int at = (ci + lane / 2) * kPB + 2 * part + (lane & 1);
+                const int pages = (p.L + a.n_q + kBlockSize - 1) / kBlockSize - p.f * kPB;
+                ids = -1;
+                if (at < pages && at < cn * kPB) {
+                    ids = __ldg(a.block_table + (size_t)p.b * a.max_blocks + (size_t)p.f * kPB + at);
+                    if (ids < 0 || ids >= a.num_blocks) {
+                        if (kv0 == 0) raise_error(a.err, SVPA_DEVERR_BAD_BLOCK);
+                        ids = -1;
+                    }
+                }
+            }
+            // (a page that is not there stays as it was: its tokens are masked, its V rows zeroed)
+            const int id0 = __shfl_sync(0xffffffffu, ids, 2 * (ci & 15)), id1 = __shfl_sync(0xffffffffu, ids, 2 * (ci & 15) + 1);
+            const size_t tile0 = ((size_t)id0 * a.Hkv + p.h) * fp4_tile_bytes(D);
+            const size_t tile1 = ((size_t)id1 * a.Hkv + p.h) * fp4_tile_bytes(D);
+            const bool second = lane >= kScaleLanes;
+#pragma unroll 1
+            for (int kv = kv0; kv < kv1; ++kv) {
+                const uint8_t *pool = (kv ? a.v_pool : a.k_pool) + lane * 16;
+                const uint32_t dst = smem_u32(kv ? sm.vc[cst] : sm.kc[cst]) + code_dst;
+                if (id0 >= 0) {
+                    cp_async_16(dst, pool + tile0);
+                    if (D == 128) cp_async_16(dst + 512, pool + tile0 + 512);
+                }
+                if (id1 >= 0) {
+                    cp_async_16(dst + kCodePage, pool + tile1);
+                    if (D == 128) cp_async_16(dst + kCodePage + 512, pool + tile1 + 512);
+                }
+                if (lane < 2 * kScaleLanes && (second ? id1 : id0) >= 0)
+                    cp_async_16(smem_u32(kv ? sm.vs[cst] : sm.ks[cst]) + scale_dst,
+                                pool + (second ? tile1 - kScaleLanes * 16 : tile0) + fp4_code_bytes(D));
+            }
+            ++ci;
+            cst = cst + 1 == kStages ? 0 : cst + 1;
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll 1
+    for (int i = 0; i < kStages - 1; ++i) copy_block();
+    bool ok = true;
+    int j = 0, unit = 0, st = 0, vb = 0, vphase = 0;
+#pragma unroll 1
+    for (; cur.next(a); ++unit) {
+        const int n = cur.p.n;
+        int left = cur.p.L + a.n_q - cur.p.f * kNB - t;  // > 0: this thread's token is one of the sequence's
+        if (kv0 == 0) {
+            const float kf = fp4_factor(a.k_factor, cur.p.h, a.err);
+            wait(ok, &sm.q_full[unit & 1], unit >> 1, a.err);
+            prepare_queries<D, NP>(sm, a, unit & 1, unit, kf, threadIdx.x);
+            fence_proxy_async_smem();
+            warp_arrive(&sm.q_ready[unit & 1]);
+        }
+#pragma unroll 1
+        for (int i = 0; i < n; ++i, ++j, left -= kNB) {
+            copy_block();
+            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+            __syncwarp();
+#pragma unroll 1
+            for (int kv = kv0; kv < kv1; ++kv) {
+                uint2 sc = scales_at<D>(kv ? sm.vs[st] : sm.ks[st], t);
+                if (kv) {
+                    if (left <= 0) sc = make_uint2(0u, 0u);  // (what such a slot holds is anything)
+                    if (j >= C::kVBufs) wait(ok, &sm.v_empty[vb], vphase ^ 1, a.err);
+                } else if (j >= 2) {
+                    wait(ok, &sm.k_empty[j & 1], (j - 2) >> 1, a.err);
+                    tc_fence_after();
+                }
+                decode_row<D>(kv ? sm.vc[st] : sm.kc[st], sc, kv, k_at + 64 * (j & 1), sm.v[vb] + t * 128, t);
+                if (kv) {
+                    fence_proxy_async_smem();
+                    warp_arrive(&sm.v_full[vb]);
+                    if (++vb == C::kVBufs) vb = 0, vphase ^= 1;
+                } else {
+                    tmem_st_wait();
+                    tc_fence_before();
+                    warp_arrive(&sm.k_full[j & 1]);
+                }
+            }
+            st = st + 1 == kStages ? 0 : st + 1;
+        }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
 // ---------------------------------------------------------------- the softmax
 template <int D, int NP>
-__device__ __forceinline__ void softmax_role(Smem<D, NP> &sm, const Fp4AttnArgs &a, Walk w, uint32_t tmem) {
+__device__ __forceinline__ void softmax_role(Smem<D, NP> &sm, const Fp4AttnArgs &a, const Walk &w, uint32_t tmem) {
     using C = Cfg<D, NP>;
     constexpr bool kAlt = C::kAlt;
     constexpr int NH = C::kNH, CH = C::kCH, NCH = NH / CH, kStep = kAlt ? 2 : 1;
@@ -399,24 +524,14 @@ __device__ __forceinline__ void softmax_role(Smem<D, NP> &sm, const Fp4AttnArgs 
     const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
     const uint32_t o_at = lanes + kTmemO + (kAlt ? g * NP : c0);  // this group's columns of O
     const int live = min(max(a.M - c0, 0), NH);  // columns with a query row
-    Walk &walk = sm.walk[warp - 4];
-    const Piece &p = sm.piece[warp - 4];
-    auto next_unit = [&]() -> bool {
-        int more = 0;
-        __syncwarp();
-        if (lane == 0) {
-            Walk u = walk;
-            more = u.next(a, sm.piece[warp - 4]);
-            walk = u;
-        }
-        return __shfl_sync(0xffffffffu, more, 0) != 0;
-    };
-    if (lane == 0) walk = w;
+    Cursor &cur = sm.cursor[0][warp];
+    const Piece &p = cur.p;
+    cur.begin(w);
     bool ok = true;
     int j0 = 0, unit = 0;  // the unit's first block
     uint64_t sum[NH / 2];
 #pragma unroll 1
-    for (; next_unit(); ++unit) {
+    for (; cur.next(a); ++unit) {
 #pragma unroll
         for (int i = 0; i < NH / 2; ++i) sum[i] = 0ull;
         float *m_unit = sm.m[unit & 1][g];
@@ -709,18 +824,12 @@ __global__ void __launch_bounds__(Cfg<D, NP>::kThreads, 1)
     fp4_attn_kernel(const __grid_constant__ CUtensorMap mq0, const __grid_constant__ CUtensorMap mq1,
                     const __grid_constant__ Fp4AttnArgs a) {
     using C = Cfg<D, NP>;
-    constexpr int kStages = C::kStages;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     Smem<D, NP> &sm =
         *reinterpret_cast<Smem<D, NP> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
 
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i)
-            for (int kv = 0; kv < 2; ++kv) {
-                mbar_init(&sm.raw_full[kv][i], 32);
-                mbar_init(&sm.raw_empty[kv][i], 4);
-            }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.k_full[i], 4);
             mbar_init(&sm.k_empty[i], 1);
@@ -742,7 +851,7 @@ __global__ void __launch_bounds__(Cfg<D, NP>::kThreads, 1)
         mbar_init(&sm.o_empty, 8);
         fence_mbar_init();
     }
-    if (warp == C::kCopyWarp && lane == 0) {
+    if (warp == C::kQueryWarp && lane == 0) {
         prefetch_tensormap(&mq0);
         prefetch_tensormap(&mq1);
     }
@@ -808,137 +917,35 @@ __global__ void __launch_bounds__(Cfg<D, NP>::kThreads, 1)
 
     if (warp < 4) {
         regs_dec<C::kRegsDecode>();
-        // ============================================ queries, K (and V) decoded
-        const uint32_t lanes = tmem + ((uint32_t)(32 * warp) << 16);
-        int j = 0, unit = 0;
-#pragma unroll 1
-        for (; w.next(a, p); ++unit) {
-            const float kf = fp4_factor(a.k_factor, p.h, a.err);
-            wait(ok, &sm.q_full[unit & 1], unit >> 1, a.err);
-            prepare_queries<D, NP>(sm, a, unit & 1, unit, kf, tid);
-            fence_proxy_async_smem();
-            warp_arrive(&sm.q_ready[unit & 1]);
-#pragma unroll 1
-            for (int i = 0; i < p.n; ++i, ++j) {
-                const int st = j % kStages;
-                wait(ok, &sm.raw_full[0][st], j / kStages, a.err);
-                if (j >= 2) wait(ok, &sm.k_empty[j & 1], (j - 2) >> 1, a.err);
-                tc_fence_after();
-                decode_k<D, NP>(sm, st, lanes, j & 1, tid);
-                warp_arrive(&sm.raw_empty[0][st]);
-                tmem_st_wait();
-                tc_fence_before();
-                warp_arrive(&sm.k_full[j & 1]);
-                if (!C::kAlt) {
-                    wait(ok, &sm.raw_full[1][st], j / kStages, a.err);
-                    const int vb = j % C::kVBufs;
-                    if (j >= C::kVBufs) wait(ok, &sm.v_empty[vb], j / C::kVBufs - 1, a.err);
-                    decode_v<D, NP>(sm, st, vb, tid, (p.f + i) * kNB + tid < p.L + a.n_q);
-                    warp_arrive(&sm.raw_empty[1][st]);
-                    fence_proxy_async_smem();
-                    warp_arrive(&sm.v_full[vb]);
-                }
-            }
-        }
+        decode_role<D, NP>(sm, a, w, tmem, 0, C::kAlt ? 1 : 2);
     } else if (warp < 12) {
         regs_inc<C::kRegsSoftmax>();
         softmax_role<D, NP>(sm, a, w, tmem);
     } else if (C::kAlt && warp < 16) {
         regs_dec<C::kRegsDecode>();
-        // ============================================ V decoded
-        const int t = 32 * (warp - 12) + lane;
-        int j = 0;
-#pragma unroll 1
-        while (w.next(a, p)) {
-#pragma unroll 1
-            for (int i = 0; i < p.n; ++i, ++j) {
-                const int st = j % kStages;
-                wait(ok, &sm.raw_full[1][st], j / kStages, a.err);
-                const int vb = j % C::kVBufs;
-                if (j >= C::kVBufs) wait(ok, &sm.v_empty[vb], j / C::kVBufs - 1, a.err);
-                decode_v<D, NP>(sm, st, vb, t, (p.f + i) * kNB + t < p.L + a.n_q);
-                warp_arrive(&sm.raw_empty[1][st]);
-                fence_proxy_async_smem();
-                warp_arrive(&sm.v_full[vb]);
-            }
-        }
+        decode_role<D, NP>(sm, a, w, tmem, 1, 2);
     } else {
     regs_dec<C::kRegsIssue>();
-    if (warp < C::kPvWarp) {
-        // ============================================ copies: K's, V's
-        const int kv = warp - C::kCopyWarp;
-        const uint8_t *pool = kv ? a.v_pool : a.k_pool;
-        // a lane's 16 bytes of 32 lanes' codes, where they go, and of the scales
-        constexpr int kRowChunks = D / 32, kSweeps = D / 64, kScaleLanes = D / 16;
-        const int row = lane / kRowChunks, sw = D == 128 ? (row >> 1) & 3 : (row >> 2) & 1;
-        const uint32_t code_dst = (uint32_t)(row * (D / 2) + (((lane % kRowChunks) ^ sw) << 4));
-        const uint32_t codes0 = smem_u32(kv ? sm.vc[0] : sm.kc[0]) + code_dst;
-        const uint32_t scales0 = smem_u32(kv ? sm.vs[0] : sm.ks[0]) + (lane / kScaleLanes) * 128 +
-                                 (lane % kScaleLanes) * 16;
-        int j = 0, unit = 0;
+    if (warp == C::kQueryWarp) {
+        // ============================================ the queries' copies
+        const uint64_t pol = policy_evict_first();
+        int unit = 0;
 #pragma unroll 1
         for (; ok && w.next(a, p); ++unit) {
-            if (kv == 0) {
-                if (unit >= 2) wait(ok, &sm.q_empty[unit & 1], (unit - 2) >> 1, a.err);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                if (lane == 0) {
-                    uint64_t *bar = &sm.q_full[unit & 1];
-                    const uint64_t pol = policy_evict_first();
-                    mbar_arrive_expect_tx(bar, (uint32_t)(a.M * D * 2));
-                    tma_load_4d(sm.q[unit & 1], &mq0, 0, p.h * a.G, 0, p.b, bar, pol);
-                    if (D == 128) tma_load_4d(sm.q[unit & 1] + NP * 128, &mq1, 0, p.h * a.G, 0, p.b, bar, pol);
-                }
-                __syncwarp();
+            if (unit >= 2) wait(ok, &sm.q_empty[unit & 1], (unit - 2) >> 1, a.err);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if (lane == 0) {
+                uint64_t *bar = &sm.q_full[unit & 1];
+                mbar_arrive_expect_tx(bar, (uint32_t)(a.M * D * 2));
+                tma_load_4d(sm.q[unit & 1], &mq0, 0, p.h * a.G, 0, p.b, bar, pol);
+                if (D == 128) tma_load_4d(sm.q[unit & 1] + NP * 128, &mq1, 0, p.h * a.G, 0, p.b, bar, pol);
             }
-            const int pages = (p.L + a.n_q + kBlockSize - 1) / kBlockSize - p.f * kPB;  // from the first block on
-            const int32_t *table = a.block_table + (size_t)p.b * a.max_blocks + (size_t)p.f * kPB;
-            int ids = 0;
-#pragma unroll 1
-            for (int i = 0; i < p.n; ++i, ++j) {
-                if ((i & 3) == 0) {  // 32 pages at a time
-                    const int at = i * kPB + lane;
-                    ids = -1;
-                    if (at < pages && at < p.n * kPB) {
-                        ids = __ldg(table + at);
-                        if (ids < 0 || ids >= a.num_blocks) {
-                            if (kv == 0) raise_error(a.err, SVPA_DEVERR_BAD_BLOCK);
-                            ids = -1;
-                        }
-                    }
-                }
-                const int st = j % kStages;
-                if (j >= kStages) wait(ok, &sm.raw_empty[kv][st], j / kStages - 1, a.err);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                // (a page that is not there stays as it was: its tokens are masked, its V rows zeroed)
-#pragma unroll 2
-                for (int pg = 0; pg < kPB; ++pg) {
-                    const int id = __shfl_sync(0xffffffffu, ids, (i & 3) * kPB + pg);
-                    if (id >= 0) {
-                        const uint8_t *src = pool + ((size_t)id * a.Hkv + p.h) * fp4_tile_bytes(D) + lane * 16;
-                        const uint32_t dst = codes0 + st * C::kCodes + pg * (kBlockSize * D / 2);
-#pragma unroll
-                        for (int x = 0; x < kSweeps; ++x) cp_async_16(dst + 512 * x, src + 512 * x);
-                    }
-                }
-#pragma unroll
-                for (int pg = 0; pg < kPB; pg += 32 / kScaleLanes) {
-                    const int id = __shfl_sync(0xffffffffu, ids, (i & 3) * kPB + pg + lane / kScaleLanes);
-                    if (id >= 0)
-                        cp_async_16(scales0 + st * C::kScales + pg * 128,
-                                    pool + ((size_t)id * a.Hkv + p.h) * fp4_tile_bytes(D) + fp4_code_bytes(D) +
-                                        (lane % kScaleLanes) * 16);
-                }
-                cp_async_mbar_arrive_noinc(&sm.raw_full[kv][st]);
-            }
+            __syncwarp();
         }
         // (copies in flight land before the CTA's memory is given up)
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        if (!ok && kv == 0) {
-            bool still = true;
-            for (int i = max(0, unit - 1); i <= unit; ++i) wait(still, &sm.q_full[i & 1], i >> 1, a.err);
-        }
+        bool still = true;
+        for (int i = max(0, unit - 2); i < unit; ++i) wait(still, &sm.q_full[i & 1], i >> 1, a.err);
     } else if (warp == C::kScoreWarp) {
         // ============================================ S^T = K Q^T
         const uint32_t id = idesc(NP, 0, 0);
@@ -973,7 +980,7 @@ __global__ void __launch_bounds__(Cfg<D, NP>::kThreads, 1)
             wait(ok, &sm.k_empty[(j - 1) & 1], (j - 1) >> 1, a.err);
             wait(ok, &sm.q_empty[(unit - 1) & 1], (unit - 1) >> 1, a.err);
         }
-    } else {
+    } else if (warp == C::kPvWarp) {
         // ============================================ O^T += V^T P^T
         const uint32_t id = idesc(NP, 1, 1);
         constexpr uint32_t row = NP < 64 ? 2 * NP : 128;  // bytes of a token's weights
