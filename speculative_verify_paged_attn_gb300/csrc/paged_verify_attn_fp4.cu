@@ -175,13 +175,30 @@ template <int N>
 __device__ __forceinline__ void regs_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
-// A wait that a role whose earlier wait ran out passes over.
+// A bounded wait in which the thread stays suspended between probes (the waiting
+// warps leave issue slots and shared memory to the others); a role whose earlier
+// wait ran out passes over it.
+__device__ __forceinline__ bool try_wait_suspended(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 100000;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 __device__ __forceinline__ void wait(bool &ok, uint64_t *bar, int phase, int32_t *err) {
-    if (!ok) return;
+    if (!ok || try_wait_suspended(bar, (uint32_t)(phase & 1))) return;
+    const unsigned long long t0 = global_ns();
 #pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-        if (mbar_try_wait(bar, (uint32_t)(phase & 1))) return;
-    ok = mbar_wait(bar, (uint32_t)(phase & 1), err);
+    while (!try_wait_suspended(bar, (uint32_t)(phase & 1))) {
+        if (global_ns() - t0 > kWaitLimitNs) {
+            raise_error(err, SVPA_DEVERR_TIMEOUT);
+            ok = false;
+            return;
+        }
+    }
 }
 __device__ __forceinline__ void warp_arrive(uint64_t *bar) {
     __syncwarp();
@@ -300,6 +317,15 @@ __device__ __forceinline__ uint64_t p_desc(uint32_t at) {
     return (umma_desc_sw128(at, kSlab, 8 * row) & ~(7ull << 61)) | layout << 61;
 }
 
+// A descriptor `bytes` further on (within the 14 bits of its address field).
+__device__ __forceinline__ uint64_t desc_at(uint64_t d, uint32_t bytes) {
+    uint64_t r;
+    asm("{\n\t.reg .b32 lo, hi;\n\tmov.b64 {lo, hi}, %1;\n\tadd.u32 lo, lo, %2;\n\tmov.b64 %0, {lo, hi};\n\t}"
+        : "=l"(r)
+        : "l"(d), "r"(bytes >> 4));
+    return r;
+}
+
 // f16 A and B, fp32 D, 128 rows; A and B as they lie (1: MN-major).
 __host__ __device__ constexpr uint32_t idesc(int N, int a_mn, int b_mn) {
     return (1u << 4) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
@@ -320,41 +346,34 @@ __device__ __forceinline__ void decode32(const uint4 &w, uint32_t two_scales, ui
     }
 }
 
-// Chunk c (32 codes) of token t of a landed block, and all of its scales.
-template <int D>
-__device__ __forceinline__ uint4 codes_at(const uint8_t *codes, int t, int c) {
-    // (rows of 64 or 32 bytes, with the swizzle as wide)
-    const int sw = D == 128 ? (t >> 1) & 3 : (t >> 2) & 1;
-    return *reinterpret_cast<const uint4 *>(codes + t * (D / 2) + ((c ^ sw) << 4));
+__device__ __forceinline__ uint4 ld_shared(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+    return v;
 }
-template <int D>
-__device__ __forceinline__ uint2 scales_at(const uint8_t *scales, int t) {
-    const uint8_t *at = scales + (t >> 4) * 128 + (t & 15) * (D / 16);
-    if constexpr (D == 128) return *reinterpret_cast<const uint2 *>(at);
-    else return make_uint2(*reinterpret_cast<const uint32_t *>(at), 0u);
+__device__ __forceinline__ void st_shared(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
-// Row t of the staged block to its place as an MMA operand: K's into the TMEM
-// lane, V's into shared memory.  (One rolled loop for both: the roles' loops
+// A staged row of codes (32 of them at codes ^ 16 c) to its place as an MMA
+// operand: K's into the TMEM lane at `to`, V's into shared memory (its 16-byte
+// piece k of a slab at to ^ 16 k).  (One rolled loop for both: the roles' loops
 // share an instruction cache.)
 template <int D>
-__device__ __forceinline__ void decode_row(const uint8_t *codes, uint2 scales, bool is_v, uint32_t k_at, uint8_t *v_row,
-                                           int t) {
+__device__ __forceinline__ void decode_row(uint32_t codes, uint2 scales, bool is_v, uint32_t to) {
 #pragma unroll 1
     for (int c = 0; c < D / 32; c += 2) {
         uint32_t r[32];
         const uint32_t s = c ? scales.y : scales.x;
-        decode32(codes_at<D>(codes, t, c), s, r);
-        decode32(codes_at<D>(codes, t, c + 1), s >> 16, r + 16);
+        decode32(ld_shared(codes ^ (16 * c)), s, r);
+        decode32(ld_shared(codes ^ (16 * c + 16)), s >> 16, r + 16);
         if (is_v) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                *reinterpret_cast<uint4 *>(v_row + ((k ^ (t & 7)) << 4)) =
-                    make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
-            v_row += kSlab;
+            for (int k = 0; k < 8; ++k) st_shared(to ^ (16 * k), r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+            to += kSlab;
         } else {
-            tmem_st32(k_at, r);
-            k_at += 32;
+            tmem_st32(to, r);
+            to += 32;
         }
     }
 }
@@ -419,6 +438,12 @@ __device__ __forceinline__ void decode_role(Smem<D, NP> &sm, const Fp4AttnArgs &
     const int row = lane / kRowChunks, sw = D == 128 ? (row >> 1) & 3 : (row >> 2) & 1;
     const uint32_t code_dst = (uint32_t)(2 * part * kCodePage + row * (D / 2) + (((lane % kRowChunks) ^ sw) << 4));
     const uint32_t scale_dst = (uint32_t)(2 * part * 128 + (lane / kScaleLanes) * 128 + (lane % kScaleLanes) * 16);
+    // this thread's row of a stage (the swizzle is in the address already), its scales and its V row
+    const uint32_t raw0 = smem_u32(kv0 ? sm.vc[0] : sm.kc[0]), raws0 = smem_u32(kv0 ? sm.vs[0] : sm.ks[0]);
+    const uint32_t my_codes = (uint32_t)(t * (D / 2)) + ((D == 128 ? (t >> 1) & 3 : (t >> 2) & 1) << 4);
+    const uint32_t my_scales = (uint32_t)((t >> 4) * 128 + (t & 15) * (D / 16));
+    const uint32_t v_row = smem_u32(sm.v[0]) + t * 128 + ((t & 7) << 4);
+    constexpr uint32_t kToV = sizeof(sm.kc), kToVs = sizeof(sm.ks);  // from K's stages to V's
     int ids = -1, ci = 0, cn = 0, cst = 0;  // copies: pages, block in the piece, its blocks, stage
     bool more = true;
     auto copy_block = [&]() {
@@ -442,13 +467,15 @@ __device__ __forceinline__ void decode_role(Smem<D, NP> &sm, const Fp4AttnArgs &
             }
             // (a page that is not there stays as it was: its tokens are masked, its V rows zeroed)
             const int id0 = __shfl_sync(0xffffffffu, ids, 2 * (ci & 15)), id1 = __shfl_sync(0xffffffffu, ids, 2 * (ci & 15) + 1);
-            const size_t tile0 = ((size_t)id0 * a.Hkv + p.h) * fp4_tile_bytes(D);
-            const size_t tile1 = ((size_t)id1 * a.Hkv + p.h) * fp4_tile_bytes(D);
+            // (num_blocks * Hkv is below 2^31)
+            const size_t tile0 = (size_t)(uint32_t)(id0 * a.Hkv + p.h) * fp4_tile_bytes(D);
+            const size_t tile1 = (size_t)(uint32_t)(id1 * a.Hkv + p.h) * fp4_tile_bytes(D);
             const bool second = lane >= kScaleLanes;
 #pragma unroll 1
             for (int kv = kv0; kv < kv1; ++kv) {
                 const uint8_t *pool = (kv ? a.v_pool : a.k_pool) + lane * 16;
-                const uint32_t dst = smem_u32(kv ? sm.vc[cst] : sm.kc[cst]) + code_dst;
+                const bool next = kv != kv0;
+                const uint32_t dst = raw0 + (next ? kToV : 0u) + cst * C::kCodes + code_dst;
                 if (id0 >= 0) {
                     cp_async_16(dst, pool + tile0);
                     if (D == 128) cp_async_16(dst + 512, pool + tile0 + 512);
@@ -458,7 +485,7 @@ __device__ __forceinline__ void decode_role(Smem<D, NP> &sm, const Fp4AttnArgs &
                     if (D == 128) cp_async_16(dst + kCodePage + 512, pool + tile1 + 512);
                 }
                 if (lane < 2 * kScaleLanes && (second ? id1 : id0) >= 0)
-                    cp_async_16(smem_u32(kv ? sm.vs[cst] : sm.ks[cst]) + scale_dst,
+                    cp_async_16(raws0 + (next ? kToVs : 0u) + cst * C::kScales + scale_dst,
                                 pool + (second ? tile1 - kScaleLanes * 16 : tile0) + fp4_code_bytes(D));
             }
             ++ci;
@@ -488,7 +515,11 @@ __device__ __forceinline__ void decode_role(Smem<D, NP> &sm, const Fp4AttnArgs &
             __syncwarp();
 #pragma unroll 1
             for (int kv = kv0; kv < kv1; ++kv) {
-                uint2 sc = scales_at<D>(kv ? sm.vs[st] : sm.ks[st], t);
+                const bool next = kv != kv0;
+                const uint32_t sc_at = raws0 + (next ? kToVs : 0u) + st * C::kScales + my_scales;
+                uint2 sc = make_uint2(0u, 0u);
+                if (D == 128) asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(sc.x), "=r"(sc.y) : "r"(sc_at));
+                else asm volatile("ld.shared.b32 %0, [%1];" : "=r"(sc.x) : "r"(sc_at));
                 if (kv) {
                     if (left <= 0) sc = make_uint2(0u, 0u);  // (what such a slot holds is anything)
                     if (j >= C::kVBufs) wait(ok, &sm.v_empty[vb], vphase ^ 1, a.err);
@@ -496,7 +527,8 @@ __device__ __forceinline__ void decode_role(Smem<D, NP> &sm, const Fp4AttnArgs &
                     wait(ok, &sm.k_empty[j & 1], (j - 2) >> 1, a.err);
                     tc_fence_after();
                 }
-                decode_row<D>(kv ? sm.vc[st] : sm.kc[st], sc, kv, k_at + 64 * (j & 1), sm.v[vb] + t * 128, t);
+                decode_row<D>(raw0 + (next ? kToV : 0u) + st * C::kCodes + my_codes, sc, kv,
+                              kv ? v_row + vb * (2 * kSlab) : k_at + 64 * (j & 1));
                 if (kv) {
                     fence_proxy_async_smem();
                     warp_arrive(&sm.v_full[vb]);
@@ -961,12 +993,12 @@ __global__ void __launch_bounds__(Cfg<D, NP>::kThreads, 1)
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t qa = smem_u32(sm.q[unit & 1]);
+                const uint64_t qd = umma_desc_sw128(smem_u32(sm.q[unit & 1]), 16, 1024);
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
                         umma_bf16_tmem_a(tmem + kTmemS + (uint32_t)(sb * NP), tmem + kTmemK + 64 * (j & 1) + 8 * k,
-                                         umma_desc_sw128(qa + (k >> 2) * NP * 128 + (k & 3) * 32, 16, 1024), id,
+                                         desc_at(qd, (k >> 2) * NP * 128 + (k & 3) * 32), id,
                                          k == 0 ? 0u : 1u);
                     umma_commit(&sm.k_empty[j & 1]);
                     umma_commit(&sm.s_full[sb]);
@@ -996,13 +1028,14 @@ __global__ void __launch_bounds__(Cfg<D, NP>::kThreads, 1)
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t va = smem_u32(sm.v[vb]), pa = smem_u32(sm.p[j % C::kPBufs]);
+                const uint64_t vd = umma_desc_sw128(smem_u32(sm.v[vb]), kSlab, 1024);
+                const uint64_t pd = p_desc<NP>(smem_u32(sm.p[j % C::kPBufs]));
                 const uint32_t o = tmem + kTmemO + (C::kAlt ? (j & 1) * NP : 0);
                 const bool first = i < (C::kAlt ? 2 : 1);
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < kNB / 16; ++k)
-                        umma_bf16(o, umma_desc_sw128(va + k * 2048, kSlab, 1024), p_desc<NP>(pa + k * 16 * row), id,
+                        umma_bf16(o, desc_at(vd, k * 2048), desc_at(pd, k * 16 * row), id,
                                   first && k == 0 ? 0u : 1u);
                     umma_commit(&sm.pv_done[j & 1]);
                     umma_commit(&sm.v_empty[vb]);
