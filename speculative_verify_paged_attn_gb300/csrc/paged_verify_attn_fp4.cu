@@ -117,7 +117,8 @@ struct Cfg {
     static constexpr int kThreads = 32 * (kQueryWarp + 4);
     // registers a thread, from the 96 (128 with 16 warps) at launch: their sum
     // over the warps of a scheduler stays within 5 * 96 (4 * 128)
-    static constexpr int kRegsDecode = kAlt ? 80 : 112, kRegsIssue = 64, kRegsSoftmax = kAlt ? 128 : 160;
+    static constexpr int kRegsDecode = kAlt ? 64 : 112, kRegsIssue = NP == 64 ? 48 : 64;
+    static constexpr int kRegsSoftmax = NP == 64 ? 152 : kAlt ? 128 : 160;
     static_assert((kAlt ? 2 : 1) * kRegsDecode + kRegsIssue + 2 * kRegsSoftmax <= (kAlt ? 5 * 96 : 4 * 128),
                   "registers handed over");
     static constexpr int kNH = kAlt ? NP : 64;        // columns of a softmax thread
@@ -245,6 +246,18 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
+// Both halves times a factor, 0 where that is 0 (in place: registers).
+__device__ __forceinline__ void scale_sums(uint64_t &v, float x, float y) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .f32 a, b;\n\tmov.b64 {a, b}, %0;\n\t"
+        "setp.gt.f32 p, %1, 0f00000000;\n\tsetp.gt.f32 q, %2, 0f00000000;\n\t"
+        "mul.rn.f32 a, a, %1;\n\tmul.rn.f32 b, b, %2;\n\t"
+        "selp.f32 a, a, 0f00000000, p;\n\tselp.f32 b, b, 0f00000000, q;\n\t"
+        "mov.b64 %0, {a, b};\n\t}"
+        : "+l"(v)
+        : "f"(x), "f"(y)
+        : "memory");
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -362,19 +375,20 @@ __device__ __forceinline__ void st_shared(uint32_t at, uint32_t x, uint32_t y, u
 template <int D>
 __device__ __forceinline__ void decode_row(uint32_t codes, uint2 scales, bool is_v, uint32_t to) {
 #pragma unroll 1
-    for (int c = 0; c < D / 32; c += 2) {
-        uint32_t r[32];
-        const uint32_t s = c ? scales.y : scales.x;
-        decode32(ld_shared(codes ^ (16 * c)), s, r);
-        decode32(ld_shared(codes ^ (16 * c + 16)), s >> 16, r + 16);
+    for (int c = 0; c < D / 32; ++c) {
+        uint32_t r[16];
+        decode32(ld_shared(codes ^ (16 * c)), scales.x, r);
         if (is_v) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) st_shared(to ^ (16 * k), r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
-            to += kSlab;
+            for (int k = 0; k < 4; ++k)
+                st_shared((to ^ (16 * k)) ^ ((c & 1) << 6), r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+            if (c & 1) to += kSlab;
         } else {
-            tmem_st32(to, r);
-            to += 32;
+            tmem_st(to, r);
+            to += 16;
         }
+        scales.x = __funnelshift_r(scales.x, scales.y, 16);  // the next two
+        scales.y >>= 16;
     }
 }
 
@@ -636,24 +650,21 @@ __device__ __forceinline__ void softmax_role(Smem<D, NP> &sm, const Fp4AttnArgs 
                         const float4 *fc = reinterpret_cast<const float4 *>(sm.fac[g]);
 #pragma unroll
                         for (int x = 0; x < NH / 2; ++x) {
-                            const float2 f = reinterpret_cast<const float2 *>(fc)[x], v = unpack2(sum[x]);
-                            sum[x] = pack2(f.x > 0.f ? v.x * f.x : 0.f, f.y > 0.f ? v.y * f.y : 0.f);
+                            const float2 f = reinterpret_cast<const float2 *>(fc)[x];
+                            scale_sums(sum[x], f.x, f.y);
                         }
                         wait(ok, &sm.pv_done[(j - kStep) & 1], (j - kStep) >> 1, a.err);
                         tc_fence_after();
 #pragma unroll 1
-                        for (int ch = 0; ch < NCH; ++ch) {
-                            tmem_ld(o_at + (uint32_t)(ch * CH), s);
+                        for (int c8 = 0; c8 < NH; c8 += 8) {
+                            uint32_t o[8];
+                            tmem_ld(o_at + (uint32_t)c8, o);
                             tmem_ld_wait();
+                            const float4 f = fc[c8 / 4], f2 = fc[c8 / 4 + 1];
+                            const float fs[8] = {f.x, f.y, f.z, f.w, f2.x, f2.y, f2.z, f2.w};
 #pragma unroll
-                            for (int x = 0; x < CH; x += 4) {
-                                const float4 f = fc[(ch * CH + x) / 4];
-                                s[x] = __float_as_uint(__uint_as_float(s[x]) * f.x);
-                                s[x + 1] = __float_as_uint(__uint_as_float(s[x + 1]) * f.y);
-                                s[x + 2] = __float_as_uint(__uint_as_float(s[x + 2]) * f.z);
-                                s[x + 3] = __float_as_uint(__uint_as_float(s[x + 3]) * f.w);
-                            }
-                            tmem_st(o_at + (uint32_t)(ch * CH), s);
+                            for (int x = 0; x < 8; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * fs[x]);
+                            tmem_st(o_at + (uint32_t)c8, o);
                         }
                         tmem_st_wait();
                         tc_fence_before();
@@ -721,15 +732,15 @@ __device__ __forceinline__ void softmax_role(Smem<D, NP> &sm, const Fp4AttnArgs 
         const bool has0 = !kAlt || p.n > 1 || (j0 & 1) == 0, has1 = kAlt && (p.n > 1 || (j0 & 1) == 1);
         j0 += p.n;
 #pragma unroll
-        for (int ch = 0; ch < NCH; ++ch) {
-            float v[CH];
+        for (int c = 0; c < NH; c += 8) {  // (eight at a time: registers)
+            float v[8];
 #pragma unroll
-            for (int c = 0; c < CH; c += 2) {
-                const float2 f = unpack2(sum[(ch * CH + c) / 2]);
-                v[c] = f.x, v[c + 1] = f.y;
+            for (int k = 0; k < 8; k += 2) {
+                const float2 f = unpack2(sum[(c + k) / 2]);
+                v[k] = f.x, v[k + 1] = f.y;
             }
-            column_sums<CH>(v, lane);
-            if (lane < CH) sm.sums[unit & 1][g][quad][ch * CH + lane] = v[0];
+            column_sums<8>(v, lane);
+            if (lane < 8) sm.sums[unit & 1][g][quad][c + lane] = v[0];
         }
         if (kAlt) named_barrier_sync(kBarSoft, 256);
         else named_barrier_sync(kBarHalf0 + g, 128);
