@@ -96,115 +96,196 @@ __device__ __forceinline__ void store_row(const uint4 &x, bool live, int h, int 
     }
 }
 
+// One word (eight elements) of a query: x' = r (x wc + o ws), with o the other
+// halves of its pairs and the weights and the sines' signs in wc and ws.
+template <int D>
+__device__ __forceinline__ uint4 turn_query(const uint4 &x, const float (&wc)[8], const float (&ws)[8], bool norm,
+                                            float eps, int mate, bool turns, bool interleaved) {
+    float f[8], o[8];
+    unpack8(x, f);
+    float r = 1.f;
+    if (norm) {  // the sum in any order: queries are rounded to bf16 alone
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum = fmaf(f[j], f[j], sum);
+#pragma unroll
+        for (int k = 1; k < D / 8; k <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+        r = rsqrtf(sum * (1.f / D) + eps);
+    }
+    if (interleaved) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = f[j ^ 1];
+    } else {
+        uint4 y;
+        y.x = __shfl_sync(0xffffffffu, x.x, mate), y.y = __shfl_sync(0xffffffffu, x.y, mate);
+        y.z = __shfl_sync(0xffffffffu, x.z, mate), y.w = __shfl_sync(0xffffffffu, x.w, mate);
+        unpack8(y, o);
+    }
+    if (turns) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = r * fmaf(o[j], ws[j], f[j] * wc[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = r * (f[j] * wc[j]);
+    }
+    return pack8(f);
+}
+
+// ... of a key, each operation rounded by itself: x r w, then the turn.
+template <int D>
+__device__ __forceinline__ uint4 turn_key(const uint4 &x, const float (&wt)[8], const float (&cs)[8],
+                                          const float (&sn)[8], bool norm, float eps, int mate, bool turns, bool low,
+                                          bool interleaved, int lane) {
+    float f[8], o[8];
+    unpack8(x, f);
+    if (norm) {
+        const float r = rsqrtf(ordered_squares<D>(f, lane) * (1.f / D) + eps);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = f[j] * r * wt[j];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = interleaved ? f[j ^ 1] : __shfl_sync(0xffffffffu, f[j], mate);
+    if (turns) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            // the first of a pair less, the second more
+            f[j] = (interleaved ? (j & 1) == 0 : low) ? f[j] * cs[j] - o[j] * sn[j] : f[j] * cs[j] + o[j] * sn[j];
+        }
+    }
+    return pack8(f);
+}
+
+// A token's queries, keys and values are parts of kChunk heads; `split` warps
+// (a power of two up to 8) share a token's parts.
 template <Pages P, int D>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant__ RopeArgs a) {
     constexpr int kLanes = D / 8;              // of a head
     constexpr int kHeads = 32 / kLanes;        // a warp holds at a time
     constexpr int kChunk = kHeads * kWords;    // heads a warp takes
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long token = (long long)blockIdx.x * ((kThreads / 32) >> a.split_log) + (warp >> a.split_log);
+    if (token >= a.T) return;
+    const int t = (int)token, c = lane % kLanes;
+    int slot = 0, pos = 0;
+    if constexpr (P != Pages::kRows) slot = __ldg(a.slot_map + t);
+    if (a.R > 0) pos = __ldg(a.positions + t);
     const int qc = (a.Hq + kChunk - 1) / kChunk, kc = (a.Hkv + kChunk - 1) / kChunk;
-    const int items = qc + (P == Pages::kRows ? 1 : 2) * kc;
-    const long long item = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    if (item >= (long long)a.T * items) return;
-    const int t = (int)(item / items);
-    int part = (int)(item - (long long)t * items);
-    // queries, keys or values
-    const int kind = part < qc ? 0 : part < qc + kc ? 1 : 2;
-    part -= kind == 0 ? 0 : kind == 1 ? qc : qc + kc;
-    const int heads = kind == 0 ? a.Hq : a.Hkv, h0 = part * kChunk + lane / kLanes, c = lane % kLanes;
-    const uint16_t *src = kind == 0 ? a.q + t * a.q_stride : kind == 1 ? a.k + t * a.k_stride : a.v + t * a.v_stride;
-    uint4 x[kWords];
+    const int parts = qc + (P == Pages::kRows ? 1 : 2) * kc;
+    int part = warp & ((1 << a.split_log) - 1);
+    auto fetch = [&](int at, uint4 (&x)[kWords]) {
+        const int kind = at < qc ? 0 : at < qc + kc ? 1 : 2;
+        const int heads = kind == 0 ? a.Hq : a.Hkv, h0 = (at - (kind == 0 ? 0 : kind == 1 ? qc : qc + kc)) * kChunk + lane / kLanes;
+        const uint16_t *src = (kind == 0 ? a.q + t * a.q_stride : kind == 1 ? a.k + t * a.k_stride : a.v + t * a.v_stride) +
+                              h0 * D + c * 8;
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) {
-        const int h = h0 + i * kHeads;
-        x[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (h < heads) x[i] = __ldcs(reinterpret_cast<const uint4 *>(src + (long long)h * D) + c);
-    }
-    int slot = 0;
+        for (int i = 0; i < kWords; ++i) {
+            x[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (h0 + i * kHeads < heads) x[i] = __ldcs(reinterpret_cast<const uint4 *>(src + i * kHeads * D));
+        }
+    };
+    uint4 x[kWords];
+    if (part < parts) fetch(part, x);
     if constexpr (P != Pages::kRows) {
-        slot = __ldg(a.slot_map + t);
         if (slot < 0) return;  // a padding row
         if (slot / kBlockSize >= a.num_blocks) {
-            if (kind == 1 && part == 0 && lane == 0) raise_error(a.err, SVPA_DEVERR_BAD_BLOCK);
+            if (part == 0 && lane == 0) raise_error(a.err, SVPA_DEVERR_BAD_BLOCK);
             return;
         }
     }
-    const bool turns = kind < 2 && 8 * c < a.R;
-    float cs[8], sn[8];  // of this lane's elements (interleaved: of its four pairs)
-    if (kind < 2 && a.R > 0) {
-        const int pos = __ldg(a.positions + t);
-        if (pos < 0 || pos >= a.max_position) {
-            if (part == 0 && lane == 0) raise_error(a.err, SVPA_DEVERR_BAD_VALUE);
-            return;
-        }
-        if (turns) {
-            const float4 *row = reinterpret_cast<const float4 *>(a.cos_sin + (long long)pos * a.R);
-            const int half = a.R / 8;  // float4 of the cosines
-            const int at = a.interleaved ? c : 2 * (c < a.R / 16 ? c : c - a.R / 16);
-            const float4 u = __ldg(row + at), w = __ldg(row + half + at);
-            cs[0] = u.x, cs[1] = u.y, cs[2] = u.z, cs[3] = u.w;
-            sn[0] = w.x, sn[1] = w.y, sn[2] = w.z, sn[3] = w.w;
-            if (!a.interleaved) {
-                const float4 u2 = __ldg(row + at + 1), w2 = __ldg(row + half + at + 1);
-                cs[4] = u2.x, cs[5] = u2.y, cs[6] = u2.z, cs[7] = u2.w;
-                sn[4] = w2.x, sn[5] = w2.y, sn[6] = w2.z, sn[7] = w2.w;
-            }
-        }
+    if (a.R > 0 && (pos < 0 || pos >= a.max_position)) {
+        if (part == 0 && lane == 0) raise_error(a.err, SVPA_DEVERR_BAD_VALUE);
+        return;
     }
-    const uint16_t *weight = kind == 0 ? a.q_weight : kind == 1 ? a.k_weight : nullptr;
-    float wt[8];
-    if (weight) unpack8(__ldg(reinterpret_cast<const uint4 *>(weight) + c), wt);
-    // the lane that holds the other half of this one's pairs
-    const int low = c < a.R / 16;
-    const int mate = turns && !a.interleaved ? lane + (low ? a.R / 16 : -(a.R / 16)) : lane;
+    // the angles of this lane's elements, and the lane that holds the other half of
+    // its pairs
+    const bool turns = 8 * c < a.R, low = c < a.R / 16, interleaved = a.interleaved;
+    const int mate = turns && !interleaved ? lane + (low ? a.R / 16 : -(a.R / 16)) : lane;
+    // (loaded for the queries and again for the keys: registers)
+    auto angles = [&](float (&cs)[8], float (&sn)[8]) {
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) {
-        const int h = h0 + i * kHeads;
-        const bool live = h < heads;
-        if (part * kChunk + i * kHeads >= heads) break;  // the same for the whole warp
-        if (kind < 2) {
-            float f[8];
-            unpack8(x[i], f);
-            if (weight) {
-                float sum = 0.f;
-                if (kind == 1) {
-                    sum = ordered_squares<D>(f, lane);
-                } else {  // any order: queries are rounded to bf16 alone
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) sum = fmaf(f[j], f[j], sum);
-#pragma unroll
-                    for (int o = 1; o < kLanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                }
-                const float r = rsqrtf(sum * (1.f / D) + a.eps);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) f[j] = f[j] * r * wt[j];
-            }
-            if (a.interleaved) {
-                if (turns) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float u = f[2 * j], w = f[2 * j + 1];
-                        f[2 * j] = u * cs[j] - w * sn[j];
-                        f[2 * j + 1] = w * cs[j] + u * sn[j];
-                    }
-                }
-            } else if (a.R > 0) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float o = __shfl_sync(0xffffffffu, f[j], mate);
-                    if (turns) f[j] = low ? f[j] * cs[j] - o * sn[j] : f[j] * cs[j] + o * sn[j];
-                }
-            }
-            x[i] = pack8(f);
-        }
-        if (kind == 0) {
-            if (live) reinterpret_cast<uint4 *>(a.q_out + t * a.q_out_stride + (long long)h * D)[c] = x[i];
-        } else if constexpr (P == Pages::kRows) {
-            if (live) reinterpret_cast<uint4 *>(a.k_out + t * a.k_out_stride + (long long)h * D)[c] = x[i];
+        for (int j = 0; j < 8; ++j) cs[j] = 1.f, sn[j] = 0.f;
+        if (!turns) return;
+        const float4 *row = reinterpret_cast<const float4 *>(a.cos_sin + (long long)pos * a.R);
+        const int half = a.R / 8;  // float4 of the cosines
+        const int at = interleaved ? c : 2 * (low ? c : c - a.R / 16);
+        const float4 u = __ldg(row + at), w = __ldg(row + half + at);
+        if (interleaved) {
+            cs[0] = cs[1] = u.x, cs[2] = cs[3] = u.y, cs[4] = cs[5] = u.z, cs[6] = cs[7] = u.w;
+            sn[0] = sn[1] = w.x, sn[2] = sn[3] = w.y, sn[4] = sn[5] = w.z, sn[6] = sn[7] = w.w;
         } else {
-            store_row<P, D>(x[i], live, h, c, a.Hkv, (long long)(slot / kBlockSize) * a.Hkv, slot % kBlockSize,
-                            kind == 1 ? a.k_pool : a.v_pool, kind == 1 ? a.k_scale : a.v_scale,
-                            kind == 1 ? a.k_factor : a.v_factor, a.err);
+            const float4 u2 = __ldg(row + at + 1), w2 = __ldg(row + half + at + 1);
+            cs[0] = u.x, cs[1] = u.y, cs[2] = u.z, cs[3] = u.w, cs[4] = u2.x, cs[5] = u2.y, cs[6] = u2.z, cs[7] = u2.w;
+            sn[0] = w.x, sn[1] = w.y, sn[2] = w.z, sn[3] = w.w, sn[4] = w2.x, sn[5] = w2.y, sn[6] = w2.z, sn[7] = w2.w;
+        }
+    };
+    if (part < qc) {
+        // queries: the weights go into the angles
+        float wc[8], ws[8];
+        angles(wc, ws);
+        const uint4 *wq = reinterpret_cast<const uint4 *>(a.q_weight);
+        float wt[8], wo[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) wt[j] = wo[j] = 1.f;
+        if (wq) {
+            unpack8(__ldg(wq + c), wt);
+            unpack8(__ldg(wq + mate % kLanes), wo);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            wc[j] *= wt[j];
+            const float s = (interleaved ? wt[j ^ 1] : wo[j]) * ws[j];
+            ws[j] = (interleaved ? (j & 1) == 0 : low) ? -s : s;
+        }
+#pragma unroll 1
+        for (; part < qc; part += 1 << a.split_log) {
+            const int h0 = part * kChunk + lane / kLanes;
+            uint16_t *dst = a.q_out + t * a.q_out_stride + h0 * D + c * 8;
+            uint4 ahead[kWords];
+            if (part + (1 << a.split_log) < parts) fetch(part + (1 << a.split_log), ahead);
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) {
+                if (part * kChunk + i * kHeads >= a.Hq) break;  // the same for the whole warp
+                const uint4 y = turn_query<D>(x[i], wc, ws, wq != nullptr, a.eps, mate, turns, interleaved);
+                if (h0 + i * kHeads < a.Hq) *reinterpret_cast<uint4 *>(dst + i * kHeads * D) = y;
+            }
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) x[i] = ahead[i];
+        }
+    }
+    const long long tile = (long long)(slot / kBlockSize) * a.Hkv;
+    if (part < qc + kc) {
+        float wt[8], cs[8], sn[8];
+        angles(cs, sn);
+        if (a.k_weight) unpack8(__ldg(reinterpret_cast<const uint4 *>(a.k_weight) + c), wt);
+#pragma unroll 1
+        for (; part < qc + kc; part += 1 << a.split_log) {
+            const int h0 = (part - qc) * kChunk + lane / kLanes;
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) {
+                if ((part - qc) * kChunk + i * kHeads >= a.Hkv) break;
+                const int h = h0 + i * kHeads;
+                const uint4 y = turn_key<D>(x[i], wt, cs, sn, a.k_weight != nullptr, a.eps, mate, turns, low, interleaved, lane);
+                if constexpr (P == Pages::kRows) {
+                    if (h < a.Hkv) reinterpret_cast<uint4 *>(a.k_out + t * a.k_out_stride + (long long)h * D)[c] = y;
+                } else {
+                    store_row<P, D>(y, h < a.Hkv, h, c, a.Hkv, tile, slot % kBlockSize, a.k_pool, a.k_scale, a.k_factor,
+                                    a.err);
+                }
+            }
+            if (part + (1 << a.split_log) < parts) fetch(part + (1 << a.split_log), x);
+        }
+    }
+    if constexpr (P != Pages::kRows) {
+#pragma unroll 1
+        for (; part < parts; part += 1 << a.split_log) {
+            const int h0 = (part - qc - kc) * kChunk + lane / kLanes;
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) {
+                if ((part - qc - kc) * kChunk + i * kHeads >= a.Hkv) break;
+                const int h = h0 + i * kHeads;
+                store_row<P, D>(x[i], h < a.Hkv, h, c, a.Hkv, tile, slot % kBlockSize, a.v_pool, a.v_scale, a.v_factor, a.err);
+            }
+            if (part + (1 << a.split_log) < parts) fetch(part + (1 << a.split_log), x);
         }
     }
 }
@@ -212,77 +293,133 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
 // Row t of the pages, slot_map[t], as bf16: each value rounded once.
 template <Pages P>
 __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ ReadArgs a) {
-    const int lane = threadIdx.x & 31;
-    const int wph = a.D / 8, wpr = a.Hkv * wph;  // 16-byte words of a head and of a row
-    const int chunks = (wpr + 32 * kWords - 1) / (32 * kWords);
-    const long long item = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    if (item >= 2LL * a.T * chunks) return;
-    const int t = (int)(item / (2 * chunks)), rest = (int)(item - (long long)t * 2 * chunks);
-    const int kv = rest / chunks, c0 = (rest - kv * chunks) * 32 * kWords;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long token = (long long)blockIdx.x * ((kThreads / 32) >> a.split_log) + (warp >> a.split_log);
+    if (token >= a.T) return;
+    const int t = (int)token;
     const int slot = __ldg(a.slot_map + t);
     if (slot < 0) return;  // a padding row
     const int blk = slot / kBlockSize, at = slot % kBlockSize;
+    int part = warp & ((1 << a.split_log) - 1);
     if (blk >= a.num_blocks) {
-        if (rest == 0 && lane == 0) raise_error(a.err, SVPA_DEVERR_BAD_BLOCK);
+        if (part == 0 && lane == 0) raise_error(a.err, SVPA_DEVERR_BAD_BLOCK);
         return;
     }
-    const uint8_t *pool = kv ? a.v_pool : a.k_pool;
-    uint4 *dst = reinterpret_cast<uint4 *>(kv ? a.v + t * a.v_stride : a.k + t * a.k_stride);
-    uint4 raw[kWords];
-    float scale[kWords];
+    const long long tile0 = (long long)blk * a.Hkv;
+    if constexpr (P == Pages::kFp4) {
+        // a lane takes groups of 16 elements, K's and V's: eight bytes of codes, a
+        // scale, 32 bytes out
+        const int gph = a.D / 16, gpr = a.Hkv * gph;
+#pragma unroll 1
+        for (; part * 32 * kWords < 2 * gpr; part += 1 << a.split_log) {
+            const int c0 = part * 32 * kWords + lane;
+            uint2 codes[kWords];
+            uint32_t sc[kWords];
+            float f[kWords];
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) {
-        const int w = c0 + lane + 32 * i, h = w / wph, c = w - h * wph;
-        if (w >= wpr) break;
-        const long long tile = (long long)blk * a.Hkv + h, row = tile * kBlockSize + at;
-        if constexpr (P == Pages::kBf16) {
-            raw[i] = __ldg(reinterpret_cast<const uint4 *>(pool) + row * wph + c);
-        } else if constexpr (P == Pages::kFp8) {
-            const uint2 u = __ldg(reinterpret_cast<const uint2 *>(pool) + row * wph + c);
-            raw[i].x = u.x, raw[i].y = u.y;
-            scale[i] = __ldg((kv ? a.v_scale : a.k_scale) + row * (wph / 8) + c / 8);
-        } else {
-            const uint8_t *page = pool + tile * fp4_tile_bytes(a.D);
-            raw[i].x = __ldg(reinterpret_cast<const uint32_t *>(page + at * (a.D / 2)) + c);
-            raw[i].y = __ldg(page + fp4_code_bytes(a.D) + at * (a.D / 16) + c / 2);
-            scale[i] = fp4_factor(kv ? a.v_factor : a.k_factor, h, a.err);
-        }
-    }
+            for (int i = 0; i < kWords; ++i) {
+                const int u = c0 + 32 * i, kv = u >= gpr, w = kv ? u - gpr : u;
+                if (u >= 2 * gpr) break;
+                const int h = gph == 1 ? w : (int)__umulhi((unsigned)w, a.magic), g = w - h * gph;
+                const uint8_t *page = (kv ? a.v_pool : a.k_pool) + (tile0 + h) * fp4_tile_bytes(a.D);
+                codes[i] = __ldg(reinterpret_cast<const uint2 *>(page + at * (a.D / 2)) + g);
+                sc[i] = __ldg(page + fp4_code_bytes(a.D) + at * (a.D / 16) + g);
+                f[i] = fp4_factor(kv ? a.v_factor : a.k_factor, h, a.err);
+            }
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) {
-        const int w = c0 + lane + 32 * i;
-        if (w >= wpr) break;
-        if constexpr (P != Pages::kBf16) {
-            uint32_t p[4];
-            float f[8];
-            if constexpr (P == Pages::kFp8) {
-                p[0] = e4m3x2_to_f16x2(raw[i].x & 0xffffu), p[1] = e4m3x2_to_f16x2(raw[i].x >> 16);
-                p[2] = e4m3x2_to_f16x2(raw[i].y & 0xffffu), p[3] = e4m3x2_to_f16x2(raw[i].y >> 16);
-            } else {
+            for (int i = 0; i < kWords; ++i) {
+                const int u = c0 + 32 * i, kv = u >= gpr, w = kv ? u - gpr : u;
+                if (u >= 2 * gpr) break;
+                uint32_t p[8], out[8];
+                uint32_t half[4];
+                const uint32_t s = e4m3x2_to_f16x2(sc[i] * 0x101u);
+                e2m1x8_to_f16(codes[i].x, half);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) p[j] = mul_f16x2(half[j], s);
+                e2m1x8_to_f16(codes[i].y, half);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) p[4 + j] = mul_f16x2(half[j], s);
                 // code times scale is exact in f16, then one product with the factor
-                e2m1x8_to_f16(raw[i].x, p);
-                const uint32_t s = e4m3x2_to_f16x2(raw[i].y * 0x101u);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) p[j] = mul_f16x2(p[j], s);
+                for (int j = 0; j < 8; ++j) {
+                    const float2 v = f16x2_to_float2(p[j]);
+                    out[j] = pack_bf16x2(v.x * f[i], v.y * f[i]);
+                }
+                uint8_t *to = reinterpret_cast<uint8_t *>(kv ? a.v + t * a.v_stride : a.k + t * a.k_stride) + 32LL * w;
+                if ((reinterpret_cast<uintptr_t>(to) & 31) == 0) {
+                    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(out[0]),
+                                 "r"(out[1]), "r"(out[2]), "r"(out[3]), "r"(out[4]), "r"(out[5]), "r"(out[6]), "r"(out[7])
+                                 : "memory");
+                } else {
+                    reinterpret_cast<uint4 *>(to)[0] = make_uint4(out[0], out[1], out[2], out[3]);
+                    reinterpret_cast<uint4 *>(to)[1] = make_uint4(out[4], out[5], out[6], out[7]);
+                }
             }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 v = f16x2_to_float2(p[j]);
-                f[2 * j] = v.x * scale[i], f[2 * j + 1] = v.y * scale[i];
-            }
-            raw[i] = pack8(f);
         }
-        dst[w] = raw[i];
+    } else {
+        const int wph = a.D / 8, wpr = a.Hkv * wph;  // 16-byte words of a head and of a row
+        const int chunks = (wpr + 32 * kWords - 1) / (32 * kWords);
+#pragma unroll 1
+        for (; part < 2 * chunks; part += 1 << a.split_log) {
+            const int kv = part >= chunks, c0 = (part - kv * chunks) * 32 * kWords + lane;
+            const uint8_t *pool = kv ? a.v_pool : a.k_pool;
+            uint4 *dst = reinterpret_cast<uint4 *>(kv ? a.v + t * a.v_stride : a.k + t * a.k_stride);
+            uint4 raw[kWords];
+            float scale[kWords];
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) {
+                const int w = c0 + 32 * i, h = (int)((unsigned)w / (unsigned)wph), c = w - h * wph;
+                if (w >= wpr) break;
+                const long long row = (tile0 + h) * kBlockSize + at;
+                if constexpr (P == Pages::kBf16) {
+                    raw[i] = __ldg(reinterpret_cast<const uint4 *>(pool) + row * wph + c);
+                } else {
+                    const uint2 u = __ldg(reinterpret_cast<const uint2 *>(pool) + row * wph + c);
+                    raw[i].x = u.x, raw[i].y = u.y;
+                    scale[i] = __ldg((kv ? a.v_scale : a.k_scale) + row * (wph / 8) + c / 8);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) {
+                const int w = c0 + 32 * i;
+                if (w >= wpr) break;
+                if constexpr (P == Pages::kFp8) {
+                    const uint32_t p[4] = {e4m3x2_to_f16x2(raw[i].x & 0xffffu), e4m3x2_to_f16x2(raw[i].x >> 16),
+                                           e4m3x2_to_f16x2(raw[i].y & 0xffffu), e4m3x2_to_f16x2(raw[i].y >> 16)};
+                    float f[8];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 v = f16x2_to_float2(p[j]);
+                        f[2 * j] = v.x * scale[i], f[2 * j + 1] = v.y * scale[i];
+                    }
+                    raw[i] = pack8(f);
+                }
+                dst[w] = raw[i];
+            }
+        }
     }
 }
 
+// Warps a token (log2): few enough that a warp's angles serve several parts, and
+// enough warps for the GPU.  SPLITNOTE
+int split_log(long long tokens, int parts) {
+    const long long want = 32LL * sm_count();
+    int s = 0;
+    while (s < 3 && (tokens << s) < want && (1 << s) < parts) ++s;
+    return s;
+}
+
+unsigned grid_of(long long tokens, int split) {
+    const long long per = (kThreads / 32) >> split;  // tokens of a CTA
+    return (unsigned)((tokens + per - 1) / per);
+}
+
 template <Pages P, int D>
-cudaError_t launch(const RopeArgs &a, cudaStream_t stream) {
+cudaError_t launch(RopeArgs a, cudaStream_t stream) {
     constexpr int kChunk = 32 / (D / 8) * kWords;
     const int qc = (a.Hq + kChunk - 1) / kChunk, kc = (a.Hkv + kChunk - 1) / kChunk;
-    const long long items = (long long)a.T * (qc + (P == Pages::kRows ? 1 : 2) * kc);
-    const unsigned grid = (unsigned)((items + kThreads / 32 - 1) / (kThreads / 32));
-    rope_kernel<P, D><<<grid, kThreads, 0, stream>>>(a);
+    a.split_log = split_log(a.T, qc + (P == Pages::kRows ? 1 : 2) * kc);
+    rope_kernel<P, D><<<grid_of(a.T, a.split_log), kThreads, 0, stream>>>(a);
     return cudaGetLastError();
 }
 
@@ -302,10 +439,14 @@ cudaError_t launch_rope(const RopeArgs &a, int D, Pages pages, cudaStream_t stre
     }
 }
 
-cudaError_t launch_kv_read(const ReadArgs &a, Pages pages, cudaStream_t stream) {
-    const long long wpr = (long long)a.Hkv * (a.D / 8);
-    const long long items = 2LL * a.T * ((wpr + 32 * kWords - 1) / (32 * kWords));
-    const unsigned grid = (unsigned)((items + kThreads / 32 - 1) / (kThreads / 32));
+cudaError_t launch_kv_read(const ReadArgs &args, Pages pages, cudaStream_t stream) {
+    ReadArgs a = args;
+    const int wpr = a.Hkv * (a.D / 8);
+    const int parts = pages == Pages::kFp4 ? (wpr + 32 * kWords - 1) / (32 * kWords) : 2 * ((wpr + 32 * kWords - 1) / (32 * kWords));
+    a.split_log = parts > 4 ? 3 : parts > 2 ? 2 : parts > 1 ? 1 : 0;
+    // w / (D / 16) as a product's high word: exact for w (D / 16) < 2^32
+    a.magic = a.D >= 32 ? (unsigned)(((1ull << 32) + a.D / 16 - 1) / (a.D / 16)) : 0u;
+    const unsigned grid = grid_of(a.T, a.split_log);
     if (pages == Pages::kBf16) read_kernel<Pages::kBf16><<<grid, kThreads, 0, stream>>>(a);
     else if (pages == Pages::kFp8) read_kernel<Pages::kFp8><<<grid, kThreads, 0, stream>>>(a);
     else read_kernel<Pages::kFp4><<<grid, kThreads, 0, stream>>>(a);

@@ -30,6 +30,7 @@ struct RopeArgs {
     long long q_stride, k_stride, v_stride, q_out_stride, k_out_stride;
     int32_t T, Hq, Hkv, R, interleaved, max_position, num_blocks;
     float eps;
+    int32_t split_log;  // log2 of the warps a token (set by the launch)
 };
 cudaError_t launch_rope(const RopeArgs &a, int D, Pages pages, cudaStream_t stream);
 
@@ -46,6 +47,8 @@ struct ReadArgs {
     int32_t *err;
     long long k_stride, v_stride;
     int32_t T, Hkv, D, num_blocks;
+    int32_t split_log;  // as above
+    uint32_t magic;     // ceil(2^32 / (D / 16)) (set by the launch)
 };
 cudaError_t launch_kv_read(const ReadArgs &a, Pages pages, cudaStream_t stream);
 
