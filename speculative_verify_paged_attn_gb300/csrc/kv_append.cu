@@ -401,71 +401,53 @@ __global__ void __launch_bounds__(kWriteThreads) append_write_kernel(const __gri
     }
 }
 
-// 4-bit pages: the bf16 form's rounds of 16-byte chunks (eight elements), each
-// encoded before its store; a scale's two chunks are neighbouring lanes'.
+// 4-bit pages: a warp takes 128 16-byte words (eight elements each) of one new
+// row of K or V, all kv heads, four a lane, loaded before the wait; a scale's two
+// words are neighbouring lanes'.  256 sequences of 8 rows of 32 x 128: APPENDNOTE
+constexpr int kFp4Words = 4;
+
 __global__ void __launch_bounds__(kWriteThreads) append_write_fp4_kernel(const __grid_constant__ AppendArgs a) {
-    const int b = blockIdx.x;
+    const int b = blockIdx.x, lane = threadIdx.x & 31;
     const int L = a.context_lens[b];
     const long long end = (long long)L + a.n_new;
     if (L < 0 || (end + kBlockSize - 1) / kBlockSize > a.max_blocks) return;
     const int i = L / kBlockSize + (int)blockIdx.y;
     const long long ps = (long long)i * kBlockSize;
     if (ps >= end) return;
-    const int s0 = L > ps ? (int)(L - ps) : 0;                               // the page's first new slot
-    const int s1 = end - ps < kBlockSize ? (int)(end - ps) : kBlockSize;     // behind its last
-    const int D = a.D, Hkv = a.Hkv;
-    const int u0 = (int)blockIdx.z * kUnitsBf16;
-    const int units = min(kUnitsBf16, 2 * Hkv - u0);
-    const int cpr = D / 8;  // chunks per row
-    const int per_unit = (s1 - s0) * cpr;
-    const int total = units * per_unit;
-    auto where = [&](int w, int &kv, int &h, int &s, int &c) {
-        const int uu = w / per_unit, r = w - uu * per_unit;
-        s = s0 + r / cpr;
-        c = r - (r / cpr) * cpr;
-        kv = u0 + uu >= Hkv;
-        h = u0 + uu - kv * Hkv;
-    };
-    auto load_round = [&](int w0, uint4 (&x)[kLoads]) {
+    const int s0 = L > ps ? (int)(L - ps) : 0;                            // the page's first new slot
+    const int s1 = end - ps < kBlockSize ? (int)(end - ps) : kBlockSize;  // behind its last
+    const int D = a.D, wph = D / 8, wpr = a.Hkv * wph, chunks = (wpr + 32 * kFp4Words - 1) / (32 * kFp4Words);
+    const int item = (int)blockIdx.z * (kWriteThreads / 32) + (threadIdx.x >> 5);  // (chunk, row, K | V)
+    if (item >= 2 * (s1 - s0) * chunks) return;
+    const int kv = item & 1, at = (item >> 1) / chunks, c0 = ((item >> 1) - at * chunks) * 32 * kFp4Words + lane;
+    const int slot = s0 + at;
+    const uint4 *src = reinterpret_cast<const uint4 *>((kv ? a.new_v : a.new_k) +
+                                                       ((size_t)b * a.n_new + (size_t)(ps + slot - L)) * a.Hkv * D);
+    uint4 x[kFp4Words];
 #pragma unroll
-        for (int k = 0; k < kLoads; ++k) {
-            const int w = w0 + k * kWriteThreads;
-            x[k] = make_uint4(0u, 0u, 0u, 0u);
-            if (w < total) {
-                int kv, h, s, c;
-                where(w, kv, h, s, c);
-                const uint16_t *row = (kv ? a.new_v : a.new_k) +
-                                      (((size_t)b * a.n_new + (size_t)(ps + s - L)) * Hkv + h) * D;
-                x[k] = reinterpret_cast<const uint4 *>(row)[c];
-            }
-        }
-    };
-    // (a warp leaves as a whole: its lanes exchange maxima)
-    if ((int)(threadIdx.x & ~31u) >= total) return;
-    uint4 x[kLoads];
-    load_round(threadIdx.x, x);  // the first round overlaps the allocation kernel
+    for (int k = 0; k < kFp4Words; ++k) {
+        const int w = c0 + 32 * k;
+        x[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (w < wpr) x[k] = src[w];
+    }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (*reinterpret_cast<volatile int32_t *>(a.err) != 0) return;
     const int blk = a.block_table[(size_t)b * a.max_blocks + i];
     if (blk < 0 || blk >= a.num_blocks) return;
-    for (int w0 = threadIdx.x; (w0 & ~31) < total; w0 += kLoads * kWriteThreads) {
-        if (w0 != (int)threadIdx.x) load_round(w0, x);
+    uint8_t *pages = (kv ? a.v_pool : a.k_pool) + (size_t)blk * a.Hkv * fp4_tile_bytes(D);
 #pragma unroll
-        for (int k = 0; k < kLoads; ++k) {
-            const int w = w0 + k * kWriteThreads;
-            uint32_t amax = bf16_amax8(x[k]);
-            amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-            if (w >= total) continue;
-            if (amax > 0x7f7fu) raise_error(a.err, SVPA_DEVERR_BAD_VALUE);
-            int kv, h, s, c;
-            where(w, kv, h, s, c);
-            uint32_t scale;
-            const uint32_t codes =
-                fp4_encode8(x[k], amax, fp4_factor(kv ? a.v_factor : a.k_factor, h, a.err), scale);
-            uint8_t *page = (kv ? a.v_pool : a.k_pool) + ((size_t)blk * Hkv + h) * fp4_tile_bytes(D);
-            reinterpret_cast<uint32_t *>(page + s * (D / 2))[c] = codes;
-            if ((c & 1) == 0) page[fp4_code_bytes(D) + s * (D / 16) + c / 2] = (uint8_t)scale;
-        }
+    for (int k = 0; k < kFp4Words; ++k) {
+        const int w = c0 + 32 * k;
+        uint32_t amax = bf16_amax8(x[k]);
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        if (w >= wpr) continue;
+        if (amax > 0x7f7fu) raise_error(a.err, SVPA_DEVERR_BAD_VALUE);
+        const int h = (int)__umulhi((unsigned)w, a.magic), c = w - h * wph;
+        uint32_t scale;
+        const uint32_t codes = fp4_encode8(x[k], amax, fp4_factor(kv ? a.v_factor : a.k_factor, h, a.err), scale);
+        uint8_t *page = pages + (size_t)h * fp4_tile_bytes(D);
+        reinterpret_cast<uint32_t *>(page + slot * (D / 2))[c] = codes;
+        if ((c & 1) == 0) page[fp4_code_bytes(D) + slot * (D / 16) + c / 2] = (uint8_t)scale;
     }
 }
 
@@ -478,6 +460,8 @@ cudaError_t launch_kv_append(const AppendArgs &a, cudaStream_t stream) {
     // (sequence, touched page, group of units); launched as a programmatic
     // dependent of the allocation kernel so that its launch overlaps it
     const int units_per_cta = a.fp8 ? kWriteThreads / 32 : kUnitsBf16;
+    const int fp4_items = 2 * (a.n_new < kBlockSize ? a.n_new : kBlockSize) *
+                          ((a.Hkv * (a.D / 8) + 32 * kFp4Words - 1) / (32 * kFp4Words));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)a.B, (unsigned)((a.n_new + kBlockSize - 1) / kBlockSize + 1),
                        (unsigned)((2 * a.Hkv + units_per_cta - 1) / units_per_cta));
@@ -488,7 +472,10 @@ cudaError_t launch_kv_append(const AppendArgs &a, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (a.fp4) return cudaLaunchKernelEx(&cfg, append_write_fp4_kernel, a);
+    if (a.fp4) {
+        cfg.gridDim.z = (unsigned)((fp4_items + kWriteThreads / 32 - 1) / (kWriteThreads / 32));
+        return cudaLaunchKernelEx(&cfg, append_write_fp4_kernel, a);
+    }
     if (a.fp8) return cudaLaunchKernelEx(&cfg, append_write_kernel<true>, a);
     return cudaLaunchKernelEx(&cfg, append_write_kernel<false>, a);
 }

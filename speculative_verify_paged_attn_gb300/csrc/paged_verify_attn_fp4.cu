@@ -64,6 +64,13 @@ __device__ __forceinline__ int blocks_of(const Fp4AttnArgs &a, int L) {
     return L < 0 || pages > a.max_blocks ? 0 : (int)((pages + kPB - 1) / kPB);
 }
 
+// CTAs that get a share of W blocks: a part costs its writing and joining, as much
+// as some blocks, so that a share has kMinShare of them at least.
+constexpr int kMinShare = 1;
+__device__ __forceinline__ int shares_of(long long W) {
+    return (int)min((long long)gridDim.x, (W + kMinShare - 1) / kMinShare);
+}
+
 struct Walk {
     int b, h, f, nb, L;
     long long x, left;
@@ -721,7 +728,7 @@ __device__ __forceinline__ void softmax_role(Smem<D, NP> &sm, const Fp4AttnArgs 
         }
         // ------------------------------------------------ the unit's epilogue
         const long long W = sm.work, px = p.x - p.f;
-        const int nsh = (int)min((long long)gridDim.x, W);
+        const int nsh = shares_of(W);
         const long long first_x = (long long)blockIdx.x * W / nsh;
         auto cta_of = [&](long long x) { return (int)(((x + 1) * nsh - 1) / W); };
         const int c_first = cta_of(px), parts = cta_of(px + p.nb - 1) - c_first + 1;
@@ -931,7 +938,7 @@ __global__ void __launch_bounds__(Cfg<D, NP>::kThreads, 1)
         if (i == warp) before = W;
         W += sm.scan[i];
     }
-    const int nsh = (int)min((long long)gridDim.x, W);
+    const int nsh = shares_of(W);
     const long long xs = (int)blockIdx.x < nsh ? (long long)blockIdx.x * W / nsh : W;
     const long long xe = (int)blockIdx.x < nsh ? (long long)(blockIdx.x + 1) * W / nsh : W;
     before += incl - mine;

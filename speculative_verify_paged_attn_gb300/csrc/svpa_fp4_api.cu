@@ -255,6 +255,8 @@ svpa_status svpa_kv_append_fp4(int32_t batch, int32_t n_new, int32_t num_kv_head
     a.max_blocks = max_blocks_per_seq;
     a.num_blocks = num_blocks;
     a.fp4 = 1;
+    // w / (D / 8) as a product's high word: exact for w (D / 8) < 2^32
+    a.magic = (uint32_t)(((1ull << 32) + head_dim / 8 - 1) / (head_dim / 8));
     return from_cuda(launch_kv_append(a, static_cast<cudaStream_t>(stream)));
 }
 

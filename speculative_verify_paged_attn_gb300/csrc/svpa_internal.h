@@ -246,6 +246,7 @@ struct AppendArgs {
     const float *k_factor;     // 4-bit pages: [Hkv] or null
     const float *v_factor;
     int32_t B, n_new, Hkv, D, max_blocks, num_blocks, fp8, scale_tile, fp4;
+    uint32_t magic;            // 4-bit pages: ceil(2^32 / (D / 8))
 };
 cudaError_t launch_kv_append(const AppendArgs &a, cudaStream_t stream);
 
