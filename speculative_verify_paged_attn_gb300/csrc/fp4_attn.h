@@ -5,6 +5,11 @@
 
 namespace svpa {
 
+// A pair whose parts are to be joined: the first part's slot and their number (0: none).
+struct Fp4Join {
+    int32_t b, h, slot, parts;
+};
+
 struct Fp4AttnArgs {
     const uint8_t *k_pool;
     const uint8_t *v_pool;
@@ -15,7 +20,7 @@ struct Fp4AttnArgs {
     __nv_bfloat16 *out;
     float *lse;
     int32_t *err;
-    int32_t *tickets;  // [B * Hkv]: parts written of a pair cut between CTAs
+    Fp4Join *joins;    // [grid]: the pair that begins in a CTA's share and goes on behind it
     float *part_ml;    // [2 * grid, M, 2] (reference maximum in log2 units, sum), two parts a CTA
     float *part_acc;   // [2 * grid, M, D]
     int32_t B, n_q, Hq, Hkv, G, M, max_blocks, num_blocks;

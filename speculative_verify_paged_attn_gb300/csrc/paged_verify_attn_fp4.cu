@@ -21,8 +21,8 @@
 // block).
 //
 // Work: the 128-token blocks of all (sequence, kv head) pairs, in that order,
-// split evenly over one persistent CTA per SM; the parts of a pair that is cut
-// are merged by the CTA that writes the last of them.
+// split evenly over one persistent CTA per SM; the parts of the pairs that are
+// cut are joined by a second kernel.
 // Warps: 0-3 decode K and turn the queries to f16; 4-7 and 8-11 are the softmax
 // and the epilogue; 12-15 decode V; then a warp that copies the queries and one
 // each that issues the MMAs of either product (with 128 columns warps 0-3 decode
@@ -92,24 +92,36 @@ struct Walk {
     }
 };
 
-// A warp's place in the list and its unit, kept in shared memory: the registers
-// are for scores, sums and codes.
+// A warp's place in the list, its unit and the one after (worked out while the
+// warp waits for its unit's first data anyway), kept in shared memory: the
+// registers are for scores, sums and codes.
 struct Cursor {
     Walk w;
-    Piece p;
-    __device__ __forceinline__ void begin(const Walk &at) {
-        if ((threadIdx.x & 31) == 0) w = at;
-    }
-    __device__ __forceinline__ bool next(const Fp4AttnArgs &a) {
-        int more = 0;
-        __syncwarp();
+    Piece p[2];
+    int more, at;
+    __device__ __forceinline__ void look(const Fp4AttnArgs &a, int to) {
         if ((threadIdx.x & 31) == 0) {
             Walk u = w;
-            more = u.next(a, p);
+            more = u.next(a, p[to]);
             w = u;
         }
-        return __shfl_sync(0xffffffffu, more, 0) != 0;
+        __syncwarp();
     }
+    __device__ __forceinline__ void begin(const Fp4AttnArgs &a, const Walk &from) {
+        if ((threadIdx.x & 31) == 0) w = from, at = 1;
+        look(a, 0);
+    }
+    // Whether there is a next unit; it is unit() then.
+    __device__ __forceinline__ bool next(const Fp4AttnArgs &a) {
+        __syncwarp();
+        const int have = more, to = at;
+        __syncwarp();
+        if (!have) return false;
+        if ((threadIdx.x & 31) == 0) at = to ^ 1;
+        look(a, to);
+        return true;
+    }
+    __device__ __forceinline__ const Piece &unit() const { return p[at]; }
 };
 
 template <int D, int NP>
@@ -135,7 +147,8 @@ struct Cfg {
     static constexpr int kQ = NP * D * 2, kP = kNB * NP * 2;
     static constexpr int kCodes = kNB * D / 2, kScales = kPB * 128;
     static constexpr int kStage = 2 * (kCodes + kScales);
-    static constexpr int kRoom = (232448 - 12288 - 2 * kQ - kPBufs * kP - kVBufs * 2 * kSlab) / kStage;
+    static constexpr int kRest = 13312;  // what is behind the tiles, and their alignment
+    static constexpr int kRoom = (232448 - kRest - 2 * kQ - kPBufs * kP - kVBufs * 2 * kSlab) / kStage;
     static constexpr int kStages = kRoom < 8 ? kRoom : 8;
 };
 
@@ -164,9 +177,8 @@ struct Smem {
     long long work;                    // all blocks
     int32_t b0, h0, f0;                // this CTA's first
     uint32_t tmem_base;
-    uint32_t qmax[4];
-    int32_t last;
-    Cursor cursor[2][16];  // the warps' places in the list: [.][0..15] where they work, [1][.] where they copy
+    uint32_t qmax[2][2];
+    Cursor cursor[16], ahead[8];  // the warps' places in the list: where they work, and where they copy
 };
 
 // ---------------------------------------------------------------- small pieces
@@ -243,16 +255,6 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 // Both halves times a factor, 0 where that is 0 (in place: registers).
 __device__ __forceinline__ void scale_sums(uint64_t &v, float x, float y) {
     asm volatile(
@@ -303,7 +305,6 @@ __device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t (&r)[16]) {
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
-__device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t (&r)[32]) { tmem_st32(at, r); }
 
 // The sums over a warp's lanes of N columns: v[0] of lane l is column l % N's.
 template <int N>
@@ -404,18 +405,19 @@ __device__ __forceinline__ void decode_row(uint32_t codes, uint2 scales, bool is
 // value there is less than 2^-39 of it.  Sets the scores' multiplier.
 template <int D, int NP>
 __device__ __forceinline__ void prepare_queries(Smem<D, NP> &sm, const Fp4AttnArgs &a, int slot, int unit, float kf,
-                                                int tid) {
+                                                int tid) {  // by two warps
     constexpr int kRow = 8, kSlabs = D / 64;  // 16-byte chunks of a row of a slab
     uint4 *q = reinterpret_cast<uint4 *>(sm.q[slot]);
     const int per = a.M * kRow;
     uint32_t top = 0u;
 #pragma unroll 1
     for (int s = 0; s < kSlabs; ++s)
-        for (int i = tid; i < per; i += 128) top = max(top, bf16_amax8(q[s * NP * kRow + i]));
+#pragma unroll 2
+        for (int i = tid; i < per; i += 64) top = max(top, bf16_amax8(q[s * NP * kRow + i]));
     top = __reduce_max_sync(0xffffffffu, top);
-    if ((tid & 31) == 0) sm.qmax[tid >> 5] = top;
-    named_barrier_sync(kBarPrep, 128);
-    top = max(max(sm.qmax[0], sm.qmax[1]), max(sm.qmax[2], sm.qmax[3]));
+    if ((tid & 31) == 0) sm.qmax[unit & 1][tid >> 5] = top;
+    named_barrier_sync(kBarPrep, 64);
+    top = max(sm.qmax[unit & 1][0], sm.qmax[unit & 1][1]);
     int e = 0;
     if (top > 0x7f7fu) {
         if (tid == 0) raise_error(a.err, SVPA_DEVERR_BAD_VALUE);
@@ -426,7 +428,7 @@ __device__ __forceinline__ void prepare_queries(Smem<D, NP> &sm, const Fp4AttnAr
 #pragma unroll 1
     for (int s = 0; s < kSlabs; ++s)
 #pragma unroll 2
-        for (int i = tid; i < per; i += 128) {
+        for (int i = tid; i < per; i += 64) {
             const uint4 x = q[s * NP * kRow + i];
             uint4 y;
             y.x = pack_f16x2(bf16_lo(x.x) * scale, bf16_hi(x.x) * scale);
@@ -438,7 +440,6 @@ __device__ __forceinline__ void prepare_queries(Smem<D, NP> &sm, const Fp4AttnAr
     // (positive, so that a masked score stays -inf)
     if (tid == 0)
         sm.mult[unit & 7] = fmaxf(a.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23) * kf, 1e-30f);
-    named_barrier_sync(kBarPrep, 128);  // (qmax is free again)
 }
 
 // A decoding warp: the pages of its own 32 tokens of every block, copied 16
@@ -450,9 +451,9 @@ __device__ __forceinline__ void decode_role(Smem<D, NP> &sm, const Fp4AttnArgs &
     constexpr int kStages = C::kStages, kCodePage = kBlockSize * D / 2;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp & 3, t = 32 * part + lane;
     const uint32_t k_at = tmem + ((uint32_t)(32 * part) << 16) + kTmemK;
-    Cursor &cur = sm.cursor[0][warp], &ahead = sm.cursor[1][warp];
-    cur.begin(w);
-    ahead.begin(w);
+    Cursor &cur = sm.cursor[warp], &ahead = sm.ahead[part + (warp & 4)];
+    cur.begin(a, w);
+    ahead.begin(a, w);
     // where a lane's 16 bytes of a page's codes go (in the swizzle that makes the
     // rows' reads free of conflicts), and of two pages' scales
     constexpr int kRowChunks = D / 32, kScaleLanes = D / 16;
@@ -470,10 +471,10 @@ __device__ __forceinline__ void decode_role(Smem<D, NP> &sm, const Fp4AttnArgs &
     auto copy_block = [&]() {
         if (more && ci == cn) {
             more = ahead.next(a);
-            ci = 0, cn = more ? ahead.p.n : 0;
+            ci = 0, cn = more ? ahead.unit().n : 0;
         }
         if (more) {
-            const Piece &p = ahead.p;
+            const Piece &p = ahead.unit();
             if ((ci & 15) == 0) {  // the pages of 16 blocks, two a block
                 const int at = (ci + lane / 2) * kPB + 2 * part + (lane & 1);
                 const int pages = (p.L + a.n_q + kBlockSize - 1) / kBlockSize - p.f * kPB;
@@ -517,18 +518,12 @@ __device__ __forceinline__ void decode_role(Smem<D, NP> &sm, const Fp4AttnArgs &
 #pragma unroll 1
     for (int i = 0; i < kStages - 1; ++i) copy_block();
     bool ok = true;
-    int j = 0, unit = 0, st = 0, vb = 0, vphase = 0;
+    int j = 0, st = 0, vb = 0, vphase = 0;
 #pragma unroll 1
-    for (; cur.next(a); ++unit) {
-        const int n = cur.p.n;
-        int left = cur.p.L + a.n_q - cur.p.f * kNB - t;  // > 0: this thread's token is one of the sequence's
-        if (kv0 == 0) {
-            const float kf = fp4_factor(a.k_factor, cur.p.h, a.err);
-            wait(ok, &sm.q_full[unit & 1], unit >> 1, a.err);
-            prepare_queries<D, NP>(sm, a, unit & 1, unit, kf, threadIdx.x);
-            fence_proxy_async_smem();
-            warp_arrive(&sm.q_ready[unit & 1]);
-        }
+    while (cur.next(a)) {
+        const Piece &p = cur.unit();
+        const int n = p.n;
+        int left = p.L + a.n_q - p.f * kNB - t;  // > 0: this thread's token is one of the sequence's
 #pragma unroll 1
         for (int i = 0; i < n; ++i, ++j, left -= kNB) {
             copy_block();
@@ -577,16 +572,17 @@ __device__ __forceinline__ void softmax_role(Smem<D, NP> &sm, const Fp4AttnArgs 
     const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
     const uint32_t o_at = lanes + kTmemO + (kAlt ? g * NP : c0);  // this group's columns of O
     const int live = min(max(a.M - c0, 0), NH);  // columns with a query row
-    Cursor &cur = sm.cursor[0][warp];
-    const Piece &p = cur.p;
-    cur.begin(w);
+    Cursor &cur = sm.cursor[warp];
+    cur.begin(a, w);
     bool ok = true;
-    int j0 = 0, unit = 0;  // the unit's first block
+    int j0 = 0, unit = 0, last = 0;  // the unit's first block; whether the last unit is cut at its end
     uint64_t sum[NH / 2];
 #pragma unroll 1
     for (; cur.next(a); ++unit) {
 #pragma unroll
         for (int i = 0; i < NH / 2; ++i) sum[i] = 0ull;
+        const Piece &p = cur.unit();
+        const float fv = fp4_factor(a.v_factor, p.h, a.err);
         float *m_unit = sm.m[unit & 1][g];
         float mult = 1.f;
 #pragma unroll 1
@@ -727,13 +723,8 @@ __device__ __forceinline__ void softmax_role(Smem<D, NP> &sm, const Fp4AttnArgs 
             warp_arrive(&sm.p_full[j & 1]);
         }
         // ------------------------------------------------ the unit's epilogue
-        const long long W = sm.work, px = p.x - p.f;
-        const int nsh = shares_of(W);
-        const long long first_x = (long long)blockIdx.x * W / nsh;
-        auto cta_of = [&](long long x) { return (int)(((x + 1) * nsh - 1) / W); };
-        const int c_first = cta_of(px), parts = cta_of(px + p.nb - 1) - c_first + 1;
-        const int slot = 2 * (int)blockIdx.x + (p.x == first_x ? 0 : 1);
-        const float fv = fp4_factor(a.v_factor, p.h, a.err);
+        const bool whole = p.n == p.nb;
+        const int slot = 2 * (int)blockIdx.x + (p.x == w.x ? 0 : 1);
         const size_t row0 = (size_t)p.b * a.n_q * a.Hq + (size_t)p.h * a.G;
         // the groups with a block of this unit (their O hold something)
         const bool has0 = !kAlt || p.n > 1 || (j0 & 1) == 0, has1 = kAlt && (p.n > 1 || (j0 & 1) == 1);
@@ -769,12 +760,12 @@ __device__ __forceinline__ void softmax_role(Smem<D, NP> &sm, const Fp4AttnArgs 
             w0[ch] = m0 == m ? 1.f : ex2_approx(m0 - m);
             w1[ch] = m1 == m ? 1.f : ex2_approx(m1 - m);
             const float l = l0 * w0[ch] + l1 * w1[ch];
-            if (parts == 1) {
+            if (whole) {
                 const float inv = l > 0.f ? fv / l : 0.f;
                 w0[ch] *= inv, w1[ch] *= inv;
             }
             if (quad == 0 && lane < CE && r < a.M) {
-                if (parts > 1) reinterpret_cast<float2 *>(a.part_ml)[(size_t)slot * a.M + r] = make_float2(m, l);
+                if (!whole) reinterpret_cast<float2 *>(a.part_ml)[(size_t)slot * a.M + r] = make_float2(m, l);
                 else if (a.lse) a.lse[row0 + sm.row_off[r]] = (m + __log2f(l)) * kLn2;
             }
         }
@@ -818,7 +809,7 @@ __device__ __forceinline__ void softmax_role(Smem<D, NP> &sm, const Fp4AttnArgs 
                 if (lane >= D / 4) break;
                 const int r = e0 + ch * CE + c;
                 const float4 v = reinterpret_cast<const float4 *>(turn + c * D)[lane];
-                if (parts == 1)
+                if (whole)
                     reinterpret_cast<uint2 *>(a.out + (row0 + sm.row_off[r]) * D)[lane] =
                         make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
                 else
@@ -829,43 +820,19 @@ __device__ __forceinline__ void softmax_role(Smem<D, NP> &sm, const Fp4AttnArgs 
             tc_fence_before();
             warp_arrive(&sm.o_empty);
         }
-        if (parts == 1) continue;
-        // every part of the pair is written: the last one's CTA joins them
-        __threadfence();
-        named_barrier_sync(kBarSoft, 256);
-        if (warp == 4 && lane == 0) {
-            const int pair = p.b * a.Hkv + p.h;
-            sm.last = atomicAdd(&a.tickets[pair], 1) == parts - 1;
-            if (sm.last) a.tickets[pair] = 0;
+        last = p.f == 0 && !whole;
+    }
+    // A pair that begins in this CTA's share and goes on behind it: its parts are
+    // joined by the next kernel.
+    if (warp == 4 && lane == 0) {
+        Fp4Join d = {0, 0, 0, 0};
+        if (last > 0) {
+            const long long W = sm.work, nsh = shares_of(W);
+            const Piece &p = cur.unit();
+            d.b = p.b, d.h = p.h, d.slot = 2 * (int)blockIdx.x + (p.x == w.x ? 0 : 1);
+            d.parts = (int)(((p.x + p.nb) * nsh - 1) / W) - (int)blockIdx.x + 1;
         }
-        named_barrier_sync(kBarSoft, 256);
-        if (!sm.last) continue;
-        __threadfence();
-        // (the first part is its CTA's last piece unless the pair begins that CTA's share)
-        const int second = (long long)c_first * W / nsh == px ? 0 : 1;
-#pragma unroll 1
-        for (int r = warp - 4; r < a.M; r += 8) {
-            float m = -CUDART_INF_F, l = 0.f;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-            for (int k = 0; k < parts; ++k) {
-                const size_t row = (size_t)(2 * (c_first + k) + (k == 0 ? second : 0)) * a.M + r;
-                const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.part_ml) + row);
-                const float4 v = lane < D / 4 ? __ldcg(reinterpret_cast<const float4 *>(a.part_acc + row * D) + lane) : o;
-                if (ml.x == -CUDART_INF_F) continue;  // a part without a visible token
-                const float mn = fmaxf(m, ml.x), fo = ex2_approx(m - mn), fn = ex2_approx(ml.x - mn);
-                l = l * fo + ml.y * fn;
-                o.x = o.x * fo + v.x * fn, o.y = o.y * fo + v.y * fn;
-                o.z = o.z * fo + v.z * fn, o.w = o.w * fo + v.w * fn;
-                m = mn;
-            }
-            const float inv = l > 0.f ? fv / l : 0.f;
-            const size_t row = row0 + sm.row_off[r];
-            if (lane < D / 4)
-                reinterpret_cast<uint2 *>(a.out + row * D)[lane] =
-                    make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-            if (lane == 0 && a.lse) a.lse[row] = (m + __log2f(l)) * kLn2;
-        }
+        a.joins[blockIdx.x] = d;
     }
 }
 
@@ -879,12 +846,13 @@ __global__ void __launch_bounds__(Cfg<D, NP>::kThreads, 1)
         *reinterpret_cast<Smem<D, NP> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
 
+    asm volatile("griddepcontrol.launch_dependents;");  // the joining kernel waits for this one's end
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.k_full[i], 4);
             mbar_init(&sm.k_empty[i], 1);
             mbar_init(&sm.q_full[i], 1);
-            mbar_init(&sm.q_ready[i], 4);
+            mbar_init(&sm.q_ready[i], 2);
             mbar_init(&sm.q_empty[i], 1);
             mbar_init(&sm.p_full[i], C::kAlt ? 4 : 8);
             mbar_init(&sm.pv_done[i], 1);
@@ -976,26 +944,32 @@ __global__ void __launch_bounds__(Cfg<D, NP>::kThreads, 1)
         decode_role<D, NP>(sm, a, w, tmem, 1, 2);
     } else {
     regs_dec<C::kRegsIssue>();
-    if (warp == C::kQueryWarp) {
-        // ============================================ the queries' copies
+    if (warp == C::kQueryWarp || warp == C::kQueryWarp + 3) {
+        // ============================================ the queries: copied, and turned to f16
+        const int tid = (warp == C::kQueryWarp ? 0 : 32) + lane;
         const uint64_t pol = policy_evict_first();
         int unit = 0;
 #pragma unroll 1
-        for (; ok && w.next(a, p); ++unit) {
-            if (unit >= 2) wait(ok, &sm.q_empty[unit & 1], (unit - 2) >> 1, a.err);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            if (lane == 0) {
-                uint64_t *bar = &sm.q_full[unit & 1];
-                mbar_arrive_expect_tx(bar, (uint32_t)(a.M * D * 2));
-                tma_load_4d(sm.q[unit & 1], &mq0, 0, p.h * a.G, 0, p.b, bar, pol);
-                if (D == 128) tma_load_4d(sm.q[unit & 1] + NP * 128, &mq1, 0, p.h * a.G, 0, p.b, bar, pol);
+        for (; w.next(a, p); ++unit) {
+            const float kf = fp4_factor(a.k_factor, p.h, a.err);
+            if (warp == C::kQueryWarp) {
+                if (unit >= 2) wait(ok, &sm.q_empty[unit & 1], (unit - 2) >> 1, a.err);
+                if (ok && lane == 0) {
+                    uint64_t *bar = &sm.q_full[unit & 1];
+                    mbar_arrive_expect_tx(bar, (uint32_t)(a.M * D * 2));
+                    tma_load_4d(sm.q[unit & 1], &mq0, 0, p.h * a.G, 0, p.b, bar, pol);
+                    if (D == 128) tma_load_4d(sm.q[unit & 1] + NP * 128, &mq1, 0, p.h * a.G, 0, p.b, bar, pol);
+                }
+                __syncwarp();
             }
-            __syncwarp();
+            // (also when an earlier wait ran out: what was copied has to land)
+            bool landed = true;
+            if (ok) wait(landed, &sm.q_full[unit & 1], unit >> 1, a.err);
+            ok = ok && landed;
+            prepare_queries<D, NP>(sm, a, unit & 1, unit, kf, tid);
+            fence_proxy_async_smem();
+            warp_arrive(&sm.q_ready[unit & 1]);
         }
-        // (copies in flight land before the CTA's memory is given up)
-        bool still = true;
-        for (int i = max(0, unit - 2); i < unit; ++i) wait(still, &sm.q_full[i & 1], i >> 1, a.err);
     } else if (warp == C::kScoreWarp) {
         // ============================================ S^T = K Q^T
         const uint32_t id = idesc(NP, 0, 0);
@@ -1075,6 +1049,53 @@ __global__ void __launch_bounds__(Cfg<D, NP>::kThreads, 1)
     if (warp == C::kPvWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
+// The parts of the pairs that were cut between CTAs, a row a warp: the parts'
+// sums and accumulators weighted by their reference maxima.  CTA x of the grid
+// has the pair that begins in share x and goes on behind it, if there is one.
+constexpr int kJoinThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) fp4_join_kernel(const __grid_constant__ Fp4AttnArgs a) {
+    const int r = (int)blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const Fp4Join d = a.joins[blockIdx.x];
+    if (d.parts == 0 || r >= a.M) return;
+    const float fv = fp4_factor(a.v_factor, d.h, a.err);
+    constexpr int kAtOnce = 4;
+    float m = -CUDART_INF_F, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int k0 = 0; k0 < d.parts; k0 += kAtOnce) {
+        float2 ml[kAtOnce];
+        float4 v[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            ml[k] = make_float2(-CUDART_INF_F, 0.f);
+            v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (k0 + k >= d.parts) continue;
+            // (the parts behind the first are the first pieces of their CTAs)
+            const size_t row = (size_t)(k0 + k == 0 ? d.slot : 2 * ((int)blockIdx.x + k0 + k)) * a.M + r;
+            ml[k] = reinterpret_cast<const float2 *>(a.part_ml)[row];
+            if (lane < D / 4) v[k] = reinterpret_cast<const float4 *>(a.part_acc + row * D)[lane];
+        }
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            if (ml[k].x == -CUDART_INF_F) continue;  // none, or one without a visible token
+            const float mn = fmaxf(m, ml[k].x), fo = ex2_approx(m - mn), fn = ex2_approx(ml[k].x - mn);
+            l = l * fo + ml[k].y * fn;
+            o.x = o.x * fo + v[k].x * fn, o.y = o.y * fo + v[k].y * fn;
+            o.z = o.z * fo + v[k].z * fn, o.w = o.w * fo + v[k].w * fn;
+            m = mn;
+        }
+    }
+    const float inv = l > 0.f ? fv / l : 0.f;
+    const size_t row = (size_t)d.b * a.n_q * a.Hq + (size_t)d.h * a.G + (size_t)(r / a.G) * a.Hq + r % a.G;
+    if (lane < D / 4)
+        reinterpret_cast<uint2 *>(a.out + row * D)[lane] =
+            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    if (lane == 0 && a.lse) a.lse[row] = (m + __log2f(l)) * kLn2;
+}
+
 template <int D, int NP>
 cudaError_t launch(const CUtensorMap *mq, const Fp4AttnArgs &a, cudaStream_t st) {
     using C = Cfg<D, NP>;
@@ -1092,7 +1113,19 @@ cudaError_t launch(const CUtensorMap *mq, const Fp4AttnArgs &a, cudaStream_t st)
     });
     if (e != cudaSuccess) return e;
     fp4_attn_kernel<D, NP><<<fp4_attn_grid(), C::kThreads, smem, st>>>(mq[0], mq[1], a);
-    return cudaGetLastError();
+    const cudaError_t launched = cudaGetLastError();
+    if (launched != cudaSuccess) return launched;
+    // a programmatic dependent launch: its CTAs are there when the parts are
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)fp4_attn_grid(), (unsigned)((a.M + kJoinThreads / 32 - 1) / (kJoinThreads / 32)));
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fp4_join_kernel<D>, a);
 }
 
 template <int D>

@@ -6,7 +6,6 @@
 #include <stdint.h>
 #include <string.h>
 
-#include <algorithm>
 #include <cmath>
 
 #include "../../include/svpa.h"
@@ -103,17 +102,18 @@ svpa_status check_attn(const svpa_attn_params *p) {
     return SVPA_OK;
 }
 
-// The attention's workspace: [counters][tickets][parts' (max, sum)][parts' accumulators].
+// The attention's workspace: [other calls' counters and tickets, not touched][pairs
+// to join][parts' (max, sum)][parts' accumulators].
 struct AttnSpace {
-    size_t tickets, off_ml, off_acc, bytes;
+    size_t off_joins, off_ml, off_acc, bytes;
 };
 svpa_status attn_space(const svpa_attn_params *p, AttnSpace *sp) {
     const svpa_status s = check_attn(p);
     if (s != SVPA_OK) return s;
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     const size_t rows = (size_t)2 * fp4_attn_grid() * (p->num_q_heads / p->num_kv_heads) * p->n_q;
-    sp->tickets = (size_t)p->batch * p->num_kv_heads * sizeof(int32_t);
-    sp->off_ml = kWorkspaceCounterBytes + up(std::max(sp->tickets, kTicketBytes));
+    sp->off_joins = kWorkspaceCounterBytes + kTicketBytes;
+    sp->off_ml = sp->off_joins + up(fp4_attn_grid() * sizeof(Fp4Join));
     sp->off_acc = sp->off_ml + up(rows * 2 * sizeof(float));
     sp->bytes = sp->off_acc + up(rows * p->head_dim * sizeof(float));
     return SVPA_OK;
@@ -314,7 +314,7 @@ svpa_status svpa_paged_verify_attn_fp4(const svpa_attn_params *p, const void *q,
     a.out = static_cast<__nv_bfloat16 *>(out);
     a.lse = lse;
     a.err = error_flag;
-    a.tickets = reinterpret_cast<int32_t *>(ws + kWorkspaceCounterBytes);
+    a.joins = reinterpret_cast<Fp4Join *>(ws + sp.off_joins);
     a.part_ml = reinterpret_cast<float *>(ws + sp.off_ml);
     a.part_acc = reinterpret_cast<float *>(ws + sp.off_acc);
     a.B = p->batch;
@@ -333,12 +333,7 @@ svpa_status svpa_paged_verify_attn_fp4(const svpa_attn_params *p, const void *q,
             for (int c = j * G; c < (j + 1) * G; ++c) a.slots[i][c >> 6] |= 1ull << (c & 63);
         }
     }
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (sp.tickets > kTicketBytes) {  // where other calls keep partial results
-        const cudaError_t e = cudaMemsetAsync(a.tickets, 0, sp.tickets, st);
-        if (e != cudaSuccess) return from_cuda(e);
-    }
-    return from_cuda(launch_paged_verify_attn_fp4(mq, a, D, st));
+    return from_cuda(launch_paged_verify_attn_fp4(mq, a, D, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"
