@@ -466,16 +466,16 @@ __device__ __forceinline__ void decode_role(Smem<D, NP> &sm, const Fp4AttnArgs &
     const uint32_t my_scales = (uint32_t)((t >> 4) * 128 + (t & 15) * (D / 16));
     const uint32_t v_row = smem_u32(sm.v[0]) + t * 128 + ((t & 7) << 4);
     constexpr uint32_t kToV = sizeof(sm.kc), kToVs = sizeof(sm.ks);  // from K's stages to V's
-    int ids = -1, ci = 0, cn = 0, cst = 0;  // copies: pages, block in the piece, its blocks, stage
+    int ids = -1, ci = 0, cn = 0, cst = 0, ch = 0;  // copies: pages, block in the piece, its blocks, stage, kv head
     bool more = true;
     auto copy_block = [&]() {
         if (more && ci == cn) {
             more = ahead.next(a);
-            ci = 0, cn = more ? ahead.unit().n : 0;
+            ci = 0, cn = more ? ahead.unit().n : 0, ch = ahead.unit().h;
         }
         if (more) {
-            const Piece &p = ahead.unit();
             if ((ci & 15) == 0) {  // the pages of 16 blocks, two a block
+                const Piece &p = ahead.unit();
                 const int at = (ci + lane / 2) * kPB + 2 * part + (lane & 1);
                 const int pages = (p.L + a.n_q + kBlockSize - 1) / kBlockSize - p.f * kPB;
                 ids = -1;
@@ -490,8 +490,8 @@ __device__ __forceinline__ void decode_role(Smem<D, NP> &sm, const Fp4AttnArgs &
             // (a page that is not there stays as it was: its tokens are masked, its V rows zeroed)
             const int id0 = __shfl_sync(0xffffffffu, ids, 2 * (ci & 15)), id1 = __shfl_sync(0xffffffffu, ids, 2 * (ci & 15) + 1);
             // (num_blocks * Hkv is below 2^31)
-            const size_t tile0 = (size_t)(uint32_t)(id0 * a.Hkv + p.h) * fp4_tile_bytes(D);
-            const size_t tile1 = (size_t)(uint32_t)(id1 * a.Hkv + p.h) * fp4_tile_bytes(D);
+            const size_t tile0 = (size_t)(uint32_t)(id0 * a.Hkv + ch) * fp4_tile_bytes(D);
+            const size_t tile1 = (size_t)(uint32_t)(id1 * a.Hkv + ch) * fp4_tile_bytes(D);
             const bool second = lane >= kScaleLanes;
 #pragma unroll 1
             for (int kv = kv0; kv < kv1; ++kv) {
@@ -583,10 +583,11 @@ __device__ __forceinline__ void softmax_role(Smem<D, NP> &sm, const Fp4AttnArgs 
         for (int i = 0; i < NH / 2; ++i) sum[i] = 0ull;
         const Piece &p = cur.unit();
         const float fv = fp4_factor(a.v_factor, p.h, a.err);
+        const int n = p.n, seen = p.L - p.f * kNB;  // blocks; history from the first block on
         float *m_unit = sm.m[unit & 1][g];
         float mult = 1.f;
 #pragma unroll 1
-        for (int i = kAlt ? (g - j0) & 1 : 0; i < p.n; i += kStep) {
+        for (int i = kAlt ? (g - j0) & 1 : 0; i < n; i += kStep) {
             const int j = j0 + i, sb = j % C::kSBufs;
             const bool first = i < kStep;
             wait(ok, &sm.s_full[sb], j / C::kSBufs, a.err);
@@ -595,8 +596,8 @@ __device__ __forceinline__ void softmax_role(Smem<D, NP> &sm, const Fp4AttnArgs 
             const uint64_t mult2 = pack2(mult, mult);
             const uint32_t sa = lanes + kTmemS + (uint32_t)(sb * NP + c0);
             // which columns see this thread's token
-            const int at = (p.f + i) * kNB + t - p.L;  // >= 0: a speculative slot
-            const bool edge = (p.f + i + 1) * kNB > p.L;
+            const int at = i * kNB + t - seen;  // >= 0: a speculative slot
+            const bool edge = (i + 1) * kNB > seen;
             unsigned long long vis = ~0ull;
             if (edge && at >= 0) vis = at >= a.n_q ? 0ull : a.slots[at][kAlt ? 0 : g];
             uint8_t *pt = sm.p[kAlt ? g : 0];
