@@ -195,24 +195,12 @@ template <int N>
 __device__ __forceinline__ void regs_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
-// A bounded wait in which the thread stays suspended between probes (the waiting
-// warps leave issue slots and shared memory to the others); a role whose earlier
-// wait ran out passes over it.
-__device__ __forceinline__ bool try_wait_suspended(uint64_t *bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 100000;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
+// A bounded wait; a role whose earlier wait ran out passes over it.
 __device__ __forceinline__ void wait(bool &ok, uint64_t *bar, int phase, int32_t *err) {
-    if (!ok || try_wait_suspended(bar, (uint32_t)(phase & 1))) return;
+    if (!ok || mbar_try_wait(bar, (uint32_t)(phase & 1))) return;
     const unsigned long long t0 = global_ns();
 #pragma unroll 1
-    while (!try_wait_suspended(bar, (uint32_t)(phase & 1))) {
+    while (!mbar_try_wait(bar, (uint32_t)(phase & 1))) {
         if (global_ns() - t0 > kWaitLimitNs) {
             raise_error(err, SVPA_DEVERR_TIMEOUT);
             ok = false;
@@ -988,7 +976,7 @@ __global__ void __launch_bounds__(Cfg<D, NP>::kThreads, 1)
                 tc_fence_after();
                 const uint64_t qd = umma_desc_sw128(smem_u32(sm.q[unit & 1]), 16, 1024);
                 if (elect_one()) {
-#pragma unroll
+#pragma unroll 1
                     for (int k = 0; k < D / 16; ++k)
                         umma_bf16_tmem_a(tmem + kTmemS + (uint32_t)(sb * NP), tmem + kTmemK + 64 * (j & 1) + 8 * k,
                                          desc_at(qd, (k >> 2) * NP * 128 + (k & 3) * 32), id,
@@ -1026,7 +1014,7 @@ __global__ void __launch_bounds__(Cfg<D, NP>::kThreads, 1)
                 const uint32_t o = tmem + kTmemO + (C::kAlt ? (j & 1) * NP : 0);
                 const bool first = i < (C::kAlt ? 2 : 1);
                 if (elect_one()) {
-#pragma unroll
+#pragma unroll 1
                     for (int k = 0; k < kNB / 16; ++k)
                         umma_bf16(o, desc_at(vd, k * 2048), desc_at(pd, k * 16 * row), id,
                                   first && k == 0 ? 0u : 1u);
