@@ -143,21 +143,21 @@ struct Cfg {
     static constexpr int kNH = kAlt ? NP : 64;        // columns of a softmax thread
     static constexpr int kCH = kNH < 32 ? kNH : 32;   // ... taken at a time
     static constexpr int kEC = NP / 2;                // columns of a group in the epilogue
-    static constexpr int kSBufs = kAlt ? 4 : 2, kPBufs = kAlt ? 2 : 1, kVBufs = kAlt ? 3 : 2;
+    static constexpr int kSBufs = kAlt ? 4 : 2, kVBufs = kAlt ? 3 : 2, kQBufs = kAlt ? 2 : 1;
     static constexpr int kQ = NP * D * 2, kP = kNB * NP * 2;
     static constexpr int kCodes = kNB * D / 2, kScales = kPB * 128;
     static constexpr int kStage = 2 * (kCodes + kScales);
     static constexpr int kRest = 13312;  // what is behind the tiles, and their alignment
-    static constexpr int kRoom = (232448 - kRest - 2 * kQ - kPBufs * kP - kVBufs * 2 * kSlab) / kStage;
+    static constexpr int kRoom = (232448 - kRest - kQBufs * kQ - 2 * kP - kVBufs * 2 * kSlab) / kStage;
     static constexpr int kStages = kRoom < 8 ? kRoom : 8;
 };
 
 template <int D, int NP>
 struct Smem {
     using C = Cfg<D, NP>;
-    uint8_t q[2][C::kQ];               // [slab][NP rows][128 B], 128-byte swizzle
+    uint8_t q[C::kQBufs][C::kQ];               // [slab][NP rows][128 B], 128-byte swizzle
     uint8_t v[C::kVBufs][2 * kSlab];   // decoded V: [slab][128 tokens][128 B] (D 64: one slab)
-    uint8_t p[C::kPBufs][C::kP];       // weights: [token][NP columns]
+    uint8_t p[2][C::kP];       // weights: [token][NP columns]
     uint8_t kc[C::kStages][C::kCodes], vc[C::kStages][C::kCodes];
     uint8_t ks[C::kStages][C::kScales], vs[C::kStages][C::kScales];
     float negm[2][64];                 // a group's columns: minus the reference maxima (0: none yet)
@@ -344,7 +344,7 @@ __host__ __device__ constexpr uint32_t idesc(int N, int a_mn, int b_mn) {
 // 32 codes and their two scales to 16 f16 pairs.
 __device__ __forceinline__ void decode32(const uint4 &w, uint32_t two_scales, uint32_t *out) {
     const uint32_t s = e4m3x2_to_f16x2(two_scales & 0xffffu);
-    const uint32_t lo = __byte_perm(s, s, 0x1010), hi = __byte_perm(s, s, 0x3232);
+    const __half2 sh = *reinterpret_cast<const __half2 *>(&s); const __half2 l2 = __low2half2(sh), h2 = __high2half2(sh); const uint32_t lo = *reinterpret_cast<const uint32_t *>(&l2), hi = *reinterpret_cast<const uint32_t *>(&h2);
     const uint32_t in[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -370,7 +370,7 @@ __device__ __forceinline__ void st_shared(uint32_t at, uint32_t x, uint32_t y, u
 // share an instruction cache.)
 template <int D>
 __device__ __forceinline__ void decode_row(uint32_t codes, uint2 scales, bool is_v, uint32_t to) {
-#pragma unroll 1
+#pragma unroll 2
     for (int c = 0; c < D / 32; ++c) {
         uint32_t r[16];
         decode32(ld_shared(codes ^ (16 * c)), scales.x, r);
@@ -588,12 +588,13 @@ __device__ __forceinline__ void softmax_role(Smem<D, NP> &sm, const Fp4AttnArgs 
             const bool edge = (i + 1) * kNB > seen;
             unsigned long long vis = ~0ull;
             if (edge && at >= 0) vis = at >= a.n_q ? 0ull : a.slots[at][kAlt ? 0 : g];
-            uint8_t *pt = sm.p[kAlt ? g : 0];
+            uint8_t *pt = sm.p[j & 1];
             uint32_t s[CH];
             auto load = [&](int ch) {
                 tmem_ld(sa + (uint32_t)(ch * CH), s);
                 tmem_ld_wait();
                 if (edge) {
+                    asm volatile("" ::: "memory");  // (a branch, no predicates)
                     const uint32_t v = (uint32_t)(vis >> (ch * CH));
 #pragma unroll
                     for (int c = 0; c < CH; ++c)
@@ -663,7 +664,7 @@ __device__ __forceinline__ void softmax_role(Smem<D, NP> &sm, const Fp4AttnArgs 
                     }
                 }
                 // the weights of block j, once the products that read their place are done
-                const int before = j - C::kPBufs;
+                const int before = j - 2;
                 if (before >= 0) wait(ok, &sm.pv_done[before & 1], before >> 1, a.err);
                 const uint64_t sign2 = pack2(sign, sign);
                 float top = 0.f;
@@ -863,7 +864,7 @@ __global__ void __launch_bounds__(Cfg<D, NP>::kThreads, 1)
         prefetch_tensormap(&mq1);
     }
     // query rows past M are never copied: zeros
-    for (int i = tid; i < 2 * C::kQ / 16; i += C::kThreads)
+    for (int i = tid; i < (int)sizeof(sm.q) / 16; i += C::kThreads)
         reinterpret_cast<uint4 *>(sm.q[0])[i] = make_uint4(0u, 0u, 0u, 0u);
     if (tid < a.M) sm.row_off[tid] = tid / a.G * a.Hq + tid % a.G;
     fence_proxy_async_smem();
@@ -942,22 +943,22 @@ __global__ void __launch_bounds__(Cfg<D, NP>::kThreads, 1)
         for (; w.next(a, p); ++unit) {
             const float kf = fp4_factor(a.k_factor, p.h, a.err);
             if (warp == C::kQueryWarp) {
-                if (unit >= 2) wait(ok, &sm.q_empty[unit & 1], (unit - 2) >> 1, a.err);
+                if (unit >= C::kQBufs) wait(ok, &sm.q_empty[unit % C::kQBufs], unit / C::kQBufs - 1, a.err);
                 if (ok && lane == 0) {
-                    uint64_t *bar = &sm.q_full[unit & 1];
+                    uint64_t *bar = &sm.q_full[unit % C::kQBufs];
                     mbar_arrive_expect_tx(bar, (uint32_t)(a.M * D * 2));
-                    tma_load_4d(sm.q[unit & 1], &mq0, 0, p.h * a.G, 0, p.b, bar, pol);
-                    if (D == 128) tma_load_4d(sm.q[unit & 1] + NP * 128, &mq1, 0, p.h * a.G, 0, p.b, bar, pol);
+                    tma_load_4d(sm.q[unit % C::kQBufs], &mq0, 0, p.h * a.G, 0, p.b, bar, pol);
+                    if (D == 128) tma_load_4d(sm.q[unit % C::kQBufs] + NP * 128, &mq1, 0, p.h * a.G, 0, p.b, bar, pol);
                 }
                 __syncwarp();
             }
             // (also when an earlier wait ran out: what was copied has to land)
             bool landed = true;
-            if (ok) wait(landed, &sm.q_full[unit & 1], unit >> 1, a.err);
+            if (ok) wait(landed, &sm.q_full[unit % C::kQBufs], unit / C::kQBufs, a.err);
             ok = ok && landed;
-            prepare_queries<D, NP>(sm, a, unit & 1, unit, kf, tid);
+            prepare_queries<D, NP>(sm, a, unit % C::kQBufs, unit, kf, tid);
             fence_proxy_async_smem();
-            warp_arrive(&sm.q_ready[unit & 1]);
+            warp_arrive(&sm.q_ready[unit % C::kQBufs]);
         }
     } else if (warp == C::kScoreWarp) {
         // ============================================ S^T = K Q^T
@@ -968,13 +969,13 @@ __global__ void __launch_bounds__(Cfg<D, NP>::kThreads, 1)
 #pragma unroll 1
             for (int i = 0; i < p.n; ++i, ++j) {
                 const int sb = j % C::kSBufs;
-                if (i == 0) wait(ok, &sm.q_ready[unit & 1], unit >> 1, a.err);
+                if (i == 0) wait(ok, &sm.q_ready[unit % C::kQBufs], unit / C::kQBufs, a.err);
                 if (j >= C::kSBufs) wait(ok, &sm.s_empty[sb], j / C::kSBufs - 1, a.err);
                 wait(ok, &sm.k_full[j & 1], j >> 1, a.err);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
-                const uint64_t qd = umma_desc_sw128(smem_u32(sm.q[unit & 1]), 16, 1024);
+                const uint64_t qd = umma_desc_sw128(smem_u32(sm.q[unit % C::kQBufs]), 16, 1024);
                 if (elect_one()) {
 #pragma unroll 1
                     for (int k = 0; k < D / 16; ++k)
@@ -983,7 +984,7 @@ __global__ void __launch_bounds__(Cfg<D, NP>::kThreads, 1)
                                          k == 0 ? 0u : 1u);
                     umma_commit(&sm.k_empty[j & 1]);
                     umma_commit(&sm.s_full[sb]);
-                    if (i == p.n - 1) umma_commit(&sm.q_empty[unit & 1]);
+                    if (i == p.n - 1) umma_commit(&sm.q_empty[unit % C::kQBufs]);
                 }
                 __syncwarp();
             }
@@ -991,7 +992,7 @@ __global__ void __launch_bounds__(Cfg<D, NP>::kThreads, 1)
         // the last arrivals land before the barriers are given up
         if (ok && j > 0) {
             wait(ok, &sm.k_empty[(j - 1) & 1], (j - 1) >> 1, a.err);
-            wait(ok, &sm.q_empty[(unit - 1) & 1], (unit - 1) >> 1, a.err);
+            wait(ok, &sm.q_empty[(unit - 1) % C::kQBufs], (unit - 1) / C::kQBufs, a.err);
         }
     } else if (warp == C::kPvWarp) {
         // ============================================ O^T += V^T P^T
@@ -1010,7 +1011,7 @@ __global__ void __launch_bounds__(Cfg<D, NP>::kThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t vd = umma_desc_sw128(smem_u32(sm.v[vb]), kSlab, 1024);
-                const uint64_t pd = p_desc<NP>(smem_u32(sm.p[j % C::kPBufs]));
+                const uint64_t pd = p_desc<NP>(smem_u32(sm.p[j & 1]));
                 const uint32_t o = tmem + kTmemO + (C::kAlt ? (j & 1) * NP : 0);
                 const bool first = i < (C::kAlt ? 2 : 1);
                 if (elect_one()) {
