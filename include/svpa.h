@@ -1007,8 +1007,9 @@ svpa_status svpa_kv_append_fp4(int32_t batch, int32_t n_new, int32_t num_kv_head
                                void *v_pool, const float *k_factor, const float *v_factor,
                                int32_t *error_flag, void *stream);
 
-/* Bytes of workspace svpa_paged_verify_attn_fp4 needs for `p`; zero-filled once
- * before its first use (every completed call leaves its counters zero). */
+/* Bytes of workspace svpa_paged_verify_attn_fp4 needs for `p`.  It need not be
+ * zero-filled for this call, which does not touch its first 65792 bytes (the
+ * counters and tickets of the calls that it may be shared with). */
 svpa_status svpa_paged_verify_attn_fp4_workspace_size(const svpa_attn_params *p, size_t *bytes);
 
 /*
@@ -1020,7 +1021,8 @@ svpa_status svpa_paged_verify_attn_fp4_workspace_size(const svpa_attn_params *p,
  *  k_pool, v_pool  uint8 [num_blocks, Hkv, 9 D], 16-byte aligned
  *  k_factor, v_factor  fp32 [Hkv] or NULL (1)
  * The other arguments, the masks, `out`, `lse` and the errors are those of
- * svpa_paged_verify_attn; num_blocks * num_kv_heads below 2^31.
+ * svpa_paged_verify_attn; num_blocks * num_kv_heads below 2^31, sequences up to
+ * 2^31 - 144 tokens.  Two kernels on `stream`.
  * Codes times scales are exact; the queries are taken in f16 at one power of
  * two per (sequence, kv head) (what that drops is below 2^-39 of its largest
  * query value), the weights of the softmax are rounded to f16, scores and sums

@@ -23,15 +23,21 @@
 // Work: the 128-token blocks of all (sequence, kv head) pairs, in that order,
 // split evenly over one persistent CTA per SM; the parts of the pairs that are
 // cut are joined by a second kernel.
-// Warps: 0-3 decode K and turn the queries to f16; 4-7 and 8-11 are the softmax
-// and the epilogue; 12-15 decode V; then a warp that copies the queries and one
-// each that issues the MMAs of either product (with 128 columns warps 0-3 decode
-// V too: Cfg).  A decoding warp copies the pages of its own tokens ahead of
-// itself (cp.async), so that no other warp is waited for: by bulk copies of each
-// page's codes and scales, 32 a block at some 95 cycles each, the copies bound
-// the kernel (855 us against the 625 of a copying warp each for K and V, 64 x 1
-// queries of 64 / 8 heads behind 8K to 32K tokens).  A warp reads the TMEM lanes
-// of quadrant warp % 4.  Every role walks the same list of blocks.
+// Warps, up to 64 columns: 0-3 decode K, 12-15 decode V; 4-7 and 8-11 are two
+// softmax groups that take the blocks in turn, and the epilogue; 16 copies the
+// queries and turns them to f16 with 19; 17 and 18 issue the MMAs of P V and of S.
+// (128 columns: Cfg.)  A warp reads the TMEM lanes of quadrant warp % 4.  Every
+// role walks the same list of blocks.
+// A decoding warp copies the pages of its own tokens ahead of itself (cp.async),
+// so that it waits for no other warp.  64 x 1 queries of 64 / 8 heads of 128
+// behind 8K to 32K tokens: bulk copies of each page's codes and scales, 32 a block
+// at some 95 cycles each, 855 us; a copying warp each for K and V 624; this 437.
+//
+// What bounds it: the same workload reads 1.57 GB, 232 us at 6.8 TB/s, and neither
+// DRAM nor the tensor pipe is the limit (most of either product's MMAs, or all
+// copies, can be left out for nothing).  It is the instructions of decoding and of
+// the softmax, and what a block waits for between them: half of the decoding gives
+// 10 to 18%.  64 x 8 queries 532 us, 64 x 16 in trees over 0.5 GB 269 (floor 79).
 // All waits are bounded: a role whose wait ran out goes on without waiting.
 #include <math_constants.h>
 
@@ -64,12 +70,9 @@ __device__ __forceinline__ int blocks_of(const Fp4AttnArgs &a, int L) {
     return L < 0 || pages > a.max_blocks ? 0 : (int)((pages + kPB - 1) / kPB);
 }
 
-// CTAs that get a share of W blocks: a part costs its writing and joining, as much
-// as some blocks, so that a share has kMinShare of them at least.
-constexpr int kMinShare = 1;
-__device__ __forceinline__ int shares_of(long long W) {
-    return (int)min((long long)gridDim.x, (W + kMinShare - 1) / kMinShare);
-}
+// CTAs that get a share of W blocks.  (Shares of at least 2 to 6 blocks, against the
+// cost of writing and joining parts, are slower unless pairs happen to fill them.)
+__device__ __forceinline__ int shares_of(long long W) { return (int)min((long long)gridDim.x, W); }
 
 struct Walk {
     int b, h, f, nb, L;
@@ -155,9 +158,9 @@ struct Cfg {
 template <int D, int NP>
 struct Smem {
     using C = Cfg<D, NP>;
-    uint8_t q[C::kQBufs][C::kQ];               // [slab][NP rows][128 B], 128-byte swizzle
-    uint8_t v[C::kVBufs][2 * kSlab];   // decoded V: [slab][128 tokens][128 B] (D 64: one slab)
-    uint8_t p[2][C::kP];       // weights: [token][NP columns]
+    uint8_t q[C::kQBufs][C::kQ];      // [slab][NP rows][128 B], 128-byte swizzle
+    uint8_t v[C::kVBufs][2 * kSlab];  // decoded V: [slab][128 tokens][128 B] (D 64: one slab)
+    uint8_t p[2][C::kP];              // weights: [token][NP columns]
     uint8_t kc[C::kStages][C::kCodes], vc[C::kStages][C::kCodes];
     uint8_t ks[C::kStages][C::kScales], vs[C::kStages][C::kScales];
     float negm[2][64];                 // a group's columns: minus the reference maxima (0: none yet)
@@ -344,7 +347,10 @@ __host__ __device__ constexpr uint32_t idesc(int N, int a_mn, int b_mn) {
 // 32 codes and their two scales to 16 f16 pairs.
 __device__ __forceinline__ void decode32(const uint4 &w, uint32_t two_scales, uint32_t *out) {
     const uint32_t s = e4m3x2_to_f16x2(two_scales & 0xffffu);
-    const __half2 sh = *reinterpret_cast<const __half2 *>(&s); const __half2 l2 = __low2half2(sh), h2 = __high2half2(sh); const uint32_t lo = *reinterpret_cast<const uint32_t *>(&l2), hi = *reinterpret_cast<const uint32_t *>(&h2);
+    const __half2 pair = *reinterpret_cast<const __half2 *>(&s);
+    const __half2 first = __low2half2(pair), second = __high2half2(pair);
+    const uint32_t lo = *reinterpret_cast<const uint32_t *>(&first);
+    const uint32_t hi = *reinterpret_cast<const uint32_t *>(&second);
     const uint32_t in[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -366,8 +372,9 @@ __device__ __forceinline__ void st_shared(uint32_t at, uint32_t x, uint32_t y, u
 
 // A staged row of codes (32 of them at codes ^ 16 c) to its place as an MMA
 // operand: K's into the TMEM lane at `to`, V's into shared memory (its 16-byte
-// piece k of a slab at to ^ 16 k).  (One rolled loop for both: the roles' loops
-// share an instruction cache.)
+// piece k of a slab at to ^ 16 k).  (Two quarters of a row of 128 at a time: one,
+// 456 us for the workload above against 437; all four 431, but 3 to 6% more for
+// short sequences, whose roles' loops then miss the instruction cache.)
 template <int D>
 __device__ __forceinline__ void decode_row(uint32_t codes, uint2 scales, bool is_v, uint32_t to) {
 #pragma unroll 2
@@ -476,7 +483,8 @@ __device__ __forceinline__ void decode_role(Smem<D, NP> &sm, const Fp4AttnArgs &
                 }
             }
             // (a page that is not there stays as it was: its tokens are masked, its V rows zeroed)
-            const int id0 = __shfl_sync(0xffffffffu, ids, 2 * (ci & 15)), id1 = __shfl_sync(0xffffffffu, ids, 2 * (ci & 15) + 1);
+            const int id0 = __shfl_sync(0xffffffffu, ids, 2 * (ci & 15));
+            const int id1 = __shfl_sync(0xffffffffu, ids, 2 * (ci & 15) + 1);
             // (num_blocks * Hkv is below 2^31)
             const size_t tile0 = (size_t)(uint32_t)(id0 * a.Hkv + ch) * fp4_tile_bytes(D);
             const size_t tile1 = (size_t)(uint32_t)(id1 * a.Hkv + ch) * fp4_tile_bytes(D);
@@ -933,105 +941,106 @@ __global__ void __launch_bounds__(Cfg<D, NP>::kThreads, 1)
         regs_dec<C::kRegsDecode>();
         decode_role<D, NP>(sm, a, w, tmem, 1, 2);
     } else {
-    regs_dec<C::kRegsIssue>();
-    if (warp == C::kQueryWarp || warp == C::kQueryWarp + 3) {
-        // ============================================ the queries: copied, and turned to f16
-        const int tid = (warp == C::kQueryWarp ? 0 : 32) + lane;
-        const uint64_t pol = policy_evict_first();
-        int unit = 0;
-#pragma unroll 1
-        for (; w.next(a, p); ++unit) {
-            const float kf = fp4_factor(a.k_factor, p.h, a.err);
-            if (warp == C::kQueryWarp) {
-                if (unit >= C::kQBufs) wait(ok, &sm.q_empty[unit % C::kQBufs], unit / C::kQBufs - 1, a.err);
-                if (ok && lane == 0) {
-                    uint64_t *bar = &sm.q_full[unit % C::kQBufs];
-                    mbar_arrive_expect_tx(bar, (uint32_t)(a.M * D * 2));
-                    tma_load_4d(sm.q[unit % C::kQBufs], &mq0, 0, p.h * a.G, 0, p.b, bar, pol);
-                    if (D == 128) tma_load_4d(sm.q[unit % C::kQBufs] + NP * 128, &mq1, 0, p.h * a.G, 0, p.b, bar, pol);
+        regs_dec<C::kRegsIssue>();
+        if (warp == C::kQueryWarp || warp == C::kQueryWarp + 3) {
+            // ============================================ the queries: copied, and turned to f16
+            const int tid = (warp == C::kQueryWarp ? 0 : 32) + lane;
+            const uint64_t pol = policy_evict_first();
+            int unit = 0;
+    #pragma unroll 1
+            for (; w.next(a, p); ++unit) {
+                const float kf = fp4_factor(a.k_factor, p.h, a.err);
+                if (warp == C::kQueryWarp) {
+                    if (unit >= C::kQBufs) wait(ok, &sm.q_empty[unit % C::kQBufs], unit / C::kQBufs - 1, a.err);
+                    if (ok && lane == 0) {
+                        uint64_t *bar = &sm.q_full[unit % C::kQBufs];
+                        mbar_arrive_expect_tx(bar, (uint32_t)(a.M * D * 2));
+                        tma_load_4d(sm.q[unit % C::kQBufs], &mq0, 0, p.h * a.G, 0, p.b, bar, pol);
+                        if (D == 128)
+                            tma_load_4d(sm.q[unit % C::kQBufs] + NP * 128, &mq1, 0, p.h * a.G, 0, p.b, bar, pol);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
+                // (also when an earlier wait ran out: what was copied has to land)
+                bool landed = true;
+                if (ok) wait(landed, &sm.q_full[unit % C::kQBufs], unit / C::kQBufs, a.err);
+                ok = ok && landed;
+                prepare_queries<D, NP>(sm, a, unit % C::kQBufs, unit, kf, tid);
+                fence_proxy_async_smem();
+                warp_arrive(&sm.q_ready[unit % C::kQBufs]);
             }
-            // (also when an earlier wait ran out: what was copied has to land)
-            bool landed = true;
-            if (ok) wait(landed, &sm.q_full[unit % C::kQBufs], unit / C::kQBufs, a.err);
-            ok = ok && landed;
-            prepare_queries<D, NP>(sm, a, unit % C::kQBufs, unit, kf, tid);
-            fence_proxy_async_smem();
-            warp_arrive(&sm.q_ready[unit % C::kQBufs]);
-        }
-    } else if (warp == C::kScoreWarp) {
-        // ============================================ S^T = K Q^T
-        const uint32_t id = idesc(NP, 0, 0);
-        int j = 0, unit = 0;
-#pragma unroll 1
-        for (; ok && w.next(a, p); ++unit) {
-#pragma unroll 1
-            for (int i = 0; i < p.n; ++i, ++j) {
-                const int sb = j % C::kSBufs;
-                if (i == 0) wait(ok, &sm.q_ready[unit % C::kQBufs], unit / C::kQBufs, a.err);
-                if (j >= C::kSBufs) wait(ok, &sm.s_empty[sb], j / C::kSBufs - 1, a.err);
-                wait(ok, &sm.k_full[j & 1], j >> 1, a.err);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                tc_fence_after();
-                const uint64_t qd = umma_desc_sw128(smem_u32(sm.q[unit % C::kQBufs]), 16, 1024);
-                if (elect_one()) {
-#pragma unroll 1
-                    for (int k = 0; k < D / 16; ++k)
-                        umma_bf16_tmem_a(tmem + kTmemS + (uint32_t)(sb * NP), tmem + kTmemK + 64 * (j & 1) + 8 * k,
-                                         desc_at(qd, (k >> 2) * NP * 128 + (k & 3) * 32), id,
-                                         k == 0 ? 0u : 1u);
-                    umma_commit(&sm.k_empty[j & 1]);
-                    umma_commit(&sm.s_full[sb]);
-                    if (i == p.n - 1) umma_commit(&sm.q_empty[unit % C::kQBufs]);
+        } else if (warp == C::kScoreWarp) {
+            // ============================================ S^T = K Q^T
+            const uint32_t id = idesc(NP, 0, 0);
+            int j = 0, unit = 0;
+    #pragma unroll 1
+            for (; ok && w.next(a, p); ++unit) {
+    #pragma unroll 1
+                for (int i = 0; i < p.n; ++i, ++j) {
+                    const int sb = j % C::kSBufs;
+                    if (i == 0) wait(ok, &sm.q_ready[unit % C::kQBufs], unit / C::kQBufs, a.err);
+                    if (j >= C::kSBufs) wait(ok, &sm.s_empty[sb], j / C::kSBufs - 1, a.err);
+                    wait(ok, &sm.k_full[j & 1], j >> 1, a.err);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t qd = umma_desc_sw128(smem_u32(sm.q[unit % C::kQBufs]), 16, 1024);
+                    if (elect_one()) {
+    #pragma unroll 1
+                        for (int k = 0; k < D / 16; ++k)
+                            umma_bf16_tmem_a(tmem + kTmemS + (uint32_t)(sb * NP), tmem + kTmemK + 64 * (j & 1) + 8 * k,
+                                             desc_at(qd, (k >> 2) * NP * 128 + (k & 3) * 32), id,
+                                             k == 0 ? 0u : 1u);
+                        umma_commit(&sm.k_empty[j & 1]);
+                        umma_commit(&sm.s_full[sb]);
+                        if (i == p.n - 1) umma_commit(&sm.q_empty[unit % C::kQBufs]);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
             }
-        }
-        // the last arrivals land before the barriers are given up
-        if (ok && j > 0) {
-            wait(ok, &sm.k_empty[(j - 1) & 1], (j - 1) >> 1, a.err);
-            wait(ok, &sm.q_empty[(unit - 1) % C::kQBufs], (unit - 1) / C::kQBufs, a.err);
-        }
-    } else if (warp == C::kPvWarp) {
-        // ============================================ O^T += V^T P^T
-        const uint32_t id = idesc(NP, 1, 1);
-        constexpr uint32_t row = NP < 64 ? 2 * NP : 128;  // bytes of a token's weights
-        int j = 0, unit = 0;
-#pragma unroll 1
-        for (; ok && w.next(a, p); ++unit) {
-#pragma unroll 1
-            for (int i = 0; i < p.n; ++i, ++j) {
-                const int vb = j % C::kVBufs;
-                if (i == 0 && unit > 0) wait(ok, &sm.o_empty, unit - 1, a.err);
-                wait(ok, &sm.v_full[vb], j / C::kVBufs, a.err);
-                wait(ok, &sm.p_full[j & 1], j >> 1, a.err);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                tc_fence_after();
-                const uint64_t vd = umma_desc_sw128(smem_u32(sm.v[vb]), kSlab, 1024);
-                const uint64_t pd = p_desc<NP>(smem_u32(sm.p[j & 1]));
-                const uint32_t o = tmem + kTmemO + (C::kAlt ? (j & 1) * NP : 0);
-                const bool first = i < (C::kAlt ? 2 : 1);
-                if (elect_one()) {
-#pragma unroll 1
-                    for (int k = 0; k < kNB / 16; ++k)
-                        umma_bf16(o, desc_at(vd, k * 2048), desc_at(pd, k * 16 * row), id,
-                                  first && k == 0 ? 0u : 1u);
-                    umma_commit(&sm.pv_done[j & 1]);
-                    umma_commit(&sm.v_empty[vb]);
-                    if (i == p.n - 1) umma_commit(&sm.o_full);
+            // the last arrivals land before the barriers are given up
+            if (ok && j > 0) {
+                wait(ok, &sm.k_empty[(j - 1) & 1], (j - 1) >> 1, a.err);
+                wait(ok, &sm.q_empty[(unit - 1) % C::kQBufs], (unit - 1) / C::kQBufs, a.err);
+            }
+        } else if (warp == C::kPvWarp) {
+            // ============================================ O^T += V^T P^T
+            const uint32_t id = idesc(NP, 1, 1);
+            constexpr uint32_t row = NP < 64 ? 2 * NP : 128;  // bytes of a token's weights
+            int j = 0, unit = 0;
+    #pragma unroll 1
+            for (; ok && w.next(a, p); ++unit) {
+    #pragma unroll 1
+                for (int i = 0; i < p.n; ++i, ++j) {
+                    const int vb = j % C::kVBufs;
+                    if (i == 0 && unit > 0) wait(ok, &sm.o_empty, unit - 1, a.err);
+                    wait(ok, &sm.v_full[vb], j / C::kVBufs, a.err);
+                    wait(ok, &sm.p_full[j & 1], j >> 1, a.err);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t vd = umma_desc_sw128(smem_u32(sm.v[vb]), kSlab, 1024);
+                    const uint64_t pd = p_desc<NP>(smem_u32(sm.p[j & 1]));
+                    const uint32_t o = tmem + kTmemO + (C::kAlt ? (j & 1) * NP : 0);
+                    const bool first = i < (C::kAlt ? 2 : 1);
+                    if (elect_one()) {
+    #pragma unroll 1
+                        for (int k = 0; k < kNB / 16; ++k)
+                            umma_bf16(o, desc_at(vd, k * 2048), desc_at(pd, k * 16 * row), id,
+                                      first && k == 0 ? 0u : 1u);
+                        umma_commit(&sm.pv_done[j & 1]);
+                        umma_commit(&sm.v_empty[vb]);
+                        if (i == p.n - 1) umma_commit(&sm.o_full);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
+            }
+            if (ok && j > 0) {
+                wait(ok, &sm.pv_done[(j - 1) & 1], (j - 1) >> 1, a.err);
+                wait(ok, &sm.v_empty[(j - 1) % C::kVBufs], (j - 1) / C::kVBufs, a.err);
+                wait(ok, &sm.o_full, unit - 1, a.err);
             }
         }
-        if (ok && j > 0) {
-            wait(ok, &sm.pv_done[(j - 1) & 1], (j - 1) >> 1, a.err);
-            wait(ok, &sm.v_empty[(j - 1) % C::kVBufs], (j - 1) / C::kVBufs, a.err);
-            wait(ok, &sm.o_full, unit - 1, a.err);
-        }
-    }
     }
     tc_fence_before();
     __syncthreads();

@@ -174,9 +174,12 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant
     int part = warp & ((1 << a.split_log) - 1);
     auto fetch = [&](int at, uint4 (&x)[kWords]) {
         const int kind = at < qc ? 0 : at < qc + kc ? 1 : 2;
-        const int heads = kind == 0 ? a.Hq : a.Hkv, h0 = (at - (kind == 0 ? 0 : kind == 1 ? qc : qc + kc)) * kChunk + lane / kLanes;
-        const uint16_t *src = (kind == 0 ? a.q + t * a.q_stride : kind == 1 ? a.k + t * a.k_stride : a.v + t * a.v_stride) +
-                              h0 * D + c * 8;
+        const int heads = kind == 0 ? a.Hq : a.Hkv, begin = kind == 0 ? 0 : kind == 1 ? qc : qc + kc;
+        const int h0 = (at - begin) * kChunk + lane / kLanes;
+        const uint16_t *row = kind == 0   ? a.q + t * a.q_stride
+                              : kind == 1 ? a.k + t * a.k_stride
+                                          : a.v + t * a.v_stride;
+        const uint16_t *src = row + h0 * D + c * 8;
 #pragma unroll
         for (int i = 0; i < kWords; ++i) {
             x[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -264,7 +267,8 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant
             for (int i = 0; i < kWords; ++i) {
                 if ((part - qc) * kChunk + i * kHeads >= a.Hkv) break;
                 const int h = h0 + i * kHeads;
-                const uint4 y = turn_key<D>(x[i], wt, cs, sn, a.k_weight != nullptr, a.eps, mate, turns, low, interleaved, lane);
+                const uint4 y = turn_key<D>(x[i], wt, cs, sn, a.k_weight != nullptr, a.eps, mate, turns, low,
+                                            interleaved, lane);
                 if constexpr (P == Pages::kRows) {
                     if (h < a.Hkv) reinterpret_cast<uint4 *>(a.k_out + t * a.k_out_stride + (long long)h * D)[c] = y;
                 } else {
@@ -283,7 +287,8 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant
             for (int i = 0; i < kWords; ++i) {
                 if ((part - qc - kc) * kChunk + i * kHeads >= a.Hkv) break;
                 const int h = h0 + i * kHeads;
-                store_row<P, D>(x[i], h < a.Hkv, h, c, a.Hkv, tile, slot % kBlockSize, a.v_pool, a.v_scale, a.v_factor, a.err);
+                store_row<P, D>(x[i], h < a.Hkv, h, c, a.Hkv, tile, slot % kBlockSize, a.v_pool, a.v_scale, a.v_factor,
+                                a.err);
             }
             if (part + (1 << a.split_log) < parts) fetch(part + (1 << a.split_log), x);
         }
@@ -348,7 +353,8 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
                 uint8_t *to = reinterpret_cast<uint8_t *>(kv ? a.v + t * a.v_stride : a.k + t * a.k_stride) + 32LL * w;
                 if ((reinterpret_cast<uintptr_t>(to) & 31) == 0) {
                     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(out[0]),
-                                 "r"(out[1]), "r"(out[2]), "r"(out[3]), "r"(out[4]), "r"(out[5]), "r"(out[6]), "r"(out[7])
+                                 "r"(out[1]), "r"(out[2]), "r"(out[3]), "r"(out[4]), "r"(out[5]), "r"(out[6]),
+                                 "r"(out[7])
                                  : "memory");
                 } else {
                     reinterpret_cast<uint4 *>(to)[0] = make_uint4(out[0], out[1], out[2], out[3]);
@@ -401,11 +407,14 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
 }
 
 // Warps a token (log2): few enough that a warp's angles serve several parts, and
-// enough warps for the GPU.  SPLITNOTE
+// enough warps for the GPU.  Queries and keys of 64 + 8 heads of 128, by 1, 2, 4
+// and 8 warps a token: 8192 tokens 58.2, 55.4, 65.7 and 91.0 us (floor 45.2); 24
+// tokens 12.6, 8.2, 6.0 and 4.7.  Into 4-bit pages, 16384 tokens: 136, 133, 177
+// and 245 us (floor 93).
 int split_log(long long tokens, int parts) {
     const long long want = 32LL * sm_count();
     int s = 0;
-    while (s < 3 && (tokens << s) < want && (1 << s) < parts) ++s;
+    while (s < 3 && (1 << s) < parts && (s == 0 || (tokens << s) < want)) ++s;
     return s;
 }
 
@@ -442,7 +451,8 @@ cudaError_t launch_rope(const RopeArgs &a, int D, Pages pages, cudaStream_t stre
 cudaError_t launch_kv_read(const ReadArgs &args, Pages pages, cudaStream_t stream) {
     ReadArgs a = args;
     const int wpr = a.Hkv * (a.D / 8);
-    const int parts = pages == Pages::kFp4 ? (wpr + 32 * kWords - 1) / (32 * kWords) : 2 * ((wpr + 32 * kWords - 1) / (32 * kWords));
+    const int chunks = (wpr + 32 * kWords - 1) / (32 * kWords);
+    const int parts = pages == Pages::kFp4 ? chunks : 2 * chunks;  // (of 32 and of 16 bytes out a lane)
     a.split_log = parts > 4 ? 3 : parts > 2 ? 2 : parts > 1 ? 1 : 0;
     // w / (D / 16) as a product's high word: exact for w (D / 16) < 2^32
     a.magic = a.D >= 32 ? (unsigned)(((1ull << 32) + a.D / 16 - 1) / (a.D / 16)) : 0u;

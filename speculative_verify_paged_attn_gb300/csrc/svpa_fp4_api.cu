@@ -97,7 +97,7 @@ svpa_status check_attn(const svpa_attn_params *p) {
     if (p->head_dim != 64 && p->head_dim != 128) return SVPA_ERR_UNSUPPORTED;
     if ((long long)p->num_q_heads / p->num_kv_heads * p->n_q > kMaxRows || p->batch > 65535 ||
         p->num_kv_heads > 65535 || (long long)p->num_blocks * p->num_kv_heads > 0x7fffffffLL ||
-        p->max_blocks_per_seq > kMaxPoolBlocks)
+        p->max_blocks_per_seq > kMaxPoolBlocks - 8)  // (positions rounded up to 128 stay int32)
         return SVPA_ERR_UNSUPPORTED;
     return SVPA_OK;
 }
