@@ -30,14 +30,19 @@
 // role walks the same list of blocks.
 // A decoding warp copies the pages of its own tokens ahead of itself (cp.async),
 // so that it waits for no other warp.  64 x 1 queries of 64 / 8 heads of 128
-// behind 8K to 32K tokens: bulk copies of each page's codes and scales, 32 a block
-// at some 95 cycles each, 855 us; a copying warp each for K and V 624; this 437.
+// behind 8K to 32K tokens: tiled bulk copies of each page's codes and scales, 32 a
+// block at some 95 cycles each, 855 us; a copying warp each for K and V 624; this
+// 416; whole pages by untiled bulk copies into padded places 488, whose rows then
+// lie two to a bank.
 //
 // What bounds it: the same workload reads 1.57 GB, 232 us at 6.8 TB/s, and neither
-// DRAM nor the tensor pipe is the limit (most of either product's MMAs, or all
-// copies, can be left out for nothing).  It is the instructions of decoding and of
-// the softmax, and what a block waits for between them: half of the decoding gives
-// 10 to 18%.  64 x 8 queries 532 us, 64 x 16 in trees over 0.5 GB 269 (floor 79).
+// DRAM nor the tensor pipe is the limit (most of either product's MMAs can be left
+// out for nothing).  A warp that decodes V is busy for nine tenths of a block's
+// time (1,400 cycles: 850 decoding, 450 issuing copies); doubling those warps takes
+// the registers of the softmax and gains nothing.  Shared memory is the limit next
+// to it: pages written and read, V written and read as an operand, weights, 112 to
+// 148 KB a block, 60% of its bandwidth.  With 6 queries 514 us; 64 trees of 29
+// nodes, 32 / 8 heads, behind 1K to 8K tokens 263 (floor 79).
 // All waits are bounded: a role whose wait ran out goes on without waiting.
 #include <math_constants.h>
 
@@ -372,26 +377,32 @@ __device__ __forceinline__ void st_shared(uint32_t at, uint32_t x, uint32_t y, u
 
 // A staged row of codes (32 of them at codes ^ 16 c) to its place as an MMA
 // operand: K's into the TMEM lane at `to`, V's into shared memory (its 16-byte
-// piece k of a slab at to ^ 16 k).  (Two quarters of a row of 128 at a time: one,
-// 456 us for the workload above against 437; all four 431, but 3 to 6% more for
-// short sequences, whose roles' loops then miss the instruction cache.)
+// piece k of a slab at to ^ 16 k).  (Two quarters of a row of 128 at a time: one
+// costs 4% more; all four gain 1% on long sequences and cost short ones 3 to 6%,
+// whose roles' loops share an instruction cache.)
 template <int D>
 __device__ __forceinline__ void decode_row(uint32_t codes, uint2 scales, bool is_v, uint32_t to) {
-#pragma unroll 2
-    for (int c = 0; c < D / 32; ++c) {
+#pragma unroll 1
+    for (int c = 0; c < D / 32; c += 2) {
+        const uint4 w0 = ld_shared(codes ^ (16 * c)), w1 = ld_shared(codes ^ (16 * c + 16));
         uint32_t r[16];
-        decode32(ld_shared(codes ^ (16 * c)), scales.x, r);
+        decode32(w0, scales.x, r);
         if (is_v) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                st_shared((to ^ (16 * k)) ^ ((c & 1) << 6), r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
-            if (c & 1) to += kSlab;
+            for (int k = 0; k < 4; ++k) st_shared(to ^ (16 * k), r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
         } else {
             tmem_st(to, r);
-            to += 16;
         }
-        scales.x = __funnelshift_r(scales.x, scales.y, 16);  // the next two
-        scales.y >>= 16;
+        decode32(w1, scales.x >> 16, r);
+        if (is_v) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) st_shared(to ^ (16 * k + 64), r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+            to += kSlab;
+        } else {
+            tmem_st(to + 16, r);
+            to += 32;
+        }
+        scales.x = scales.y;  // the next two
     }
 }
 
@@ -449,12 +460,14 @@ __device__ __forceinline__ void decode_role(Smem<D, NP> &sm, const Fp4AttnArgs &
     Cursor &cur = sm.cursor[warp], &ahead = sm.ahead[part + (warp & 4)];
     cur.begin(a, w);
     ahead.begin(a, w);
-    // where a lane's 16 bytes of a page's codes go (in the swizzle that makes the
-    // rows' reads free of conflicts), and of two pages' scales
+    // half a warp copies a page, 256 bytes of its codes at a time: where a lane's 16
+    // go (in the swizzle that makes the rows' reads free of conflicts; 128
+    // dimensions: ^ 32 in the odd quarters), and those of the scales
     constexpr int kRowChunks = D / 32, kScaleLanes = D / 16;
-    const int row = lane / kRowChunks, sw = D == 128 ? (row >> 1) & 3 : (row >> 2) & 1;
-    const uint32_t code_dst = (uint32_t)(2 * part * kCodePage + row * (D / 2) + (((lane % kRowChunks) ^ sw) << 4));
-    const uint32_t scale_dst = (uint32_t)(2 * part * 128 + (lane / kScaleLanes) * 128 + (lane % kScaleLanes) * 16);
+    const int half = lane >> 4, hl = lane & 15, page = 2 * part + half;
+    const uint32_t code_dst = (uint32_t)(page * kCodePage + (hl / kRowChunks) * (D / 2) +
+                                         (((hl % kRowChunks) ^ (hl >> 3)) << 4));
+    const uint32_t scale_dst = (uint32_t)(page * 128 + hl * 16);
     // this thread's row of a stage (the swizzle is in the address already), its scales and its V row
     const uint32_t raw0 = smem_u32(kv0 ? sm.vc[0] : sm.kc[0]), raws0 = smem_u32(kv0 ? sm.vs[0] : sm.ks[0]);
     const uint32_t my_codes = (uint32_t)(t * (D / 2)) + ((D == 128 ? (t >> 1) & 3 : (t >> 2) & 1) << 4);
@@ -483,28 +496,21 @@ __device__ __forceinline__ void decode_role(Smem<D, NP> &sm, const Fp4AttnArgs &
                 }
             }
             // (a page that is not there stays as it was: its tokens are masked, its V rows zeroed)
-            const int id0 = __shfl_sync(0xffffffffu, ids, 2 * (ci & 15));
-            const int id1 = __shfl_sync(0xffffffffu, ids, 2 * (ci & 15) + 1);
-            // (num_blocks * Hkv is below 2^31)
-            const size_t tile0 = (size_t)(uint32_t)(id0 * a.Hkv + ch) * fp4_tile_bytes(D);
-            const size_t tile1 = (size_t)(uint32_t)(id1 * a.Hkv + ch) * fp4_tile_bytes(D);
-            const bool second = lane >= kScaleLanes;
+            const int id = __shfl_sync(0xffffffffu, ids, 2 * (ci & 15) + half);
+            if (id >= 0) {
+                // (num_blocks * Hkv is below 2^31)
+                const size_t at = (size_t)(uint32_t)(id * a.Hkv + ch) * fp4_tile_bytes(D) + (uint32_t)(16 * hl);
 #pragma unroll 1
-            for (int kv = kv0; kv < kv1; ++kv) {
-                const uint8_t *pool = (kv ? a.v_pool : a.k_pool) + lane * 16;
-                const bool next = kv != kv0;
-                const uint32_t dst = raw0 + (next ? kToV : 0u) + cst * C::kCodes + code_dst;
-                if (id0 >= 0) {
-                    cp_async_16(dst, pool + tile0);
-                    if (D == 128) cp_async_16(dst + 512, pool + tile0 + 512);
+                for (int kv = kv0; kv < kv1; ++kv) {
+                    const uint8_t *src = (kv ? a.v_pool : a.k_pool) + at;
+                    const bool next = kv != kv0;
+                    const uint32_t dst = raw0 + (next ? kToV : 0u) + cst * C::kCodes + code_dst;
+#pragma unroll
+                    for (int k = 0; k < kCodePage / 256; ++k)
+                        cp_async_16((D == 128 && (k & 1) ? dst ^ 32 : dst) + 256 * k, src + 256 * k);
+                    if (hl < kScaleLanes)
+                        cp_async_16(raws0 + (next ? kToVs : 0u) + cst * C::kScales + scale_dst, src + kCodePage);
                 }
-                if (id1 >= 0) {
-                    cp_async_16(dst + kCodePage, pool + tile1);
-                    if (D == 128) cp_async_16(dst + kCodePage + 512, pool + tile1 + 512);
-                }
-                if (lane < 2 * kScaleLanes && (second ? id1 : id0) >= 0)
-                    cp_async_16(raws0 + (next ? kToVs : 0u) + cst * C::kScales + scale_dst,
-                                pool + (second ? tile1 - kScaleLanes * 16 : tile0) + fp4_code_bytes(D));
             }
             ++ci;
             cst = cst + 1 == kStages ? 0 : cst + 1;
@@ -522,8 +528,7 @@ __device__ __forceinline__ void decode_role(Smem<D, NP> &sm, const Fp4AttnArgs &
         int left = p.L + a.n_q - p.f * kNB - t;  // > 0: this thread's token is one of the sequence's
 #pragma unroll 1
         for (int i = 0; i < n; ++i, ++j, left -= kNB) {
-            copy_block();
-            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
             __syncwarp();
 #pragma unroll 1
             for (int kv = kv0; kv < kv1; ++kv) {
@@ -551,6 +556,7 @@ __device__ __forceinline__ void decode_role(Smem<D, NP> &sm, const Fp4AttnArgs &
                     warp_arrive(&sm.k_full[j & 1]);
                 }
             }
+            copy_block();  // (behind the arrivals: the products begin meanwhile)
             st = st + 1 == kStages ? 0 : st + 1;
         }
     }
