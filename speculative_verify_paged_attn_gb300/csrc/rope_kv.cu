@@ -295,8 +295,9 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant
     }
 }
 
-// Row t of the pages, slot_map[t], as bf16: each value rounded once.
-template <Pages P>
+// Row t of the pages, slot_map[t], as bf16: each value rounded once.  A lane takes W
+// groups at a time.
+template <Pages P, int W>
 __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ ReadArgs a) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long token = (long long)blockIdx.x * ((kThreads / 32) >> a.split_log) + (warp >> a.split_log);
@@ -316,13 +317,13 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
         // scale, 32 bytes out
         const int gph = a.D / 16, gpr = a.Hkv * gph;
 #pragma unroll 1
-        for (; part * 32 * kWords < 2 * gpr; part += 1 << a.split_log) {
-            const int c0 = part * 32 * kWords + lane;
-            uint2 codes[kWords];
-            uint32_t sc[kWords];
-            float f[kWords];
+        for (; part * 32 * W < 2 * gpr; part += 1 << a.split_log) {
+            const int c0 = part * 32 * W + lane;
+            uint2 codes[W];
+            uint32_t sc[W];
+            float f[W];
 #pragma unroll
-            for (int i = 0; i < kWords; ++i) {
+            for (int i = 0; i < W; ++i) {
                 const int u = c0 + 32 * i, kv = u >= gpr, w = kv ? u - gpr : u;
                 if (u >= 2 * gpr) break;
                 const int h = gph == 1 ? w : (int)__umulhi((unsigned)w, a.magic), g = w - h * gph;
@@ -332,7 +333,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
                 f[i] = fp4_factor(kv ? a.v_factor : a.k_factor, h, a.err);
             }
 #pragma unroll
-            for (int i = 0; i < kWords; ++i) {
+            for (int i = 0; i < W; ++i) {
                 const int u = c0 + 32 * i, kv = u >= gpr, w = kv ? u - gpr : u;
                 if (u >= 2 * gpr) break;
                 uint32_t p[8], out[8];
@@ -364,16 +365,16 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
         }
     } else {
         const int wph = a.D / 8, wpr = a.Hkv * wph;  // 16-byte words of a head and of a row
-        const int chunks = (wpr + 32 * kWords - 1) / (32 * kWords);
+        const int chunks = (wpr + 32 * W - 1) / (32 * W);
 #pragma unroll 1
         for (; part < 2 * chunks; part += 1 << a.split_log) {
-            const int kv = part >= chunks, c0 = (part - kv * chunks) * 32 * kWords + lane;
+            const int kv = part >= chunks, c0 = (part - kv * chunks) * 32 * W + lane;
             const uint8_t *pool = kv ? a.v_pool : a.k_pool;
             uint4 *dst = reinterpret_cast<uint4 *>(kv ? a.v + t * a.v_stride : a.k + t * a.k_stride);
-            uint4 raw[kWords];
-            float scale[kWords];
+            uint4 raw[W];
+            float scale[W];
 #pragma unroll
-            for (int i = 0; i < kWords; ++i) {
+            for (int i = 0; i < W; ++i) {
                 const int w = c0 + 32 * i, h = (int)((unsigned)w / (unsigned)wph), c = w - h * wph;
                 if (w >= wpr) break;
                 const long long row = (tile0 + h) * kBlockSize + at;
@@ -386,7 +387,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
                 }
             }
 #pragma unroll
-            for (int i = 0; i < kWords; ++i) {
+            for (int i = 0; i < W; ++i) {
                 const int w = c0 + 32 * i;
                 if (w >= wpr) break;
                 if constexpr (P == Pages::kFp8) {
@@ -448,19 +449,33 @@ cudaError_t launch_rope(const RopeArgs &a, int D, Pages pages, cudaStream_t stre
     }
 }
 
-cudaError_t launch_kv_read(const ReadArgs &args, Pages pages, cudaStream_t stream) {
-    ReadArgs a = args;
-    const int wpr = a.Hkv * (a.D / 8);
-    const int chunks = (wpr + 32 * kWords - 1) / (32 * kWords);
-    const int parts = pages == Pages::kFp4 ? chunks : 2 * chunks;  // (of 32 and of 16 bytes out a lane)
+namespace {
+
+template <Pages P, int W>
+cudaError_t launch_read(ReadArgs a, cudaStream_t stream) {
+    const int wpr = a.Hkv * (a.D / 8), chunks = (wpr + 32 * W - 1) / (32 * W);
+    const int parts = P == Pages::kFp4 ? chunks : 2 * chunks;  // (of 32 and of 16 bytes out a lane)
     a.split_log = parts > 4 ? 3 : parts > 2 ? 2 : parts > 1 ? 1 : 0;
     // w / (D / 16) as a product's high word: exact for w (D / 16) < 2^32
     a.magic = a.D >= 32 ? (unsigned)(((1ull << 32) + a.D / 16 - 1) / (a.D / 16)) : 0u;
-    const unsigned grid = grid_of(a.T, a.split_log);
-    if (pages == Pages::kBf16) read_kernel<Pages::kBf16><<<grid, kThreads, 0, stream>>>(a);
-    else if (pages == Pages::kFp8) read_kernel<Pages::kFp8><<<grid, kThreads, 0, stream>>>(a);
-    else read_kernel<Pages::kFp4><<<grid, kThreads, 0, stream>>>(a);
+    read_kernel<P, W><<<grid_of(a.T, a.split_log), kThreads, 0, stream>>>(a);
     return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv_read(const ReadArgs &a, Pages pages, cudaStream_t stream) {
+    if (pages == Pages::kBf16) return launch_read<Pages::kBf16, kWords>(a, stream);
+    if (pages == Pages::kFp8) return launch_read<Pages::kFp8, kWords>(a, stream);
+    // A group a lane while all warps run at once, four then, and eight of long rows
+    // of many tokens.  By 1, 4 and 8: 700 tokens of 8 heads of 128 2.4, 3.0 and 3.1
+    // us; 65536 of them 80.4, 58.1 and 58.7 (floor 50.8); 16000 of 32 heads 65.1, 58.0
+    // and 54.2 (floor 49.6), 600 of them 3.6, 3.9 and 4.7.
+    const int wpr = a.Hkv * (a.D / 8);  // groups of a token's K and V
+    const long long warps = (long long)a.T * ((wpr + 31) / 32);
+    if (warps <= 64LL * sm_count()) return launch_read<Pages::kFp4, 1>(a, stream);
+    if (wpr >= 256 && warps > 512LL * sm_count()) return launch_read<Pages::kFp4, 8>(a, stream);
+    return launch_read<Pages::kFp4, kWords>(a, stream);
 }
 
 }  // namespace svpa

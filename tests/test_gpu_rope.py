@@ -349,3 +349,25 @@ def test_far_slots():
     want = F.values(*F.encode(x.k, torch.ones(hkv, device=DEV)), torch.ones(hkv, device=DEV))
     assert torch.equal(ko.double(), want)
     assert int((pool != 0).flatten(1).any(1).sum()) == 4
+
+
+@pytest.mark.parametrize("t,hkv,d", [(1, 1, 64), (300, 32, 128), (3000, 8, 128), (9000, 3, 128), (5000, 40, 128),
+                                     (4999, 33, 128)])
+def test_reads_of_any_length(t, hkv, d):
+    """Few rows, many, and many of long rows: every slot of a pool in an order of its own, two pages never named."""
+    g = gen(t)
+    blocks = -(-t // BS) + 2
+    pool = [torch.randint(0, 256, (blocks, hkv, 9 * d), generator=g, device=DEV).to(torch.uint8) for _ in range(2)]
+    for p in pool:  # scales that the writes store
+        p[..., 8 * d:] &= 0x7f
+        p[..., 8 * d:].clamp_(max=0x7e)
+    slots = torch.randperm((blocks - 2) * BS, generator=g, device=DEV)[:t].to(torch.int32)
+    out = torch.full((2, t, hkv + 1, d), float("nan"), dtype=BF, device=DEV)
+    kf, vf = factors(hkv, t), factors(hkv, t + 1)
+    err = ints([0])
+    svpa.kv_read(slots, *pool, out[0, :, :hkv], out[1, :, :hkv], error_flag=err, fp4=True, k_factor=kf, v_factor=vf)
+    assert svpa.check_error(err) == 0
+    for got, p, f in zip(out, pool, (kf, vf)):
+        want = F.pool_values(p, f)[slots.long() // BS, slots.long() % BS]
+        # code times scale is exact; one product in fp32, one rounding to bf16
+        assert torch.equal(got[:, :hkv], want.float().to(BF)) and torch.isnan(got[:, hkv:]).all()
