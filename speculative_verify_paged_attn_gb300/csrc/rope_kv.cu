@@ -26,7 +26,7 @@ namespace svpa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWords = 4;  // 16-byte words a lane takes
+constexpr int kWords = 4;  // 16-byte words a lane takes (few tokens: 1 or 2)
 
 __device__ __forceinline__ void unpack8(const uint4 &x, float (&f)[8]) {
     f[0] = bf16_lo(x.x), f[1] = bf16_hi(x.x), f[2] = bf16_lo(x.y), f[3] = bf16_hi(x.y);
@@ -155,13 +155,13 @@ __device__ __forceinline__ uint4 turn_key(const uint4 &x, const float (&wt)[8], 
     return pack8(f);
 }
 
-// A token's queries, keys and values are parts of kChunk heads; `split` warps
-// (a power of two up to 8) share a token's parts.
-template <Pages P, int D>
+// A token's queries, keys and values are parts of kChunk heads; 1 << split_log
+// warps of each of gridDim.y CTAs share them.
+template <Pages P, int D, int W>
 __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant__ RopeArgs a) {
     constexpr int kLanes = D / 8;              // of a head
     constexpr int kHeads = 32 / kLanes;        // a warp holds at a time
-    constexpr int kChunk = kHeads * kWords;    // heads a warp takes
+    constexpr int kChunk = kHeads * W;    // heads a warp takes
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long token = (long long)blockIdx.x * ((kThreads / 32) >> a.split_log) + (warp >> a.split_log);
     if (token >= a.T) return;
@@ -171,8 +171,9 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant
     if (a.R > 0) pos = __ldg(a.positions + t);
     const int qc = (a.Hq + kChunk - 1) / kChunk, kc = (a.Hkv + kChunk - 1) / kChunk;
     const int parts = qc + (P == Pages::kRows ? 1 : 2) * kc;
-    int part = warp & ((1 << a.split_log) - 1);
-    auto fetch = [&](int at, uint4 (&x)[kWords]) {
+    const int stride = (int)gridDim.y << a.split_log;
+    int part = (warp & ((1 << a.split_log) - 1)) + ((int)blockIdx.y << a.split_log);
+    auto fetch = [&](int at, uint4 (&x)[W]) {
         const int kind = at < qc ? 0 : at < qc + kc ? 1 : 2;
         const int heads = kind == 0 ? a.Hq : a.Hkv, begin = kind == 0 ? 0 : kind == 1 ? qc : qc + kc;
         const int h0 = (at - begin) * kChunk + lane / kLanes;
@@ -181,12 +182,12 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant
                                           : a.v + t * a.v_stride;
         const uint16_t *src = row + h0 * D + c * 8;
 #pragma unroll
-        for (int i = 0; i < kWords; ++i) {
+        for (int i = 0; i < W; ++i) {
             x[i] = make_uint4(0u, 0u, 0u, 0u);
             if (h0 + i * kHeads < heads) x[i] = __ldcs(reinterpret_cast<const uint4 *>(src + i * kHeads * D));
         }
     };
-    uint4 x[kWords];
+    uint4 x[W];
     if (part < parts) fetch(part, x);
     if constexpr (P != Pages::kRows) {
         if (slot < 0) return;  // a padding row
@@ -240,19 +241,19 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant
             ws[j] = (interleaved ? (j & 1) == 0 : low) ? -s : s;
         }
 #pragma unroll 1
-        for (; part < qc; part += 1 << a.split_log) {
+        for (; part < qc; part += stride) {
             const int h0 = part * kChunk + lane / kLanes;
             uint16_t *dst = a.q_out + t * a.q_out_stride + h0 * D + c * 8;
-            uint4 ahead[kWords];
-            if (part + (1 << a.split_log) < parts) fetch(part + (1 << a.split_log), ahead);
+            uint4 ahead[W];
+            if (part + stride < parts) fetch(part + stride, ahead);
 #pragma unroll
-            for (int i = 0; i < kWords; ++i) {
+            for (int i = 0; i < W; ++i) {
                 if (part * kChunk + i * kHeads >= a.Hq) break;  // the same for the whole warp
                 const uint4 y = turn_query<D>(x[i], wc, ws, wq != nullptr, a.eps, mate, turns, interleaved);
                 if (h0 + i * kHeads < a.Hq) *reinterpret_cast<uint4 *>(dst + i * kHeads * D) = y;
             }
 #pragma unroll
-            for (int i = 0; i < kWords; ++i) x[i] = ahead[i];
+            for (int i = 0; i < W; ++i) x[i] = ahead[i];
         }
     }
     const long long tile = (long long)(slot / kBlockSize) * a.Hkv;
@@ -261,10 +262,10 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant
         angles(cs, sn);
         if (a.k_weight) unpack8(__ldg(reinterpret_cast<const uint4 *>(a.k_weight) + c), wt);
 #pragma unroll 1
-        for (; part < qc + kc; part += 1 << a.split_log) {
+        for (; part < qc + kc; part += stride) {
             const int h0 = (part - qc) * kChunk + lane / kLanes;
 #pragma unroll
-            for (int i = 0; i < kWords; ++i) {
+            for (int i = 0; i < W; ++i) {
                 if ((part - qc) * kChunk + i * kHeads >= a.Hkv) break;
                 const int h = h0 + i * kHeads;
                 const uint4 y = turn_key<D>(x[i], wt, cs, sn, a.k_weight != nullptr, a.eps, mate, turns, low,
@@ -276,21 +277,21 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant
                                     a.err);
                 }
             }
-            if (part + (1 << a.split_log) < parts) fetch(part + (1 << a.split_log), x);
+            if (part + stride < parts) fetch(part + stride, x);
         }
     }
     if constexpr (P != Pages::kRows) {
 #pragma unroll 1
-        for (; part < parts; part += 1 << a.split_log) {
+        for (; part < parts; part += stride) {
             const int h0 = (part - qc - kc) * kChunk + lane / kLanes;
 #pragma unroll
-            for (int i = 0; i < kWords; ++i) {
+            for (int i = 0; i < W; ++i) {
                 if ((part - qc - kc) * kChunk + i * kHeads >= a.Hkv) break;
                 const int h = h0 + i * kHeads;
                 store_row<P, D>(x[i], h < a.Hkv, h, c, a.Hkv, tile, slot % kBlockSize, a.v_pool, a.v_scale, a.v_factor,
                                 a.err);
             }
-            if (part + (1 << a.split_log) < parts) fetch(part + (1 << a.split_log), x);
+            if (part + stride < parts) fetch(part + stride, x);
         }
     }
 }
@@ -424,13 +425,34 @@ unsigned grid_of(long long tokens, int split) {
     return (unsigned)((tokens + per - 1) / per);
 }
 
-template <Pages P, int D>
+// (the parts of a token, of W words a lane)
+template <Pages P, int D, int W>
+int parts_of(const RopeArgs &a) {
+    constexpr int kChunk = 32 / (D / 8) * W;
+    return (a.Hq + kChunk - 1) / kChunk + (P == Pages::kRows ? 1 : 2) * ((a.Hkv + kChunk - 1) / kChunk);
+}
+
+template <Pages P, int D, int W>
 cudaError_t launch(RopeArgs a, cudaStream_t stream) {
-    constexpr int kChunk = 32 / (D / 8) * kWords;
-    const int qc = (a.Hq + kChunk - 1) / kChunk, kc = (a.Hkv + kChunk - 1) / kChunk;
-    a.split_log = split_log(a.T, qc + (P == Pages::kRows ? 1 : 2) * kc);
-    rope_kernel<P, D><<<grid_of(a.T, a.split_log), kThreads, 0, stream>>>(a);
+    const int parts = parts_of<P, D, W>(a);
+    a.split_log = split_log(a.T, parts);
+    // few tokens: more CTAs for each (up to 64 warps)
+    const bool few = a.split_log == 3 && (long long)a.T * 8 < 32LL * sm_count();
+    const unsigned more = few ? (unsigned)min((parts + 7) / 8, 8) : 1u;
+    rope_kernel<P, D, W><<<dim3(grid_of(a.T, a.split_log), more), kThreads, 0, stream>>>(a);
     return cudaGetLastError();
+}
+
+// Words a lane: all of a token's loads at once, one or two words a lane, while the
+// GPU has the warps for it.  64 + 8 heads of 128 by 1, 2 and 4: 24 tokens 2.5, 2.7
+// and 3.2 us (4.7 in one CTA a token); 100 tokens 4.3, 3.3 and 3.9; 600 tokens 13.0,
+// 9.8 and 8.7.  Into 4-bit pages: 57 tokens 3.4, 3.9 and 5.2 us (6.7 in one CTA a
+// token), 200 tokens 6.8, 6.1 and 6.4, 1200 tokens 29.5, 21.5 and 22.6.
+template <Pages P, int D>
+cudaError_t launch(const RopeArgs &a, cudaStream_t stream) {
+    if ((long long)a.T * parts_of<P, D, 1>(a) <= 16LL * sm_count()) return launch<P, D, 1>(a, stream);
+    if ((long long)a.T * parts_of<P, D, 2>(a) <= 24LL * sm_count()) return launch<P, D, 2>(a, stream);
+    return launch<P, D, kWords>(a, stream);
 }
 
 template <Pages P>
