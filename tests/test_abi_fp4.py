@@ -147,7 +147,8 @@ def attn_status(lib, null=(), odd=(), mask=None, bytes_=1 << 40, **kw):
     (dict(sm_scale=0.0), 1), (dict(sm_scale=float("inf")), 1), (dict(split_pages=-1), 1), (dict(variant=1), 1),
     (dict(scale_tile=64), 1), (dict(kv_dtype=0), 1), (dict(kv_dtype=1), 1), (dict(head_dim=96), 2),
     (dict(n_q=33), 2), (dict(batch=65536), 2), (dict(num_blocks=1 << 30, num_kv_heads=2), 2),
-    (dict(max_blocks_per_seq=1 << 27), 2), (dict(max_blocks_per_seq=(1 << 27) - 8), 2), (dict(batch=0), 0), (dict(mask=[1, 2, 3]), 1), (dict(mask=[1, 3, 15]), 1),
+    (dict(max_blocks_per_seq=1 << 27), 2), (dict(max_blocks_per_seq=(1 << 27) - 8), 2), (dict(batch=0), 0),
+    (dict(mask=[1, 2, 3]), 1), (dict(mask=[1, 3, 15]), 1),
     (dict(bytes_=255), 6),
 ])
 def test_attention_sizes(lib, kw, status):
