@@ -498,27 +498,38 @@ def _page_args(k_pool, v_pool, k_scale, v_scale, k_factor, v_factor, Hkv: int, D
                   _arr(k_factor, _F32, Hkv, "k_factor"), _arr(v_factor, _F32, Hkv, "v_factor")]
 
 
-def _rows(t, like, what: str) -> int:
-    """The token stride of bf16 rows t [T, H, D] of `like`'s shape."""
-    if t.dtype is not _BF16 or t.dim() != 3 or t.shape != like.shape:
-        raise SvpaError(1, f"{what}: bf16 [tokens, heads, head_dim] of {tuple(like.shape)} expected")
-    return _row_stride(t, what)
+def _rows(t, shape, what: str) -> int:
+    """The token stride of bf16 rows t of that shape [T, H, D] (as _row_stride)."""
+    if t.dtype is not _BF16 or t.shape != shape or len(shape) != 3:
+        raise SvpaError(1, f"{what}: bf16 [tokens, heads, head_dim] of {tuple(shape)} expected")
+    tokens, heads, d = shape
+    s0, s1, s2 = t.stride()
+    if tokens > 0 and (s2 != 1 or (heads > 1 and s1 != d)):
+        raise SvpaError(1, f"{what}: the values of a token are not contiguous")
+    return s0 if tokens > 1 else heads * d
 
 
 def _rope_params(q, k, v, q_out, k_out, cos_sin, eps, interleaved, kind=SVPA_KV_BF16, num_blocks=1,
                  scale_tile=0) -> RopeParams:
-    T, Hkv, D = k.shape
-    if cos_sin is not None and cos_sin.dim() != 2:
-        raise SvpaError(1, "cos_sin: [max_position, rotary_dim] expected")
+    shape = k.shape
+    T, Hkv, D = shape
+    rows, rot = 1, 0
+    if cos_sin is not None:
+        if cos_sin.dim() != 2:
+            raise SvpaError(1, "cos_sin: [max_position, rotary_dim] expected")
+        rows, rot = cos_sin.shape
     if (q is None) != (q_out is None):
         raise SvpaError(1, "q and q_out: both or neither")
-    ks = _rows(k, k, "k")
-    if q is not None and (q.shape[0] != T or q.shape[2] != D):
-        raise SvpaError(1, "q: the tokens and head dimension of k expected")
-    return RopeParams(T, 0 if q is None else q.shape[1], Hkv, D, 0 if cos_sin is None else cos_sin.shape[1],
-                      int(interleaved), 1 if cos_sin is None else cos_sin.shape[0], 16, num_blocks, kind, scale_tile,
-                      float(eps), 0 if q is None else _rows(q, q, "q"), ks, ks if v is None else _rows(v, k, "v"),
-                      0 if q is None else _rows(q_out, q, "q_out"), ks if k_out is None else _rows(k_out, k, "k_out"))
+    ks = _rows(k, shape, "k")
+    Hq = qs = qos = 0
+    if q is not None:
+        qshape = q.shape
+        qs, qos, Hq = _rows(q, qshape, "q"), _rows(q_out, qshape, "q_out"), qshape[1]
+        if qshape[0] != T or qshape[2] != D:
+            raise SvpaError(1, "q: the tokens and head dimension of k expected")
+    return RopeParams(T, Hq, Hkv, D, rot, int(interleaved), rows, 16, num_blocks, kind, scale_tile, float(eps), qs, ks,
+                      ks if v is None else _rows(v, shape, "v"), qos,
+                      ks if k_out is None else _rows(k_out, shape, "k_out"))
 
 
 def qk_norm_rope(q, k, positions, cos_sin, q_out, k_out, *, error_flag, q_weight=None, k_weight=None, eps=1e-6,
@@ -565,7 +576,7 @@ def kv_read(slot_map, k_pool, v_pool, k_out, v_out, *, error_flag, k_scale=None,
     pages as bf16 rows k_out, v_out [T, Hkv, D]."""
     T, Hkv, D = k_out.shape
     kind, pages = _page_args(k_pool, v_pool, k_scale, v_scale, k_factor, v_factor, Hkv, D, fp4)
-    ks, vs = _rows(k_out, k_out, "k_out"), _rows(v_out, k_out, "v_out")
+    ks, vs = _rows(k_out, k_out.shape, "k_out"), _rows(v_out, k_out.shape, "v_out")
     st = load().svpa_kv_read(T, Hkv, D, 16, k_pool.shape[0], kind, scale_tile, _arr(slot_map, _I32, T, "slot_map"),
                              *pages, _p(k_out), _p(v_out), ks, vs, _arr(error_flag, _I32, 1, "error_flag"),
                              _stream(stream))
