@@ -286,3 +286,45 @@ def test_empty_batch():
     c.p.batch = 0
     c.call()
     assert svpa.check_error(c.err) == 0 and torch.isnan(c.out).all()
+
+
+def test_pages_far_in_the_pool():
+    """Pools of more than 2^32 bytes: the same sequences in pages at their ends."""
+    c = Case([200, 33], 3, 8, 2, 64, seed=11)
+    c.call()
+    c.check()
+    near, lse = c.out.clone(), c.lse.clone()
+    blocks = 3_800_000  # 4.4 GB each
+    shift = blocks - c.p.num_blocks
+    far = [torch.zeros((blocks, 2, 9 * 64), dtype=torch.uint8, device=DEV) for _ in range(2)]
+    for big, small in zip(far, (c.kp, c.vp)):
+        big[shift:] = small
+    p = svpa.attn_params(2, 3, 8, 2, 64, c.w, blocks, kv_fp4=True, sm_scale=c.scale)
+    table = torch.where(c.table < c.p.num_blocks, c.table + shift, c.table)
+    c.out.fill_(float("nan"))
+    svpa.paged_verify_attn_fp4(p, c.q, *far, table, c.cl, c.out, workspace=c.ws, error_flag=c.err, k_factor=c.kf,
+                               v_factor=c.vf, lse=c.lse)
+    assert svpa.check_error(c.err) == 0 and torch.equal(c.out, near) and torch.equal(c.lse, lse)
+
+
+def test_captured_graphs_of_one_workspace_in_turn():
+    a, b = Case([900, 40], 5, 16, 2, 128, seed=12), Case([300] * 7, 1, 8, 8, 64, seed=13)
+    ws = torch.zeros(max(a.ws.numel(), b.ws.numel()), dtype=torch.uint8, device=DEV)
+    graphs, side = [], torch.cuda.Stream()
+    for c in (a, b):
+        c.call(ws=ws)
+        c.check()
+        c.first = c.out.clone(), c.lse.clone()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            c.call(ws=ws)
+        graphs.append(g)
+    for _ in range(3):
+        for c, g in zip((a, b), graphs):
+            c.out.fill_(float("nan"))
+            g.replay()
+    torch.cuda.synchronize()
+    for c in (a, b):
+        assert svpa.check_error(c.err) == 0
+        assert torch.equal(c.first[0], c.out) and torch.equal(c.first[1], c.lse)

@@ -371,3 +371,14 @@ def test_reads_of_any_length(t, hkv, d):
         want = F.pool_values(p, f)[slots.long() // BS, slots.long() % BS]
         # code times scale is exact; one product in fp32, one rounding to bf16
         assert torch.equal(got[:, :hkv], want.float().to(BF)) and torch.isnan(got[:, hkv:]).all()
+
+
+@pytest.mark.parametrize("t", [1, 60, 61, 200, 300, 620, 1300, 2600])
+def test_a_token_does_not_depend_on_the_others(t):
+    """The same tokens alone and among many: each number of words a lane and of warps a token."""
+    x = Rows(2600, 64, 8, 128, 128, fused=True, seed=7)
+    q, k = x.rotated()
+    y = Rows(2600, 64, 8, 128, 128, fused=True, seed=7)
+    y.t, y.q, y.k, y.v, y.pos = t, y.q[:t], y.k[:t], y.v[:t], y.pos[:t]
+    got = y.rotated()
+    assert torch.equal(got[0], q[:t]) and torch.equal(got[1], k[:t])
