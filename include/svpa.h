@@ -996,7 +996,10 @@ svpa_status svpa_kv_read(int32_t num_tokens, int32_t num_kv_heads, int32_t head_
  * svpa_kv_append for 4-bit pages: the same allocation, copy-on-write and
  * errors; each new row is encoded by itself, history rows keep their codes and
  * slots past the last row are left as they were.  k_factor, v_factor: fp32
- * [Hkv] or NULL.  head_dim a multiple of 16 up to 1024.  Two kernels.
+ * [Hkv] or NULL.  A value that is not finite and a factor out of range raise
+ * SVPA_DEVERR_BAD_VALUE before the first row is written: here too no row is
+ * written when any bit is set.  head_dim a multiple of 16 up to 1024.  Two
+ * kernels.
  */
 svpa_status svpa_kv_append_fp4(int32_t batch, int32_t n_new, int32_t num_kv_heads,
                                int32_t head_dim, int32_t block_size,

@@ -62,12 +62,40 @@ __device__ int pop_block(const AppendArgs &a) {
     return blk;
 }
 
+// 4-bit pages: every value is finite and every head's factor in range.  CTA
+// `part` of `parts` takes its share of the new rows, kCheckWords 16-byte words a
+// thread in flight; they are in L2 when the write kernel reads them.
+constexpr int kCheckWords = 8;
+
+__device__ void check_rows_fp4(const AppendArgs &a, int part, int parts) {
+    const size_t words = (size_t)a.B * a.n_new * a.Hkv * (a.D / 8);  // of K and of V
+    const uint4 *k = reinterpret_cast<const uint4 *>(a.new_k), *v = reinterpret_cast<const uint4 *>(a.new_v);
+    uint32_t top = 0u;
+    for (size_t w0 = (size_t)part * kCheckWords * kAllocThreads + threadIdx.x; w0 < 2 * words;
+         w0 += (size_t)parts * kCheckWords * kAllocThreads) {
+        uint4 x[kCheckWords];
+#pragma unroll
+        for (int i = 0; i < kCheckWords; ++i) {
+            const size_t w = w0 + (size_t)i * kAllocThreads;
+            x[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (w < 2 * words) x[i] = w < words ? k[w] : v[w - words];
+        }
+#pragma unroll
+        for (int i = 0; i < kCheckWords; ++i) top = max(top, bf16_amax8(x[i]));
+    }
+    if (top > 0x7f7fu) raise_error(a.err, SVPA_DEVERR_BAD_VALUE);
+    if (part != 0) return;
+    for (int h = threadIdx.x; h < a.Hkv; h += kAllocThreads)
+        fp4_factor(a.k_factor, h, a.err), fp4_factor(a.v_factor, h, a.err);
+}
+
 __global__ void __launch_bounds__(kAllocThreads) append_alloc_kernel(const __grid_constant__ AppendArgs a) {
     __shared__ int s_src[kMaxAppendPages], s_dst[kMaxAppendPages];
     __shared__ int s_ncow;
     // the write kernel may be scheduled now; it waits for this grid's completion
     asm volatile("griddepcontrol.launch_dependents;");
     const int b = blockIdx.x;
+    if (b >= a.B) return check_rows_fp4(a, b - a.B, (int)gridDim.x - a.B);
     const int L = a.context_lens[b];
     const long long end = (long long)L + a.n_new;
     if (threadIdx.x == 0) s_ncow = 0;
@@ -403,9 +431,10 @@ __global__ void __launch_bounds__(kWriteThreads) append_write_kernel(const __gri
 
 // 4-bit pages: a warp takes 128 16-byte words (eight elements each) of one new
 // row of K or V, all kv heads, four a lane, loaded before the wait; a scale's two
-// words are neighbouring lanes'.  256 sequences of 8 rows of 32 heads of 128: 18.4
-// us with the allocation before it (33 in the bf16 form's rounds with 64-bit
-// divisions and loads behind the wait; 6.3 for its bytes).
+// words are neighbouring lanes'.  256 sequences of 8 rows of 32 heads of 128: 20.1
+// us with the allocation and the check before it (18.8 without the check; 33 in
+// the bf16 form's rounds with 64-bit divisions and loads behind the wait; 6.3 for
+// its bytes).
 constexpr int kFp4Words = 4;
 
 __global__ void __launch_bounds__(kWriteThreads) append_write_fp4_kernel(const __grid_constant__ AppendArgs a) {
@@ -443,10 +472,11 @@ __global__ void __launch_bounds__(kWriteThreads) append_write_fp4_kernel(const _
         uint32_t amax = bf16_amax8(x[k]);
         amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         if (w >= wpr) continue;
-        if (amax > 0x7f7fu) raise_error(a.err, SVPA_DEVERR_BAD_VALUE);
         const int h = (int)__umulhi((unsigned)w, a.magic), c = w - h * wph;
+        // (values and factors have been checked)
+        const float *factor = kv ? a.v_factor : a.k_factor;
         uint32_t scale;
-        const uint32_t codes = fp4_encode8(x[k], amax, fp4_factor(kv ? a.v_factor : a.k_factor, h, a.err), scale);
+        const uint32_t codes = fp4_encode8(x[k], amax, factor ? __ldg(factor + h) : 1.f, scale);
         uint8_t *page = pages + (size_t)h * fp4_tile_bytes(D);
         reinterpret_cast<uint32_t *>(page + slot * (D / 2))[c] = codes;
         if ((c & 1) == 0) page[fp4_code_bytes(D) + slot * (D / 16) + c / 2] = (uint8_t)scale;
@@ -456,7 +486,14 @@ __global__ void __launch_bounds__(kWriteThreads) append_write_fp4_kernel(const _
 }  // namespace
 
 cudaError_t launch_kv_append(const AppendArgs &a, cudaStream_t stream) {
-    append_alloc_kernel<<<a.B, kAllocThreads, 0, stream>>>(a);
+    size_t checks = 0;  // CTAs behind the sequences' own
+    if (a.fp4) {
+        const size_t words = (size_t)2 * a.B * a.n_new * a.Hkv * (a.D / 8), per = (size_t)kCheckWords * kAllocThreads;
+        const size_t most = (size_t)8 * sm_count();
+        checks = (words + per - 1) / per;
+        if (checks > most) checks = most;
+    }
+    append_alloc_kernel<<<(unsigned)(a.B + checks), kAllocThreads, 0, stream>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     // (sequence, touched page, group of units); launched as a programmatic
