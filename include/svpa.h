@@ -1028,10 +1028,12 @@ svpa_status svpa_paged_verify_attn_fp4_workspace_size(const svpa_attn_params *p,
  * 2^31 - 144 tokens.  Two kernels on `stream`.
  * Codes times scales are exact; the queries are taken in f16 at one power of
  * two per (sequence, kv head) (what that drops is below 2^-39 of its largest
- * query value), the weights of the softmax are rounded to f16, scores and sums
- * are fp32.  Scale bytes of positions that a query sees are those that the
- * writes store (0 to 0x7e).  A query that is not finite raises
- * SVPA_DEVERR_BAD_VALUE.
+ * query value), scores and sums are fp32.  The weights of the softmax are
+ * rounded to f16 for their product with V: by up to 2^-11 of themselves, or,
+ * below 2^-19 of the row's largest weight, by up to 2^-30 of that one (2^17 such
+ * tokens change a row by less than 2^-13 of their largest value).  Scale bytes
+ * of positions that a query sees are those that the writes store (0 to 0x7e).  A
+ * query that is not finite raises SVPA_DEVERR_BAD_VALUE.
  */
 svpa_status svpa_paged_verify_attn_fp4(const svpa_attn_params *p, const void *q,
                                        const void *k_pool, const void *v_pool,
