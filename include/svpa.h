@@ -970,9 +970,10 @@ svpa_status svpa_rope_kv_write(const svpa_rope_params *p, const void *q, const v
                                int32_t *error_flag, void *stream);
 
 /*
- * Rows of pages back as bf16, through a slot map: the inverse of the writes
- * (an FP8 or 4-bit value rounded to bf16 once).  A prompt whose first part is
- * held in 4 bits goes on over bf16 pages with it.
+ * Rows of pages back as bf16, through a slot map: the inverse of the writes.
+ * An FP8 code times its scale, and a 4-bit code times its scale (exact) times
+ * its head's factor, is one fp32 product, which is then rounded to bf16.  A
+ * prompt whose first part is held in 4 bits goes on over bf16 pages with it.
  *
  *  slot_map     int32 [T]: row t is read from page slot_map[t] / 16, row
  *               slot_map[t] % 16; negative: row t of the outputs is left as it

@@ -297,8 +297,8 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant
     }
 }
 
-// Row t of the pages, slot_map[t], as bf16: each value rounded once.  A lane takes W
-// groups at a time.
+// Row t of the pages, slot_map[t], as bf16: one fp32 product with the scale or the
+// factor, then one rounding.  A lane takes W groups at a time.
 template <Pages P, int W>
 __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ ReadArgs a) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
