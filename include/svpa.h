@@ -947,13 +947,15 @@ svpa_status svpa_qk_norm_rope(const svpa_rope_params *p, const void *q, const vo
  * svpa_qk_norm_rope with the keys, and the values as they are, written into
  * their pages through a slot map, as svpa_kv_write does with finished rows:
  * the pages hold what they would hold after svpa_qk_norm_rope and a write of
- * its bf16 rows.
+ * its bf16 rows.  (A value that 4 bits cannot hold is reported, and what its 16
+ * elements hold then is not defined; the other rows are written.)
  *
  *  v            bf16 [T, Hkv, D], tokens v_stride apart
  *  slot_map     int32 [T]: row t goes to page slot_map[t] / 16, row
- *               slot_map[t] % 16; negative: a padding row, of which nothing is
- *               read or written, its query included; past the pool:
- *               SVPA_DEVERR_BAD_BLOCK.  Two rows with the same slot: what that
+ *               slot_map[t] % 16; negative: a padding row, whose values,
+ *               query and position may be anything and of which nothing is
+ *               written, its query included; past the pool:
+ *               SVPA_DEVERR_BAD_BLOCK, and that row is not written.  Two rows with the same slot: what that
  *               slot holds is unspecified.  Other slots are left as they were.
  *  k_pool, v_pool  bf16 or E4M3 [num_blocks, Hkv, 16, D], or 4-bit pages
  *  k_scale, v_scale  FP8: fp32 [num_blocks, Hkv, 16, D / 64], as svpa_kv_write;
