@@ -491,7 +491,7 @@ def _page_args(k_pool, v_pool, k_scale, v_scale, k_factor, v_factor, Hkv: int, D
     """The pool, scale and factor pointers of a call on pages of any kind, and its kv_dtype."""
     kind, pool = _page_kind(k_pool, fp4)
     blocks = k_pool.shape[0]
-    page = blocks * Hkv * (9 * D if fp4 else 16 * D)
+    page = blocks * Hkv * (fp4_page_bytes(D) if fp4 else 16 * D)
     scales = blocks * Hkv * 16 * (D // 64) if kind == SVPA_KV_FP8_E4M3 else 0
     return kind, [_arr(k_pool, pool, page, "k_pool"), _arr(v_pool, pool, page, "v_pool"),
                   _arr(k_scale, _F32, scales, "k_scale"), _arr(v_scale, _F32, scales, "v_scale"),
@@ -591,7 +591,7 @@ def kv_append_fp4(new_k, new_v, block_table, context_lens, refcount, free_stack,
     pages uint8 [num_blocks, Hkv, 9 D]."""
     B, n_new, Hkv, D = new_k.shape
     blocks, n = k_pool.shape[0], B * n_new * Hkv * D
-    page = blocks * Hkv * 9 * D
+    page = blocks * Hkv * fp4_page_bytes(D)
     st = load().svpa_kv_append_fp4(
         B, n_new, Hkv, D, 16, block_table.shape[1], blocks, _arr(new_k, _BF16, n, "new_k"),
         _arr(new_v, _BF16, n, "new_v"), _arr(block_table, _I32, B * block_table.shape[1], "block_table"),
@@ -620,7 +620,7 @@ def paged_verify_attn_fp4(params: AttnParams, q, k_pool, v_pool, block_table, co
     if m is not None and len(m) < params.n_q:
         raise SvpaError(1, "svpa_paged_verify_attn_fp4: one ancestor mask per query")
     b, d, h = params.batch, params.head_dim, params.num_kv_heads
-    rows, page = b * params.n_q * params.num_q_heads, params.num_blocks * h * 9 * d
+    rows, page = b * params.n_q * params.num_q_heads, params.num_blocks * h * fp4_page_bytes(d)
     st = load().svpa_paged_verify_attn_fp4(
         ctypes.byref(params), _arr(q, _BF16, rows * d, "q"), _arr(k_pool, _U8, page, "k_pool"),
         _arr(v_pool, _U8, page, "v_pool"), _arr(k_factor, _F32, h, "k_factor"), _arr(v_factor, _F32, h, "v_factor"),
