@@ -925,7 +925,8 @@ typedef struct svpa_rope_params {
  *   n = x / sqrt(mean(x^2) + eps) * weight       (x itself without a weight)
  *   (a, b) -> (a cos - b sin, b cos + a sin)     for its R / 2 pairs, with the
  *                                                 angles of positions[t]
- * in fp32, rounded to bf16 once.
+ * in fp32 (which a row of magnitudes beyond 2^59 can leave), rounded to bf16
+ * once.
  *
  *  q, k         bf16 [T, Hq, D], [T, Hkv, D], tokens q_stride, k_stride apart
  *  positions    int32 [T], 0..max_position - 1 (not read when R is 0); another
@@ -955,8 +956,9 @@ svpa_status svpa_qk_norm_rope(const svpa_rope_params *p, const void *q, const vo
  *               slot_map[t] % 16; negative: a padding row, whose values,
  *               query and position may be anything and of which nothing is
  *               written, its query included; past the pool:
- *               SVPA_DEVERR_BAD_BLOCK, and that row is not written.  Two rows with the same slot: what that
- *               slot holds is unspecified.  Other slots are left as they were.
+ *               SVPA_DEVERR_BAD_BLOCK, and that row is not written.  Two rows
+ *               with the same slot: what that slot holds is unspecified.  Other
+ *               slots are left as they were.
  *  k_pool, v_pool  bf16 or E4M3 [num_blocks, Hkv, 16, D], or 4-bit pages
  *  k_scale, v_scale  FP8: fp32 [num_blocks, Hkv, 16, D / 64], as svpa_kv_write;
  *               else NULL

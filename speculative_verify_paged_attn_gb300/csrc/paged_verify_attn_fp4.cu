@@ -39,17 +39,20 @@
 // so that it waits for no other warp.  64 x 1 queries of 64 / 8 heads of 128
 // behind 8K to 32K tokens: tiled bulk copies of each page's codes and scales, 32 a
 // block at some 95 cycles each, 855 us; a copying warp each for K and V 624; this
-// 416; whole pages by untiled bulk copies into padded places 488, whose rows then
-// lie two to a bank.
+// 532, and 414 with the later steps; whole pages by untiled bulk copies into padded
+// places 488, whose rows then lie two to a bank.
 //
-// What bounds it: the same workload reads 1.57 GB, 232 us at 6.8 TB/s, and neither
-// DRAM nor the tensor pipe is the limit (most of either product's MMAs can be left
-// out for nothing).  A warp that decodes V is busy for nine tenths of a block's
-// time (1,400 cycles: 850 decoding, 450 issuing copies); doubling those warps takes
-// the registers of the softmax and gains nothing.  Shared memory is the limit next
-// to it: pages written and read, V written and read as an operand, weights, 112 to
-// 148 KB a block, 60% of its bandwidth.  With 6 queries 514 us; 64 trees of 29
-// nodes, 32 / 8 heads, behind 1K to 8K tokens 263 (floor 79).
+// The same workload reads 1.57 GB: 232 us at 6.8 TB/s.  No unit is saturated at 414:
+// DRAM 56%; shared memory 60% (112 KB a block of 1,500 cycles; with 6 queries, 519
+// us, 979 wavefronts and 64 KB of operands in 1,950); with 6 queries the tensor pipe
+// 26% and the issue slots 59%.  The busiest warps are V's, 1,300 of a block's 1,500
+// cycles (850 decoding, 450 issuing copies).  Left out, by 1 and by 6 queries: all
+// copies 402, 510; all decoding 344, 457; all but one column's softmax 411, 441; seven
+// eighths of both products' MMAs 409, 490; all of that but the scores' MMAs at once
+// 335, 352.  So two thirds of the time and more is the chain of handovers of a block
+// between the roles (scores, vote, weights, product), which two blocks in flight do
+// not cover; which links of it has not been measured.  29-node trees of 32/8 heads, 64 behind 1K to 8K
+// tokens: 264 (79 for their products).
 // All waits are bounded: a role whose wait ran out goes on without waiting.
 #include <math_constants.h>
 
@@ -503,7 +506,9 @@ __device__ __forceinline__ void decode_role(Smem<D, NP> &sm, const Fp4AttnArgs &
                     }
                 }
             }
-            // (a page that is not there stays as it was: its tokens are masked, its V rows zeroed)
+            // (A page behind the sequence's last is not copied: its tokens are masked, their V
+            // rows zeroed.  Nor is one whose id was refused: what the stage held goes into that
+            // sequence's rows, and the call reports it.)
             const int id = __shfl_sync(0xffffffffu, ids, 2 * (ci & 15) + half);
             if (id >= 0) {
                 // (num_blocks * Hkv is below 2^31)

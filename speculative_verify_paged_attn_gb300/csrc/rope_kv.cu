@@ -17,8 +17,9 @@
 // bytes), a head is D / 8 lanes, and a warp takes up to four words a lane of one
 // token's queries, keys or values, all in flight together; a pair's other half
 // comes by a shuffle.  The token's cosines and sines are read once for the
-// warp's heads.  8192 tokens of 64 + 8 heads of 128: 55.5 us, 81% of the copy rate;
-// bound by instructions (67% of the issue slots) before memory.
+// warp's heads.  8192 tokens of 64 + 8 heads of 128: 55.6 us, 81% of the copy rate.
+// No unit is saturated (issue slots 68%, ALU 49%, a third of the warps resident):
+// an issue waits as long for memory as for shuffles.
 #include "fp4.cuh"
 #include "rope_kv.h"
 
